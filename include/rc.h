@@ -496,6 +496,174 @@ int rc_decode_attention(const rc_decode_args* args, void* workspace, size_t work
 #define RC_DECODE_STATIC_SCRATCH_BYTES ((size_t)32 << 20)
 int rc_decode_attention_noalloc(const rc_decode_args* args, void* stream);
 
+/* Norms of queries and keys for each head, with the position rotation in the same pass: what a
+ * model does to q and k between its projections and rc_extend_attention / rc_decode_attention.
+ * For every head row x (d elements) of q and of k:
+ *   n_j = x_j * w_j / sqrt(mean_j(x_j^2) + eps)           (w = q_weight or k_weight; NULL: n = x)
+ *   a' = a cos - b sin,  b' = b cos + a sin               for the pairs (a, b) of the first
+ *                                                         rotary_dim elements of n
+ * in fp32, rounded once to dtype. Pair i is (n_i, n_{i + rotary_dim/2}), or (n_{2i}, n_{2i+1}) when
+ * `interleaved`; its cosine and sine are rope[position][i] and rope[position][rotary_dim/2 + i]
+ * (rc_rope_table). rotary_dim 0: norms only. q [T, Hq, d] and k [T, Hkv, d] with strides in
+ * elements (slices of a fused projection); elements of a head are contiguous. Outputs may be the
+ * inputs themselves (same pointer and strides), else they must not overlap them. num_q_heads or
+ * num_kv_heads 0: that part is left out. positions [T] device int32; a token whose position is
+ * outside [0, max_position) sets the device status word and its rows are not written.
+ * head_dim a multiple of 8 up to 256, rotary_dim a multiple of 16; pointers and strides multiples
+ * of 16 bytes. */
+typedef struct rc_qk_norm_rope_args {
+  int32_t dtype;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float eps;
+  int64_t num_tokens;
+  int64_t max_position;      /* rows of rope */
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  const void* k;
+  int64_t k_token_stride, k_head_stride;
+  const void* q_weight;      /* [d] in dtype, or NULL */
+  const void* k_weight;
+  const int32_t* positions;  /* [T]; NULL when rotary_dim = 0 */
+  const float* rope;         /* [max_position, rotary_dim] fp32 */
+  void* q_out;
+  int64_t q_out_token_stride, q_out_head_stride;
+  void* k_out;
+  int64_t k_out_token_stride, k_out_head_stride;
+} rc_qk_norm_rope_args;
+int rc_qk_norm_rope(const rc_qk_norm_rope_args* args, void* stream);
+
+/* The rotation's table, computed in double precision on the host: out[p][i] = scale *
+ * cos((first_position + p) * inv_freq[i]) for i < num_pairs, then the sines; out is host fp32
+ * [num_positions, 2 * num_pairs]. inv_freq (host) carries any frequency scaling, scale any factor
+ * on the rotated values. num_pairs a multiple of 8 up to 128. */
+int rc_rope_table(const double* inv_freq, int32_t num_pairs, int64_t first_position,
+                  int64_t num_positions, double scale, float* out);
+
+/* Appends keys and values to the paged cache, the keys normalised and rotated on the way. Request
+ * b's new tokens t = qo_indptr[b] + i stand at positions prefix_len[b] + i; token t's key (norm with
+ * k_weight unless NULL, rotation unless rotary_dim = 0; formulas of rc_qk_norm_rope, rounded once)
+ * goes to k_pool[out_loc[t]], its value as it is to v_pool[out_loc[t]]. Rows of k, v and out_loc
+ * past qo_indptr[B] (a padded batch) are not read. Slots of out_loc are distinct.
+ * With `bounds` (layout of rc_kv_block_bounds) the bounds of the request's row req_idx[b] follow: a
+ * block of positions that the new tokens begin gets the bounds of their stored keys, a block that
+ * tokens before prefix_len[b] began takes the minimum and maximum with what it holds. Rows of one
+ * call are distinct. A request outside the arrays, its row's blocks or the table sets the device
+ * status word and is skipped; so is a token whose slot is outside the pool.
+ * k, v [T, Hkv, d] with strides in elements, heads' elements contiguous; head_dim, rotary_dim and
+ * alignment as for rc_qk_norm_rope. */
+typedef struct rc_kv_append_args {
+  int32_t dtype;
+  int32_t num_reqs;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float eps;
+  int32_t block;             /* positions per block of bounds: 16, 32, 64 or 128 */
+  int64_t num_tokens;        /* rows of k, v and out_loc, >= qo_indptr[B] */
+  int64_t num_slots;
+  int64_t max_position;
+  const void* k;
+  int64_t k_token_stride, k_head_stride;
+  const void* v;
+  int64_t v_token_stride, v_head_stride;
+  const int32_t* out_loc;    /* [T] */
+  const int32_t* qo_indptr;  /* [B + 1] */
+  const int32_t* prefix_len; /* [B] */
+  const void* k_weight;
+  const float* rope;
+  void* k_pool;
+  void* v_pool;
+  void* bounds;              /* NULL: none */
+  const int32_t* req_idx;    /* [B], used with bounds */
+  int32_t max_reqs;          /* rows of bounds */
+  int32_t max_blocks;        /* blocks per row of bounds */
+} rc_kv_append_args;
+int rc_kv_append(const rc_kv_append_args* args, void* stream);
+
+/* Bounds of cached keys, block by block: for row n with seq_len[n] cached tokens and every block of
+ * `block` positions they reach, KV head and dimension, the least and the greatest key element over
+ * the block's positions below seq_len[n] (a NaN among them gives NaN):
+ *   bounds[layer][req_idx[n]][blk][h][0][e] = min_p k_pool[layer][req_to_token[req_idx[n]][p]][h][e]
+ *   bounds[..][1][e]                        = max_p ...
+ * bounds [num_layers, max_reqs, max_blocks, Hkv, 2, d] in dtype; other entries are not written.
+ * k_pool [num_layers, num_slots, Hkv, d]. A row outside the table or the bounds sets the device
+ * status word and is skipped; so is a token whose slot is outside the pool. max_ctx <= 2^24. */
+typedef struct rc_kv_block_bounds_args {
+  int32_t dtype;
+  int32_t num_layers;
+  int32_t num_rows;
+  int32_t num_kv_heads;
+  int32_t head_dim;          /* a multiple of 8 up to 256 */
+  int32_t max_reqs;          /* rows of req_to_token and of bounds */
+  int32_t max_ctx;           /* columns of req_to_token */
+  int32_t block;             /* 16, 32, 64 or 128 */
+  int32_t max_blocks;
+  int64_t num_slots;
+  const int32_t* seq_len;    /* [num_rows] */
+  const int32_t* req_idx;    /* [num_rows] */
+  const int32_t* req_to_token;
+  const void* k_pool;
+  void* bounds;
+} rc_kv_block_bounds_args;
+int rc_kv_block_bounds(const rc_kv_block_bounds_args* args, void* stream);
+
+/* Block-sparse decode attention. Query row n attends to the cached tokens of its request's row
+ * req_idx[n] at positions below seq_len[n] (its own token included, already in the pool:
+ * rc_kv_append) that lie in the blocks selected for (n, KV head):
+ *   score of block b  = max over the KV head's query heads of sum_e (q_e >= 0 ? q_e hi_e : q_e lo_e),
+ *                       lo / hi = bounds[req_idx[n]][b][h][0 / 1]: no key inside the bounds has a
+ *                       larger product with that query. A score of NaN or +inf counts as the largest
+ *                       finite number.
+ *   selected          = of the have = ceil(seq_len[n] / block) blocks the first sink_blocks, the last
+ *                       recent_blocks (recent_blocks >= 1: the block of the newest token), and those
+ *                       with the largest scores up to top_blocks in all; of equal scores the lower
+ *                       block number. Decided as by 64-bit scores, so it depends on no summation
+ *                       order.
+ *   o[n, h] = softmax(sm_scale * <q, k>) v over the selected tokens; lse [Hq] fp32 natural log
+ *             (optional); selected [num_rows, Hkv, top_blocks] int32 (optional): block numbers in
+ *             ascending order, then -1.
+ * A request may have several rows (a chunk of new tokens: rows of growing seq_len). A row with
+ * seq_len 0 gets o = 0, lse = -inf, selected = -1; so does a row whose seq_len or req_idx is out of
+ * range, which also sets the device status word. A slot outside the pool sets it and that token
+ * weighs nothing. sm_scale > 0; Hq / Hkv <= 16; head_dim 64 or 128; tensors 16-byte aligned. */
+typedef struct rc_sparse_decode_args {
+  int32_t dtype;
+  int32_t num_rows;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t max_reqs;          /* rows of req_to_token and of bounds */
+  int32_t max_ctx;           /* columns of req_to_token */
+  int32_t block;             /* 16, 32, 64 or 128 */
+  int32_t max_blocks;        /* blocks per row of bounds */
+  int32_t max_seq_len;       /* >= every seq_len (host-known; sizes grid and workspace) */
+  int32_t top_blocks;
+  int32_t sink_blocks;
+  int32_t recent_blocks;
+  int64_t num_slots;
+  float sm_scale;
+  const void* q;             /* [num_rows, Hq, d] */
+  const int32_t* seq_len;    /* [num_rows] */
+  const int32_t* req_idx;    /* [num_rows] */
+  const int32_t* req_to_token;
+  const void* k_pool;        /* this layer's planes [num_slots, Hkv, d] */
+  const void* v_pool;
+  const void* bounds;        /* this layer's [max_reqs, max_blocks, Hkv, 2, d] */
+  void* o;                   /* [num_rows, Hq, d] */
+  float* lse;
+  int32_t* selected;
+} rc_sparse_decode_args;
+/* Workspace bytes for these sizes (device memory, 16-byte aligned, no initialisation needed). Calls
+ * that may overlap on the GPU need a workspace each. */
+int rc_sparse_decode_workspace_bytes(const rc_sparse_decode_args* args, size_t* out_bytes);
+int rc_sparse_decode_attention(const rc_sparse_decode_args* args, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* Test hook; the pages have no counterpart. Bound, in nanoseconds, of every wait inside the
  * extend kernel (0 restores the default, 2 s). With a short bound waits give up: the kernel
  * records code 3 in the device status word, stops issuing work and returns without hanging; its

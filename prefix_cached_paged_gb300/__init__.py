@@ -17,11 +17,14 @@ import numpy as np
 
 from ._lib import (RC_DTYPE_BF16, RC_DTYPE_F32, RC_ERR_CUDA, RC_ERR_DEVICE, RC_ERR_INSUFFICIENT,
                    RC_ERR_INVALID, RC_ERR_OOM, RC_OK, RC_SCHED_FCFS, RC_SCHED_LSPF, RcDecodeArgs,
-                   RcError, RcExtendArgs, RcKvCopyArgs, RcSlotWriteArgs, RcStackPlan,
+                   RcError, RcExtendArgs, RcKvAppendArgs, RcKvBlockBoundsArgs, RcKvCopyArgs,
+                   RcQkNormRopeArgs, RcSlotWriteArgs, RcSparseDecodeArgs, RcStackPlan,
                    RcStackPlanArgs, RcStats, check, lib)
 
 __all__ = [
     "Pool", "RadixTree", "RcError", "slot_table_write", "extend_attention", "decode_attention",
+    "rope_table", "qk_norm_rope", "kv_append", "kv_block_bounds", "sparse_decode_attention",
+    "sparse_decode_workspace_bytes",
     "decode_workspace_bytes", "decode_attention_noalloc", "device_status", "launch_count", "RC_OK", "RC_ERR_INVALID",
     "RC_ERR_OOM", "RC_ERR_INSUFFICIENT", "RC_ERR_CUDA", "RC_ERR_DEVICE", "RC_SCHED_LSPF",
     "RC_SCHED_FCFS",
@@ -490,6 +493,257 @@ def decode_attention_noalloc(q, k_new, v_new, out_loc, seq_len, req_idx, req_to_
                      o, lse, sm_scale, max_total_tokens, kv_chunk)
     check(lib().rc_decode_attention_noalloc(ctypes.byref(a), _stream(stream)),
           "rc_decode_attention_noalloc")
+
+
+# ------------------------------------------------------------------ norms, rotation, append, sparse
+def _on_device(fn, dev, **tensors):
+    """Every given tensor is on the current device: the call launches on a stream of it."""
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} must be a CUDA tensor on the current device (cuda:{dev})")
+
+
+def _typed(fn, dtype, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+
+
+def _shaped(fn, name, t, *shape):
+    """Contiguous, and of this shape (None: any size)."""
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected "
+                         f"{tuple('*' if w is None else w for w in shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous")
+
+
+def _head_strides(fn, name, t, out=False):
+    """(token stride, head stride) in elements of a [T, H, d] tensor whose heads are contiguous."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{fn}: {name} must be [tokens, heads, d] with contiguous heads")
+    st = [t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1)]
+    if out and any(st[i] == 0 and t.shape[i] > 1 for i in (0, 1)):
+        raise ValueError(f"{fn}: {name} is expanded: its rows share memory")
+    return st
+
+
+def rope_table(inv_freq, num_positions: int, *, first_position: int = 0,
+               scale: float = 1.0) -> np.ndarray:
+    """rc_rope_table: float32 numpy array [num_positions, 2 * len(inv_freq)] of the rotation's
+    cosines and sines, computed in double precision on the host. inv_freq: one frequency per
+    rotated pair (for the usual base: base ** (-2 i / rotary_dim)), a multiple of 8 of them."""
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if f.ndim != 1:
+        raise ValueError("rope_table: inv_freq must be one-dimensional")
+    out = np.empty((max(int(num_positions), 0), 2 * len(f)), dtype=np.float32)
+    check(lib().rc_rope_table(_p(f), len(f), int(first_position), int(num_positions),
+                              float(scale), _p(out)), "rc_rope_table")
+    return out
+
+
+def qk_norm_rope(q, k, positions=None, rope=None, *, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False, q_out=None, k_out=None, stream=None):
+    """Norms of queries and keys for each head with the position rotation in the same pass (see
+    rc_qk_norm_rope). q [T, Hq, d] and k [T, Hkv, d]: CUDA tensors whose heads are contiguous, any
+    token and head strides (slices of a fused projection); either may be None. positions: int32
+    [T]; rope: fp32 [max_position, rotary_dim] (rope_table) or None for norms only; q_weight /
+    k_weight: [d] or None for no norm. q_out / k_out: where the results go, in place when None."""
+    fn = "qk_norm_rope"
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError(f"{fn}: neither q nor k is given")
+    if (q is None and (q_out is not None or q_weight is not None)) or \
+            (k is None and (k_out is not None or k_weight is not None)):
+        raise ValueError(f"{fn}: a weight or an output without its input")
+    if rope is None and q_weight is None and k_weight is None:
+        raise ValueError(f"{fn}: neither a rotation nor a norm is given")
+    dev = _torch().cuda.current_device()
+    _on_device(fn, dev, q=q, k=k, positions=positions, rope=rope, q_weight=q_weight,
+               k_weight=k_weight, q_out=q_out, k_out=k_out)
+    code = _dtype_code(x)
+    _typed(fn, x.dtype, q=q, k=k, q_weight=q_weight, k_weight=k_weight, q_out=q_out, k_out=k_out)
+    T, d = x.shape[0], x.shape[-1]
+    a = RcQkNormRopeArgs(dtype=code, head_dim=d, interleaved=1 if interleaved else 0, eps=eps,
+                         num_tokens=T)
+    if rope is not None:
+        if positions is None:
+            raise ValueError(f"{fn}: the rotation needs positions")
+        _typed(fn, _torch().float32, rope=rope)
+        _typed(fn, _torch().int32, positions=positions)
+        _shaped(fn, "rope", rope, None, None)
+        _shaped(fn, "positions", positions, T)
+        a.max_position, a.rotary_dim = rope.shape
+        a.rope, a.positions = rope.data_ptr(), positions.data_ptr()
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        a.q_token_stride, a.q_head_stride = _head_strides(fn, "q", q)
+        a.q_out_token_stride, a.q_out_head_stride = _head_strides(fn, "q_out", q_out, True)
+        if q_out.shape != q.shape:
+            raise ValueError(f"{fn}: q_out must have q's shape")
+        a.num_q_heads, a.q, a.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        if q_weight is not None:
+            _shaped(fn, "q_weight", q_weight, d)
+            a.q_weight = q_weight.data_ptr()
+    if k is not None:
+        k_out = k if k_out is None else k_out
+        a.k_token_stride, a.k_head_stride = _head_strides(fn, "k", k)
+        a.k_out_token_stride, a.k_out_head_stride = _head_strides(fn, "k_out", k_out, True)
+        if k_out.shape != k.shape or k.shape[0] != T or k.shape[2] != d:
+            raise ValueError(f"{fn}: q, k and k_out do not agree in shape")
+        a.num_kv_heads, a.k, a.k_out = k.shape[1], k.data_ptr(), k_out.data_ptr()
+        if k_weight is not None:
+            _shaped(fn, "k_weight", k_weight, d)
+            a.k_weight = k_weight.data_ptr()
+    check(lib().rc_qk_norm_rope(ctypes.byref(a), _stream(stream)), "rc_qk_norm_rope")
+
+
+def kv_append(k, v, out_loc, qo_indptr, prefix_len, k_pool, v_pool, *, rope=None, k_weight=None,
+              eps=1e-6, interleaved=False, bounds=None, req_idx=None, block=64, stream=None):
+    """Append the new tokens' keys (normalised with k_weight and rotated by rope, each optional)
+    and values to one layer's planes [num_slots, Hkv, d] (see rc_kv_append). k, v [T, Hkv, d] with
+    any token and head strides; out_loc [T], qo_indptr [B + 1], prefix_len [B], req_idx [B] int32.
+    bounds: one layer's block bounds [max_reqs, max_blocks, Hkv, 2, d], updated for the blocks the
+    tokens fall into (with req_idx)."""
+    fn = "kv_append"
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    _on_device(fn, dev, k=k, v=v, out_loc=out_loc, qo_indptr=qo_indptr, prefix_len=prefix_len,
+               k_pool=k_pool, v_pool=v_pool, rope=rope, k_weight=k_weight, bounds=bounds,
+               req_idx=req_idx)
+    code = _dtype_code(k_pool)
+    _typed(fn, k_pool.dtype, k=k, v=v, v_pool=v_pool, k_weight=k_weight, bounds=bounds)
+    _typed(fn, torch.int32, out_loc=out_loc, qo_indptr=qo_indptr, prefix_len=prefix_len,
+           req_idx=req_idx)
+    _shaped(fn, "k_pool", k_pool, None, None, None)
+    S, Hkv, d = k_pool.shape
+    _shaped(fn, "v_pool", v_pool, S, Hkv, d)
+    kt, kh = _head_strides(fn, "k", k)
+    vt, vh = _head_strides(fn, "v", v)
+    T, B = k.shape[0], prefix_len.numel()
+    if tuple(k.shape) != (T, Hkv, d) or tuple(v.shape) != (T, Hkv, d):
+        raise ValueError(f"{fn}: k and v must be [T, {Hkv}, {d}]")
+    _shaped(fn, "out_loc", out_loc, T)
+    _shaped(fn, "prefix_len", prefix_len, B)
+    _shaped(fn, "qo_indptr", qo_indptr, B + 1)
+    a = RcKvAppendArgs(dtype=code, num_reqs=B, num_kv_heads=Hkv, head_dim=d,
+                       interleaved=1 if interleaved else 0, eps=eps, block=block, num_tokens=T,
+                       num_slots=S, k=k.data_ptr(), k_token_stride=kt, k_head_stride=kh,
+                       v=v.data_ptr(), v_token_stride=vt, v_head_stride=vh,
+                       out_loc=out_loc.data_ptr(), qo_indptr=qo_indptr.data_ptr(),
+                       prefix_len=prefix_len.data_ptr(), k_pool=k_pool.data_ptr(),
+                       v_pool=v_pool.data_ptr())
+    if rope is not None:
+        _typed(fn, torch.float32, rope=rope)
+        _shaped(fn, "rope", rope, None, None)
+        a.max_position, a.rotary_dim = rope.shape
+        a.rope = rope.data_ptr()
+    if k_weight is not None:
+        _shaped(fn, "k_weight", k_weight, d)
+        a.k_weight = k_weight.data_ptr()
+    if bounds is not None:
+        if req_idx is None:
+            raise ValueError(f"{fn}: bounds need req_idx")
+        _shaped(fn, "bounds", bounds, None, None, Hkv, 2, d)
+        _shaped(fn, "req_idx", req_idx, B)
+        a.max_reqs, a.max_blocks = bounds.shape[:2]
+        a.bounds, a.req_idx = bounds.data_ptr(), req_idx.data_ptr()
+    check(lib().rc_kv_append(ctypes.byref(a), _stream(stream)), "rc_kv_append")
+
+
+def kv_block_bounds(k_pool, req_to_token, req_idx, seq_len, bounds, *, block=64, stream=None):
+    """Build the block bounds of cached contexts (see rc_kv_block_bounds): row req_idx[n]'s first
+    seq_len[n] tokens. k_pool [num_slots, Hkv, d] with bounds [max_reqs, max_blocks, Hkv, 2, d], or
+    both with a leading layers dimension."""
+    fn = "kv_block_bounds"
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    _on_device(fn, dev, k_pool=k_pool, req_to_token=req_to_token, req_idx=req_idx,
+               seq_len=seq_len, bounds=bounds)
+    code = _dtype_code(k_pool)
+    _typed(fn, k_pool.dtype, bounds=bounds)
+    _typed(fn, torch.int32, req_to_token=req_to_token, req_idx=req_idx, seq_len=seq_len)
+    if k_pool.dim() not in (3, 4) or bounds.dim() != k_pool.dim() + 2:
+        raise ValueError(f"{fn}: k_pool and bounds must both have a layers dimension or neither")
+    lead = k_pool.shape[:-3]
+    S, Hkv, d = k_pool.shape[-3:]
+    _shaped(fn, "req_to_token", req_to_token, None, None)
+    R, C = req_to_token.shape
+    _shaped(fn, "k_pool", k_pool, *lead, S, Hkv, d)
+    _shaped(fn, "bounds", bounds, *lead, R, None, Hkv, 2, d)
+    _shaped(fn, "seq_len", seq_len, None)
+    _shaped(fn, "req_idx", req_idx, seq_len.numel())
+    a = RcKvBlockBoundsArgs(dtype=code, num_layers=lead[0] if lead else 1,
+                            num_rows=seq_len.numel(), num_kv_heads=Hkv, head_dim=d, max_reqs=R,
+                            max_ctx=C, block=block, max_blocks=bounds.shape[-4], num_slots=S,
+                            seq_len=seq_len.data_ptr(), req_idx=req_idx.data_ptr(),
+                            req_to_token=req_to_token.data_ptr(), k_pool=k_pool.data_ptr(),
+                            bounds=bounds.data_ptr())
+    check(lib().rc_kv_block_bounds(ctypes.byref(a), _stream(stream)), "rc_kv_block_bounds")
+
+
+def sparse_decode_workspace_bytes(q, k_pool, *, max_seq_len, block, top_blocks) -> int:
+    """Workspace of sparse_decode_attention for these sizes (rc_sparse_decode_workspace_bytes)."""
+    N, Hq, d = q.shape
+    a = RcSparseDecodeArgs(dtype=_dtype_code(q), num_rows=N, num_q_heads=Hq,
+                           num_kv_heads=k_pool.shape[1], head_dim=d, block=block,
+                           max_seq_len=max_seq_len, top_blocks=top_blocks, recent_blocks=1)
+    n = ctypes.c_size_t()
+    check(lib().rc_sparse_decode_workspace_bytes(ctypes.byref(a), ctypes.byref(n)),
+          "rc_sparse_decode_workspace_bytes")
+    return int(n.value)
+
+
+def sparse_decode_attention(q, seq_len, req_idx, req_to_token, k_pool, v_pool, bounds, o,
+                            workspace, *, sm_scale, max_seq_len, block, top_blocks,
+                            sink_blocks=1, recent_blocks=1, lse=None, selected=None, stream=None):
+    """Decode attention of one layer over the blocks that their bounds select for each query row
+    and KV head (see rc_sparse_decode_attention). q, o [N, Hq, d]; seq_len, req_idx [N] int32, a
+    row's own token already in the pool (kv_append); bounds: this layer's block bounds
+    [max_reqs, max_blocks, Hkv, 2, d]; workspace: a uint8 CUDA tensor of at least
+    sparse_decode_workspace_bytes(...) bytes; lse fp32 [N, Hq] and selected int32
+    [N, Hkv, top_blocks] optional."""
+    fn = "sparse_decode_attention"
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    _on_device(fn, dev, q=q, seq_len=seq_len, req_idx=req_idx, req_to_token=req_to_token,
+               k_pool=k_pool, v_pool=v_pool, bounds=bounds, o=o, workspace=workspace, lse=lse,
+               selected=selected)
+    code = _dtype_code(q)
+    _typed(fn, q.dtype, k_pool=k_pool, v_pool=v_pool, bounds=bounds, o=o)
+    _typed(fn, torch.int32, seq_len=seq_len, req_idx=req_idx, req_to_token=req_to_token,
+           selected=selected)
+    _typed(fn, torch.float32, lse=lse)
+    _shaped(fn, "q", q, None, None, None)
+    N, Hq, d = q.shape
+    _shaped(fn, "o", o, N, Hq, d)
+    _shaped(fn, "k_pool", k_pool, None, None, d)
+    S, Hkv, _ = k_pool.shape
+    _shaped(fn, "v_pool", v_pool, S, Hkv, d)
+    _shaped(fn, "req_to_token", req_to_token, None, None)
+    R, C = req_to_token.shape
+    _shaped(fn, "bounds", bounds, R, None, Hkv, 2, d)
+    _shaped(fn, "seq_len", seq_len, N)
+    _shaped(fn, "req_idx", req_idx, N)
+    if not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be contiguous")
+    if lse is not None:
+        _shaped(fn, "lse", lse, N, Hq)
+    if selected is not None:
+        _shaped(fn, "selected", selected, N, Hkv, top_blocks)
+    a = RcSparseDecodeArgs(dtype=code, num_rows=N, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=d,
+                           max_reqs=R, max_ctx=C, block=block, max_blocks=bounds.shape[1],
+                           max_seq_len=max_seq_len, top_blocks=top_blocks,
+                           sink_blocks=sink_blocks, recent_blocks=recent_blocks, num_slots=S,
+                           sm_scale=sm_scale, q=q.data_ptr(), seq_len=seq_len.data_ptr(),
+                           req_idx=req_idx.data_ptr(), req_to_token=req_to_token.data_ptr(),
+                           k_pool=k_pool.data_ptr(), v_pool=v_pool.data_ptr(),
+                           bounds=bounds.data_ptr(), o=o.data_ptr(),
+                           lse=0 if lse is None else lse.data_ptr(),
+                           selected=0 if selected is None else selected.data_ptr())
+    check(lib().rc_sparse_decode_attention(ctypes.byref(a), ctypes.c_void_p(workspace.data_ptr()),
+                                           workspace.numel() * workspace.element_size(),
+                                           _stream(stream)), "rc_sparse_decode_attention")
 
 
 def device_status(stream=None) -> int:

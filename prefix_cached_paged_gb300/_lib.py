@@ -68,6 +68,12 @@ SIGNATURES = {
     "rc_decode_workspace_bytes": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_size_t)]),
     "rc_decode_attention": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
     "rc_decode_attention_noalloc": (ctypes.c_int, [_P, _P]),
+    "rc_qk_norm_rope": (ctypes.c_int, [_P, _P]),
+    "rc_rope_table": (ctypes.c_int, [_P, _I32, _I64, _I64, ctypes.c_double, _P]),
+    "rc_kv_append": (ctypes.c_int, [_P, _P]),
+    "rc_kv_block_bounds": (ctypes.c_int, [_P, _P]),
+    "rc_sparse_decode_workspace_bytes": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_size_t)]),
+    "rc_sparse_decode_attention": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
     "rc_device_status": (ctypes.c_int, [ctypes.POINTER(_I32), _P]),
     "rc_debug_set_wait_limit_ns": (ctypes.c_int, [_U64]),
     "rc_plan_extend_stacking": (ctypes.c_int, [_P, _P]),
@@ -132,6 +138,46 @@ class RcDecodeArgs(ctypes.Structure):
                 ("k_pool", _P), ("v_pool", _P), ("o", _P), ("lse", _P),
                 ("num_groups", _I32), ("group_indptr", _P), ("group_members", _P),
                 ("group_shared", _P), ("reuse_plan", _I32)]
+
+
+class RcQkNormRopeArgs(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("num_q_heads", _I32), ("num_kv_heads", _I32),
+                ("head_dim", _I32), ("rotary_dim", _I32), ("interleaved", _I32),
+                ("eps", ctypes.c_float), ("num_tokens", _I64), ("max_position", _I64),
+                ("q", _P), ("q_token_stride", _I64), ("q_head_stride", _I64),
+                ("k", _P), ("k_token_stride", _I64), ("k_head_stride", _I64),
+                ("q_weight", _P), ("k_weight", _P), ("positions", _P), ("rope", _P),
+                ("q_out", _P), ("q_out_token_stride", _I64), ("q_out_head_stride", _I64),
+                ("k_out", _P), ("k_out_token_stride", _I64), ("k_out_head_stride", _I64)]
+
+
+class RcKvAppendArgs(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("num_reqs", _I32), ("num_kv_heads", _I32), ("head_dim", _I32),
+                ("rotary_dim", _I32), ("interleaved", _I32), ("eps", ctypes.c_float),
+                ("block", _I32), ("num_tokens", _I64), ("num_slots", _I64),
+                ("max_position", _I64), ("k", _P), ("k_token_stride", _I64),
+                ("k_head_stride", _I64), ("v", _P), ("v_token_stride", _I64),
+                ("v_head_stride", _I64), ("out_loc", _P), ("qo_indptr", _P), ("prefix_len", _P),
+                ("k_weight", _P), ("rope", _P), ("k_pool", _P), ("v_pool", _P), ("bounds", _P),
+                ("req_idx", _P), ("max_reqs", _I32), ("max_blocks", _I32)]
+
+
+class RcKvBlockBoundsArgs(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("num_layers", _I32), ("num_rows", _I32),
+                ("num_kv_heads", _I32), ("head_dim", _I32), ("max_reqs", _I32),
+                ("max_ctx", _I32), ("block", _I32), ("max_blocks", _I32), ("num_slots", _I64),
+                ("seq_len", _P), ("req_idx", _P), ("req_to_token", _P), ("k_pool", _P),
+                ("bounds", _P)]
+
+
+class RcSparseDecodeArgs(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("num_rows", _I32), ("num_q_heads", _I32),
+                ("num_kv_heads", _I32), ("head_dim", _I32), ("max_reqs", _I32),
+                ("max_ctx", _I32), ("block", _I32), ("max_blocks", _I32), ("max_seq_len", _I32),
+                ("top_blocks", _I32), ("sink_blocks", _I32), ("recent_blocks", _I32),
+                ("num_slots", _I64), ("sm_scale", ctypes.c_float), ("q", _P), ("seq_len", _P),
+                ("req_idx", _P), ("req_to_token", _P), ("k_pool", _P), ("v_pool", _P),
+                ("bounds", _P), ("o", _P), ("lse", _P), ("selected", _P)]
 
 
 _lib = None
