@@ -12,24 +12,13 @@
 
 #include "host_common.h"
 #include "norm_rope.cuh"
+#include "warp_mma.cuh"
 
 namespace rc {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWindow = 1024;   // requests whose item offsets a CTA holds at a time
-
-// min / max that keep a NaN: a block with such a key is never hidden from the selection
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 
 // off[k] = items of the window's requests before k (off[n] = all), each of n <= kWindow requests
 // having count(k) items. All threads of the CTA call it.

@@ -3,17 +3,16 @@
 //
 // A block's box (lo_d, hi_d: the least and greatest of its keys in each dimension) bounds q.k from
 // above by s = sum_d (q_d >= 0 ? q_d hi_d : q_d lo_d); the largest s over the query heads of a KV head
-// ranks the block. Three kernels:
-//   score:  every (row, KV head, block) gets its rank as an ordered 64-bit integer;
-//   select: one CTA per (row, KV head) finds the top_blocks-th largest and writes the chosen block
-//           numbers in ascending order;
+// ranks the block. Kernels:
+//   select: a cluster of CTAs per (row, KV head) scores its blocks; the first CTA finds the
+//           top_blocks best and writes their numbers in ascending order;
 //   attend: one CTA per (row, KV head, part of the selected tokens), softmax in fp32 with running
 //           maximum and sum; partial states are joined by the merge kernel.
 #include <algorithm>
 #include <cmath>
 
 #include "host_common.h"
-#include "norm_rope.cuh"
+#include "warp_mma.cuh"
 
 namespace rc {
 namespace {
@@ -22,7 +21,9 @@ constexpr int kPart = 256;      // selected tokens per attention CTA
 constexpr int kMaxGroup = 16;   // query heads per KV head
 
 struct Workspace {
-  unsigned long long* rank;   // [rows * Hkv * nb]
+  float* score;               // [rows * Hkv * nb], fp32
+  float* tsum;                // [rows * Hkv * nb], magnitudes of their terms
+  unsigned long long* rank;   // [rows * Hkv * nb], 64-bit ranks of the blocks near the border
   int* sel;                   // [rows * Hkv * top]
   float* plse;                // [rows * Hkv * parts * G], base 2
   float* po;                  // [rows * Hkv * parts * G * D]
@@ -43,6 +44,10 @@ Workspace carve(void* base, const Params& p, size_t* total) {
   Workspace w{};
   char* b = (char*)base;
   size_t o = 0;
+  w.score = (float*)(b + o);
+  o += align256((size_t)units * p.nb * 4);
+  w.tsum = (float*)(b + o);
+  o += align256((size_t)units * p.nb * 4);
   w.rank = (unsigned long long*)(b + o);
   o += align256((size_t)units * p.nb * 8);
   w.sel = (int*)(b + o);
@@ -65,123 +70,415 @@ __device__ __forceinline__ int row_len(const Params& p, int64_t n, bool report) 
   return L;
 }
 
-// Larger score <=> larger integer; the forced blocks rank above every score.
+// ---------------------------------------------------------------- scores
+// Scores are computed in fp32 next to t = sum_d of the magnitudes of their terms. A score's fp32
+// error is at most kScoreError * t: bf16 products are exact, a matrix instruction adds 16 of them
+// and its accumulator with at most 2^-23 of the largest lost per addend, and each of four chains
+// has at most 4 instructions (d = 128: 16 for the 2 d products), so 4 * 17 * 2^-23 = 2^-16.9 with
+// the joining sums; the fp32 path's chains are shorter. Selection recomputes in 64 bits wherever
+// twice that bound reaches across the border, so the result is that of 64-bit scores.
+constexpr float kScoreError = 1.0f / 65536;
+constexpr int kSelThreads = 256;
+
+// Scores of 16 blocks against the query heads of a KV head by one warp, boxes and queries straight
+// from global memory into matrix fragments: the dot product does not care in which order the
+// dimensions come, so lane (gid, tig) takes 16 contiguous bytes of a row where the instruction
+// wants four pairs, the same ones for both operands. [q-, q+] . [lo, hi] needs no comparison:
+// one of q+ = max(q, 0) and q- = min(q, 0) is zero. (0 * inf gives a NaN that the definition has
+// not: a score that is not finite sends its unit to the 64-bit path.)
+template <int D, int NT>
+__device__ void score_tiles(const Params& p, int64_t n, int g, int have, int tile0, int tile_step,
+                            float* score, float* tsum) {
+  constexpr int J = D / 32;   // 32-element groups of a row
+  const rc_sparse_decode_args& a = p.a;
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  uint4 q[NT][J];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int h = t * 8 + gid;
+    const uint4* src = (const uint4*)((const __nv_bfloat16*)a.q +
+                                      (n * a.num_q_heads + (int64_t)g * p.G + h) * D);
+#pragma unroll
+    for (int j = 0; j < J; ++j) q[t][j] = h < p.G ? src[j * 4 + tig] : make_uint4(0, 0, 0, 0);
+  }
+  const __nv_bfloat16* boxes = (const __nv_bfloat16*)a.bounds +
+                               ((int64_t)a.req_idx[n] * a.max_blocks * a.num_kv_heads + g) * 2 * D;
+  const int64_t stride = (int64_t)a.num_kv_heads * 2 * D;
+  for (int tile = tile0; tile * 16 < have; tile += tile_step) {
+    const int r0 = tile * 16 + gid, r1 = r0 + 8;
+    const uint4* b0 = (const uint4*)(boxes + r0 * stride);
+    const uint4* b1 = (const uint4*)(boxes + r1 * stride);
+    uint4 x[2 * J], y[2 * J];
+#pragma unroll
+    for (int j = 0; j < 2 * J; ++j) {
+      x[j] = r0 < have ? b0[j * 4 + tig] : make_uint4(0, 0, 0, 0);
+      y[j] = r1 < have ? b1[j * 4 + tig] : make_uint4(0, 0, 0, 0);
+    }
+    float best0 = -INFINITY, best1 = -INFINITY, t0 = 0.f, t1 = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float c[4][4] = {}, m[4] = {};
+      constexpr uint32_t kAbs = 0x7fff7fffu;
+#pragma unroll
+      for (int j = 0; j < 2 * J; ++j) {
+        const uint4 qq = q[t][j % J];
+        uint4 w;   // q- beside lo (the first half of a row), q+ beside hi
+        if (j < J)
+          w = make_uint4(min_nan_bf16x2(qq.x, 0), min_nan_bf16x2(qq.y, 0), min_nan_bf16x2(qq.z, 0),
+                         min_nan_bf16x2(qq.w, 0));
+        else
+          w = make_uint4(max_nan_bf16x2(qq.x, 0), max_nan_bf16x2(qq.y, 0), max_nan_bf16x2(qq.z, 0),
+                         max_nan_bf16x2(qq.w, 0));
+        mma_bf16(c[j % 4], x[j].x, y[j].x, x[j].y, y[j].y, w.x, w.y);
+        mma_bf16(c[j % 4], x[j].z, y[j].z, x[j].w, y[j].w, w.z, w.w);
+        mma_bf16(m, x[j].x & kAbs, y[j].x & kAbs, x[j].y & kAbs, y[j].y & kAbs, w.x & kAbs,
+                 w.y & kAbs);
+        mma_bf16(m, x[j].z & kAbs, y[j].z & kAbs, x[j].w & kAbs, y[j].w & kAbs, w.z & kAbs,
+                 w.w & kAbs);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (t * 8 + 2 * tig + e < p.G) {
+          best0 = max_nan(best0, (c[0][e] + c[1][e]) + (c[2][e] + c[3][e]));
+          best1 = max_nan(best1, (c[0][2 + e] + c[1][2 + e]) + (c[2][2 + e] + c[3][2 + e]));
+          t0 = max_nan(t0, m[e]);
+          t1 = max_nan(t1, m[2 + e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      best0 = max_nan(best0, __shfl_xor_sync(0xffffffffu, best0, o));
+      best1 = max_nan(best1, __shfl_xor_sync(0xffffffffu, best1, o));
+      t0 = max_nan(t0, __shfl_xor_sync(0xffffffffu, t0, o));
+      t1 = max_nan(t1, __shfl_xor_sync(0xffffffffu, t1, o));
+    }
+    if (tig == 0 && r0 < have) {
+      score[r0] = best0;
+      tsum[r0] = t0;
+    }
+    if (tig == 0 && r1 < have) {
+      score[r1] = best1;
+      tsum[r1] = t1;
+    }
+  }
+}
+
+// The fp32 form: one warp per block, lanes over the dimensions.
+template <int D>
+__device__ void score_blocks_f32(const Params& p, int64_t n, int g, int have, int b0, int step,
+                                 float* score, float* tsum) {
+  constexpr int E = D / 32;
+  const rc_sparse_decode_args& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const float* q = (const float*)a.q + (n * a.num_q_heads + (int64_t)g * p.G) * D + lane * E;
+  const float* boxes = (const float*)a.bounds +
+                       ((int64_t)a.req_idx[n] * a.max_blocks * a.num_kv_heads + g) * 2 * D + lane * E;
+  for (int b = b0; b < have; b += step) {
+    const float* box = boxes + (int64_t)b * a.num_kv_heads * 2 * D;
+    float lo[E], hi[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      lo[e] = box[e];
+      hi[e] = box[D + e];
+    }
+    float best = -INFINITY, tm = 0.f;
+    for (int h = 0; h < p.G; ++h) {
+      float s = 0.f, t = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float x = q[h * D + e];
+        const float y = x >= 0.f ? hi[e] : lo[e];
+        s = fmaf(x, y, s);
+        t = fmaf(fabsf(x), fabsf(y), t);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+      }
+      best = max_nan(best, s);
+      tm = max_nan(tm, t);
+    }
+    if (lane == 0) {
+      score[b] = best;
+      tsum[b] = tm;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- selection
+// Larger score <=> larger integer.
+__device__ __forceinline__ uint32_t order32(float s) {
+  const int b = __float_as_int(s + 0.f);   // -0 ranks as 0
+  return (uint32_t)(b < 0 ? ~b : (b | (1 << 31)));
+}
 __device__ __forceinline__ unsigned long long order64(double s) {
   if (!(s < 1.7976931348623157e308)) s = 1.7976931348623157e308;   // NaN, +inf
   if (s < -1.7976931348623157e308) s = -1.7976931348623157e308;
-  if (s == 0.0) s = 0.0;                                            // -0 ranks as 0
-  const long long b = __double_as_longlong(s);
+  const long long b = __double_as_longlong(s + 0.0);
   return (unsigned long long)(b < 0 ? ~b : (b | (1ll << 63)));
 }
-constexpr unsigned long long kForced = ~0ull;
 
-// One warp per (row, KV head, block).
-template <typename T>
-__global__ void __launch_bounds__(256) sparse_score_kernel(Params p) {
-  const rc_sparse_decode_args& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = blockIdx.x;
-  const int64_t n = unit / a.num_kv_heads;
-  const int g = (int)(unit - n * a.num_kv_heads);
-  const int L = row_len(p, n, blockIdx.y == 0 && threadIdx.x == 0 && g == 0);
-  const int have = (L + a.block - 1) / a.block;
-  const int d = a.head_dim;
-  for (int b = blockIdx.y * 8 + (threadIdx.x >> 5); b < have; b += gridDim.y * 8) {
-    unsigned long long rank = 0;
-    if (b < a.sink_blocks || b >= have - a.recent_blocks) {
-      rank = kForced;
-    } else {
-      const T* box = (const T*)a.bounds +
-                     ((((int64_t)a.req_idx[n] * a.max_blocks + b) * a.num_kv_heads + g) * 2) * d;
-      for (int h = 0; h < p.G; ++h) {
-        const T* q = (const T*)a.q + (n * a.num_q_heads + (int64_t)g * p.G + h) * d;
-        double s = 0.0;
-        for (int e = lane; e < d; e += 32) {
-          const double qe = Elem<T>::to_f(q[e]);
-          s += qe * (double)Elem<T>::to_f(qe >= 0.0 ? box[d + e] : box[e]);
-        }
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        rank = max(rank, order64(s));
-      }
-    }
-    if (lane == 0) p.w.rank[unit * p.nb + b] = rank;
-  }
+struct SelectShared {
+  int hist[256];
+  int wsum[2][kSelThreads / 32];
+  int bin, above;
+  uint32_t lo, hi;
+  float tmax;
+};
+
+// Sum over the CTA (all threads get it).
+__device__ __forceinline__ int block_sum(SelectShared& s, int x) {
+  x = __reduce_add_sync(0xffffffffu, x);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s.wsum[0][threadIdx.x >> 5] = x;
+  __syncthreads();
+  int r = 0;
+#pragma unroll
+  for (int w = 0; w < kSelThreads / 32; ++w) r += s.wsum[0][w];
+  return r;
 }
 
-// One CTA per (row, KV head): the largest threshold that at least `top` ranks reach, bit by bit;
-// blocks above it are chosen, and of those that equal it the lowest-numbered.
-__global__ void __launch_bounds__(256) sparse_select_kernel(Params p) {
+// The k-th largest (k >= 1) of the values key(i), i < n, for which ok(i); there are at least k.
+// A radix search that begins below the digits all of them share.
+template <typename K, typename Key, typename Ok>
+__device__ K kth_largest(SelectShared& s, int n, int k, K lo, K hi, Key key, Ok ok) {
+  int shift = lo == hi ? 0 : (int)(sizeof(K) * 8) - __clzll((unsigned long long)(lo ^ hi)) +
+                                 (int)(64 - sizeof(K) * 8);
+  K prefix = shift >= (int)sizeof(K) * 8 ? 0 : (hi >> shift) << shift;
+  while (shift > 0) {
+    const int bits = min(shift, 8);
+    const int low = shift - bits;
+    s.hist[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kSelThreads) {
+      if (!ok(i)) continue;
+      const K x = key(i);
+      if (shift >= (int)sizeof(K) * 8 || (x >> shift) == (prefix >> shift))
+        atomicAdd(&s.hist[(int)((x >> low) & (K)((1 << bits) - 1))], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {   // bin that holds the k-th largest, from the top
+      const int lane = threadIdx.x;
+      int c[8], sum = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        c[e] = s.hist[255 - (lane * 8 + e)];
+        sum += c[e];
+      }
+      int run = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+      }
+      int before = run - sum;
+      if (before < k && run >= k) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (before < k && before + c[e] >= k) {
+            s.bin = 255 - (lane * 8 + e);
+            s.above = before;
+          }
+          before += c[e];
+        }
+      }
+    }
+    __syncthreads();
+    prefix |= (K)s.bin << low;
+    k -= s.above;
+    shift = low;
+    __syncthreads();
+  }
+  return prefix;
+}
+
+// The 64-bit rank of block b: the largest score over the KV head's queries. One warp.
+template <typename T>
+__device__ unsigned long long exact_rank(const Params& p, int64_t n, int g, int b) {
   const rc_sparse_decode_args& a = p.a;
-  __shared__ int total;
-  __shared__ int wsum[2][8];
-  const int64_t unit = blockIdx.x;
+  const int lane = threadIdx.x & 31, d = a.head_dim;
+  const T* box = (const T*)a.bounds +
+                 ((((int64_t)a.req_idx[n] * a.max_blocks + b) * a.num_kv_heads + g) * 2) * d;
+  unsigned long long rank = 0;
+  for (int h = 0; h < p.G; ++h) {
+    const T* q = (const T*)a.q + (n * a.num_q_heads + (int64_t)g * p.G + h) * d;
+    double s = 0.0;
+    for (int e = lane; e < d; e += 32) {
+      const float x = Elem<T>::to_f(q[e]);
+      s += (double)x * (double)Elem<T>::to_f(x >= 0.f ? box[d + e] : box[e]);
+    }
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    rank = max(rank, order64(s));
+  }
+  return rank;
+}
+
+// A cluster of CTAs scores the blocks of one (row, KV head); its first CTA selects.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kSelThreads) sparse_select_kernel(Params p, int cluster) {
+  __shared__ SelectShared sh;
+  const rc_sparse_decode_args& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int64_t unit = blockIdx.x / cluster;
+  const int rank = blockIdx.x - (int)unit * cluster;
   const int64_t n = unit / a.num_kv_heads;
-  const int L = row_len(p, n, false);
+  const int g = (int)(unit - n * a.num_kv_heads);
+  const int L = row_len(p, n, rank == 0 && tid == 0 && g == 0);
   const int have = (L + a.block - 1) / a.block;
   const int take = min(have, a.top_blocks);
+  float* score = p.w.score + unit * p.nb;
+  float* tsum = p.w.tsum + unit * p.nb;
+  const bool choose = take < have;   // else every block is taken and none is scored
+  if (choose) {
+    const int w0 = rank * (kSelThreads / 32) + wid, ws = cluster * (kSelThreads / 32);
+    if constexpr (sizeof(T) == 2)
+      score_tiles<D, NT>(p, n, g, have, w0, ws, score, tsum);
+    else
+      score_blocks_f32<D>(p, n, g, have, w0, ws, score, tsum);
+  }
+  if (cluster > 1) {
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::
+                     : "memory");
+    if (rank) return;
+  } else {
+    __syncthreads();
+  }
   int* out = p.w.sel + unit * a.top_blocks;
   int* user = a.selected ? a.selected + unit * a.top_blocks : nullptr;
-  const unsigned long long* rank = p.w.rank + unit * p.nb;
-  for (int i = take + threadIdx.x; i < a.top_blocks; i += 256) {
-    out[i] = -1;
-    if (user) user[i] = -1;
-  }
-  if (take == 0) return;
-  unsigned long long thr = 0;
-  int above = 0;   // ranks > thr
-  if (take < have) {
-    for (int bit = 63; bit >= 0; --bit) {
-      const unsigned long long t = thr | (1ull << bit);
-      int c = 0;
-      for (int b = threadIdx.x; b < have; b += 256) c += rank[b] >= t;
-      if (threadIdx.x == 0) total = 0;
-      __syncthreads();
-      atomicAdd(&total, c);
-      __syncthreads();
-      if (total >= take) thr = t;
-      __syncthreads();
+  for (int i = tid; i < a.top_blocks; i += kSelThreads) {
+    const int b = !choose && i < take ? i : -1;
+    if (!choose || i >= take) {
+      out[i] = b;
+      if (user) user[i] = b;
     }
-    int c = 0;
-    for (int b = threadIdx.x; b < have; b += 256) c += rank[b] > thr;
-    if (threadIdx.x == 0) total = 0;
-    __syncthreads();
-    atomicAdd(&total, c);
-    __syncthreads();
-    above = total;
   }
-  const int equal_take = take < have ? take - above : have;
-  // compaction in block order: running counts of chosen and of equal blocks
+  if (!choose) return;
+
+  // blocks [f0, f1) are scored ones; the others are forced
+  const int f0 = min(a.sink_blocks, have), f1 = max(f0, have - a.recent_blocks);
+  const int m = f1 - f0, k = take - (have - m);   // k of the m scored blocks are taken
+  score += f0;
+  tsum += f0;
+  int need64 = 0;    // scored blocks whose 64-bit ranks decide
+  int in = 0;        // scored blocks that are taken whatever those say
+  float hi_s = 0.f, lo_s = 0.f;
+  bool all64 = false;
+  if (k > 0) {
+    uint32_t lo = 0xffffffffu, hi = 0;
+    float tmax = 0.f;
+    bool finite = true;
+    for (int i = tid; i < m; i += kSelThreads) {
+      const float s = score[i], t = tsum[i];
+      const uint32_t o = order32(s);
+      lo = min(lo, o);
+      hi = max(hi, o);
+      tmax = fmaxf(tmax, t);
+      finite = finite && fabsf(s) < INFINITY && t < INFINITY;
+    }
+    if (tid == 0) {
+      sh.lo = 0xffffffffu;
+      sh.hi = 0;
+      sh.tmax = 0.f;
+    }
+    all64 = __syncthreads_or(!finite);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(tmax));   // tmax >= 0
+    if (lane == 0) {
+      atomicMin(&sh.lo, lo);
+      atomicMax(&sh.hi, hi);
+      atomicMax((unsigned int*)&sh.tmax, tb);
+    }
+    __syncthreads();
+    if (!all64) {
+      const uint32_t thr = kth_largest<uint32_t>(
+          sh, m, k, sh.lo, sh.hi, [&](int i) { return order32(score[i]); },
+          [](int) { return true; });
+      const float ts = __uint_as_float(thr & (1u << 31) ? thr & ~(1u << 31) : ~thr);
+      const float e2 = 2.f * kScoreError * 1.0001f * sh.tmax;
+      hi_s = ts + e2;
+      lo_s = ts - e2;
+      int ci = 0, ca = 0;
+      for (int i = tid; i < m; i += kSelThreads) {
+        const float s = score[i];
+        ci += s > hi_s;
+        ca += s >= lo_s && s <= hi_s;
+      }
+      in = block_sum(sh, ci);
+      need64 = block_sum(sh, ca);
+    } else {
+      need64 = m;
+    }
+  }
+  const int rest = k - in;   // to be taken of the need64 near the border
+  unsigned long long* r64 = p.w.rank + unit * p.nb + f0;
+  auto near = [&](int i) { return all64 || (score[i] >= lo_s && score[i] <= hi_s); };
+  unsigned long long thr64 = 0;
+  int ties = 0;   // blocks of rank thr64 that are taken, the lowest-numbered ones
+  const bool exact = k > 0 && need64 > rest;
+  if (exact) {
+    for (int i0 = wid * 32; i0 < m; i0 += kSelThreads) {
+      const int i = i0 + lane;
+      unsigned todo = __ballot_sync(0xffffffffu, i < m && near(i));
+      while (todo) {
+        const int j = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const unsigned long long r = exact_rank<T>(p, n, g, f0 + i0 + j);
+        if (lane == 0) r64[i0 + j] = r;
+      }
+    }
+    __syncthreads();
+    thr64 = kth_largest<unsigned long long>(
+        sh, m, rest, 0ull, ~0ull, [&](int i) { return r64[i]; }, near);
+    int c = 0;
+    for (int i = tid; i < m; i += kSelThreads) c += near(i) && r64[i] > thr64;
+    ties = rest - block_sum(sh, c);
+  }
+  // the chosen blocks in ascending order
   int done = 0, eq_done = 0;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  for (int b0 = 0; b0 < have; b0 += 256) {
-    const int b = b0 + threadIdx.x;
-    const unsigned long long rk = b < have ? rank[b] : 0;
-    const bool eq = b < have && rk == thr && take < have;
+  for (int b0 = 0; b0 < have; b0 += kSelThreads) {
+    const int b = b0 + tid, i = b - f0;
+    bool pick = b < have && (b < f0 || b >= f1), eq = false;
+    if (b >= f0 && b < f1 && k > 0) {
+      if (near(i)) {
+        if (exact) {
+          pick = r64[i] > thr64;
+          eq = r64[i] == thr64;
+        } else {
+          pick = true;
+        }
+      } else {
+        pick = score[i] > hi_s;
+      }
+    }
     const unsigned me = __ballot_sync(0xffffffffu, eq);
     __syncthreads();
-    if (lane == 0) wsum[0][wid] = __popc(me);
+    if (lane == 0) sh.wsum[0][wid] = __popc(me);
     __syncthreads();
     int ebase = eq_done;
-    for (int w = 0; w < wid; ++w) ebase += wsum[0][w];
-    const bool pick = b < have && (take == have || rk > thr ||
-                                   (eq && ebase + __popc(me & ((1u << lane) - 1)) < equal_take));
+    for (int w = 0; w < wid; ++w) ebase += sh.wsum[0][w];
+    if (eq && ebase + __popc(me & ((1u << lane) - 1)) < ties) pick = true;
     const unsigned mp = __ballot_sync(0xffffffffu, pick);
-    if (lane == 0) wsum[1][wid] = __popc(mp);
+    if (lane == 0) sh.wsum[1][wid] = __popc(mp);
     __syncthreads();
     int base = done;
-    for (int w = 0; w < wid; ++w) base += wsum[1][w];
+    for (int w = 0; w < wid; ++w) base += sh.wsum[1][w];
     if (pick) {
       const int at = base + __popc(mp & ((1u << lane) - 1));
       out[at] = b;
       if (user) user[at] = b;
     }
-    for (int w = 0; w < 8; ++w) {
-      done += wsum[1][w];
-      eq_done += wsum[0][w];
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      done += sh.wsum[1][w];
+      eq_done += sh.wsum[0][w];
     }
   }
 }
 
+// ---------------------------------------------------------------- attention
 // One CTA of 4 warps per (row, KV head, part): warp w takes every 4th token of the part.
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(128) sparse_attend_kernel(Params p) {
@@ -313,7 +610,7 @@ int validate(const rc_sparse_decode_args* a, const char* fn) {
                    a->recent_blocks >= 1 &&
                    (int64_t)a->sink_blocks + a->recent_blocks <= a->top_blocks,
                "%s: top_blocks must hold the sink blocks and at least one recent block", fn);
-  RC_CHECK_ARG((int64_t)a->num_rows * a->num_q_heads < (1ll << 31), "%s: too many rows", fn);
+  RC_CHECK_ARG((int64_t)a->num_rows * a->num_q_heads < (1ll << 28), "%s: too many rows", fn);
   return RC_OK;
 }
 
@@ -336,17 +633,45 @@ void launch_attend(const Params& p, dim3 grid, cudaStream_t s) {
   else sparse_attend_kernel<T, D, 16><<<grid, 128, 0, s>>>(p);
 }
 
-template <typename T>
+template <typename T, int D, int NT>
+cudaError_t launch_select(const Params& p, unsigned units, cudaStream_t s) {
+  // a CTA's 8 warps score 128 blocks (bf16) or 64 (fp32: 8 blocks a warp) before one works twice;
+  // up to 8 CTAs share the work of one unit
+  const int per_cta = sizeof(T) == 2 ? 128 : 64;
+  int cluster = 1;
+  while (cluster < 8 && cluster * per_cta < p.nb) cluster *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(units * cluster);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sparse_select_kernel<T, D, NT>, p, cluster);
+}
+
+template <typename T, int D>
 int launch(const Params& p, cudaStream_t s) {
   const unsigned units = (unsigned)(p.a.num_rows * p.a.num_kv_heads);
-  sparse_score_kernel<T><<<dim3(units, std::min((p.nb + 7) / 8, 64)), 256, 0, s>>>(p);
-  sparse_select_kernel<<<units, 256, 0, s>>>(p);
-  const dim3 grid(units, p.parts);
-  if (p.a.head_dim == 128) launch_attend<T, 128>(p, grid, s);
-  else launch_attend<T, 64>(p, grid, s);
-  sparse_merge_kernel<T><<<p.a.num_rows * p.a.num_q_heads, p.a.head_dim, 0, s>>>(p);
-  count_launches(4);
+  cudaError_t e;
+  if constexpr (sizeof(T) == 2)
+    e = p.G <= 8 ? launch_select<T, D, 1>(p, units, s) : launch_select<T, D, 2>(p, units, s);
+  else
+    e = launch_select<T, D, 1>(p, units, s);
+  if (e != cudaSuccess)
+    return fail(RC_ERR_CUDA, "rc_sparse_decode_attention: launch failed: %s", cudaGetErrorString(e));
+  launch_attend<T, D>(p, dim3(units, p.parts), s);
+  sparse_merge_kernel<T><<<p.a.num_rows * p.a.num_q_heads, D, 0, s>>>(p);
+  count_launches(3);
   return check_launch("rc_sparse_decode_attention");
+}
+
+template <typename T>
+int launch_d(const Params& p, cudaStream_t s) {
+  return p.a.head_dim == 128 ? launch<T, 128>(p, s) : launch<T, 64>(p, s);
 }
 
 }  // namespace
@@ -388,6 +713,6 @@ extern "C" int rc_sparse_decode_attention(const rc_sparse_decode_args* a, void* 
                need);
   p.status = rc::device_status_ptr();
   if (!p.status) return rc::fail(RC_ERR_CUDA, "%s: no device status word", fn);
-  return a->dtype == RC_DTYPE_BF16 ? rc::launch<__nv_bfloat16>(p, (cudaStream_t)stream)
-                                   : rc::launch<float>(p, (cudaStream_t)stream);
+  return a->dtype == RC_DTYPE_BF16 ? rc::launch_d<__nv_bfloat16>(p, (cudaStream_t)stream)
+                                   : rc::launch_d<float>(p, (cudaStream_t)stream);
 }
