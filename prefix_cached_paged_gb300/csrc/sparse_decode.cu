@@ -7,7 +7,7 @@
 //   select: a cluster of CTAs per (row, KV head) scores its blocks; the first CTA finds the
 //           top_blocks best and writes their numbers in ascending order;
 //   attend: one CTA per (row, KV head, part of the selected tokens), softmax in fp32 with running
-//           maximum and sum; partial states are joined by the merge kernel.
+//           maximum and sum; the last CTA of a unit to finish joins its parts' states.
 #include <algorithm>
 #include <cmath>
 
@@ -17,7 +17,9 @@
 namespace rc {
 namespace {
 
-constexpr int kPart = 256;      // selected tokens per attention CTA
+constexpr int kMaxPart = 512;   // selected tokens per attention CTA, at most
+constexpr int kMinPart = 64;    // and at least: one stage for each of its warps
+constexpr int kEnoughCtas = 456;   // three per SM
 constexpr int kMaxGroup = 16;   // query heads per KV head
 
 struct Workspace {
@@ -25,6 +27,7 @@ struct Workspace {
   float* tsum;                // [rows * Hkv * nb], magnitudes of their terms
   unsigned long long* rank;   // [rows * Hkv * nb], 64-bit ranks of the blocks near the border
   int* sel;                   // [rows * Hkv * top]
+  int* count;                 // [rows * Hkv] parts finished
   float* plse;                // [rows * Hkv * parts * G], base 2
   float* po;                  // [rows * Hkv * parts * G * D]
 };
@@ -34,6 +37,7 @@ struct Params {
   rc_sparse_decode_args a;
   Workspace w;
   int nb;      // blocks of max_seq_len
+  int part_tokens;   // selected tokens per attention CTA
   int parts;   // attention CTAs per (row, KV head)
   int G;
   int* status;
@@ -52,6 +56,8 @@ Workspace carve(void* base, const Params& p, size_t* total) {
   o += align256((size_t)units * p.nb * 8);
   w.sel = (int*)(b + o);
   o += align256((size_t)units * p.a.top_blocks * 4);
+  w.count = (int*)(b + o);
+  o += align256((size_t)units * 4);
   w.plse = (float*)(b + o);
   o += align256((size_t)units * p.parts * p.G * 4);
   w.po = (float*)(b + o);
@@ -345,6 +351,7 @@ __global__ void __launch_bounds__(kSelThreads) sparse_select_kernel(Params p, in
   } else {
     __syncthreads();
   }
+  if (tid == 0) p.w.count[unit] = 0;
   int* out = p.w.sel + unit * a.top_blocks;
   int* user = a.selected ? a.selected + unit * a.top_blocks : nullptr;
   for (int i = tid; i < a.top_blocks; i += kSelThreads) {
@@ -479,59 +486,316 @@ __global__ void __launch_bounds__(kSelThreads) sparse_select_kernel(Params p, in
 }
 
 // ---------------------------------------------------------------- attention
-// One CTA of 4 warps per (row, KV head, part): warp w takes every 4th token of the part.
-template <typename T, int D, int G>
-__global__ void __launch_bounds__(128) sparse_attend_kernel(Params p) {
-  constexpr int E = D / 32;
+// What an attention CTA works on: tokens [t0, t1) of the selected tokens of a unit = (row, KV head),
+// token t standing at position sel[t / block] * block + t % block. The newest block is selected and
+// comes last, so it alone may be short and the selected tokens are the first `count`.
+struct Part {
+  int64_t unit, n;
+  int g, L, t0, t1, parts;   // parts that have tokens (at least 1)
+};
+__device__ __forceinline__ bool part_of(const Params& p, Part& w) {
   const rc_sparse_decode_args& a = p.a;
-  __shared__ float q_s[G][D];
-  __shared__ float sm[4][G], sl[4][G], so[4][G][D];
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int64_t unit = blockIdx.x;
-  const int part = blockIdx.y;
-  const int64_t n = unit / a.num_kv_heads;
-  const int g = (int)(unit - n * a.num_kv_heads);
-  const int L = row_len(p, n, false);
-  const int Gr = p.G;
-  const int have = (L + a.block - 1) / a.block;
-  const int take = min(have, a.top_blocks);
-  const int t0 = part * kPart, t1 = min(take * a.block, t0 + kPart);
-  const int* sel = p.w.sel + unit * a.top_blocks;
-  const int32_t* rt = a.req_to_token + (int64_t)(L ? a.req_idx[n] : 0) * a.max_ctx;
-  const float scale = a.sm_scale * kLog2e;
-  for (int e = threadIdx.x; e < Gr * D; e += 128)
-    (&q_s[0][0])[e] =
-        Elem<T>::to_f(((const T*)a.q)[(n * a.num_q_heads + (int64_t)g * Gr) * D + e]) * scale;
-  __syncthreads();
-  float m[G], l[G], acc[G][E];
+  w.unit = blockIdx.x / p.parts;
+  const int part = blockIdx.x - (int)w.unit * p.parts;
+  w.n = w.unit / a.num_kv_heads;
+  w.g = (int)(w.unit - w.n * a.num_kv_heads);
+  w.L = row_len(p, w.n, false);
+  const int have = (w.L + a.block - 1) / a.block;
+  const int count = have <= a.top_blocks ? w.L : (a.top_blocks - 1) * a.block + w.L -
+                                                     (have - 1) * a.block;
+  w.parts = max(1, (count + p.part_tokens - 1) / p.part_tokens);
+  w.t0 = part * p.part_tokens;
+  w.t1 = min(count, w.t0 + p.part_tokens);
+  return part < w.parts;
+}
+
+// Slots of the part's tokens into shared memory (-1: outside the pool, recorded).
+__device__ __forceinline__ void load_slots(const Params& p, const Part& w, int* slots) {
+  const rc_sparse_decode_args& a = p.a;
+  const int* sel = p.w.sel + w.unit * a.top_blocks;
+  const int shift = __ffs(a.block) - 1;
+  for (int t = w.t0 + threadIdx.x; t < w.t1; t += blockDim.x) {
+    const int pos = (sel[t >> shift] << shift) + (t & (a.block - 1));
+    int s = a.req_to_token[(int64_t)a.req_idx[w.n] * a.max_ctx + pos];
+    if (s < 0 || s >= a.num_slots) {
+      set_status(p.status, kStatusSlotRange);
+      s = -1;
+    }
+    slots[t - w.t0] = s;
+  }
+}
+
+// The end of an attention CTA, all 128 threads: joins the four warps' states (m base 2, l, and
+// unnormalised o, in shared memory) and writes the outputs, or the part's state with the CTA that
+// finishes a unit last joining its parts in their order. The unit's counter was zeroed by the
+// selection kernel.
+template <typename T, int D>
+__device__ void finish_part(const Params& p, const Part& w, const float* sm, const float* sl,
+                            const float* so, int* last) {
+  const rc_sparse_decode_args& a = p.a;
+  const int G = p.G;
+  const int64_t o0 = (w.n * a.num_q_heads + (int64_t)w.g * G) * D;
+  const int64_t l0 = w.n * a.num_q_heads + (int64_t)w.g * G;
+  const int part = blockIdx.x - (int)w.unit * p.parts;
+  for (int x = threadIdx.x; x < G * D; x += 128) {
+    const int h = x / D;
+    const float M = fmaxf(fmaxf(sm[h], sm[G + h]), fmaxf(sm[2 * G + h], sm[3 * G + h]));
+    float den = 0.f, num = 0.f;
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
+    for (int v = 0; v < 4; ++v) {
+      const float mv = sm[v * G + h];
+      const float c = mv == -INFINITY ? 1.f : exp2f(mv - M);   // an empty state is all zeros
+      den = fmaf(sl[v * G + h], c, den);
+      num = fmaf(so[v * G * D + x], c, num);
+    }
+    const float o = den == 0.f ? 0.f : num / den;
+    const float lse = den == 0.f ? -INFINITY : M + log2f(den);
+    if (w.parts == 1) {
+      ((T*)a.o)[o0 + x] = Elem<T>::from_f(o);
+      if (a.lse && x % D == 0) a.lse[l0 + h] = den == 0.f ? -INFINITY : lse * kLn2;
+    } else {
+      const int64_t pi = (w.unit * p.parts + part) * G;
+      p.w.po[pi * D + x] = o;
+      if (x % D == 0) p.w.plse[pi + h] = lse;
+    }
+  }
+  if (w.parts == 1) return;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) *last = atomicAdd(&p.w.count[w.unit], 1) == w.parts - 1;
+  __syncthreads();
+  if (!*last) return;
+  __threadfence();
+  for (int x = threadIdx.x; x < G * D; x += 128) {
+    const int h = x / D;
+    const int64_t pi = w.unit * p.parts * G;
+    float M = -INFINITY;
+    for (int c = 0; c < w.parts; ++c) M = fmaxf(M, __ldcg(&p.w.plse[pi + c * G + h]));
+    float num = 0.f, den = 0.f;
+    for (int c = 0; c < w.parts; ++c) {
+      const float pl = __ldcg(&p.w.plse[pi + c * G + h]);
+      const float k = pl == -INFINITY ? 0.f : exp2f(pl - M);
+      den += k;
+      num = fmaf(k, __ldcg(&p.w.po[(pi + c * G) * D + x]), num);
+    }
+    ((T*)a.o)[o0 + x] = Elem<T>::from_f(den == 0.f ? 0.f : num / den);
+    if (a.lse && x % D == 0) a.lse[l0 + h] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
+  }
+}
+
+// bf16: one CTA of 4 warps per part. A warp streams every 4th stage of 16 tokens through its own
+// ring: 16-byte copies of the tokens' K and V rows, completion by copy groups. The two
+// contractions run on warp-level matrix instructions with the tokens as M and the KV head's query
+// heads as N (NT tiles of 8): S^T = K Q^T, O^T += V^T P^T. K fragments by ldmatrix, V^T by its
+// transposing form (rows padded by 16 bytes: no bank conflicts), Q^T in registers, P^T from the
+// accumulators by movmatrix. P goes in as a bf16 part and its bf16 remainder, so P.V keeps 16 bits
+// of the weights.
+template <int D>
+struct AttendCfg {
+  static constexpr int TOK = 16, STAGES = 2;
+  static constexpr int RB = D * 2, RS = RB + 16;
+  static constexpr int STAGE = TOK * 2 * RS;
+  static constexpr int RING = 4 * STAGES * STAGE;   // bytes for the CTA
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(128) sparse_attend_mma_kernel(Params p) {
+  using C = AttendCfg<D>;
+  constexpr int KS = D / 16;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ float sm[4 * kMaxGroup], sl[4 * kMaxGroup];
+  __shared__ int last;
+  const rc_sparse_decode_args& a = p.a;
+  int* slots = (int*)(smem + C::RING);
+  Part w;
+  if (!part_of(p, w)) return;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
+  const int G = p.G, n = w.t1 - w.t0;
+  load_slots(p, w, slots);
+
+  uint32_t qb[NT][KS][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int h = t * 8 + gid;
+    const __nv_bfloat16* q = (const __nv_bfloat16*)a.q +
+                             (w.n * a.num_q_heads + (int64_t)w.g * G + (h < G ? h : 0)) * D;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      qb[t][k][0] = h < G ? *(const uint32_t*)(q + k * 16 + tig * 2) : 0u;
+      qb[t][k][1] = h < G ? *(const uint32_t*)(q + k * 16 + tig * 2 + 8) : 0u;
+    }
+  }
+  __syncthreads();
+
+  const uint32_t ring = smem_u32(smem) + wid * C::STAGES * C::STAGE;
+  const char* kp = (const char*)a.k_pool + (int64_t)w.g * C::RB;
+  const char* vp = (const char*)a.v_pool + (int64_t)w.g * C::RB;
+  const int64_t slot_bytes = (int64_t)a.num_kv_heads * C::RB;
+  constexpr int CPR = C::RB / 16, RPI = 32 / CPR;   // 16-byte copies per row, rows per copy step
+  const int cc = (lane % CPR) * 16, rsub = lane / CPR;
+  auto issue = [&](int s, int buf) {   // stage s of the part: tokens 16 s ..
+    const uint32_t kd = ring + buf * C::STAGE + cc;
+#pragma unroll
+    for (int i = 0; i < C::TOK / RPI; ++i) {
+      const int t = i * RPI + rsub, at = s * C::TOK + t;
+      const int slot = at < n ? slots[at] : -1;
+      const int64_t off = (int64_t)max(slot, 0) * slot_bytes + cc;
+      cp_async16_or_zero(kd + t * C::RS, kp + off, slot >= 0);
+      cp_async16_or_zero(kd + (C::TOK + t) * C::RS, vp + off, slot >= 0);
+    }
+  };
+
+  const float qscale = a.sm_scale * kLog2e;
+  const int k_row = (lane & 7) + ((lane >> 3) & 1) * 8, k_col = (lane >> 4) * 8;
+  const int v_row = (lane & 7) + (lane >> 4) * 8, v_col = ((lane >> 3) & 1) * 8;
+  float acc[NT][KS][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t][0] = m[t][1] = -INFINITY;
+    l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
+  }
+  const int stages = (n + C::TOK - 1) / C::TOK;
+  if (wid < stages) issue(wid, 0);
+  cp_async_commit();
+  int buf = 0;
+  for (int s = wid; s < stages; s += 4, buf ^= 1) {
+    if (s + 4 < stages) issue(s + 4, buf ^ 1);
+    cp_async_commit();
+    cp_async_wait<1>();
+    __syncwarp();
+    const uint32_t kb = ring + buf * C::STAGE, vb = kb + C::TOK * C::RS;
+    float sc[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      uint32_t r[4];
+      ldmatrix_x4(kb + k_row * C::RS + (k * 16 + k_col) * 2, r);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mma_bf16(sc[t], r[0], r[1], r[2], r[3], qb[t][k][0], qb[t][k][1]);
+    }
+    const int at = s * C::TOK + gid;
+    const bool ok0 = at < n && slots[at] >= 0, ok1 = at + 8 < n && slots[at + 8] >= 0;
+    uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {   // query heads 8 t + 2 tig + e
+        sc[t][e] = ok0 ? sc[t][e] * qscale : -INFINITY;
+        sc[t][2 + e] = ok1 ? sc[t][2 + e] * qscale : -INFINITY;
+        float x = fmaxf(sc[t][e], sc[t][2 + e]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+        // the running maximum moves only when it grows by more than 2^8
+        const float mo = m[t][e], mx = fmaxf(mo, x);
+        const bool grow = mx > mo + 8.f;
+        const float mn = grow ? mx : mo;
+        const float al = grow && mo != -INFINITY ? exp2f(mo - mn) : 1.f;
+        m[t][e] = mn;
+        const float u = mn == -INFINITY ? 0.f : mn;   // nothing but masked tokens so far
+        sc[t][e] = exp2f(sc[t][e] - u);
+        sc[t][2 + e] = exp2f(sc[t][2 + e] - u);
+        l[t][e] = l[t][e] * al + sc[t][e] + sc[t][2 + e];
+        if (__any_sync(0xffffffffu, al != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            acc[t][i][e] *= al;
+            acc[t][i][2 + e] *= al;
+          }
+        }
+      }
+      const uint32_t hx = pack2_bf16(sc[t][0], sc[t][1]), hy = pack2_bf16(sc[t][2], sc[t][3]);
+      ph[t][0] = movmatrix_trans(hx);
+      ph[t][1] = movmatrix_trans(hy);
+      pl[t][0] = movmatrix_trans(pack2_bf16(sc[t][0] - bf16lo(hx), sc[t][1] - bf16hi(hx)));
+      pl[t][1] = movmatrix_trans(pack2_bf16(sc[t][2] - bf16lo(hy), sc[t][3] - bf16hi(hy)));
+    }
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      uint32_t r[4];
+      ldmatrix_x4_trans(vb + v_row * C::RS + (i * 16 + v_col) * 2, r);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mma_bf16(acc[t][i], r[0], r[1], r[2], r[3], ph[t][0], ph[t][1]);
+        mma_bf16(acc[t][i], r[0], r[1], r[2], r[3], pl[t][0], pl[t][1]);
+      }
+    }
+    __syncwarp();   // the buffer may be filled again
+  }
+  cp_async_wait<0>();
+  __syncthreads();   // the rings become the warps' states
+  float* so = (float*)smem;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float x = l[t][e];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      const int h = t * 8 + 2 * tig + e;
+      if (h < G) {
+        if (gid == 0) {
+          sm[wid * G + h] = m[t][e];
+          sl[wid * G + h] = x;
+        }
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          so[(wid * G + h) * D + i * 16 + gid] = acc[t][i][e];
+          so[(wid * G + h) * D + i * 16 + 8 + gid] = acc[t][i][2 + e];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  finish_part<__nv_bfloat16, D>(p, w, sm, sl, so, &last);
+}
+
+// fp32: one CTA of 4 warps per part, warp w takes every 4th token; lanes over the dimensions.
+template <int D, int GM>
+__global__ void __launch_bounds__(128) sparse_attend_f32_kernel(Params p) {
+  constexpr int E = D / 32;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ float q_s[GM * D];
+  __shared__ float sm[4 * GM], sl[4 * GM];
+  __shared__ int last;
+  const rc_sparse_decode_args& a = p.a;
+  float* so = (float*)smem;                     // [4][G][D]
+  int* slots = (int*)(so + 4 * GM * D);
+  Part w;
+  if (!part_of(p, w)) return;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int G = p.G, n = w.t1 - w.t0;
+  load_slots(p, w, slots);
+  const float scale = a.sm_scale * kLog2e;
+  for (int e = threadIdx.x; e < G * D; e += 128)
+    q_s[e] = ((const float*)a.q)[(w.n * a.num_q_heads + (int64_t)w.g * G) * D + e] * scale;
+  __syncthreads();
+  float m[GM], l[GM], acc[GM][E];
+#pragma unroll
+  for (int h = 0; h < GM; ++h) {
     m[h] = -INFINITY;
     l[h] = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[h][e] = 0.f;
   }
-  for (int t = t0 + wid; t < t1; t += 4) {
-    const int pos = sel[t / a.block] * a.block + t % a.block;
-    if (pos >= L) continue;
-    const int slot = rt[pos];
-    if (slot < 0 || slot >= a.num_slots) {
-      if (lane == 0) set_status(p.status, kStatusSlotRange);
-      continue;
-    }
-    const int64_t r = ((int64_t)slot * a.num_kv_heads + g) * D;
+  for (int t = wid; t < n; t += 4) {
+    const int slot = slots[t];
+    if (slot < 0) continue;
+    const int64_t r = ((int64_t)slot * a.num_kv_heads + w.g) * D;
     float k[E], v[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      k[e] = Elem<T>::to_f(((const T*)a.k_pool)[r + e * 32 + lane]);
-      v[e] = Elem<T>::to_f(((const T*)a.v_pool)[r + e * 32 + lane]);
+      k[e] = ((const float*)a.k_pool)[r + e * 32 + lane];
+      v[e] = ((const float*)a.v_pool)[r + e * 32 + lane];
     }
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      if (h >= Gr) break;
+    for (int h = 0; h < GM; ++h) {
+      if (h >= G) break;
       float s = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(q_s[h][e * 32 + lane], k[e], s);
+      for (int e = 0; e < E; ++e) s = fmaf(q_s[h * D + e * 32 + lane], k[e], s);
 #pragma unroll
       for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       const float mn = fmaxf(m[h], s);
@@ -545,51 +809,17 @@ __global__ void __launch_bounds__(128) sparse_attend_kernel(Params p) {
     }
   }
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
+  for (int h = 0; h < GM; ++h) {
+    if (h >= G) break;
     if (lane == 0) {
-      sm[wid][h] = m[h];
-      sl[wid][h] = l[h];
+      sm[wid * G + h] = m[h];
+      sl[wid * G + h] = l[h];
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) so[wid][h][e * 32 + lane] = acc[h][e];
+    for (int e = 0; e < E; ++e) so[(wid * G + h) * D + e * 32 + lane] = acc[h][e];
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < Gr * D; x += 128) {
-    const int h = x / D, e = x - h * D;
-    float M = fmaxf(fmaxf(sm[0][h], sm[1][h]), fmaxf(sm[2][h], sm[3][h]));
-    float den = 0.f, num = 0.f;
-    for (int w = 0; w < 4; ++w) {
-      const float c = sm[w][h] == -INFINITY ? 1.f : exp2f(sm[w][h] - M);
-      den = fmaf(sl[w][h], c, den);
-      num = fmaf(so[w][h][e], c, num);
-    }
-    const int64_t pi = (unit * p.parts + part) * Gr + h;
-    p.w.po[pi * D + e] = den == 0.f ? 0.f : num / den;
-    if (e == 0) p.w.plse[pi] = den == 0.f ? -INFINITY : M + log2f(den);
-  }
-}
-
-template <typename T>
-__global__ void sparse_merge_kernel(Params p) {
-  const rc_sparse_decode_args& a = p.a;
-  const int64_t x = blockIdx.x;   // row * Hq + query head
-  const int64_t n = x / a.num_q_heads;
-  const int hq = (int)(x - n * a.num_q_heads);
-  const int g = hq / p.G, h = hq - g * p.G;
-  const int D = a.head_dim, e = threadIdx.x;
-  const int64_t unit = n * a.num_kv_heads + g;
-  float M = -INFINITY;
-  for (int c = 0; c < p.parts; ++c) M = fmaxf(M, p.w.plse[(unit * p.parts + c) * p.G + h]);
-  float num = 0.f, den = 0.f;
-  for (int c = 0; c < p.parts; ++c) {
-    const int64_t pi = (unit * p.parts + c) * p.G + h;
-    const float pl = p.w.plse[pi];
-    const float w = pl == -INFINITY ? 0.f : exp2f(pl - M);
-    den += w;
-    num = fmaf(w, p.w.po[pi * D + e], num);
-  }
-  ((T*)a.o)[x * D + e] = Elem<T>::from_f(den == 0.f ? 0.f : num / den);
-  if (a.lse && e == 0) a.lse[x] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
+  finish_part<float, D>(p, w, sm, sl, so, &last);
 }
 
 int validate(const rc_sparse_decode_args* a, const char* fn) {
@@ -620,17 +850,43 @@ Params params_of(const rc_sparse_decode_args* a) {
   p.G = a->num_q_heads / a->num_kv_heads;
   p.nb = std::max(1, (a->max_seq_len + a->block - 1) / a->block);
   const int64_t tokens = (int64_t)std::min(p.nb, a->top_blocks) * a->block;
-  p.parts = (int)((tokens + kPart - 1) / kPart);
+  // parts as long as kMaxPart leaves enough CTAs to fill the GPU, shorter ones for few rows
+  const int64_t units = (int64_t)a->num_rows * a->num_kv_heads;
+  int64_t part = kMaxPart;
+  while (part > kMinPart && units * ((tokens + part - 1) / part) < kEnoughCtas) part /= 2;
+  p.part_tokens = (int)part;
+  p.parts = (int)((tokens + part - 1) / part);
   return p;
 }
 
-template <typename T, int D>
-void launch_attend(const Params& p, dim3 grid, cudaStream_t s) {
-  if (p.G <= 1) sparse_attend_kernel<T, D, 1><<<grid, 128, 0, s>>>(p);
-  else if (p.G <= 2) sparse_attend_kernel<T, D, 2><<<grid, 128, 0, s>>>(p);
-  else if (p.G <= 4) sparse_attend_kernel<T, D, 4><<<grid, 128, 0, s>>>(p);
-  else if (p.G <= 8) sparse_attend_kernel<T, D, 8><<<grid, 128, 0, s>>>(p);
-  else sparse_attend_kernel<T, D, 16><<<grid, 128, 0, s>>>(p);
+// Launches an attention kernel with more dynamic shared memory than the default allows.
+template <typename K>
+cudaError_t launch_attend(K kernel, PerDevice<int>& setup, int max_smem, int smem, const Params& p,
+                          unsigned units, cudaStream_t s) {
+  const int* unused = nullptr;
+  const cudaError_t e = setup.get(
+      [&](int&) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
+      },
+      &unused);
+  if (e != cudaSuccess) return e;
+  kernel<<<units * (unsigned)p.parts, 128, smem, s>>>(p);
+  return cudaGetLastError();
+}
+template <int D, int NT>
+cudaError_t attend_bf16(const Params& p, unsigned units, cudaStream_t s) {
+  static PerDevice<int> setup;
+  constexpr int base = AttendCfg<D>::RING;
+  static_assert(base >= 4 * 8 * NT * D * 4, "the warps' states fit the rings");
+  return launch_attend(sparse_attend_mma_kernel<D, NT>, setup, base + kMaxPart * 4,
+                       base + p.part_tokens * 4, p, units, s);
+}
+template <int D, int GM>
+cudaError_t attend_f32(const Params& p, unsigned units, cudaStream_t s) {
+  static PerDevice<int> setup;
+  constexpr int base = 4 * GM * D * 4;
+  return launch_attend(sparse_attend_f32_kernel<D, GM>, setup, base + kMaxPart * 4,
+                       base + p.part_tokens * 4, p, units, s);
 }
 
 template <typename T, int D, int NT>
@@ -663,9 +919,16 @@ int launch(const Params& p, cudaStream_t s) {
     e = launch_select<T, D, 1>(p, units, s);
   if (e != cudaSuccess)
     return fail(RC_ERR_CUDA, "rc_sparse_decode_attention: launch failed: %s", cudaGetErrorString(e));
-  launch_attend<T, D>(p, dim3(units, p.parts), s);
-  sparse_merge_kernel<T><<<p.a.num_rows * p.a.num_q_heads, D, 0, s>>>(p);
-  count_launches(3);
+  if constexpr (sizeof(T) == 2)
+    e = p.G <= 8 ? attend_bf16<D, 1>(p, units, s) : attend_bf16<D, 2>(p, units, s);
+  else
+    e = p.G <= 1   ? attend_f32<D, 1>(p, units, s)
+        : p.G <= 4 ? attend_f32<D, 4>(p, units, s)
+        : p.G <= 8 ? attend_f32<D, 8>(p, units, s)
+                   : attend_f32<D, 16>(p, units, s);
+  if (e != cudaSuccess)
+    return fail(RC_ERR_CUDA, "rc_sparse_decode_attention: launch failed: %s", cudaGetErrorString(e));
+  count_launches(2);
   return check_launch("rc_sparse_decode_attention");
 }
 
@@ -705,8 +968,8 @@ extern "C" int rc_sparse_decode_attention(const rc_sparse_decode_args* a, void* 
                        (uintptr_t)a->bounds | (uintptr_t)a->o | (uintptr_t)workspace;
   RC_CHECK_ARG((al & 15) == 0, "%s: tensors and workspace must be 16-byte aligned", fn);
   rc::Params p = rc::params_of(a);
-  RC_CHECK_ARG(p.parts <= 65535, "%s: top_blocks %d of %d tokens are too many", fn, a->top_blocks,
-               a->block);
+  RC_CHECK_ARG((int64_t)a->num_rows * a->num_kv_heads * p.parts < (1ll << 31),
+               "%s: too many rows for top_blocks %d of %d tokens", fn, a->top_blocks, a->block);
   size_t need = 0;
   p.w = rc::carve(workspace, p, &need);
   RC_CHECK_ARG(workspace_bytes >= need, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes,
