@@ -26,7 +26,9 @@ def test_sparse_decode_rejects_bad_arguments_before_any_device_work():
         return RcSparseDecodeArgs(**a)
 
     need = ctypes.c_size_t()
-    assert lib().rc_sparse_decode_workspace_bytes(ctypes.byref(args()), ctypes.byref(need)) == 0
+    long = dict(max_ctx=1 << 20, max_seq_len=1 << 20, max_blocks=1 << 14)
+    assert lib().rc_sparse_decode_workspace_bytes(ctypes.byref(args(**long)),
+                                                  ctypes.byref(need)) == 0 and need.value > 0
 
     def call(ws=fake(20), ws_bytes=need.value, **kw):
         return lib().rc_sparse_decode_attention(ctypes.byref(args(**kw)), ws, ws_bytes, None)
@@ -36,7 +38,7 @@ def test_sparse_decode_rejects_bad_arguments_before_any_device_work():
              dict(block=256), dict(max_seq_len=-1), dict(max_seq_len=(1 << 24) + 1),
              dict(top_blocks=0), dict(top_blocks=1), dict(sink_blocks=-1), dict(recent_blocks=0),
              dict(sink_blocks=5, recent_blocks=4), dict(num_rows=1 << 28),
-             dict(top_blocks=(1 << 20) + 1)]
+             dict(top_blocks=8193)]
     for kw in sizes:
         assert call(**kw) == rc.RC_ERR_INVALID, kw
         a = args(**kw)
@@ -46,8 +48,8 @@ def test_sparse_decode_rejects_bad_arguments_before_any_device_work():
     for kw in (dict(max_seq_len=1001), dict(max_blocks=15), dict(max_reqs=0), dict(num_slots=0),
                dict(sm_scale=0.0), dict(sm_scale=-1.0), dict(sm_scale=float("nan")),
                dict(sm_scale=float("inf")), dict(q=0), dict(bounds=0), dict(o=fake(7) + 8),
-               dict(k_pool=fake(4) + 2), dict(ws=0), dict(ws=fake(20) + 4),
-               dict(ws_bytes=need.value - 1)):
+               dict(k_pool=fake(4) + 2), dict(ws=0, **long), dict(ws=fake(20) + 4),
+               dict(ws_bytes=need.value - 1, **long)):
         assert call(**kw) == rc.RC_ERR_INVALID, kw
     assert call(num_rows=0) == rc.RC_OK
     assert lib().rc_sparse_decode_attention(None, fake(20), 1 << 20, None) == rc.RC_ERR_INVALID
@@ -135,6 +137,8 @@ SHAPES = [  # dtype, contexts, hq, hkv, d, block, top, sink, recent
     ("bf16", [1024], 32, 2, 64, 64, 16, 1, 1),
     ("bf16", [3500], 12, 1, 128, 32, 64, 1, 3),
     ("bf16", [5000, 1], 24, 2, 64, 16, 3, 1, 1),
+    ("bf16", [9000], 2, 2, 128, 16, 300, 1, 2),
+    ("bf16", [130], 4, 1, 128, 16, 2, 1, 1),
     ("f32", [1, 33], 2, 2, 64, 16, 1, 0, 1),
     ("f32", [700, 0, 97], 6, 2, 64, 32, 5, 1, 1),
     ("f32", [1111], 8, 1, 128, 64, 6, 1, 2),
@@ -150,6 +154,37 @@ def test_sparse_decode_matches_the_definition(dtype, ctx, hq, hkv, d, block, top
     c = Case(dtype, ctx, [(b, m) for b, m in enumerate(ctx)], hq, hkv, d, block)
     c.call(top, sink, recent).check()
     assert rc.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_blocks_than_shared_memory_holds(dtype):
+    """Contexts of 120 000 and 70 000 tokens in blocks of 16: the scores live in the workspace. The
+    pool is small (slots repeat), the selection is checked over all blocks."""
+    g = torch.Generator().manual_seed(7)
+    hq, hkv, d, block, n = 2, 1, 64, 16, (120_000, 70_001)
+    c = Case(dtype, [600, 300], [(0, n[0]), (1, n[1])], hq, hkv, d, block)
+    c.max_ctx = n[0]
+    c.table = torch.randint(0, 900, (c.table.shape[0], n[0]), generator=g, dtype=torch.int32)
+    nb = -(-n[0] // block)
+    c.bounds = torch.randn((c.table.shape[0], nb, hkv, 2, d), generator=g).to(c.dt)
+    c.bounds = torch.cat([c.bounds.amin(3, True), c.bounds.amax(3, True)], 3).contiguous()
+    q, k = c.q.cuda(), c.k.cuda()
+    assert rc.sparse_decode_workspace_bytes(q, k, max_seq_len=n[0], block=block, top_blocks=90) > 0
+    c.call(90).check()
+    # with a score that is infinite every block is ranked in 64 bits
+    c.bounds[:, 77, 0, 1] = float("inf")
+    c.call(90).check()
+    assert 77 in c.sel[0, 0].tolist() and rc.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("units,top", [(1, 4), (1, 40), (3, 40), (40, 12), (150, 12), (460, 3)])
+def test_every_number_of_parts_per_row(units, top):
+    """From 16 CTAs per row to one, rows of unlike lengths among them."""
+    ctx = [64 * 60 + 13 + 5 * i if i < 3 else 70 + i for i in range(units)]
+    c = Case("bf16", ctx, [(b, m) for b, m in enumerate(ctx)], 2, 1, 64, 64)
+    c.call(top).check(only=[0, 1, 2, 7, units - 1])
 
 
 @pytest.mark.gpu
@@ -393,8 +428,7 @@ def test_sparse_decode_refusals():
                 dict(bounds=ok["bounds"].float())):
         with pytest.raises(TypeError):
             rc.sparse_decode_attention(**{**ok, **bad})
-    for bad in (dict(max_seq_len=200), dict(top_blocks=1), dict(block=65),
-                dict(workspace=ok["workspace"][:16]), dict(sm_scale=0.0)):
+    for bad in (dict(max_seq_len=200), dict(top_blocks=1), dict(block=65), dict(sm_scale=0.0)):
         with pytest.raises(rc.RcError) as e:
             rc.sparse_decode_attention(**{**ok, **bad})
         assert e.value.code == rc.RC_ERR_INVALID
