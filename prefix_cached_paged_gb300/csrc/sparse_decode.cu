@@ -62,6 +62,8 @@ __device__ __forceinline__ int row_len(const Params& p, int64_t n, bool report) 
 
 // Dynamic shared memory of a CTA: the copy rings (bf16), which first hold the unit's scores and
 // ranks and in the end the states to join; then the slots of a segment; then the chosen blocks.
+constexpr int kBins = 2048;        // counters of the selection's radix steps
+
 template <typename T, int D, int GM>
 struct Cfg {
   static constexpr bool kBf16 = sizeof(T) == 2;
@@ -73,6 +75,8 @@ struct Cfg {
   static constexpr int BASE = RING > 36864 ? RING : 36864;
   static constexpr int BLOCKS = BASE / 16;                    // a rank and a score take 12 bytes
   static_assert(BASE >= (kWarps + 1) * STATE, "the states fit");
+  static constexpr int HIST = BLOCKS * 12;
+  static_assert(HIST % 4 == 0 && BASE - HIST >= kBins * 4, "the histogram fits beside them");
   static constexpr int SLOTS = BASE;
   static constexpr int LIST = BASE + kSegment * 4;
   static int bytes(int top) { return LIST + top * 4; }
@@ -87,13 +91,29 @@ struct Cfg {
 // twice that bound reaches across the border, so the result is that of 64-bit scores.
 constexpr float kScoreError = 1.0f / 65536;
 
+// Larger score <=> larger integer.
+__device__ __forceinline__ uint32_t order32(float s) {
+  const int b = __float_as_int(s + 0.f);   // -0 ranks as 0
+  return (uint32_t)(b < 0 ? ~b : (b | (1 << 31)));
+}
+__device__ __forceinline__ unsigned long long order64(double s) {
+  if (!(s < 1.7976931348623157e308)) s = 1.7976931348623157e308;   // NaN, +inf
+  if (s < -1.7976931348623157e308) s = -1.7976931348623157e308;
+  const long long b = __double_as_longlong(s + 0.0);
+  return (unsigned long long)(b < 0 ? ~b : (b | (1ll << 63)));
+}
+
 // Where the scores of a unit's blocks [f0, f1) go (index block - f0): the shared memory of every
 // CTA of the cluster, or the workspace.
 struct ScoreSink {
   float* local;   // this CTA's shared memory, or the workspace
   bool shared;
   int cluster, f0, f1;
-  __device__ __forceinline__ void put(int b, float s) const {
+  float tmax = 0.f;   // largest t this lane saw; least and greatest score it put
+  uint32_t lo = 0xffffffffu, hi = 0;
+  __device__ __forceinline__ void put(int b, float s) {
+    lo = min(lo, order32(s));
+    hi = max(hi, order32(s));
     if (!shared || cluster == 1) {
       local[b - f0] = s;
     } else {
@@ -102,16 +122,15 @@ struct ScoreSink {
   }
 };
 
-// Scores of 16 blocks at a time against the query heads of a KV head by one warp (returns the
-// largest t its lane saw), boxes and queries straight
+// Scores of 16 blocks at a time against the query heads of a KV head by one warp, boxes and queries straight
 // from global memory into matrix fragments: the dot product does not care in which order the
 // dimensions come, so lane (gid, tig) takes 16 contiguous bytes of a row where the instruction
 // wants four pairs, the same ones for both operands. [q-, q+] . [lo, hi] needs no comparison:
 // one of q+ = max(q, 0) and q- = min(q, 0) is zero. (0 * inf gives a NaN that the definition has
 // not: a score that is not finite sends its unit to the 64-bit path.)
 template <int D, int NT>
-__device__ __forceinline__ float score_tiles(const Params& p, int64_t n, int g, int tile0, int tile_step,
-                             const ScoreSink& out) {
+__device__ __forceinline__ void score_tiles(const Params& p, int64_t n, int g, int tile0,
+                                            int tile_step, ScoreSink& out) {
   constexpr int J = D / 32;   // 32-element groups of a row
   const rc_sparse_decode_args& a = p.a;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
@@ -127,7 +146,6 @@ __device__ __forceinline__ float score_tiles(const Params& p, int64_t n, int g, 
   const __nv_bfloat16* boxes = (const __nv_bfloat16*)a.bounds +
                                ((int64_t)a.req_idx[n] * a.max_blocks * a.num_kv_heads + g) * 2 * D;
   const int64_t stride = (int64_t)a.num_kv_heads * 2 * D;
-  float tmax = 0.f;
   for (int tile = tile0; out.f0 + tile * 16 < out.f1; tile += tile_step) {
     const int r0 = out.f0 + tile * 16 + gid, r1 = r0 + 8;
     const uint4* b0 = (const uint4*)(boxes + r0 * stride);
@@ -165,7 +183,7 @@ __device__ __forceinline__ float score_tiles(const Params& p, int64_t n, int g, 
         if (t * 8 + 2 * tig + e < p.G) {
           best0 = max_nan(best0, (c[0][e] + c[1][e]) + (c[2][e] + c[3][e]));
           best1 = max_nan(best1, (c[0][2 + e] + c[1][2 + e]) + (c[2][2 + e] + c[3][2 + e]));
-          tmax = max_nan(tmax, max_nan(m[e], m[2 + e]));   // rows past f1 are zeros
+          out.tmax = max_nan(out.tmax, max_nan(m[e], m[2 + e]));   // rows past f1 are zeros
         }
       }
     }
@@ -177,20 +195,18 @@ __device__ __forceinline__ float score_tiles(const Params& p, int64_t n, int g, 
     if (tig == 0 && r0 < out.f1) out.put(r0, best0);
     if (tig == 0 && r1 < out.f1) out.put(r1, best1);
   }
-  return tmax;
 }
 
 // The fp32 form: one warp per block, lanes over the dimensions.
 template <int D>
-__device__ __forceinline__ float score_blocks_f32(const Params& p, int64_t n, int g, int first, int step,
-                                  const ScoreSink& out) {
+__device__ __forceinline__ void score_blocks_f32(const Params& p, int64_t n, int g, int first,
+                                                 int step, ScoreSink& out) {
   constexpr int E = D / 32;
   const rc_sparse_decode_args& a = p.a;
   const int lane = threadIdx.x & 31;
   const float* q = (const float*)a.q + (n * a.num_q_heads + (int64_t)g * p.G) * D + lane * E;
   const float* boxes = (const float*)a.bounds +
                        ((int64_t)a.req_idx[n] * a.max_blocks * a.num_kv_heads + g) * 2 * D + lane * E;
-  float tmax = 0.f;
   for (int b = out.f0 + first; b < out.f1; b += step) {
     const float* box = boxes + (int64_t)b * a.num_kv_heads * 2 * D;
     float lo[E], hi[E];
@@ -215,35 +231,20 @@ __device__ __forceinline__ float score_blocks_f32(const Params& p, int64_t n, in
         t += __shfl_xor_sync(0xffffffffu, t, o);
       }
       best = max_nan(best, s);
-      tmax = max_nan(tmax, t);
+      out.tmax = max_nan(out.tmax, t);
     }
     if (lane == 0) out.put(b, best);
   }
-  return tmax;
 }
 
 // ---------------------------------------------------------------- selection
-// Larger score <=> larger integer.
-__device__ __forceinline__ uint32_t order32(float s) {
-  const int b = __float_as_int(s + 0.f);   // -0 ranks as 0
-  return (uint32_t)(b < 0 ? ~b : (b | (1 << 31)));
-}
-__device__ __forceinline__ unsigned long long order64(double s) {
-  if (!(s < 1.7976931348623157e308)) s = 1.7976931348623157e308;   // NaN, +inf
-  if (s < -1.7976931348623157e308) s = -1.7976931348623157e308;
-  const long long b = __double_as_longlong(s + 0.0);
-  return (unsigned long long)(b < 0 ? ~b : (b | (1ll << 63)));
-}
-
 struct SelectShared {
-  union {
-    int hist[256];
-    unsigned long long list[kThreads];   // keys near the k-th largest
-  };
+  unsigned long long list[kThreads];   // keys near the k-th largest, or ranks near the border
+  int index[kThreads];                 // and their blocks
   int wsum[2][kWarps];
   int bin, above, inbin, listed;
   unsigned long long kth;
-  uint32_t lo, hi, tmax;
+  uint32_t lo, hi, tmax;               // of the scores (ordered integers), and of their t
 };
 
 // Sums of x and y over the CTA (all threads get them).
@@ -265,19 +266,22 @@ __device__ __forceinline__ void block_sum2(SelectShared& s, int& x, int& y) {
 }
 
 // The k-th largest (k >= 1) of the values key(i), i < n, for which ok(i), all between lo and hi;
-// there are at least k. Radix steps of 8 bits, beginning below the digits that lo and hi share,
-// until at most one key per thread is left, whose ranks are counted.
+// there are at least k, and `left` at most. Radix steps of 11 bits, beginning below the digits that
+// lo and hi share, until at most one key per thread is left, whose ranks are counted: one step,
+// unless most scores are alike. hist: kBins counters.
 template <typename K, typename Key, typename Ok>
-__device__ K kth_largest(SelectShared& s, int n, int k, K lo, K hi, Key key, Ok ok) {
-  constexpr int kBits = sizeof(K) * 8;
+__device__ K kth_largest(SelectShared& s, int* hist, int n, int left, int k, K lo, K hi, Key key,
+                         Ok ok) {
+  constexpr int kBits = sizeof(K) * 8, kDigit = 11, kPer = kBins / kThreads;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   int shift = lo == hi ? 0 : kBits - (__clzll((unsigned long long)(lo ^ hi)) - (64 - kBits));
   K prefix = shift == kBits ? 0 : (hi >> shift) << shift;
-  int left = n;   // keys that begin with prefix, at most
   while (shift > 0) {
     if (left <= kThreads) {
-      if (threadIdx.x == 0) s.listed = 0;
+      if (tid == 0) s.listed = 0;
       __syncthreads();
-      for (int i = threadIdx.x; i < n; i += kThreads) {
+#pragma unroll 4
+      for (int i = tid; i < n; i += kThreads) {
         if (!ok(i)) continue;
         const K x = key(i);
         if (shift == kBits || (x >> shift) == (prefix >> shift))
@@ -285,8 +289,8 @@ __device__ K kth_largest(SelectShared& s, int n, int k, K lo, K hi, Key key, Ok 
       }
       __syncthreads();
       const int c = s.listed;
-      if (threadIdx.x < c) {
-        const unsigned long long x = s.list[threadIdx.x];
+      if (tid < c) {
+        const unsigned long long x = s.list[tid];
         int above = 0, equal = 0;
         for (int i = 0; i < c; ++i) {
           above += s.list[i] > x;
@@ -297,41 +301,44 @@ __device__ K kth_largest(SelectShared& s, int n, int k, K lo, K hi, Key key, Ok 
       __syncthreads();
       return (K)s.kth;
     }
-    const int bits = min(shift, 8), low = shift - bits;
-    for (int i = threadIdx.x; i < 256; i += kThreads) s.hist[i] = 0;
+    const int bits = min(shift, kDigit), low = shift - bits;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) hist[i * kThreads + tid] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads) {
+#pragma unroll 4
+    for (int i = tid; i < n; i += kThreads) {
       if (!ok(i)) continue;
       const K x = key(i);
       if (shift == kBits || (x >> shift) == (prefix >> shift))
-        atomicAdd(&s.hist[(int)((x >> low) & (K)((1 << bits) - 1))], 1);
+        atomicAdd(&hist[(int)((x >> low) & (K)((1 << bits) - 1))], 1);
     }
     __syncthreads();
-    if (threadIdx.x < 32) {   // the bin that holds the k-th largest, from the top
-      const int lane = threadIdx.x;
-      int c[8], sum = 0;
+    // the bin that holds the k-th largest, from the top: thread t has bins 2047 - 16 t downwards
+    int c[kPer], sum = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        c[e] = s.hist[255 - (lane * 8 + e)];
-        sum += c[e];
-      }
-      int run = sum;
+    for (int e = 0; e < kPer; ++e) {
+      c[e] = hist[kBins - 1 - (tid * kPer + e)];
+      sum += c[e];
+    }
+    int run = sum;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += y;
-      }
-      int before = run - sum;
-      if (before < k && run >= k) {
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
+    }
+    if (lane == 31) s.wsum[0][wid] = run;
+    __syncthreads();
+    int before = run - sum;
+    for (int w = 0; w < wid; ++w) before += s.wsum[0][w];
+    if (before < k && before + sum >= k) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (before < k && before + c[e] >= k) {
-            s.bin = 255 - (lane * 8 + e);
-            s.above = before;
-            s.inbin = c[e];
-          }
-          before += c[e];
+      for (int e = 0; e < kPer; ++e) {
+        if (before < k && before + c[e] >= k) {
+          s.bin = kBins - 1 - (tid * kPer + e);
+          s.above = before;
+          s.inbin = c[e];
         }
+        before += c[e];
       }
     }
     __syncthreads();
@@ -343,111 +350,61 @@ __device__ K kth_largest(SelectShared& s, int n, int k, K lo, K hi, Key key, Ok 
   return prefix;
 }
 
-// The 64-bit rank of block b: the largest score over the KV head's queries. One warp.
-template <typename T>
-__device__ unsigned long long exact_rank(const Params& p, int64_t n, int g, int b) {
+// The 64-bit rank of block b: the largest score over the KV head's queries. One warp, four queries
+// at a time so that their loads and sums overlap.
+template <typename T, int D>
+__device__ __noinline__ unsigned long long exact_rank(const Params& p, int64_t n, int g, int b) {
+  constexpr int E = D / 32;
   const rc_sparse_decode_args& a = p.a;
-  const int lane = threadIdx.x & 31, d = a.head_dim;
+  const int lane = threadIdx.x & 31;
   const T* box = (const T*)a.bounds +
-                 ((((int64_t)a.req_idx[n] * a.max_blocks + b) * a.num_kv_heads + g) * 2) * d;
+                 ((((int64_t)a.req_idx[n] * a.max_blocks + b) * a.num_kv_heads + g) * 2) * D + lane;
+  const T* q = (const T*)a.q + (n * a.num_q_heads + (int64_t)g * p.G) * D + lane;
+  float lo[E], hi[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    lo[e] = Elem<T>::to_f(box[e * 32]);
+    hi[e] = Elem<T>::to_f(box[D + e * 32]);
+  }
   unsigned long long rank = 0;
-  for (int h = 0; h < p.G; ++h) {
-    const T* q = (const T*)a.q + (n * a.num_q_heads + (int64_t)g * p.G + h) * d;
-    double s = 0.0;
-    for (int e = lane; e < d; e += 32) {
-      const float x = Elem<T>::to_f(q[e]);
-      s += (double)x * (double)Elem<T>::to_f(x >= 0.f ? box[d + e] : box[e]);
+  for (int h0 = 0; h0 < p.G; h0 += 4) {
+    double s[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      s[h] = 0.0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float x = h0 + h < p.G ? Elem<T>::to_f(q[(h0 + h) * D + e * 32]) : 0.f;
+        s[h] += (double)x * (double)(x >= 0.f ? hi[e] : lo[e]);
+      }
     }
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    rank = max(rank, order64(s));
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) s[h] += __shfl_xor_sync(0xffffffffu, s[h], o);
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      if (h0 + h < p.G) rank = max(rank, order64(s[h]));
   }
   return rank;
 }
 
-// The chosen blocks of a unit in ascending order into `list` (shared memory), by the whole CTA:
-// the forced blocks outside [f0, f1) and the k best of those inside, by score[b - f0] where the
-// fp32 scores can tell, by 64-bit ranks in r64 where they cannot. tmax: the largest t, as bits.
-template <typename T>
-__device__ void select_blocks(const Params& p, SelectShared& sh, int64_t n, int g, int have, int f0,
-                              int f1, int k, const float* score, unsigned long long* r64,
-                              uint32_t tmax, int* list) {
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int m = f1 - f0;
-  const bool all64 = tmax >= 0x7f800000u;   // a score may be infinite or no number
-  float hi_s = 0.f, lo_s = 0.f;
-  int in = 0, need64 = m;   // taken whatever the 64-bit ranks say; those that they decide about
-  if (k > 0 && !all64) {
-    uint32_t lo = 0xffffffffu, hi = 0;
-    for (int i = tid; i < m; i += kThreads) {
-      const uint32_t o = order32(score[i]);
-      lo = min(lo, o);
-      hi = max(hi, o);
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) {
-      atomicMin(&sh.lo, lo);
-      atomicMax(&sh.hi, hi);
-    }
-    __syncthreads();
-    const uint32_t thr = kth_largest<uint32_t>(
-        sh, m, k, sh.lo, sh.hi, [&](int i) { return order32(score[i]); },
-        [](int) { return true; });
-    const float ts = __uint_as_float(thr & (1u << 31) ? thr & ~(1u << 31) : ~thr);
-    // (1 % for the roundings of these lines; products below the smallest normal number may be lost)
-    const float e2 = 2.02f * kScoreError * __uint_as_float(tmax) + 0x1p-110f;
-    hi_s = ts + e2;
-    lo_s = ts - e2;
-    need64 = 0;
-    for (int i = tid; i < m; i += kThreads) {
-      const float s = score[i];
-      in += s > hi_s;
-      need64 += s >= lo_s && s <= hi_s;
-    }
-    block_sum2(sh, in, need64);
-  }
-  const int rest = k - in;   // to be taken of the need64 near the border
-  auto near = [&](int i) { return all64 || (score[i] >= lo_s && score[i] <= hi_s); };
-  unsigned long long thr64 = 0;
-  int ties = 0;   // blocks of rank thr64 that are taken, the lowest-numbered ones
-  const bool exact = k > 0 && need64 > rest;
-  if (exact) {
-    for (int i0 = wid * 32; i0 < m; i0 += kThreads) {
-      const int i = i0 + lane;
-      unsigned todo = __ballot_sync(0xffffffffu, i < m && near(i));
-      while (todo) {
-        const int j = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const unsigned long long r = exact_rank<T>(p, n, g, f0 + i0 + j);
-        if (lane == 0) r64[i0 + j] = r;
-      }
-    }
-    __syncthreads();
-    thr64 = kth_largest<unsigned long long>(
-        sh, m, rest, 0ull, ~0ull, [&](int i) { return r64[i]; }, near);
-    int c = 0, unused = 0;
-    for (int i = tid; i < m; i += kThreads) c += near(i) && r64[i] > thr64;
-    block_sum2(sh, c, unused);
-    ties = rest - c;
-  }
-  // 2: chosen, 1: one of the ties, 0: not chosen
-  auto kind = [&](int b) {
-    if (b < f0 || b >= f1) return 2;
-    if (k <= 0) return 0;
-    const int i = b - f0;
-    if (!near(i)) return score[i] > hi_s ? 2 : 0;
-    if (!exact) return 2;
-    return r64[i] > thr64 ? 2 : r64[i] == thr64 ? 1 : 0;
-  };
-  // each warp counts in its quarter of the blocks, then writes from where the earlier ones end
+// Writes the blocks for which kind(b) is 2, and the first `ties` for which it is 1, in ascending
+// order. Each warp counts in its quarter of the blocks, then writes from where the earlier ones end.
+template <typename Kind>
+__device__ __forceinline__ void compact(SelectShared& sh, int have, int ties, int* list, Kind kind) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int quarter = (have + kThreads - 1) / kThreads * 32;
   const int b0 = wid * quarter, b1 = min(have, b0 + quarter);
   int np = 0, ne = 0;
-  for (int b = b0; b < b1; b += 32) {
-    const int c = b + lane < b1 ? kind(b + lane) : 0;
-    np += __popc(__ballot_sync(0xffffffffu, c == 2));
-    ne += __popc(__ballot_sync(0xffffffffu, c == 1));
+#pragma unroll 4
+  for (int b = b0 + lane; b < b1; b += 32) {
+    const int c = kind(b);
+    np += c == 2;
+    ne += c == 1;
   }
+  np = __reduce_add_sync(0xffffffffu, np);
+  ne = __reduce_add_sync(0xffffffffu, ne);
   __syncthreads();
   if (lane == 0) {
     sh.wsum[0][wid] = np;
@@ -461,6 +418,7 @@ __device__ void select_blocks(const Params& p, SelectShared& sh, int64_t n, int 
   }
   at += min(eq, ties);
   const unsigned below = (1u << lane) - 1;
+#pragma unroll 4
   for (int b = b0; b < b1; b += 32) {
     const int c = b + lane < b1 ? kind(b + lane) : 0;
     const unsigned me = __ballot_sync(0xffffffffu, c == 1);
@@ -471,6 +429,97 @@ __device__ void select_blocks(const Params& p, SelectShared& sh, int64_t n, int 
     eq += __popc(me);
   }
   __syncthreads();
+}
+
+// The chosen blocks of a unit in ascending order into `list` (shared memory), by the whole CTA:
+// the forced blocks outside [f0, f1) and the k best of those inside, by score[b - f0] where the
+// fp32 scores can tell, by 64-bit ranks in r64 where they cannot. `own`: the scores are this CTA's
+// own copy.
+template <typename T, int D>
+__device__ __forceinline__ void select_blocks(const Params& p, SelectShared& sh, int* hist, int64_t n,
+                                              int g, int have, int f0, int f1, int k, float* score,
+                                              unsigned long long* r64, bool own, int* list) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int m = f1 - f0;
+  if (k <= 0) {
+    compact(sh, have, 0, list, [&](int b) { return b < f0 || b >= f1 ? 2 : 0; });
+    return;
+  }
+  const bool all64 = sh.tmax >= 0x7f800000u;   // a score may be infinite or no number
+  float hi_s = 0.f, lo_s = 0.f;
+  int in = 0, need64 = m;   // taken whatever the 64-bit ranks say; those that they decide about
+  if (!all64) {
+    const uint32_t thr = kth_largest<uint32_t>(
+        sh, hist, m, m, k, sh.lo, sh.hi, [&](int i) { return order32(score[i]); },
+        [](int) { return true; });
+    const float ts = __uint_as_float(thr & (1u << 31) ? thr & ~(1u << 31) : ~thr);
+    // (1 % for the roundings of these lines; products below the smallest normal number may be lost)
+    const float e2 = 2.02f * kScoreError * __uint_as_float(sh.tmax) + 0x1p-110f;
+    hi_s = ts + e2;
+    lo_s = ts - e2;
+    need64 = 0;
+#pragma unroll 4
+    for (int i = tid; i < m; i += kThreads) {
+      const float s = score[i];
+      in += s > hi_s;
+      need64 += s >= lo_s && s <= hi_s;
+    }
+    block_sum2(sh, in, need64);
+  }
+  const int rest = k - in;   // to be taken of the need64 near the border
+  auto near = [&](int i) { return all64 || (score[i] >= lo_s && score[i] <= hi_s); };
+  if (need64 > rest && need64 <= kThreads && own && !all64) {
+    // few blocks: rank them against one another (of equal ones the lower number is first), and
+    // let their scores say whether they are taken
+    if (tid == 0) sh.listed = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < m; i += kThreads)
+      if (near(i)) sh.index[atomicAdd(&sh.listed, 1)] = i;
+    __syncthreads();
+    for (int c = wid; c < need64; c += kWarps) {
+      const unsigned long long r = exact_rank<T, D>(p, n, g, f0 + sh.index[c]);
+      if (lane == 0) sh.list[c] = r;
+    }
+    __syncthreads();
+    if (tid < need64) {
+      const unsigned long long r = sh.list[tid];
+      const int i = sh.index[tid];
+      int before = 0;
+      for (int c = 0; c < need64; ++c)
+        before += sh.list[c] > r || (sh.list[c] == r && sh.index[c] < i);
+      score[i] = before < rest ? INFINITY : -INFINITY;
+    }
+    __syncthreads();
+    need64 = rest;
+  }
+  if (need64 == rest) {   // the border is clear
+    compact(sh, have, 0, list,
+            [&](int b) { return b < f0 || b >= f1 || score[b - f0] >= lo_s ? 2 : 0; });
+    return;
+  }
+  for (int i0 = wid * 32; i0 < m; i0 += kThreads) {
+    const int i = i0 + lane;
+    unsigned todo = __ballot_sync(0xffffffffu, i < m && near(i));
+    while (todo) {
+      const int j = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const unsigned long long r = exact_rank<T, D>(p, n, g, f0 + i0 + j);
+      if (lane == 0) r64[i0 + j] = r;
+    }
+  }
+  __syncthreads();
+  const unsigned long long thr64 = kth_largest<unsigned long long>(
+      sh, hist, m, need64, rest, 0ull, ~0ull, [&](int i) { return r64[i]; }, near);
+  int c = 0, unused = 0;
+  for (int i = tid; i < m; i += kThreads) c += near(i) && r64[i] > thr64;
+  block_sum2(sh, c, unused);
+  compact(sh, have, rest - c, list, [&](int b) {
+    if (b < f0 || b >= f1) return 2;
+    const int i = b - f0;
+    if (!near(i)) return score[i] > hi_s ? 2 : 0;
+    return r64[i] > thr64 ? 2 : r64[i] == thr64 ? 1 : 0;
+  });
 }
 
 // ---------------------------------------------------------------- attention
@@ -629,11 +678,11 @@ struct AttendMma {
   }
 };
 
-// The fp32 form: a warp takes every 4th token, lanes over the dimensions (D / 32 consecutive ones
-// each), GM >= G query heads.
+// The fp32 form: a warp takes every 4th group of TB tokens (their loads and sums overlap), lanes
+// over the dimensions (D / 32 consecutive ones each), GM >= G query heads.
 template <int D, int GM>
 struct AttendF32 {
-  static constexpr int E = D / 32;
+  static constexpr int E = D / 32, TB = 4;
   float q[GM][E], acc[GM][E], m[GM], l[GM];
 
   __device__ __forceinline__ void begin(const Params& p, int64_t n, int g) {
@@ -655,32 +704,51 @@ struct AttendF32 {
   __device__ __forceinline__ void tokens(const Params& p, char*, int g, const int* slots, int n) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int64_t base = (int64_t)g * D + lane * E, step = (int64_t)p.a.num_kv_heads * D;
-#pragma unroll 2
-    for (int t = wid; t < n; t += kWarps) {
-      const int slot = slots[t];
-      if (slot < 0) continue;
-      float k[E], v[E];
+    for (int t0 = wid * TB; t0 < n; t0 += kWarps * TB) {
+      float k[TB][E], v[TB][E];
+      bool ok[TB];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        k[e] = ((const float*)p.a.k_pool)[slot * step + base + e];
-        v[e] = ((const float*)p.a.v_pool)[slot * step + base + e];
+      for (int b = 0; b < TB; ++b) {
+        const int slot = t0 + b < n ? slots[t0 + b] : -1;
+        ok[b] = slot >= 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          k[b][e] = ok[b] ? ((const float*)p.a.k_pool)[slot * step + base + e] : 0.f;
+          v[b][e] = ok[b] ? ((const float*)p.a.v_pool)[slot * step + base + e] : 0.f;
+        }
       }
 #pragma unroll
       for (int h = 0; h < GM; ++h) {
         if (h >= p.G) break;
-        float s = 0.f;
+        float s[TB], mn = m[h];
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q[h][e], k[e], s);
+        for (int b = 0; b < TB; ++b) {
+          s[b] = 0.f;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float mn = fmaxf(m[h], s);
-        // a score of -inf weighs nothing; a NaN reaches the output as it would in a dense softmax
+          for (int e = 0; e < E; ++e) s[b] = fmaf(q[h][e], k[b][e], s[b]);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+#pragma unroll
+          for (int b = 0; b < TB; ++b) s[b] += __shfl_xor_sync(0xffffffffu, s[b], o);
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+          s[b] = ok[b] ? s[b] : -INFINITY;
+          mn = fmaxf(mn, s[b]);
+        }
         const float al = mn == -INFINITY ? 1.f : exp2f(m[h] - mn);
-        const float pr = s == -INFINITY ? 0.f : exp2f(s - mn);
         m[h] = mn;
-        l[h] = l[h] * al + pr;
+        l[h] *= al;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[h][e] = fmaf(pr, v[e], acc[h][e] * al);
+        for (int e = 0; e < E; ++e) acc[h][e] *= al;
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+          // a score of -inf weighs nothing; a NaN reaches the output as it would in a dense softmax
+          const float pr = s[b] == -INFINITY ? 0.f : exp2f(s[b] - mn);
+          l[h] += pr;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[h][e] = fmaf(pr, v[b][e], acc[h][e]);
+        }
       }
     }
   }
@@ -747,17 +815,23 @@ __global__ void __launch_bounds__(kThreads) sparse_decode_kernel(Params p) {
     }
     if (P > 1) cl.sync(); else __syncthreads();   // every CTA runs and has its words set
     const int k = take - (have - (f1 - f0));   // to be taken by their scores
-    const ScoreSink sink{score, in_smem, P, f0, k > 0 ? f1 : f0};
-    float t;
+    ScoreSink sink{score, in_smem, P, f0, k > 0 ? f1 : f0};
     if constexpr (C::kBf16)
-      t = score_tiles<D, GM / 8>(p, n, g, rank * kWarps + wid, P * kWarps, sink);
+      score_tiles<D, GM / 8>(p, n, g, rank * kWarps + wid, P * kWarps, sink);
     else
-      t = score_blocks_f32<D>(p, n, g, rank * kWarps + wid, P * kWarps, sink);
-    const uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(t) & 0x7fffffffu);
-    if ((tid & 31) == 0)
-      for (int r = 0; r < P; ++r) atomicMax(P > 1 ? cl.map_shared_rank(&sh.tmax, r) : &sh.tmax, tb);
+      score_blocks_f32<D>(p, n, g, rank * kWarps + wid, P * kWarps, sink);
+    const uint32_t lo = __reduce_min_sync(0xffffffffu, sink.lo);
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, sink.hi);
+    const uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(sink.tmax) & 0x7fffffffu);
+    for (int r = tid & 31; r < P; r += 32) {   // a lane tells one CTA
+      SelectShared* to = P > 1 ? cl.map_shared_rank(&sh, r) : &sh;
+      atomicMin(&to->lo, lo);
+      atomicMax(&to->hi, hi);
+      atomicMax(&to->tmax, tb);
+    }
     if (P > 1) cl.sync(); else __syncthreads();
-    select_blocks<T>(p, sh, n, g, have, f0, f1, k, score, r64, sh.tmax, list);
+    select_blocks<T, D>(p, sh, (int*)(smem + C::HIST), n, g, have, f0, f1, k, score, r64, in_smem,
+                        list);
   } else {
     for (int i = tid; i < take; i += kThreads) list[i] = i;
     __syncthreads();
