@@ -84,12 +84,12 @@ struct Cfg {
 
 // ---------------------------------------------------------------- scores
 // Scores are computed in fp32 next to t = sum_d of the magnitudes of their terms. A score's fp32
-// error is at most kScoreError * t: bf16 products are exact, a matrix instruction adds 16 of them
-// and its accumulator with at most 2^-23 of the largest lost per addend, and each of four chains
-// has at most 4 instructions (d = 128: 16 for the 2 d products), so 4 * 17 * 2^-23 = 2^-16.9 with
-// the joining sums; the fp32 path's chains are shorter. Selection recomputes in 64 bits wherever
-// twice that bound reaches across the border, so the result is that of 64-bit scores.
-constexpr float kScoreError = 1.0f / 65536;
+// error is at most kScoreError * t: bf16 products are exact, a matrix instruction that begins at
+// zero adds 16 of them with at most 2^-23 of the largest lost per addend, 16 * 2^-23 of its share
+// of t, and the 16 results (d = 128: 2 d products) are added in fp32, 16 * 2^-24 of t: 2^-18.4 in
+// all. The fp32 path's chains are shorter. Selection looks closer wherever twice that bound reaches
+// across the border, in the end in 64 bits, so the result is that of 64-bit scores.
+constexpr float kScoreError = 0x1p-18f;
 
 // Larger score <=> larger integer.
 __device__ __forceinline__ uint32_t order32(float s) {
@@ -159,7 +159,7 @@ __device__ __forceinline__ void score_tiles(const Params& p, int64_t n, int g, i
     float best0 = -INFINITY, best1 = -INFINITY;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float c[4][4] = {}, m[4] = {};
+      float c[4] = {}, m[4] = {};
       constexpr uint32_t kAbs = 0x7fff7fffu;
 #pragma unroll
       for (int j = 0; j < 2 * J; ++j) {
@@ -171,8 +171,11 @@ __device__ __forceinline__ void score_tiles(const Params& p, int64_t n, int g, i
         else
           w = make_uint4(max_nan_bf16x2(qq.x, 0), max_nan_bf16x2(qq.y, 0), max_nan_bf16x2(qq.z, 0),
                          max_nan_bf16x2(qq.w, 0));
-        mma_bf16(c[j % 4], x[j].x, y[j].x, x[j].y, y[j].y, w.x, w.y);
-        mma_bf16(c[j % 4], x[j].z, y[j].z, x[j].w, y[j].w, w.z, w.w);
+        float z0[4] = {}, z1[4] = {};
+        mma_bf16(z0, x[j].x, y[j].x, x[j].y, y[j].y, w.x, w.y);
+        mma_bf16(z1, x[j].z, y[j].z, x[j].w, y[j].w, w.z, w.w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] += z0[e] + z1[e];
         mma_bf16(m, x[j].x & kAbs, y[j].x & kAbs, x[j].y & kAbs, y[j].y & kAbs, w.x & kAbs,
                  w.y & kAbs);
         mma_bf16(m, x[j].z & kAbs, y[j].z & kAbs, x[j].w & kAbs, y[j].w & kAbs, w.z & kAbs,
@@ -181,8 +184,8 @@ __device__ __forceinline__ void score_tiles(const Params& p, int64_t n, int g, i
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (t * 8 + 2 * tig + e < p.G) {
-          best0 = max_nan(best0, (c[0][e] + c[1][e]) + (c[2][e] + c[3][e]));
-          best1 = max_nan(best1, (c[0][2 + e] + c[1][2 + e]) + (c[2][2 + e] + c[3][2 + e]));
+          best0 = max_nan(best0, c[e]);
+          best1 = max_nan(best1, c[2 + e]);
           out.tmax = max_nan(out.tmax, max_nan(m[e], m[2 + e]));   // rows past f1 are zeros
         }
       }
@@ -389,22 +392,81 @@ __device__ __noinline__ unsigned long long exact_rank(const Params& p, int64_t n
   return rank;
 }
 
-// Writes the blocks for which kind(b) is 2, and the first `ties` for which it is 1, in ascending
-// order. Each warp counts in its quarter of the blocks, then writes from where the earlier ones end.
-template <typename Kind>
-__device__ __forceinline__ void compact(SelectShared& sh, int have, int ties, int* list, Kind kind) {
+// The score of block b in twice the precision of fp32, one warp: every product and every sum is
+// kept with its rounding error (the error-free transformations of Dekker and Knuth, accumulated as
+// in Ogita, Rump and Oishi, "Accurate sum and dot product", 2005). The errors' own sum is fp32: at
+// most 512 addends, each at most 2^-24 of the partial sums of a tree of depth 13, so what is lost is
+// below 512 * 13 * 2^-48 * t < 2^-35 * t. Far cheaper than doubles, of which an SM adds two a clock.
+constexpr double kFineError = 0x1p-34;
+__device__ __forceinline__ void two_sum(float& s, float& err, float b) {
+  const float a = s;
+  s = __fadd_rn(a, b);
+  const float bb = __fsub_rn(s, a);
+  err = __fadd_rn(err, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb)));
+}
+template <typename T, int D>
+__device__ __forceinline__ double fine_score(const Params& p, int64_t n, int g, int b) {
+  constexpr int E = D / 32, H = 4;
+  const rc_sparse_decode_args& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const T* box = (const T*)a.bounds +
+                 ((((int64_t)a.req_idx[n] * a.max_blocks + b) * a.num_kv_heads + g) * 2) * D + lane;
+  const T* q = (const T*)a.q + (n * a.num_q_heads + (int64_t)g * p.G) * D + lane;
+  float lo[E], hi[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    lo[e] = Elem<T>::to_f(box[e * 32]);
+    hi[e] = Elem<T>::to_f(box[D + e * 32]);
+  }
+  double best = -INFINITY;
+  for (int h0 = 0; h0 < p.G; h0 += H) {
+    float s[H], c[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      s[h] = c[h] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float x = h0 + h < p.G ? Elem<T>::to_f(q[(h0 + h) * D + e * 32]) : 0.f;
+        const float y = x >= 0.f ? hi[e] : lo[e];
+        const float xy = __fmul_rn(x, y);
+        two_sum(s[h], c[h], xy);
+        if constexpr (sizeof(T) == 4) c[h] = __fadd_rn(c[h], __fmaf_rn(x, y, -xy));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const float s2 = __shfl_xor_sync(0xffffffffu, s[h], o);
+        c[h] = __fadd_rn(c[h], __shfl_xor_sync(0xffffffffu, c[h], o));
+        two_sum(s[h], c[h], s2);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (h0 + h < p.G) best = fmax(best, (double)s[h] + (double)c[h]);
+  }
+  return best;
+}
+
+// Writes first + i for every i < m for which kind(i) is 2, and for the first `ties` for which it is
+// 1, in ascending order. Each warp counts in its quarter of them, then writes from where the
+// earlier ones end.
+template <bool kTies, typename Kind>
+__device__ __forceinline__ void compact(SelectShared& sh, int m, int first, int ties, int* list,
+                                        Kind kind) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int quarter = (have + kThreads - 1) / kThreads * 32;
-  const int b0 = wid * quarter, b1 = min(have, b0 + quarter);
+  const int quarter = (m + kThreads - 1) / kThreads * 32;
+  const int i0 = wid * quarter, i1 = min(m, i0 + quarter);
   int np = 0, ne = 0;
 #pragma unroll 4
-  for (int b = b0 + lane; b < b1; b += 32) {
-    const int c = kind(b);
+  for (int i = i0 + lane; i < i1; i += 32) {
+    const int c = kind(i);
     np += c == 2;
-    ne += c == 1;
+    if (kTies) ne += c == 1;
   }
   np = __reduce_add_sync(0xffffffffu, np);
-  ne = __reduce_add_sync(0xffffffffu, ne);
+  if (kTies) ne = __reduce_add_sync(0xffffffffu, ne);
   __syncthreads();
   if (lane == 0) {
     sh.wsum[0][wid] = np;
@@ -416,86 +478,94 @@ __device__ __forceinline__ void compact(SelectShared& sh, int have, int ties, in
     at += sh.wsum[0][w];
     eq += sh.wsum[1][w];
   }
-  at += min(eq, ties);
+  if (kTies) at += min(eq, ties);
   const unsigned below = (1u << lane) - 1;
 #pragma unroll 4
-  for (int b = b0; b < b1; b += 32) {
-    const int c = b + lane < b1 ? kind(b + lane) : 0;
-    const unsigned me = __ballot_sync(0xffffffffu, c == 1);
-    const bool pick = c == 2 || (c == 1 && eq + __popc(me & below) < ties);
+  for (int i = i0; i < i1; i += 32) {
+    const int c = i + lane < i1 ? kind(i + lane) : 0;
+    bool pick = c == 2;
+    if (kTies) {
+      const unsigned me = __ballot_sync(0xffffffffu, c == 1);
+      pick = pick || (c == 1 && eq + __popc(me & below) < ties);
+      eq += __popc(me);
+    }
     const unsigned mp = __ballot_sync(0xffffffffu, pick);
-    if (pick) list[at + __popc(mp & below)] = b + lane;
+    if (pick) list[at + __popc(mp & below)] = first + i + lane;
     at += __popc(mp);
-    eq += __popc(me);
   }
   __syncthreads();
 }
 
-// The chosen blocks of a unit in ascending order into `list` (shared memory), by the whole CTA:
-// the forced blocks outside [f0, f1) and the k best of those inside, by score[b - f0] where the
-// fp32 scores can tell, by 64-bit ranks in r64 where they cannot. `own`: the scores are this CTA's
-// own copy.
-template <typename T, int D>
+// The k best of a unit's scored blocks [f0, f0 + m) in ascending order into `list` (shared memory),
+// by the whole CTA, 1 <= k < m: by score[b - f0] where the fp32 scores can tell, then by finer ones
+// where a few blocks are near the border, then by 64-bit ranks in r64. kOwn: the scores are this
+// CTA's own copy in shared memory (else in the workspace, the cluster's).
+template <typename T, int D, bool kOwn>
 __device__ __forceinline__ void select_blocks(const Params& p, SelectShared& sh, int* hist, int64_t n,
-                                              int g, int have, int f0, int f1, int k, float* score,
-                                              unsigned long long* r64, bool own, int* list) {
+                                              int g, int f0, int m, int k, float* score,
+                                              unsigned long long* r64, int* list) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int m = f1 - f0;
-  if (k <= 0) {
-    compact(sh, have, 0, list, [&](int b) { return b < f0 || b >= f1 ? 2 : 0; });
-    return;
-  }
-  const bool all64 = sh.tmax >= 0x7f800000u;   // a score may be infinite or no number
+  const bool all64 = sh.tmax >= 0x7e800000u;   // 2^126: sums may overflow, or be no numbers
+  const float tmax = __uint_as_float(sh.tmax);
   float hi_s = 0.f, lo_s = 0.f;
-  int in = 0, need64 = m;   // taken whatever the 64-bit ranks say; those that they decide about
+  int in = 0, close = m;   // taken whatever finer scores say; those that they decide about
   if (!all64) {
     const uint32_t thr = kth_largest<uint32_t>(
         sh, hist, m, m, k, sh.lo, sh.hi, [&](int i) { return order32(score[i]); },
         [](int) { return true; });
     const float ts = __uint_as_float(thr & (1u << 31) ? thr & ~(1u << 31) : ~thr);
     // (1 % for the roundings of these lines; products below the smallest normal number may be lost)
-    const float e2 = 2.02f * kScoreError * __uint_as_float(sh.tmax) + 0x1p-110f;
+    const float e2 = 2.02f * kScoreError * tmax + 0x1p-110f;
     hi_s = ts + e2;
     lo_s = ts - e2;
-    need64 = 0;
+    close = 0;
 #pragma unroll 4
     for (int i = tid; i < m; i += kThreads) {
       const float s = score[i];
       in += s > hi_s;
-      need64 += s >= lo_s && s <= hi_s;
+      close += s >= lo_s && s <= hi_s;
     }
-    block_sum2(sh, in, need64);
+    block_sum2(sh, in, close);
   }
-  const int rest = k - in;   // to be taken of the need64 near the border
+  const int rest = k - in;   // to be taken of the `close`
   auto near = [&](int i) { return all64 || (score[i] >= lo_s && score[i] <= hi_s); };
-  if (need64 > rest && need64 <= kThreads && own && !all64) {
-    // few blocks: rank them against one another (of equal ones the lower number is first), and
-    // let their scores say whether they are taken
+  bool clear = close == rest;
+  if (kOwn && !clear && close <= kThreads && !all64) {
     if (tid == 0) sh.listed = 0;
     __syncthreads();
 #pragma unroll 4
     for (int i = tid; i < m; i += kThreads)
       if (near(i)) sh.index[atomicAdd(&sh.listed, 1)] = i;
     __syncthreads();
-    for (int c = wid; c < need64; c += kWarps) {
-      const unsigned long long r = exact_rank<T, D>(p, n, g, f0 + sh.index[c]);
-      if (lane == 0) sh.list[c] = r;
+    for (int c = wid; c < close; c += kWarps) {
+      const double f = fine_score<T, D>(p, n, g, f0 + sh.index[c]);
+      if (lane == 0) sh.list[c] = (unsigned long long)__double_as_longlong(f);
     }
     __syncthreads();
-    if (tid < need64) {
-      const unsigned long long r = sh.list[tid];
-      const int i = sh.index[tid];
-      int before = 0;
-      for (int c = 0; c < need64; ++c)
-        before += sh.list[c] > r || (sh.list[c] == r && sh.index[c] < i);
-      score[i] = before < rest ? INFINITY : -INFINITY;
+    const double f = tid < close ? __longlong_as_double((long long)sh.list[tid]) : 0.0;
+    if (tid < close) {
+      int above = 0, equal = 0;
+      for (int c = 0; c < close; ++c) {
+        const double x = __longlong_as_double((long long)sh.list[c]);
+        above += x > f;
+        equal += x == f;
+      }
+      if (above < rest && above + equal >= rest) sh.kth = (unsigned long long)__double_as_longlong(f);
     }
     __syncthreads();
-    need64 = rest;
+    const double t = __longlong_as_double((long long)sh.kth);
+    const double w = 2.0 * kFineError * tmax + 0x1p-120;
+    int take = tid < close && f >= t - w, unused = 0;
+    const bool mine = take;
+    block_sum2(sh, take, unused);
+    if (take == rest) {   // no block left out is as near as the error bound
+      if (tid < close) score[sh.index[tid]] = mine ? INFINITY : -INFINITY;
+      __syncthreads();
+      clear = true;
+    }
   }
-  if (need64 == rest) {   // the border is clear
-    compact(sh, have, 0, list,
-            [&](int b) { return b < f0 || b >= f1 || score[b - f0] >= lo_s ? 2 : 0; });
+  if (clear) {
+    compact<false>(sh, m, f0, 0, list, [&](int i) { return score[i] >= lo_s ? 2 : 0; });
     return;
   }
   for (int i0 = wid * 32; i0 < m; i0 += kThreads) {
@@ -510,13 +580,11 @@ __device__ __forceinline__ void select_blocks(const Params& p, SelectShared& sh,
   }
   __syncthreads();
   const unsigned long long thr64 = kth_largest<unsigned long long>(
-      sh, hist, m, need64, rest, 0ull, ~0ull, [&](int i) { return r64[i]; }, near);
+      sh, hist, m, close, rest, 0ull, ~0ull, [&](int i) { return r64[i]; }, near);
   int c = 0, unused = 0;
   for (int i = tid; i < m; i += kThreads) c += near(i) && r64[i] > thr64;
   block_sum2(sh, c, unused);
-  compact(sh, have, rest - c, list, [&](int b) {
-    if (b < f0 || b >= f1) return 2;
-    const int i = b - f0;
+  compact<true>(sh, m, f0, rest - c, list, [&](int i) {
     if (!near(i)) return score[i] > hi_s ? 2 : 0;
     return r64[i] > thr64 ? 2 : r64[i] == thr64 ? 1 : 0;
   });
@@ -806,32 +874,42 @@ __global__ void __launch_bounds__(kThreads) sparse_decode_kernel(Params p) {
   const bool choose = take < have;   // else every block is taken and none is scored
   if (choose) {
     const int f0 = min(a.sink_blocks, have), f1 = max(f0, have - a.recent_blocks);
-    const bool in_smem = p.nb <= C::BLOCKS;
-    unsigned long long* r64 = in_smem ? (unsigned long long*)smem : p.w.rank + unit * p.nb;
-    float* score = in_smem ? (float*)(r64 + C::BLOCKS) : p.w.score + unit * p.nb;
-    if (tid == 0) {
-      sh.lo = 0xffffffffu;
-      sh.hi = sh.tmax = 0;
+    const int m = f1 - f0, k = take - (have - m);   // k of m blocks are taken by their scores
+    for (int i = tid; i < f0; i += kThreads) list[i] = i;
+    for (int i = tid; i < have - f1; i += kThreads) list[f0 + k + i] = f1 + i;
+    if (k > 0) {
+      const bool own = p.nb <= C::BLOCKS;
+      unsigned long long* r64_s = (unsigned long long*)smem;
+      float* score_s = (float*)(r64_s + C::BLOCKS);
+      if (tid == 0) {
+        sh.lo = 0xffffffffu;
+        sh.hi = sh.tmax = 0;
+      }
+      if (P > 1) cl.sync(); else __syncthreads();   // every CTA runs and has its words set
+      ScoreSink sink{own ? score_s : p.w.score + unit * p.nb, own, P, f0, f1};
+      if constexpr (C::kBf16)
+        score_tiles<D, GM / 8>(p, n, g, rank * kWarps + wid, P * kWarps, sink);
+      else
+        score_blocks_f32<D>(p, n, g, rank * kWarps + wid, P * kWarps, sink);
+      const uint32_t lo = __reduce_min_sync(0xffffffffu, sink.lo);
+      const uint32_t hi = __reduce_max_sync(0xffffffffu, sink.hi);
+      const uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(sink.tmax) & 0x7fffffffu);
+      for (int r = tid & 31; r < P; r += 32) {   // a lane tells one CTA
+        SelectShared* to = P > 1 ? cl.map_shared_rank(&sh, r) : &sh;
+        atomicMin(&to->lo, lo);
+        atomicMax(&to->hi, hi);
+        atomicMax(&to->tmax, tb);
+      }
+      if (P > 1) cl.sync(); else __syncthreads();
+      int* hist = (int*)(smem + C::HIST);
+      if (own)
+        select_blocks<T, D, true>(p, sh, hist, n, g, f0, m, k, score_s, r64_s, list + f0);
+      else
+        select_blocks<T, D, false>(p, sh, hist, n, g, f0, m, k, p.w.score + unit * p.nb,
+                                   p.w.rank + unit * p.nb, list + f0);
+    } else {
+      __syncthreads();
     }
-    if (P > 1) cl.sync(); else __syncthreads();   // every CTA runs and has its words set
-    const int k = take - (have - (f1 - f0));   // to be taken by their scores
-    ScoreSink sink{score, in_smem, P, f0, k > 0 ? f1 : f0};
-    if constexpr (C::kBf16)
-      score_tiles<D, GM / 8>(p, n, g, rank * kWarps + wid, P * kWarps, sink);
-    else
-      score_blocks_f32<D>(p, n, g, rank * kWarps + wid, P * kWarps, sink);
-    const uint32_t lo = __reduce_min_sync(0xffffffffu, sink.lo);
-    const uint32_t hi = __reduce_max_sync(0xffffffffu, sink.hi);
-    const uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(sink.tmax) & 0x7fffffffu);
-    for (int r = tid & 31; r < P; r += 32) {   // a lane tells one CTA
-      SelectShared* to = P > 1 ? cl.map_shared_rank(&sh, r) : &sh;
-      atomicMin(&to->lo, lo);
-      atomicMax(&to->hi, hi);
-      atomicMax(&to->tmax, tb);
-    }
-    if (P > 1) cl.sync(); else __syncthreads();
-    select_blocks<T, D>(p, sh, (int*)(smem + C::HIST), n, g, have, f0, f1, k, score, r64, in_smem,
-                        list);
   } else {
     for (int i = tid; i < take; i += kThreads) list[i] = i;
     __syncthreads();

@@ -229,10 +229,12 @@ def test_equal_scores_take_the_lowest_blocks(dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_scores_a_hair_apart_are_told_apart(dtype):
-    """Blocks whose scores differ by less than an fp32 sum can resolve: one large term and its
-    negative cancel, a tiny one decides; in fp32 the order of the sum would choose."""
-    d, block, nb = 128, 16, 24
+@pytest.mark.parametrize("step,nb", [(2.0 ** -20, 24), (2.0 ** -40, 24), (2.0 ** -40, 250)])
+def test_scores_a_hair_apart_are_told_apart(dtype, step, nb):
+    """Blocks whose scores differ by less than an fp32 sum can resolve (one large term and its
+    negative cancel, a tiny one decides; in fp32 the order of the sum would choose), or a sum of
+    twice that precision, few of them and many."""
+    d, block = 128, 16
     c = Case(dtype, [nb * block], [(0, nb * block)], 2, 1, d, block)
     r = int(c.req[0])
     c.q[:] = 0.0
@@ -242,7 +244,7 @@ def test_scores_a_hair_apart_are_told_apart(dtype):
     box = torch.zeros((nb, 1, 2, d))
     box[:, 0, :, 0], box[:, 0, :, 60] = 1024.0, -1024.0
     tiny = torch.randperm(nb, generator=torch.Generator().manual_seed(4)).float()
-    box[:, 0, :, 127] = (1 + tiny)[:, None] * 2.0 ** -20      # 1024 holds 2^-13 at most in fp32
+    box[:, 0, :, 127] = (1 + tiny)[:, None] * step      # 1024 holds 2^-13 at most in fp32
     c.bounds[r, :nb] = box.to(c.dt)
     c.call(9, sink=0).check()
     top = sorted(sorted(range(nb - 1), key=lambda b: -float(tiny[b]))[:8]) + [nb - 1]
