@@ -496,36 +496,49 @@ def decode_attention_noalloc(q, k_new, v_new, out_loc, seq_len, req_idx, req_to_
 
 
 # ------------------------------------------------------------------ norms, rotation, append, sparse
-def _on_device(fn, dev, **tensors):
-    """Every given tensor is on the current device: the call launches on a stream of it."""
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{fn}: {name} must be a CUDA tensor on the current device (cuda:{dev})")
+def _raw_stream(dev, stream):
+    """The stream to launch on, as an integer: the given one, or device dev's current one."""
+    return (_torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
-def _typed(fn, dtype, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != dtype:
+def _require(fn, dev, tensors):
+    """Each (name, tensor, dtype, shape) is a contiguous CUDA tensor on the current device (the call
+    launches on a stream of it), of that dtype and shape."""
+    for name, t, dtype, shape in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} must be a CUDA tensor on the current device "
+                             f"(cuda:{dev})")
+        if t.dtype is not dtype:
             raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous")
 
 
-def _shaped(fn, name, t, *shape):
-    """Contiguous, and of this shape (None: any size)."""
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected "
-                         f"{tuple('*' if w is None else w for w in shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be contiguous")
+def _dims(fn, name, t, n):
+    """The shape of an n-dimensional tensor."""
+    if t.dim() != n:
+        raise ValueError(f"{fn}: {name} must have {n} dimensions, not {t.dim()}")
+    return t.shape
 
 
-def _head_strides(fn, name, t, out=False):
+def _heads(fn, dev, name, t, dtype, shape, out=False):
     """(token stride, head stride) in elements of a [T, H, d] tensor whose heads are contiguous."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{fn}: {name} must be [tokens, heads, d] with contiguous heads")
-    st = [t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1)]
-    if out and any(st[i] == 0 and t.shape[i] > 1 for i in (0, 1)):
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor on the current device (cuda:{dev})")
+    if t.dtype is not dtype:
+        raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st, sh, se = t.stride()
+    if se != 1 and shape[2] > 1:
+        raise ValueError(f"{fn}: the heads of {name} must be contiguous")
+    # the stride of a dimension of size 1 says nothing
+    st, sh = st if shape[0] > 1 else 0, sh if shape[1] > 1 else 0
+    if out and ((st == 0 and shape[0] > 1) or (sh == 0 and shape[1] > 1)):
         raise ValueError(f"{fn}: {name} is expanded: its rows share memory")
-    return st
+    return st, sh
 
 
 def rope_table(inv_freq, num_positions: int, *, first_position: int = 0,
@@ -550,6 +563,8 @@ def qk_norm_rope(q, k, positions=None, rope=None, *, q_weight=None, k_weight=Non
     [T]; rope: fp32 [max_position, rotary_dim] (rope_table) or None for norms only; q_weight /
     k_weight: [d] or None for no norm. q_out / k_out: where the results go, in place when None."""
     fn = "qk_norm_rope"
+    torch = _torch()
+    dev = torch.cuda.current_device()
     x = q if q is not None else k
     if x is None:
         raise ValueError(f"{fn}: neither q nor k is given")
@@ -558,44 +573,45 @@ def qk_norm_rope(q, k, positions=None, rope=None, *, q_weight=None, k_weight=Non
         raise ValueError(f"{fn}: a weight or an output without its input")
     if rope is None and q_weight is None and k_weight is None:
         raise ValueError(f"{fn}: neither a rotation nor a norm is given")
-    dev = _torch().cuda.current_device()
-    _on_device(fn, dev, q=q, k=k, positions=positions, rope=rope, q_weight=q_weight,
-               k_weight=k_weight, q_out=q_out, k_out=k_out)
-    code = _dtype_code(x)
-    _typed(fn, x.dtype, q=q, k=k, q_weight=q_weight, k_weight=k_weight, q_out=q_out, k_out=k_out)
-    T, d = x.shape[0], x.shape[-1]
-    a = RcQkNormRopeArgs(dtype=code, head_dim=d, interleaved=1 if interleaved else 0, eps=eps,
-                         num_tokens=T)
+    T, _, d = _dims(fn, "q" if q is not None else "k", x, 3)
+    dt = x.dtype
+    a = RcQkNormRopeArgs(_dtype_code(x), 0, 0, d, 0, 1 if interleaved else 0, eps, T)
     if rope is not None:
         if positions is None:
             raise ValueError(f"{fn}: the rotation needs positions")
-        _typed(fn, _torch().float32, rope=rope)
-        _typed(fn, _torch().int32, positions=positions)
-        _shaped(fn, "rope", rope, None, None)
-        _shaped(fn, "positions", positions, T)
-        a.max_position, a.rotary_dim = rope.shape
+        a.max_position, a.rotary_dim = _dims(fn, "rope", rope, 2)
+        _require(fn, dev, (("rope", rope, torch.float32, rope.shape),
+                           ("positions", positions, torch.int32, (T,))))
         a.rope, a.positions = rope.data_ptr(), positions.data_ptr()
     if q is not None:
-        q_out = q if q_out is None else q_out
-        a.q_token_stride, a.q_head_stride = _head_strides(fn, "q", q)
-        a.q_out_token_stride, a.q_out_head_stride = _head_strides(fn, "q_out", q_out, True)
-        if q_out.shape != q.shape:
-            raise ValueError(f"{fn}: q_out must have q's shape")
-        a.num_q_heads, a.q, a.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        shape = (T, q.shape[1], d)
+        a.num_q_heads, a.q = shape[1], q.data_ptr()
+        a.q_token_stride, a.q_head_stride = _heads(fn, dev, "q", q, dt, shape, q_out is None)
+        if q_out is None:
+            a.q_out, a.q_out_token_stride, a.q_out_head_stride = a.q, a.q_token_stride, \
+                a.q_head_stride
+        else:
+            a.q_out = q_out.data_ptr()
+            a.q_out_token_stride, a.q_out_head_stride = _heads(fn, dev, "q_out", q_out, dt, shape,
+                                                               True)
         if q_weight is not None:
-            _shaped(fn, "q_weight", q_weight, d)
+            _require(fn, dev, (("q_weight", q_weight, dt, (d,)),))
             a.q_weight = q_weight.data_ptr()
     if k is not None:
-        k_out = k if k_out is None else k_out
-        a.k_token_stride, a.k_head_stride = _head_strides(fn, "k", k)
-        a.k_out_token_stride, a.k_out_head_stride = _head_strides(fn, "k_out", k_out, True)
-        if k_out.shape != k.shape or k.shape[0] != T or k.shape[2] != d:
-            raise ValueError(f"{fn}: q, k and k_out do not agree in shape")
-        a.num_kv_heads, a.k, a.k_out = k.shape[1], k.data_ptr(), k_out.data_ptr()
+        shape = (T, _dims(fn, "k", k, 3)[1], d)
+        a.num_kv_heads, a.k = shape[1], k.data_ptr()
+        a.k_token_stride, a.k_head_stride = _heads(fn, dev, "k", k, dt, shape, k_out is None)
+        if k_out is None:
+            a.k_out, a.k_out_token_stride, a.k_out_head_stride = a.k, a.k_token_stride, \
+                a.k_head_stride
+        else:
+            a.k_out = k_out.data_ptr()
+            a.k_out_token_stride, a.k_out_head_stride = _heads(fn, dev, "k_out", k_out, dt, shape,
+                                                               True)
         if k_weight is not None:
-            _shaped(fn, "k_weight", k_weight, d)
+            _require(fn, dev, (("k_weight", k_weight, dt, (d,)),))
             a.k_weight = k_weight.data_ptr()
-    check(lib().rc_qk_norm_rope(ctypes.byref(a), _stream(stream)), "rc_qk_norm_rope")
+    check(lib().rc_qk_norm_rope(ctypes.byref(a), _raw_stream(dev, stream)), "rc_qk_norm_rope")
 
 
 def kv_append(k, v, out_loc, qo_indptr, prefix_len, k_pool, v_pool, *, rope=None, k_weight=None,
@@ -608,47 +624,34 @@ def kv_append(k, v, out_loc, qo_indptr, prefix_len, k_pool, v_pool, *, rope=None
     fn = "kv_append"
     torch = _torch()
     dev = torch.cuda.current_device()
-    _on_device(fn, dev, k=k, v=v, out_loc=out_loc, qo_indptr=qo_indptr, prefix_len=prefix_len,
-               k_pool=k_pool, v_pool=v_pool, rope=rope, k_weight=k_weight, bounds=bounds,
-               req_idx=req_idx)
-    code = _dtype_code(k_pool)
-    _typed(fn, k_pool.dtype, k=k, v=v, v_pool=v_pool, k_weight=k_weight, bounds=bounds)
-    _typed(fn, torch.int32, out_loc=out_loc, qo_indptr=qo_indptr, prefix_len=prefix_len,
-           req_idx=req_idx)
-    _shaped(fn, "k_pool", k_pool, None, None, None)
-    S, Hkv, d = k_pool.shape
-    _shaped(fn, "v_pool", v_pool, S, Hkv, d)
-    kt, kh = _head_strides(fn, "k", k)
-    vt, vh = _head_strides(fn, "v", v)
-    T, B = k.shape[0], prefix_len.numel()
-    if tuple(k.shape) != (T, Hkv, d) or tuple(v.shape) != (T, Hkv, d):
-        raise ValueError(f"{fn}: k and v must be [T, {Hkv}, {d}]")
-    _shaped(fn, "out_loc", out_loc, T)
-    _shaped(fn, "prefix_len", prefix_len, B)
-    _shaped(fn, "qo_indptr", qo_indptr, B + 1)
-    a = RcKvAppendArgs(dtype=code, num_reqs=B, num_kv_heads=Hkv, head_dim=d,
-                       interleaved=1 if interleaved else 0, eps=eps, block=block, num_tokens=T,
-                       num_slots=S, k=k.data_ptr(), k_token_stride=kt, k_head_stride=kh,
-                       v=v.data_ptr(), v_token_stride=vt, v_head_stride=vh,
-                       out_loc=out_loc.data_ptr(), qo_indptr=qo_indptr.data_ptr(),
-                       prefix_len=prefix_len.data_ptr(), k_pool=k_pool.data_ptr(),
-                       v_pool=v_pool.data_ptr())
+    dt, i32 = k_pool.dtype, torch.int32
+    S, Hkv, d = _dims(fn, "k_pool", k_pool, 3)
+    T, B = _dims(fn, "k", k, 3)[0], prefix_len.numel()
+    kt, kh = _heads(fn, dev, "k", k, dt, (T, Hkv, d))
+    vt, vh = _heads(fn, dev, "v", v, dt, (T, Hkv, d))
+    _require(fn, dev, (("k_pool", k_pool, dt, (S, Hkv, d)), ("v_pool", v_pool, dt, (S, Hkv, d)),
+                       ("out_loc", out_loc, i32, (T,)), ("qo_indptr", qo_indptr, i32, (B + 1,)),
+                       ("prefix_len", prefix_len, i32, (B,))))
+    a = RcKvAppendArgs(_dtype_code(k_pool), B, Hkv, d, 0, 1 if interleaved else 0, eps, block, T, S,
+                       0, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, out_loc.data_ptr(),
+                       qo_indptr.data_ptr(), prefix_len.data_ptr(), 0, 0, k_pool.data_ptr(),
+                       v_pool.data_ptr())
     if rope is not None:
-        _typed(fn, torch.float32, rope=rope)
-        _shaped(fn, "rope", rope, None, None)
-        a.max_position, a.rotary_dim = rope.shape
+        a.max_position, a.rotary_dim = _dims(fn, "rope", rope, 2)
+        _require(fn, dev, (("rope", rope, torch.float32, rope.shape),))
         a.rope = rope.data_ptr()
     if k_weight is not None:
-        _shaped(fn, "k_weight", k_weight, d)
+        _require(fn, dev, (("k_weight", k_weight, dt, (d,)),))
         a.k_weight = k_weight.data_ptr()
     if bounds is not None:
         if req_idx is None:
             raise ValueError(f"{fn}: bounds need req_idx")
-        _shaped(fn, "bounds", bounds, None, None, Hkv, 2, d)
-        _shaped(fn, "req_idx", req_idx, B)
-        a.max_reqs, a.max_blocks = bounds.shape[:2]
+        R, nb = _dims(fn, "bounds", bounds, 5)[:2]
+        _require(fn, dev, (("bounds", bounds, dt, (R, nb, Hkv, 2, d)),
+                           ("req_idx", req_idx, i32, (B,))))
+        a.max_reqs, a.max_blocks = R, nb
         a.bounds, a.req_idx = bounds.data_ptr(), req_idx.data_ptr()
-    check(lib().rc_kv_append(ctypes.byref(a), _stream(stream)), "rc_kv_append")
+    check(lib().rc_kv_append(ctypes.byref(a), _raw_stream(dev, stream)), "rc_kv_append")
 
 
 def kv_block_bounds(k_pool, req_to_token, req_idx, seq_len, bounds, *, block=64, stream=None):
@@ -658,28 +661,21 @@ def kv_block_bounds(k_pool, req_to_token, req_idx, seq_len, bounds, *, block=64,
     fn = "kv_block_bounds"
     torch = _torch()
     dev = torch.cuda.current_device()
-    _on_device(fn, dev, k_pool=k_pool, req_to_token=req_to_token, req_idx=req_idx,
-               seq_len=seq_len, bounds=bounds)
-    code = _dtype_code(k_pool)
-    _typed(fn, k_pool.dtype, bounds=bounds)
-    _typed(fn, torch.int32, req_to_token=req_to_token, req_idx=req_idx, seq_len=seq_len)
     if k_pool.dim() not in (3, 4) or bounds.dim() != k_pool.dim() + 2:
         raise ValueError(f"{fn}: k_pool and bounds must both have a layers dimension or neither")
-    lead = k_pool.shape[:-3]
-    S, Hkv, d = k_pool.shape[-3:]
-    _shaped(fn, "req_to_token", req_to_token, None, None)
-    R, C = req_to_token.shape
-    _shaped(fn, "k_pool", k_pool, *lead, S, Hkv, d)
-    _shaped(fn, "bounds", bounds, *lead, R, None, Hkv, 2, d)
-    _shaped(fn, "seq_len", seq_len, None)
-    _shaped(fn, "req_idx", req_idx, seq_len.numel())
-    a = RcKvBlockBoundsArgs(dtype=code, num_layers=lead[0] if lead else 1,
-                            num_rows=seq_len.numel(), num_kv_heads=Hkv, head_dim=d, max_reqs=R,
-                            max_ctx=C, block=block, max_blocks=bounds.shape[-4], num_slots=S,
-                            seq_len=seq_len.data_ptr(), req_idx=req_idx.data_ptr(),
-                            req_to_token=req_to_token.data_ptr(), k_pool=k_pool.data_ptr(),
-                            bounds=bounds.data_ptr())
-    check(lib().rc_kv_block_bounds(ctypes.byref(a), _stream(stream)), "rc_kv_block_bounds")
+    dt, i32 = k_pool.dtype, torch.int32
+    *lead, S, Hkv, d = k_pool.shape
+    R, C = _dims(fn, "req_to_token", req_to_token, 2)
+    N, nb = seq_len.numel(), bounds.shape[-4]
+    _require(fn, dev, (("k_pool", k_pool, dt, k_pool.shape),
+                       ("bounds", bounds, dt, (*lead, R, nb, Hkv, 2, d)),
+                       ("req_to_token", req_to_token, i32, (R, C)), ("seq_len", seq_len, i32, (N,)),
+                       ("req_idx", req_idx, i32, (N,))))
+    a = RcKvBlockBoundsArgs(_dtype_code(k_pool), lead[0] if lead else 1, N, Hkv, d, R, C, block, nb,
+                            S, seq_len.data_ptr(), req_idx.data_ptr(), req_to_token.data_ptr(),
+                            k_pool.data_ptr(), bounds.data_ptr())
+    check(lib().rc_kv_block_bounds(ctypes.byref(a), _raw_stream(dev, stream)),
+          "rc_kv_block_bounds")
 
 
 def sparse_decode_workspace_bytes(q, k_pool, *, max_seq_len, block, top_blocks) -> int:
@@ -706,44 +702,29 @@ def sparse_decode_attention(q, seq_len, req_idx, req_to_token, k_pool, v_pool, b
     fn = "sparse_decode_attention"
     torch = _torch()
     dev = torch.cuda.current_device()
-    _on_device(fn, dev, q=q, seq_len=seq_len, req_idx=req_idx, req_to_token=req_to_token,
-               k_pool=k_pool, v_pool=v_pool, bounds=bounds, o=o, workspace=workspace, lse=lse,
-               selected=selected)
-    code = _dtype_code(q)
-    _typed(fn, q.dtype, k_pool=k_pool, v_pool=v_pool, bounds=bounds, o=o)
-    _typed(fn, torch.int32, seq_len=seq_len, req_idx=req_idx, req_to_token=req_to_token,
-           selected=selected)
-    _typed(fn, torch.float32, lse=lse)
-    _shaped(fn, "q", q, None, None, None)
-    N, Hq, d = q.shape
-    _shaped(fn, "o", o, N, Hq, d)
-    _shaped(fn, "k_pool", k_pool, None, None, d)
-    S, Hkv, _ = k_pool.shape
-    _shaped(fn, "v_pool", v_pool, S, Hkv, d)
-    _shaped(fn, "req_to_token", req_to_token, None, None)
-    R, C = req_to_token.shape
-    _shaped(fn, "bounds", bounds, R, None, Hkv, 2, d)
-    _shaped(fn, "seq_len", seq_len, N)
-    _shaped(fn, "req_idx", req_idx, N)
-    if not workspace.is_contiguous():
-        raise ValueError(f"{fn}: workspace must be contiguous")
+    dt, i32 = q.dtype, torch.int32
+    N, Hq, d = _dims(fn, "q", q, 3)
+    S, Hkv, _ = _dims(fn, "k_pool", k_pool, 3)
+    R, C = _dims(fn, "req_to_token", req_to_token, 2)
+    nb = _dims(fn, "bounds", bounds, 5)[1]
+    _require(fn, dev, (("q", q, dt, (N, Hq, d)), ("o", o, dt, (N, Hq, d)),
+                       ("k_pool", k_pool, dt, (S, Hkv, d)), ("v_pool", v_pool, dt, (S, Hkv, d)),
+                       ("bounds", bounds, dt, (R, nb, Hkv, 2, d)),
+                       ("req_to_token", req_to_token, i32, (R, C)),
+                       ("seq_len", seq_len, i32, (N,)), ("req_idx", req_idx, i32, (N,)),
+                       ("workspace", workspace, torch.uint8, workspace.shape)))
+    a = RcSparseDecodeArgs(_dtype_code(q), N, Hq, Hkv, d, R, C, block, nb, max_seq_len, top_blocks,
+                           sink_blocks, recent_blocks, S, sm_scale, q.data_ptr(),
+                           seq_len.data_ptr(), req_idx.data_ptr(), req_to_token.data_ptr(),
+                           k_pool.data_ptr(), v_pool.data_ptr(), bounds.data_ptr(), o.data_ptr())
     if lse is not None:
-        _shaped(fn, "lse", lse, N, Hq)
+        _require(fn, dev, (("lse", lse, torch.float32, (N, Hq)),))
+        a.lse = lse.data_ptr()
     if selected is not None:
-        _shaped(fn, "selected", selected, N, Hkv, top_blocks)
-    a = RcSparseDecodeArgs(dtype=code, num_rows=N, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=d,
-                           max_reqs=R, max_ctx=C, block=block, max_blocks=bounds.shape[1],
-                           max_seq_len=max_seq_len, top_blocks=top_blocks,
-                           sink_blocks=sink_blocks, recent_blocks=recent_blocks, num_slots=S,
-                           sm_scale=sm_scale, q=q.data_ptr(), seq_len=seq_len.data_ptr(),
-                           req_idx=req_idx.data_ptr(), req_to_token=req_to_token.data_ptr(),
-                           k_pool=k_pool.data_ptr(), v_pool=v_pool.data_ptr(),
-                           bounds=bounds.data_ptr(), o=o.data_ptr(),
-                           lse=0 if lse is None else lse.data_ptr(),
-                           selected=0 if selected is None else selected.data_ptr())
-    check(lib().rc_sparse_decode_attention(ctypes.byref(a), ctypes.c_void_p(workspace.data_ptr()),
-                                           workspace.numel() * workspace.element_size(),
-                                           _stream(stream)), "rc_sparse_decode_attention")
+        _require(fn, dev, (("selected", selected, i32, (N, Hkv, top_blocks)),))
+        a.selected = selected.data_ptr()
+    check(lib().rc_sparse_decode_attention(ctypes.byref(a), workspace.data_ptr(), workspace.numel(),
+                                           _raw_stream(dev, stream)), "rc_sparse_decode_attention")
 
 
 def device_status(stream=None) -> int:
