@@ -13,18 +13,28 @@
   decode_end     insert the finished sequences (context + generated tokens) or free the generated
                  tokens' slots, unlock, release rows.
 
+Between a model's projections and attention, at a batch's positions (an extend or a decode batch):
+
+  norm_rope      norms of queries and keys for each head and the position rotation (the engine's
+                 `rope` table), in place or into given tensors;
+  append_layer   append one layer's new K/V to the cache (norm and rotation on the way, if wanted)
+                 and, with `sparse_block`, extend the block bounds of the batch's rows;
+  sparse_layer   attention of one layer over the blocks that the bounds select for each query and
+                 KV head, after append_layer: decode steps, and short chunks of new tokens.
+
 The model's projections (q, k_new, v_new per layer) are the caller's: this module never
 computes them.
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 
 import numpy as np
 
 from . import (DEFAULT_KV_CHUNK, decode_attention, decode_workspace_bytes, extend_attention,
-               extend_workspace_bytes, kv_copy, plan_extend_stacking, shared_context_groups,
-               MAX_STACK_LEVELS)
+               extend_workspace_bytes, kv_append, kv_block_bounds, kv_copy, plan_extend_stacking,
+               qk_norm_rope, shared_context_groups, sparse_decode_attention,
+               sparse_decode_workspace_bytes, MAX_STACK_LEVELS)
 from .runtime import DeviceKV, HostCache, Plan
 
 
@@ -40,6 +50,11 @@ class ExtendBatch:
     max_prefix_len: int
     stack: object = None       # (device ranges, device shared, max_group_rows) or None
     workspace: object = None   # device scratch of the stacked pass
+    token_pos: object = None   # device int32 [T]: position of each new token (see Engine.rope)
+    token_len: object = None   # device int32 [T]: position + 1, what its query may see
+    token_row: object = None   # device int32 [T]: its request's slot-table row
+    max_len: int = 0           # longest request
+    bounded: set = field(default_factory=set)   # layers whose bounds hold the new tokens
 
     @property
     def num_tokens(self) -> int:
@@ -61,6 +76,10 @@ class DecodeBatch:
     context_rows: object = None  # host int32 [B, max_ctx]: each context's slots (decode_begin)
     context_len: object = None   # host int64 [B]
     gen_slots: list = None       # host int32 [B] per decode_step: the generated tokens' slots
+    steps: int = 0               # decode_steps taken
+    token_pos: object = None     # device int32 [B]: position of the step's new tokens
+    one_each: object = None      # device int32 [B + 1]: 0, 1, .. B
+    bounded: dict = field(default_factory=dict)   # layer -> steps whose tokens its bounds hold
 
 
 # shortest shared prefix worth a stacked pass: two key tiles
@@ -68,10 +87,14 @@ STACK_MIN_SHARED = 256
 
 
 class Engine:
+    rope = None        # fp32 table [positions, rotary_dim] on the device, or None
+    sparse_block = 0   # positions per block of the bounds, 0: none are kept
+    bounds = None      # [layers, max_reqs, blocks, Hkv, 2, d]
+
     def __init__(self, layers, n_q_heads, n_kv_heads, head_dim, dtype, num_slots, max_reqs,
                  max_ctx, initial_order=None, device="cuda", kv_chunk=0, share_decode=True,
                  stack_extend=True, host_tier_slots=0, host_planes=None,
-                 stack_levels=MAX_STACK_LEVELS, fold_extend=True):
+                 stack_levels=MAX_STACK_LEVELS, fold_extend=True, rope=None, sparse_block=0):
         self.layers = layers
         self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
         self.sm_scale = 1.0 / float(np.sqrt(head_dim))
@@ -91,6 +114,23 @@ class Engine:
             else:
                 self.host_k = torch.empty(shape, dtype=dtype, pin_memory=True)
                 self.host_v = torch.empty(shape, dtype=dtype, pin_memory=True)
+        # rope: the rotation's fp32 table [positions, rotary_dim] (rope_table), at least max_ctx
+        # positions, for norm_rope and append_layer
+        if rope is not None:
+            self.rope = self.dev.torch.as_tensor(rope, device=self.dev.device).contiguous()
+            if self.rope.dtype != self.dev.torch.float32 or self.rope.dim() != 2 or \
+                    self.rope.shape[0] < max_ctx:
+                raise ValueError(f"rope must be an fp32 table of at least {max_ctx} positions")
+        # sparse_block: positions per block of the bounds that sparse_layer selects blocks by
+        # (16, 32, 64 or 128; 0: no bounds are kept)
+        self.sparse_block = int(sparse_block)
+        if self.sparse_block:
+            if self.sparse_block not in (16, 32, 64, 128):
+                raise ValueError("sparse_block must be 0, 16, 32, 64 or 128")
+            nb = -(-max_ctx // self.sparse_block)
+            self.bounds = self.dev.torch.empty((layers, max_reqs, nb, n_kv_heads, 2, head_dim),
+                                               dtype=dtype, device=self.dev.device)
+        self._sparse_ws = None
         self.max_ctx = max_ctx
         self.kv_chunk = kv_chunk
         # decode reads a context prefix that several requests share once for all of them
@@ -152,7 +192,13 @@ class Engine:
                                               plan.out_loc])
         S = plan.lengths - plan.prefix_len
         batch = ExtendBatch(plan, row_ids, qo, pl, ri, ol, int(S.max()) if B else 0,
-                            int(plan.prefix_len.max()) if B else 0)
+                            int(plan.prefix_len.max()) if B else 0,
+                            max_len=int(plan.lengths.max()) if B else 0)
+        if self.rope is not None or self.sparse_block:
+            T = plan.num_tokens
+            pos = np.arange(T) - np.repeat(plan.qo_indptr[:-1] - plan.prefix_len, S)
+            batch.token_pos, batch.token_len, batch.token_row = self.dev.upload_i32(
+                [pos, pos + 1, np.repeat(row_ids, S)])
         if self.stack_extend and B > 1:
             # stacking groups over the levels of the tree, each kept where it is estimated to pay
             G = self.n_q_heads // self.n_kv_heads
@@ -229,8 +275,13 @@ class Engine:
         if batch.gen_slots is not None:
             batch.gen_slots.append(batch.new_slots.copy())
         batch.step_id = object()   # the lengths changed: the next layer plans again
-        batch.dev_seq_len, batch.dev_req_idx, batch.dev_out_loc = self.dev.upload_i32(
-            [batch.seq_len, batch.row_ids, batch.new_slots])
+        meta = [batch.seq_len, batch.row_ids, batch.new_slots]
+        if self.rope is not None or self.sparse_block:
+            meta += [cols, np.arange(B + 1)]
+        batch.dev_seq_len, batch.dev_req_idx, batch.dev_out_loc, *more = self.dev.upload_i32(meta)
+        if more:
+            batch.token_pos, batch.one_each = more
+        batch.steps += 1
         return batch
 
     def workspace(self, q, k_new, max_total_tokens):
@@ -256,6 +307,82 @@ class Engine:
                          kv_chunk=self.kv_chunk, lse=lse, groups=batch.groups,
                          reuse_plan=reuse)
         self._ws_plan = key     # the workspace now holds this step's plan
+
+    # ---------------------------------------------------------------- norms, rotation, sparse
+    def _metadata(self, batch, what):
+        if batch.token_pos is None:
+            raise ValueError(f"{what}: the engine was made without rope and sparse_block, or no "
+                             "decode_step has been taken")
+
+    def norm_rope(self, batch, q=None, k=None, *, q_weight=None, k_weight=None, eps=1e-6,
+                  interleaved=False, q_out=None, k_out=None):
+        """Norms of q [T, Hq, d] and k [T, Hkv, d] for each head (with the given weights) and, if
+        the engine has a rope table, their rotation to the positions of the batch's new tokens; in
+        place unless q_out / k_out are given (qk_norm_rope)."""
+        self._metadata(batch, "norm_rope")
+        qk_norm_rope(q, k, batch.token_pos if self.rope is not None else None, self.rope,
+                     q_weight=q_weight, k_weight=k_weight, eps=eps, interleaved=interleaved,
+                     q_out=q_out, k_out=k_out)
+
+    def append_layer(self, batch, layer: int, k, v, *, rotate=True, k_weight=None, eps=1e-6,
+                     interleaved=False):
+        """Append the new tokens' k and v [T, Hkv, d] of one layer to the cache (kv_append). rotate:
+        the keys are rotated by the engine's table on the way (False for keys that norm_rope has
+        rotated already). With sparse_block the layer's block bounds follow; a batch's first append
+        of a layer, and one after steps that only decode_layer has written, builds the bounds of
+        what is cached from the cache first."""
+        self._metadata(batch, "append_layer")
+        if isinstance(batch, DecodeBatch):
+            loc, ip, pre, req = batch.dev_out_loc, batch.one_each, batch.token_pos, \
+                batch.dev_req_idx
+            current = batch.bounded.get(layer, -1) >= batch.steps - 1
+        else:
+            loc, ip, pre, req = batch.out_loc, batch.qo_indptr, batch.prefix_len, batch.req_idx
+            current = layer in batch.bounded
+        bounds = None
+        if self.sparse_block:
+            bounds = self.bounds[layer]
+            if not current:
+                kv_block_bounds(self.dev.k[layer], self.dev.req_to_token, req, pre, bounds,
+                                block=self.sparse_block)
+        kv_append(k, v, loc, ip, pre, self.dev.k[layer], self.dev.v[layer],
+                  rope=self.rope if rotate else None, k_weight=k_weight, eps=eps,
+                  interleaved=interleaved, bounds=bounds,
+                  req_idx=req if self.sparse_block else None, block=self.sparse_block or 64)
+        if isinstance(batch, DecodeBatch):
+            batch.bounded[layer] = batch.steps
+        else:
+            batch.bounded.add(layer)
+
+    def sparse_layer(self, batch, layer: int, q, o, *, top_blocks, sink_blocks=1, recent_blocks=1,
+                     lse=None, selected=None):
+        """Attention of one layer over the blocks selected for each query row and KV head
+        (sparse_decode_attention): a decode batch's new tokens, or every new token of an extend
+        batch, each seeing what its position may. append_layer of this layer and step comes
+        first."""
+        if not self.sparse_block:
+            raise ValueError("sparse_layer: the engine was made without sparse_block")
+        self._metadata(batch, "sparse_layer")
+        if isinstance(batch, DecodeBatch):
+            length, row, longest = batch.dev_seq_len, batch.dev_req_idx, int(batch.seq_len.max()) \
+                if len(batch.seq_len) else 0
+            current = batch.bounded.get(layer, -1) == batch.steps
+        else:
+            length, row, longest = batch.token_len, batch.token_row, batch.max_len
+            current = layer in batch.bounded
+        if not current:
+            raise ValueError(f"sparse_layer: append_layer of layer {layer} comes first")
+        need = sparse_decode_workspace_bytes(q, self.dev.k[layer], max_seq_len=longest,
+                                             block=self.sparse_block, top_blocks=top_blocks)
+        if self._sparse_ws is None or self._sparse_ws.numel() < need:
+            self._sparse_ws = self.dev.torch.empty(need, dtype=self.dev.torch.uint8,
+                                                   device=self.dev.device)
+        sparse_decode_attention(q, length, row, self.dev.req_to_token, self.dev.k[layer],
+                                self.dev.v[layer], self.bounds[layer], o, self._sparse_ws,
+                                sm_scale=self.sm_scale, max_seq_len=longest,
+                                block=self.sparse_block, top_blocks=top_blocks,
+                                sink_blocks=sink_blocks, recent_blocks=recent_blocks, lse=lse,
+                                selected=selected)
 
     def decode_end(self, batch: DecodeBatch, seqs=None):
         """The requests leave decoding. With `seqs` (each request's context followed by the
