@@ -53,8 +53,8 @@ __device__ void window_offsets(int* off, int* warp_sums, int n, F count) {
   __syncthreads();
 }
 // the request k of the window with off[k] <= item < off[k + 1]
-__device__ __forceinline__ int find_request(const int* off, int item) {
-  int lo = 0, hi = kWindow;
+__device__ __forceinline__ int find_request(const int* off, int n, int item) {
+  int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (off[mid] <= item) lo = mid; else hi = mid;
@@ -89,13 +89,46 @@ __device__ __forceinline__ Span span_of(const rc_kv_append_args& a, int b, int* 
   return s;
 }
 
-template <typename T, int L>
+// Least and greatest elements of 16-byte chunks, NaN kept: pairs of bf16, or single fp32.
+template <typename T>
+struct Extremes;
+template <>
+struct Extremes<__nv_bfloat16> {
+  static constexpr uint32_t kLo = 0x7f807f80u, kHi = 0xff80ff80u;   // inf, -inf
+  static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) { return min_nan_bf16x2(a, b); }
+  static __device__ __forceinline__ uint32_t hi(uint32_t a, uint32_t b) { return max_nan_bf16x2(a, b); }
+};
+template <>
+struct Extremes<float> {
+  static constexpr uint32_t kLo = 0x7f800000u, kHi = 0xff800000u;
+  static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) {
+    return __float_as_uint(min_nan(__uint_as_float(a), __uint_as_float(b)));
+  }
+  static __device__ __forceinline__ uint32_t hi(uint32_t a, uint32_t b) {
+    return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+  }
+};
+template <typename T>
+__device__ __forceinline__ void lower(uint4& a, const uint4& b) {
+  a = make_uint4(Extremes<T>::lo(a.x, b.x), Extremes<T>::lo(a.y, b.y), Extremes<T>::lo(a.z, b.z),
+                 Extremes<T>::lo(a.w, b.w));
+}
+template <typename T>
+__device__ __forceinline__ void raise(uint4& a, const uint4& b) {
+  a = make_uint4(Extremes<T>::hi(a.x, b.x), Extremes<T>::hi(a.y, b.y), Extremes<T>::hi(a.z, b.z),
+                 Extremes<T>::hi(a.w, b.w));
+}
+__device__ __forceinline__ uint4 splat(uint32_t x) { return make_uint4(x, x, x, x); }
+
+// TOK tokens of a thread are in flight together.
+template <typename T, int L, int TOK>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a, int heads_per_cta,
                                                              int head_groups, int* status) {
   constexpr int ROWS = kThreads / L;   // (token, head) rows a pass of the CTA covers
+  constexpr int N = Raw<T>::N;
   __shared__ int off[kWindow + 1];
   __shared__ int warp_sums[kThreads / 32];
-  __shared__ float red[kThreads * 32];   // lo and hi of 16 elements per thread
+  __shared__ uint4 red[4 * N][kThreads];   // extremes of 16 elements per thread
   const int d = a.head_dim, r = a.rotary_dim;
   const bool inter = a.interleaved != 0;
   const int i = threadIdx.x % L, row_in = threadIdx.x / L;
@@ -103,142 +136,159 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a
   const int W = ROWS / heads_per_cta;   // tokens a pass covers; threads past W * heads idle
   const LaneChunks lc = lane_chunks(i, d, r, inter);
   const T* kw = (const T*)a.k_weight;
-  float g0[8], g1[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) g0[e] = g1[e] = 1.f;
-  if (kw && lc.c0 >= 0) load8(kw + lc.c0 * 8, g0);
-  if (kw && lc.c1 >= 0) load8(kw + lc.c1 * 8, g1);
 
   for (int b0 = 0; b0 < a.num_reqs; b0 += kWindow) {
-    window_offsets(off, warp_sums, min(kWindow, a.num_reqs - b0), [&](int k) {
+    const int nreq = min(kWindow, a.num_reqs - b0);
+    window_offsets(off, warp_sums, nreq, [&](int k) {
       const Span s = span_of(a, b0 + k, status, blockIdx.x == 0);
       return s.S ? (s.P + s.S - 1) / a.block - s.P / a.block + 1 : 0;
     });
     const int64_t items = (int64_t)off[kWindow] * head_groups;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
       const int job = (int)(it / head_groups), hg = (int)(it - (int64_t)job * head_groups);
-      const int k = find_request(off, job);
+      const int k = find_request(off, nreq, job);
       const Span s = span_of(a, b0 + k, status, false);
       const int blk = s.P / a.block + (job - off[k]);
       const int p0 = max(s.P, blk * a.block);
       const int p1 = (int)min((int64_t)s.P + s.S, (int64_t)(blk + 1) * a.block);
       const int h = hg * heads_per_cta + hl;
       const bool mine = h < a.num_kv_heads && w < W;
-      float lo[16], hi[16];
+      const bool m0 = mine && lc.c0 >= 0, m1 = mine && lc.c1 >= 0;
+      T* cell = (T*)a.bounds +
+                ((((int64_t)s.row * a.max_blocks + blk) * a.num_kv_heads + h) * 2) * d;
+      Raw<T> lo0, lo1, hi0, hi1;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) { lo[e] = INFINITY; hi[e] = -INFINITY; }
-      for (int p = p0; p < p1; p += W) {   // the same count for every thread: shuffles inside
-        const int pos = p + w;
-        const int64_t t = s.t0 + (pos - s.P);
-        bool live = mine && pos < p1;
-        int64_t dst = 0;
-        if (live) {
-          const int sl = a.out_loc[t];
-          if (sl < 0 || sl >= a.num_slots) {
+      for (int c = 0; c < N; ++c) {
+        lo0.v[c] = lo1.v[c] = splat(Extremes<T>::kLo);
+        hi0.v[c] = hi1.v[c] = splat(Extremes<T>::kHi);
+      }
+      if (a.bounds && w == 0 && blk * a.block < s.P) {   // cached tokens began the block
+        if (m0) {
+          lo0.load(cell + lc.c0 * 8);
+          hi0.load(cell + d + lc.c0 * 8);
+        }
+        if (m1) {
+          lo1.load(cell + lc.c1 * 8);
+          hi1.load(cell + d + lc.c1 * 8);
+        }
+      }
+      for (int p = p0; p < p1; p += W * TOK) {   // the same count for every thread: shuffles inside
+        Raw<T> x0[TOK], x1[TOK], y0[TOK], y1[TOK];
+        LaneAngles ang[TOK];
+        int slot[TOK];
+#pragma unroll
+        for (int u = 0; u < TOK; ++u) {
+          const int pos = p + u * W + w;
+          const int64_t t = s.t0 + (int64_t)(pos - s.P);
+          const bool in = pos < p1;
+          slot[u] = mine && in ? a.out_loc[t] : 0;
+          const T* ks = (const T*)a.k + t * a.k_token_stride + (int64_t)h * a.k_head_stride;
+          const T* vs = (const T*)a.v + t * a.v_token_stride + (int64_t)h * a.v_head_stride;
+          x0[u].clear();
+          x1[u].clear();
+          if (m0 && in) x0[u].load(ks + lc.c0 * 8);
+          if (m1 && in) x1[u].load(ks + lc.c1 * 8);
+          if (m0 && in) y0[u].load(vs + lc.c0 * 8);
+          if (m1 && in) y1[u].load(vs + lc.c1 * 8);
+          if (lc.rot && mine && in) load_angles(a.rope + (int64_t)pos * r, i, r, ang[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < TOK; ++u) {
+          const bool in = p + u * W + w < p1;
+          bool live = mine && in;
+          if (live && (slot[u] < 0 || slot[u] >= a.num_slots)) {
             if (i == 0) set_status(status, kStatusSlotRange);
             live = false;
-          } else {
-            dst = ((int64_t)sl * a.num_kv_heads + h) * d;
           }
-        }
-        const bool v0 = live && lc.c0 >= 0, v1 = live && lc.c1 >= 0;
-        const T* ks = (const T*)a.k + t * a.k_token_stride + (int64_t)h * a.k_head_stride;
-        const T* vs = (const T*)a.v + t * a.v_token_stride + (int64_t)h * a.v_head_stride;
-        float x[8] = {}, y[8] = {};
-        if (v0) load8(ks + lc.c0 * 8, x);
-        if (v1) load8(ks + lc.c1 * 8, y);
-        if (v0) copy8((T*)a.v_pool + dst + lc.c0 * 8, vs + lc.c0 * 8);
-        if (v1) copy8((T*)a.v_pool + dst + lc.c1 * 8, vs + lc.c1 * 8);
-        if (kw) {
-          const float inv = norm_scale<L>(x, y, d, a.eps);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[e] *= inv * g0[e];
-            y[e] *= inv * g1[e];
+          if (kw || r) {
+            float x[8], y[8];
+            x0[u].get(x);
+            x1[u].get(y);
+            if (kw) {
+              const float inv = norm_scale<L>(x, y, d, a.eps);
+              if (m0) scale8(x, inv, kw + lc.c0 * 8);
+              if (m1) scale8(y, inv, kw + lc.c1 * 8);
+            }
+            if (lc.rot) rotate_pairs(x, y, inter, ang[u]);
+            x0[u].set(x);
+            x1[u].set(y);
           }
-        }
-        if (r && live && lc.rot) {
-          LaneAngles ang;
-          load_angles(a.rope + (int64_t)pos * r, i, r, ang);
-          rotate_pairs(x, y, inter, ang);
-        }
-        if (v0) store8((T*)a.k_pool + dst + lc.c0 * 8, x);
-        if (v1) store8((T*)a.k_pool + dst + lc.c1 * 8, y);
-        if (a.bounds && live) {
-          // the bounds are those of the stored (rounded) keys
+          const int64_t dst = ((int64_t)slot[u] * a.num_kv_heads + h) * d;
+          if (live && lc.c0 >= 0) {
+            x0[u].store((T*)a.k_pool + dst + lc.c0 * 8);
+            y0[u].store((T*)a.v_pool + dst + lc.c0 * 8);
+          }
+          if (live && lc.c1 >= 0) {
+            x1[u].store((T*)a.k_pool + dst + lc.c1 * 8);
+            y1[u].store((T*)a.v_pool + dst + lc.c1 * 8);
+          }
+          if (a.bounds && live) {   // the extremes of the stored (rounded) keys
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float xr = Elem<T>::to_f(Elem<T>::from_f(x[e]));
-            const float yr = Elem<T>::to_f(Elem<T>::from_f(y[e]));
-            lo[e] = min_nan(lo[e], xr);
-            hi[e] = max_nan(hi[e], xr);
-            lo[8 + e] = min_nan(lo[8 + e], yr);
-            hi[8 + e] = max_nan(hi[8 + e], yr);
+            for (int c = 0; c < N; ++c) {
+              lower<T>(lo0.v[c], x0[u].v[c]);
+              raise<T>(hi0.v[c], x0[u].v[c]);
+              lower<T>(lo1.v[c], x1[u].v[c]);
+              raise<T>(hi1.v[c], x1[u].v[c]);
+            }
           }
         }
       }
       if (!a.bounds) continue;
       if (W > 1 && p1 - p0 > 1) {   // join the token lanes (uniform over the CTA)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          red[e * kThreads + threadIdx.x] = lo[e];
-          red[(16 + e) * kThreads + threadIdx.x] = hi[e];
+        for (int c = 0; c < N; ++c) {
+          red[c][threadIdx.x] = lo0.v[c];
+          red[N + c][threadIdx.x] = lo1.v[c];
+          red[2 * N + c][threadIdx.x] = hi0.v[c];
+          red[3 * N + c][threadIdx.x] = hi1.v[c];
         }
         __syncthreads();
         if (w == 0) {
           for (int u = 1; u < W && p0 + u < p1; ++u) {
             const int o = threadIdx.x + u * heads_per_cta * L;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              lo[e] = min_nan(lo[e], red[e * kThreads + o]);
-              hi[e] = max_nan(hi[e], red[(16 + e) * kThreads + o]);
+            for (int c = 0; c < N; ++c) {
+              lower<T>(lo0.v[c], red[c][o]);
+              lower<T>(lo1.v[c], red[N + c][o]);
+              raise<T>(hi0.v[c], red[2 * N + c][o]);
+              raise<T>(hi1.v[c], red[3 * N + c][o]);
             }
           }
         }
         __syncthreads();
       }
-      if (w == 0 && mine) {
-        T* cell = (T*)a.bounds +
-                  ((((int64_t)s.row * a.max_blocks + blk) * a.num_kv_heads + h) * 2) * d;
-        const bool began = blk * a.block >= s.P;   // no cached token lies in this block
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int cc = c ? lc.c1 : lc.c0;
-          if (cc < 0) continue;
-          if (!began) {
-            float v[8];
-            load8(cell + cc * 8, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) lo[c * 8 + e] = min_nan(lo[c * 8 + e], v[e]);
-            load8(cell + d + cc * 8, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) hi[c * 8 + e] = max_nan(hi[c * 8 + e], v[e]);
-          }
-          store8(cell + cc * 8, lo + c * 8);
-          store8(cell + d + cc * 8, hi + c * 8);
-        }
+      if (w == 0 && m0) {
+        lo0.store(cell + lc.c0 * 8);
+        hi0.store(cell + d + lc.c0 * 8);
+      }
+      if (w == 0 && m1) {
+        lo1.store(cell + lc.c1 * 8);
+        hi1.store(cell + d + lc.c1 * 8);
       }
     }
   }
 }
 
 // ---------------------------------------------------------------- bounds of cached keys
-// Work items are (layer, row, block, column group of 16-byte chunks); a thread keeps the bounds of
-// one chunk over every W-th token of the block.
+// Work items are (layer, row, block, column group of 16-byte chunks); a thread keeps the extremes
+// of one chunk over every W-th token of the block, kFly of them in flight.
+constexpr int kFly = 8;
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_bounds_args a,
                                                                    int chunks_per_cta, int col_groups,
                                                                    int* status) {
-  constexpr int V = 8;   // elements of a chunk
+  constexpr int V = 16 / (int)sizeof(T);   // elements of a chunk
   __shared__ int off[kWindow + 1];
   __shared__ int warp_sums[kThreads / 32];
-  __shared__ float red[kThreads * 2 * V];
+  __shared__ uint4 red[2][kThreads];
   const int d = a.head_dim;
   const int chunks = a.num_kv_heads * d / V;
   const int cl = threadIdx.x % chunks_per_cta, w = threadIdx.x / chunks_per_cta;
   const int W = kThreads / chunks_per_cta;
   for (int b0 = 0; b0 < a.num_rows; b0 += kWindow) {
-    window_offsets(off, warp_sums, min(kWindow, a.num_rows - b0), [&](int k) {
+    const int nreq = min(kWindow, a.num_rows - b0);
+    window_offsets(off, warp_sums, nreq, [&](int k) {
       const int L = a.seq_len[b0 + k], row = a.req_idx[b0 + k];
       if (L < 0 || L > a.max_ctx || row < 0 || row >= a.max_reqs ||
           (L - 1) / a.block >= a.max_blocks) {
@@ -253,46 +303,48 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
       const int64_t layer = it / per_layer;
       const int64_t rest = it - layer * per_layer;
       const int job = (int)(rest / col_groups), cg = (int)(rest - (int64_t)job * col_groups);
-      const int k = find_request(off, job);
+      const int k = find_request(off, nreq, job);
       const int L = a.seq_len[b0 + k], row = a.req_idx[b0 + k];
       const int blk = job - off[k];
       const int p0 = blk * a.block, p1 = (int)min((int64_t)L, (int64_t)p0 + a.block);
       const int c = cg * chunks_per_cta + cl;
       const bool mine = c < chunks && w < W;
       const int32_t* rt = a.req_to_token + (int64_t)row * a.max_ctx;
-      const T* kp = (const T*)a.k_pool + layer * a.num_slots * a.num_kv_heads * d;
-      float lo[V], hi[V];
+      const uint4* kp = (const uint4*)((const T*)a.k_pool +
+                                       layer * a.num_slots * a.num_kv_heads * d) + c;
+      uint4 lo = splat(Extremes<T>::kLo), hi = splat(Extremes<T>::kHi);
+      for (int p = p0 + w; mine && p < p1; p += W * kFly) {
+        int slot[kFly];
+        uint4 v[kFly];
 #pragma unroll
-      for (int e = 0; e < V; ++e) { lo[e] = INFINITY; hi[e] = -INFINITY; }
-      for (int p = p0 + w; mine && p < p1; p += W) {
-        const int sl = rt[p];
-        if (sl < 0 || sl >= a.num_slots) {
-          if (cl == 0) set_status(status, kStatusSlotRange);
-          continue;
+        for (int u = 0; u < kFly; ++u) slot[u] = p + u * W < p1 ? rt[p + u * W] : -2;
+#pragma unroll
+        for (int u = 0; u < kFly; ++u) {
+          if (slot[u] == -2 && p + u * W >= p1) continue;
+          if (slot[u] < 0 || slot[u] >= a.num_slots) {
+            if (cl == 0) set_status(status, kStatusSlotRange);
+            slot[u] = -2;
+          } else {
+            v[u] = kp[(int64_t)slot[u] * chunks];
+          }
         }
-        float v[V];
-        load8(kp + (int64_t)sl * a.num_kv_heads * d + c * V, v);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          lo[e] = min_nan(lo[e], v[e]);
-          hi[e] = max_nan(hi[e], v[e]);
+        for (int u = 0; u < kFly; ++u) {
+          if (slot[u] != -2) {
+            lower<T>(lo, v[u]);
+            raise<T>(hi, v[u]);
+          }
         }
       }
       if (W > 1) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          red[e * kThreads + threadIdx.x] = lo[e];
-          red[(V + e) * kThreads + threadIdx.x] = hi[e];
-        }
+        red[0][threadIdx.x] = lo;
+        red[1][threadIdx.x] = hi;
         __syncthreads();
         if (w == 0) {
           for (int u = 1; u < W; ++u) {
             const int o = threadIdx.x + u * chunks_per_cta;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              lo[e] = min_nan(lo[e], red[e * kThreads + o]);
-              hi[e] = max_nan(hi[e], red[(V + e) * kThreads + o]);
-            }
+            lower<T>(lo, red[0][o]);
+            raise<T>(hi, red[1][o]);
           }
         }
         __syncthreads();
@@ -301,8 +353,8 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
         const int h = c * V / d, e0 = c * V - h * d;
         T* cell = (T*)a.bounds +
                   ((((layer * a.max_reqs + row) * a.max_blocks + blk) * a.num_kv_heads + h) * 2) * d;
-        store8(cell + e0, lo);
-        store8(cell + d + e0, hi);
+        *(uint4*)(cell + e0) = lo;
+        *(uint4*)(cell + d + e0) = hi;
       }
     }
   }
@@ -310,26 +362,27 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
 
 bool block_ok(int block) { return block == 16 || block == 32 || block == 64 || block == 128; }
 
-int sm_count(int* out) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return fail(RC_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
-  return RC_OK;
-}
-
-template <typename T>
+template <typename T, int L>
 void launch_append(const rc_kv_append_args& a, int sms, int* st, cudaStream_t s) {
-  const int L = head_lanes(a.head_dim);
-  const int hpc = std::min(a.num_kv_heads, kThreads / L);
+  // single tokens: every thread a head; prompts: 8 tokens of a block beside one another
+  const bool prompts = a.num_tokens >= 16 * (int64_t)a.num_reqs;
+  const int hpc = std::min(a.num_kv_heads, prompts ? std::max(1, kThreads / L / 8) : kThreads / L);
   const int hg = (a.num_kv_heads + hpc - 1) / hpc;
   // blocks the tokens can touch: each request begins and ends inside at most two more
   const int64_t most = (a.num_tokens / a.block + 2 * (int64_t)a.num_reqs) * hg;
   const int grid = (int)std::min<int64_t>(std::max<int64_t>(most, 1), (int64_t)sms * 4);
-  switch (L) {
-    case 4: kv_append_kernel<T, 4><<<grid, kThreads, 0, s>>>(a, hpc, hg, st); break;
-    case 8: kv_append_kernel<T, 8><<<grid, kThreads, 0, s>>>(a, hpc, hg, st); break;
-    default: kv_append_kernel<T, 16><<<grid, kThreads, 0, s>>>(a, hpc, hg, st); break;
+  if (prompts)
+    kv_append_kernel<T, L, 2><<<grid, kThreads, 0, s>>>(a, hpc, hg, st);
+  else
+    kv_append_kernel<T, L, 1><<<grid, kThreads, 0, s>>>(a, hpc, hg, st);
+}
+
+template <typename T>
+void launch_append(const rc_kv_append_args& a, int sms, int* st, cudaStream_t s) {
+  switch (head_lanes(a.head_dim)) {
+    case 4: launch_append<T, 4>(a, sms, st, s); break;
+    case 8: launch_append<T, 8>(a, sms, st, s); break;
+    default: launch_append<T, 16>(a, sms, st, s); break;
   }
 }
 
@@ -362,7 +415,7 @@ extern "C" int rc_kv_append(const rc_kv_append_args* a, void* stream) {
   int* st = rc::device_status_ptr();
   if (!st) return rc::fail(RC_ERR_CUDA, "%s: no device status word", fn);
   int sms = 0;
-  const int e = rc::sm_count(&sms);
+  const int e = rc::sm_count(fn, &sms);
   if (e != RC_OK) return e;
   if (a->dtype == RC_DTYPE_BF16)
     rc::launch_append<__nv_bfloat16>(*a, sms, st, (cudaStream_t)stream);
@@ -391,9 +444,9 @@ extern "C" int rc_kv_block_bounds(const rc_kv_block_bounds_args* a, void* stream
   int* st = rc::device_status_ptr();
   if (!st) return rc::fail(RC_ERR_CUDA, "%s: no device status word", fn);
   int sms = 0;
-  const int e = rc::sm_count(&sms);
+  const int e = rc::sm_count(fn, &sms);
   if (e != RC_OK) return e;
-  const int chunks = a->num_kv_heads * a->head_dim / 8;
+  const int chunks = a->num_kv_heads * a->head_dim * (a->dtype == RC_DTYPE_BF16 ? 2 : 4) / 16;
   const int cpc = std::min(chunks, rc::kThreads);
   const int cg = (chunks + cpc - 1) / cpc;
   const int64_t most = (int64_t)a->num_layers * a->num_rows * a->max_blocks * cg;

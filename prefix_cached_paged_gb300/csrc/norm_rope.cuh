@@ -41,13 +41,26 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
   ((float4*)p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-__device__ __forceinline__ void copy8(__nv_bfloat16* d, const __nv_bfloat16* s) {
-  *(uint4*)d = *(const uint4*)s;
-}
-__device__ __forceinline__ void copy8(float* d, const float* s) {
-  ((uint4*)d)[0] = ((const uint4*)s)[0];
-  ((uint4*)d)[1] = ((const uint4*)s)[1];
-}
+// 8 elements as they are stored: one 16-byte chunk of bf16, two of fp32
+template <typename T>
+struct Raw {
+  static constexpr int N = (int)sizeof(T) / 2;
+  uint4 v[N];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = ((const uint4*)p)[i];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) ((uint4*)p)[i] = v[i];
+  }
+  __device__ __forceinline__ void get(float* f) const { load8((const T*)v, f); }
+  __device__ __forceinline__ void set(const float* f) { store8((T*)v, f); }
+};
 
 // The two chunks of lane i in a row of d elements whose first r are rotated; -1: none.
 struct LaneChunks {
@@ -88,31 +101,42 @@ __device__ __forceinline__ float norm_scale(const float* x, const float* y, int 
   for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
 #pragma unroll
   for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  return rsqrtf(ss / (float)d + eps);
+  return rsqrtf(__fadd_rn(__fdiv_rn(ss, (float)d), eps));
 }
 
-// (a, b) -> (a cos - b sin, b cos + a sin) on a lane's 8 pairs
+// (a, b) -> (a cos - b sin, b cos + a sin) on a lane's 8 pairs, each as one product and one fused
+// multiply-add: written out, so that every kernel rounds alike and a key has the same bits
+// whichever entry point rotated it.
+__device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
+  const float p = a, q = b;
+  a = __fmaf_rn(p, c, -__fmul_rn(q, s));
+  b = __fmaf_rn(q, c, __fmul_rn(p, s));
+}
 __device__ __forceinline__ void rotate_pairs(float* x, float* y, bool interleaved,
                                              const LaneAngles& a) {
   if (interleaved) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float p = x[2 * e], q = x[2 * e + 1], u = y[2 * e], v = y[2 * e + 1];
-      x[2 * e] = p * a.c[e] - q * a.s[e];
-      x[2 * e + 1] = q * a.c[e] + p * a.s[e];
-      y[2 * e] = u * a.c[e + 4] - v * a.s[e + 4];
-      y[2 * e + 1] = v * a.c[e + 4] + u * a.s[e + 4];
+      rotate_pair(x[2 * e], x[2 * e + 1], a.c[e], a.s[e]);
+      rotate_pair(y[2 * e], y[2 * e + 1], a.c[e + 4], a.s[e + 4]);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float p = x[e], q = y[e];
-      x[e] = p * a.c[e] - q * a.s[e];
-      y[e] = q * a.c[e] + p * a.s[e];
-    }
+    for (int e = 0; e < 8; ++e) rotate_pair(x[e], y[e], a.c[e], a.s[e]);
   }
 }
 
+// v_e *= scale * w_e
+template <typename T>
+__device__ __forceinline__ void scale8(float* v, float scale, const T* w) {
+  float g[8];
+  load8(w, g);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], __fmul_rn(scale, g[e]));
+}
+
+// Streaming multiprocessors of the current device.
+int sm_count(const char* fn, int* out);
 // Host-side checks shared by the entry points: head_dim, rotation and table.
 int check_norm_rope(const char* fn, int head_dim, int rotary_dim, int64_t max_position,
                     const float* rope, float eps, bool any_weight);

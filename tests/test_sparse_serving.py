@@ -33,6 +33,10 @@ class Model:
         return x[:, :self.hq], x[:, self.hq:self.hq + self.hkv], x[:, self.hq + self.hkv:]
 
 
+def _bits(t):
+    return t.view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32)
+
+
 def _engine(m, **kw):
     from prefix_cached_paged_gb300.serving import Engine
     return Engine(m.layers, m.hq, m.hkv, m.d, m.dt, 4096, 16, 600, synth.permutation(5, 4096),
@@ -94,8 +98,8 @@ def test_a_model_step_through_the_engine(dtype, hq, hkv, d, rot, inter, block):
             with pytest.raises(ValueError):
                 eng.sparse_layer(b, layer, qo, o, top_blocks=top)
             eng.append_layer(b, layer, k, v, k_weight=wk, **kw)
-            assert torch.equal(eng.dev.k[layer], k_before)
-            assert torch.equal(eng.dev.v[layer], v_before)
+            assert torch.equal(_bits(eng.dev.k[layer]), _bits(k_before))
+            assert torch.equal(_bits(eng.dev.v[layer]), _bits(v_before))
             lse = torch.empty((T, hq), device="cuda")
             sel = torch.empty((T, hkv, top), dtype=torch.int32, device="cuda")
             eng.sparse_layer(b, layer, qo, o, top_blocks=top, lse=lse, selected=sel)
