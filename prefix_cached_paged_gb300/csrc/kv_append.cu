@@ -1,13 +1,13 @@
 // Appending keys and values to the paged cache, the keys normalised and rotated on the way, and
 // the bounds of cached keys block by block that sparse_decode.cu selects blocks with.
 //
-// Work items are (request, block of positions the new tokens touch, group of KV heads), so one CTA
-// owns every new key of a (block, head) and reduces its bounds without atomics: a block that the
-// new tokens begin gets their bounds, a block that cached tokens began takes the minimum and
-// maximum with what it holds (which makes a repeated append of the same tokens change nothing).
-// CTAs walk the items grid-stride; requests are taken in windows of kWindow, whose item offsets
-// each CTA sums up in shared memory, so neither their number nor their lengths need to be known on
-// the host.
+// Work items are (request, block of positions the new tokens touch, a few KV heads), one warp each,
+// so a warp owns every new key of a (block, head) and reduces its bounds without atomics: a block
+// that the new tokens begin gets their bounds, a block that cached tokens began takes the minimum
+// and maximum with what it holds (which makes a repeated append of the same tokens change nothing).
+// Requests are taken in windows of kWindow, whose item offsets each CTA sums up in shared memory, so
+// neither their number nor their lengths need to be known on the host; the warps of the resident
+// CTAs then walk the items with a grid stride.
 #include <algorithm>
 
 #include "host_common.h"
@@ -118,24 +118,43 @@ __device__ __forceinline__ void raise(uint4& a, const uint4& b) {
   a = make_uint4(Extremes<T>::hi(a.x, b.x), Extremes<T>::hi(a.y, b.y), Extremes<T>::hi(a.z, b.z),
                  Extremes<T>::hi(a.w, b.w));
 }
+__device__ __forceinline__ uint4 shfl_xor4(const uint4& v, int o) {
+  return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o),
+                    __shfl_xor_sync(0xffffffffu, v.z, o), __shfl_xor_sync(0xffffffffu, v.w, o));
+}
 __device__ __forceinline__ uint4 splat(uint32_t x) { return make_uint4(x, x, x, x); }
 
-// TOK tokens of a thread are in flight together.
-template <typename T, int L, int TOK>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a, int heads_per_cta,
-                                                             int head_groups, int* status) {
-  constexpr int ROWS = kThreads / L;   // (token, head) rows a pass of the CTA covers
-  constexpr int N = Raw<T>::N;
+// Each warp streams its tokens through a ring of kStages groups in shared memory by 16-byte
+// asynchronous copies. A lane reads only what it copied itself, so the ring needs no barrier, and
+// the bytes in flight cost no registers.
+constexpr int kStages = 3;
+constexpr int kWarps = kThreads / 32;
+
+// A warp's lanes are 32 / L rows: `heads` KV heads beside one another (a power of two), the other
+// rows later tokens of the block. A group is TOK tokens of each row.
+template <typename T>
+constexpr int append_tokens() { return 4 / (int)sizeof(T); }
+template <typename T>
+constexpr int append_smem() { return kWarps * kStages * append_tokens<T>() * 4 * Raw<T>::N * 512; }
+
+template <typename T, int L>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a, int heads,
+                                                             int* status) {
+  constexpr int N = Raw<T>::N, TOK = append_tokens<T>();
+  extern __shared__ __align__(128) char ring[];
   __shared__ int off[kWindow + 1];
-  __shared__ int warp_sums[kThreads / 32];
-  __shared__ uint4 red[4 * N][kThreads];   // extremes of 16 elements per thread
+  __shared__ int warp_sums[kWarps];
   const int d = a.head_dim, r = a.rotary_dim;
   const bool inter = a.interleaved != 0;
-  const int i = threadIdx.x % L, row_in = threadIdx.x / L;
-  const int hl = row_in % heads_per_cta, w = row_in / heads_per_cta;
-  const int W = ROWS / heads_per_cta;   // tokens a pass covers; threads past W * heads idle
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int i = lane % L, row_in = lane / L;
+  const int hl = row_in & (heads - 1), w = row_in / heads, W = 32 / L / heads;
+  const int head_groups = (a.num_kv_heads + heads - 1) / heads;
   const LaneChunks lc = lane_chunks(i, d, r, inter);
   const T* kw = (const T*)a.k_weight;
+  // chunk c (K: 2 N, then V: 2 N) of token u of stage st of this lane
+  char* mine_ring = ring + wid * (kStages * TOK * 4 * N * 512) + lane * 16;
+  auto cell_of = [&](int st, int u, int c) { return mine_ring + ((st * TOK + u) * 4 * N + c) * 512; };
 
   for (int b0 = 0; b0 < a.num_reqs; b0 += kWindow) {
     const int nreq = min(kWindow, a.num_reqs - b0);
@@ -144,16 +163,47 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a
       return s.S ? (s.P + s.S - 1) / a.block - s.P / a.block + 1 : 0;
     });
     const int64_t items = (int64_t)off[kWindow] * head_groups;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    // neighbouring items go to different CTAs: few items spread over the SMs
+    for (int64_t it = (int64_t)wid * gridDim.x + blockIdx.x; it < items;
+         it += (int64_t)gridDim.x * kWarps) {
       const int job = (int)(it / head_groups), hg = (int)(it - (int64_t)job * head_groups);
       const int k = find_request(off, nreq, job);
       const Span s = span_of(a, b0 + k, status, false);
       const int blk = s.P / a.block + (job - off[k]);
       const int p0 = max(s.P, blk * a.block);
-      const int p1 = (int)min((int64_t)s.P + s.S, (int64_t)(blk + 1) * a.block);
-      const int h = hg * heads_per_cta + hl;
-      const bool mine = h < a.num_kv_heads && w < W;
+      const int n = (int)(min((int64_t)s.P + s.S, (int64_t)(blk + 1) * a.block) - p0);
+      const int64_t tok0 = (int64_t)s.t0 + (p0 - s.P);
+      const int h = hg * heads + hl;
+      const bool mine = h < a.num_kv_heads;
       const bool m0 = mine && lc.c0 >= 0, m1 = mine && lc.c1 >= 0;
+      const T* ksrc = (const T*)a.k + tok0 * a.k_token_stride + (int64_t)h * a.k_head_stride;
+      const T* vsrc = (const T*)a.v + tok0 * a.v_token_stride + (int64_t)h * a.v_head_stride;
+      const int groups = (n + W * TOK - 1) / (W * TOK);
+      auto issue = [&](int gr) {
+        if (gr < groups) {
+          const int st = gr % kStages;
+#pragma unroll
+          for (int u = 0; u < TOK; ++u) {
+            const int at = (gr * TOK + u) * W + w;
+            const T* ks = ksrc + at * a.k_token_stride;
+            const T* vs = vsrc + at * a.v_token_stride;
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+              if (m0 && at < n) {
+                cp_async16(smem_u32(cell_of(st, u, c)), (const uint4*)(ks + lc.c0 * 8) + c);
+                cp_async16(smem_u32(cell_of(st, u, 2 * N + c)), (const uint4*)(vs + lc.c0 * 8) + c);
+              }
+              if (m1 && at < n) {
+                cp_async16(smem_u32(cell_of(st, u, N + c)), (const uint4*)(ks + lc.c1 * 8) + c);
+                cp_async16(smem_u32(cell_of(st, u, 3 * N + c)), (const uint4*)(vs + lc.c1 * 8) + c);
+              }
+            }
+          }
+        }
+        cp_async_commit();
+      };
+#pragma unroll
+      for (int gr = 0; gr < kStages - 1; ++gr) issue(gr);
       T* cell = (T*)a.bounds +
                 ((((int64_t)s.row * a.max_blocks + blk) * a.num_kv_heads + h) * 2) * d;
       Raw<T> lo0, lo1, hi0, hi1;
@@ -172,90 +222,78 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a
           hi1.load(cell + d + lc.c1 * 8);
         }
       }
-      for (int p = p0; p < p1; p += W * TOK) {   // the same count for every thread: shuffles inside
-        Raw<T> x0[TOK], x1[TOK], y0[TOK], y1[TOK];
+      for (int gr = 0; gr < groups; ++gr) {   // the same count for every lane: shuffles inside
+        issue(gr + kStages - 1);
+        const int st = gr % kStages;
         LaneAngles ang[TOK];
         int slot[TOK];
 #pragma unroll
         for (int u = 0; u < TOK; ++u) {
-          const int pos = p + u * W + w;
-          const int64_t t = s.t0 + (int64_t)(pos - s.P);
-          const bool in = pos < p1;
-          slot[u] = mine && in ? a.out_loc[t] : 0;
-          const T* ks = (const T*)a.k + t * a.k_token_stride + (int64_t)h * a.k_head_stride;
-          const T* vs = (const T*)a.v + t * a.v_token_stride + (int64_t)h * a.v_head_stride;
-          x0[u].clear();
-          x1[u].clear();
-          if (m0 && in) x0[u].load(ks + lc.c0 * 8);
-          if (m1 && in) x1[u].load(ks + lc.c1 * 8);
-          if (m0 && in) y0[u].load(vs + lc.c0 * 8);
-          if (m1 && in) y1[u].load(vs + lc.c1 * 8);
-          if (lc.rot && mine && in) load_angles(a.rope + (int64_t)pos * r, i, r, ang[u]);
+          const int at = (gr * TOK + u) * W + w;
+          const bool in = mine && at < n;
+          slot[u] = in ? a.out_loc[tok0 + at] : 0;
+          if (lc.rot && in) load_angles(a.rope + (int64_t)(p0 + at) * r, i, r, ang[u]);
         }
+        cp_async_wait<kStages - 1>();
 #pragma unroll
         for (int u = 0; u < TOK; ++u) {
-          const bool in = p + u * W + w < p1;
-          bool live = mine && in;
+          bool live = mine && (gr * TOK + u) * W + w < n;
           if (live && (slot[u] < 0 || slot[u] >= a.num_slots)) {
             if (i == 0) set_status(status, kStatusSlotRange);
             live = false;
           }
+          Raw<T> x0, x1;
+          x0.clear();
+          x1.clear();
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            if (m0 && live) x0.v[c] = *(const uint4*)cell_of(st, u, c);
+            if (m1 && live) x1.v[c] = *(const uint4*)cell_of(st, u, N + c);
+          }
+          const int64_t dst = ((int64_t)slot[u] * a.num_kv_heads + h) * d;
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            if (m0 && live)
+              ((uint4*)((T*)a.v_pool + dst + lc.c0 * 8))[c] = *(const uint4*)cell_of(st, u, 2 * N + c);
+            if (m1 && live)
+              ((uint4*)((T*)a.v_pool + dst + lc.c1 * 8))[c] = *(const uint4*)cell_of(st, u, 3 * N + c);
+          }
           if (kw || r) {
             float x[8], y[8];
-            x0[u].get(x);
-            x1[u].get(y);
+            x0.get(x);
+            x1.get(y);
             if (kw) {
               const float inv = norm_scale<L>(x, y, d, a.eps);
               if (m0) scale8(x, inv, kw + lc.c0 * 8);
               if (m1) scale8(y, inv, kw + lc.c1 * 8);
             }
             if (lc.rot) rotate_pairs(x, y, inter, ang[u]);
-            x0[u].set(x);
-            x1[u].set(y);
+            x0.set(x);
+            x1.set(y);
           }
-          const int64_t dst = ((int64_t)slot[u] * a.num_kv_heads + h) * d;
-          if (live && lc.c0 >= 0) {
-            x0[u].store((T*)a.k_pool + dst + lc.c0 * 8);
-            y0[u].store((T*)a.v_pool + dst + lc.c0 * 8);
-          }
-          if (live && lc.c1 >= 0) {
-            x1[u].store((T*)a.k_pool + dst + lc.c1 * 8);
-            y1[u].store((T*)a.v_pool + dst + lc.c1 * 8);
-          }
+          if (m0 && live) x0.store((T*)a.k_pool + dst + lc.c0 * 8);
+          if (m1 && live) x1.store((T*)a.k_pool + dst + lc.c1 * 8);
           if (a.bounds && live) {   // the extremes of the stored (rounded) keys
 #pragma unroll
             for (int c = 0; c < N; ++c) {
-              lower<T>(lo0.v[c], x0[u].v[c]);
-              raise<T>(hi0.v[c], x0[u].v[c]);
-              lower<T>(lo1.v[c], x1[u].v[c]);
-              raise<T>(hi1.v[c], x1[u].v[c]);
+              lower<T>(lo0.v[c], x0.v[c]);
+              raise<T>(hi0.v[c], x0.v[c]);
+              lower<T>(lo1.v[c], x1.v[c]);
+              raise<T>(hi1.v[c], x1.v[c]);
             }
           }
         }
       }
+      cp_async_wait<0>();
       if (!a.bounds) continue;
-      if (W > 1 && p1 - p0 > 1) {   // join the token lanes (uniform over the CTA)
+      for (int o = L * heads; o < 32; o <<= 1) {   // join the token rows
 #pragma unroll
         for (int c = 0; c < N; ++c) {
-          red[c][threadIdx.x] = lo0.v[c];
-          red[N + c][threadIdx.x] = lo1.v[c];
-          red[2 * N + c][threadIdx.x] = hi0.v[c];
-          red[3 * N + c][threadIdx.x] = hi1.v[c];
+          lower<T>(lo0.v[c], shfl_xor4(lo0.v[c], o));
+          lower<T>(lo1.v[c], shfl_xor4(lo1.v[c], o));
+          raise<T>(hi0.v[c], shfl_xor4(hi0.v[c], o));
+          raise<T>(hi1.v[c], shfl_xor4(hi1.v[c], o));
         }
-        __syncthreads();
-        if (w == 0) {
-          for (int u = 1; u < W && p0 + u < p1; ++u) {
-            const int o = threadIdx.x + u * heads_per_cta * L;
-#pragma unroll
-            for (int c = 0; c < N; ++c) {
-              lower<T>(lo0.v[c], red[c][o]);
-              lower<T>(lo1.v[c], red[N + c][o]);
-              raise<T>(hi0.v[c], red[2 * N + c][o]);
-              raise<T>(hi1.v[c], red[3 * N + c][o]);
-            }
-          }
-        }
-        __syncthreads();
       }
       if (w == 0 && m0) {
         lo0.store(cell + lc.c0 * 8);
@@ -270,22 +308,26 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a
 }
 
 // ---------------------------------------------------------------- bounds of cached keys
-// Work items are (layer, row, block, column group of 16-byte chunks); a thread keeps the extremes
-// of one chunk over every W-th token of the block, kFly of them in flight.
+// Work items are (layer, row, block, group of at most 32 16-byte chunks of a token's keys), one warp
+// each: `cols` chunks (a power of two) beside one another, the other lanes later tokens of the
+// block. A group is kFly tokens of each. The block's slots are loaded 32 at a time, coalesced, and
+// handed to the lanes by shuffles.
 constexpr int kFly = 8;
+constexpr int kBoundsSmem = kWarps * kStages * kFly * 512;
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_bounds_args a,
-                                                                   int chunks_per_cta, int col_groups,
+__global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_bounds_args a, int cols,
                                                                    int* status) {
   constexpr int V = 16 / (int)sizeof(T);   // elements of a chunk
+  extern __shared__ __align__(128) char ring[];
   __shared__ int off[kWindow + 1];
-  __shared__ int warp_sums[kThreads / 32];
-  __shared__ uint4 red[2][kThreads];
+  __shared__ int warp_sums[kWarps];
   const int d = a.head_dim;
   const int chunks = a.num_kv_heads * d / V;
-  const int cl = threadIdx.x % chunks_per_cta, w = threadIdx.x / chunks_per_cta;
-  const int W = kThreads / chunks_per_cta;
+  const int col_groups = (chunks + cols - 1) / cols;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int cl = lane & (cols - 1), w = lane / cols, W = 32 / cols;
+  char* mine_ring = ring + wid * (kStages * kFly * 512) + lane * 16;
   for (int b0 = 0; b0 < a.num_rows; b0 += kWindow) {
     const int nreq = min(kWindow, a.num_rows - b0);
     window_offsets(off, warp_sums, nreq, [&](int k) {
@@ -299,55 +341,69 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
     });
     const int64_t per_layer = (int64_t)off[kWindow] * col_groups;
     const int64_t items = per_layer * a.num_layers;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    for (int64_t it = (int64_t)wid * gridDim.x + blockIdx.x; it < items;
+         it += (int64_t)gridDim.x * kWarps) {
       const int64_t layer = it / per_layer;
       const int64_t rest = it - layer * per_layer;
       const int job = (int)(rest / col_groups), cg = (int)(rest - (int64_t)job * col_groups);
       const int k = find_request(off, nreq, job);
       const int L = a.seq_len[b0 + k], row = a.req_idx[b0 + k];
       const int blk = job - off[k];
-      const int p0 = blk * a.block, p1 = (int)min((int64_t)L, (int64_t)p0 + a.block);
-      const int c = cg * chunks_per_cta + cl;
-      const bool mine = c < chunks && w < W;
-      const int32_t* rt = a.req_to_token + (int64_t)row * a.max_ctx;
-      const uint4* kp = (const uint4*)((const T*)a.k_pool +
-                                       layer * a.num_slots * a.num_kv_heads * d) + c;
-      uint4 lo = splat(Extremes<T>::kLo), hi = splat(Extremes<T>::kHi);
-      for (int p = p0 + w; mine && p < p1; p += W * kFly) {
-        int slot[kFly];
-        uint4 v[kFly];
+      const int p0 = blk * a.block, n = (int)min((int64_t)a.block, (int64_t)L - p0);
+      const int c = cg * cols + cl;
+      const bool mine = c < chunks;
+      const int32_t* rt = a.req_to_token + (int64_t)row * a.max_ctx + p0;
+      const char* kp = (const char*)a.k_pool +
+                       ((layer * a.num_slots * chunks) + (mine ? c : 0)) * 16;
+      int slots = -1;   // of tokens 32 j + lane, -1: nothing to read
+      uint32_t have = 0;   // bit u of group gr at gr % kStages * kFly: this lane copied a token
+      const int groups = (n + W * kFly - 1) / (W * kFly);
+      auto issue = [&](int gr) {
+        if (gr < groups) {
+          if (gr * W * kFly % 32 == 0) {
+            const int t = gr * W * kFly + lane;
+            slots = t < n ? rt[t] : -1;
+            if (t < n && (slots < 0 || slots >= a.num_slots)) {
+              set_status(status, kStatusSlotRange);
+              slots = -1;
+            }
+          }
+          const int st = gr % kStages;
 #pragma unroll
-        for (int u = 0; u < kFly; ++u) slot[u] = p + u * W < p1 ? rt[p + u * W] : -2;
-#pragma unroll
-        for (int u = 0; u < kFly; ++u) {
-          if (slot[u] == -2 && p + u * W >= p1) continue;
-          if (slot[u] < 0 || slot[u] >= a.num_slots) {
-            if (cl == 0) set_status(status, kStatusSlotRange);
-            slot[u] = -2;
-          } else {
-            v[u] = kp[(int64_t)slot[u] * chunks];
+          for (int u = 0; u < kFly; ++u) {
+            const int at = (gr * kFly + u) * W + w;
+            const int slot = __shfl_sync(0xffffffffu, slots, at & 31);
+            const uint32_t bit = 1u << (st * kFly + u);
+            if (mine && at < n && slot >= 0) {
+              cp_async16(smem_u32(mine_ring + (st * kFly + u) * 512), kp + (int64_t)slot * chunks * 16);
+              have |= bit;
+            } else {
+              have &= ~bit;
+            }
           }
         }
+        cp_async_commit();
+      };
+#pragma unroll
+      for (int gr = 0; gr < kStages - 1; ++gr) issue(gr);
+      uint4 lo = splat(Extremes<T>::kLo), hi = splat(Extremes<T>::kHi);
+      for (int gr = 0; gr < groups; ++gr) {
+        issue(gr + kStages - 1);
+        cp_async_wait<kStages - 1>();
+        const int st = gr % kStages;
 #pragma unroll
         for (int u = 0; u < kFly; ++u) {
-          if (slot[u] != -2) {
-            lower<T>(lo, v[u]);
-            raise<T>(hi, v[u]);
+          if (have >> (st * kFly + u) & 1) {
+            const uint4 v = *(const uint4*)(mine_ring + (st * kFly + u) * 512);
+            lower<T>(lo, v);
+            raise<T>(hi, v);
           }
         }
       }
-      if (W > 1) {
-        red[0][threadIdx.x] = lo;
-        red[1][threadIdx.x] = hi;
-        __syncthreads();
-        if (w == 0) {
-          for (int u = 1; u < W; ++u) {
-            const int o = threadIdx.x + u * chunks_per_cta;
-            lower<T>(lo, red[0][o]);
-            raise<T>(hi, red[1][o]);
-          }
-        }
-        __syncthreads();
+      cp_async_wait<0>();
+      for (int o = cols; o < 32; o <<= 1) {   // join the token lanes
+        lower<T>(lo, shfl_xor4(lo, o));
+        raise<T>(hi, shfl_xor4(hi, o));
       }
       if (w == 0 && mine) {
         const int h = c * V / d, e0 = c * V - h * d;
@@ -360,30 +416,69 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
   }
 }
 
+// Launches a grid of as many CTAs as are resident at once, or fewer where there is less to do.
+template <typename K, typename A>
+int launch_resident(const char* fn, K kernel, PerDevice<int>& setup, int64_t items, const A& a,
+                    int width, int smem, int* st, cudaStream_t s) {
+  const int* resident = nullptr;
+  const cudaError_t e = setup.get(
+      [&](int& n) {
+        int dev = 0, sms = 0, per = 0;
+        cudaError_t r = cudaGetDevice(&dev);
+        if (r == cudaSuccess) r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (r == cudaSuccess)
+          r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (r == cudaSuccess)
+          r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, smem);
+        n = std::max(1, sms * per);
+        return r;
+      },
+      &resident);
+  if (e != cudaSuccess) return fail(RC_ERR_CUDA, "%s: setup: %s", fn, cudaGetErrorString(e));
+  kernel<<<(unsigned)std::min<int64_t>(std::max<int64_t>(items, 1), *resident), kThreads, smem, s>>>(
+      a, width, st);
+  count_launches(1);
+  return check_launch(fn);
+}
+
 bool block_ok(int block) { return block == 16 || block == 32 || block == 64 || block == 128; }
 
+int pow2_at_least(int x) {
+  int p = 1;
+  while (p < x) p *= 2;
+  return p;
+}
+
 template <typename T, int L>
-void launch_append(const rc_kv_append_args& a, int sms, int* st, cudaStream_t s) {
-  // single tokens: every thread a head; prompts: 8 tokens of a block beside one another
+int launch_append(const char* fn, const rc_kv_append_args& a, int* st, cudaStream_t s) {
+  // single tokens: every row of a warp a head; prompts: one head, tokens of its block beside one another
   const bool prompts = a.num_tokens >= 16 * (int64_t)a.num_reqs;
-  const int hpc = std::min(a.num_kv_heads, prompts ? std::max(1, kThreads / L / 8) : kThreads / L);
-  const int hg = (a.num_kv_heads + hpc - 1) / hpc;
+  const int heads = std::min(pow2_at_least(a.num_kv_heads), prompts ? std::max(1, 8 / L) : 32 / L);
   // blocks the tokens can touch: each request begins and ends inside at most two more
-  const int64_t most = (a.num_tokens / a.block + 2 * (int64_t)a.num_reqs) * hg;
-  const int grid = (int)std::min<int64_t>(std::max<int64_t>(most, 1), (int64_t)sms * 4);
-  if (prompts)
-    kv_append_kernel<T, L, 2><<<grid, kThreads, 0, s>>>(a, hpc, hg, st);
-  else
-    kv_append_kernel<T, L, 1><<<grid, kThreads, 0, s>>>(a, hpc, hg, st);
+  const int64_t items = (a.num_tokens / a.block + 2 * (int64_t)a.num_reqs) *
+                        ((a.num_kv_heads + heads - 1) / heads);
+  static PerDevice<int> setup;
+  return launch_resident(fn, kv_append_kernel<T, L>, setup, items, a, heads, append_smem<T>(), st, s);
 }
 
 template <typename T>
-void launch_append(const rc_kv_append_args& a, int sms, int* st, cudaStream_t s) {
+int launch_append(const char* fn, const rc_kv_append_args& a, int* st, cudaStream_t s) {
   switch (head_lanes(a.head_dim)) {
-    case 4: launch_append<T, 4>(a, sms, st, s); break;
-    case 8: launch_append<T, 8>(a, sms, st, s); break;
-    default: launch_append<T, 16>(a, sms, st, s); break;
+    case 4: return launch_append<T, 4>(fn, a, st, s);
+    case 8: return launch_append<T, 8>(fn, a, st, s);
+    default: return launch_append<T, 16>(fn, a, st, s);
   }
+}
+
+template <typename T>
+int launch_bounds(const char* fn, const rc_kv_block_bounds_args& a, int* st, cudaStream_t s) {
+  const int chunks = a.num_kv_heads * a.head_dim * (int)sizeof(T) / 16;
+  const int cols = std::min(32, pow2_at_least(chunks));
+  const int64_t items = (int64_t)a.num_layers * a.num_rows * a.max_blocks *
+                        ((chunks + cols - 1) / cols);
+  static PerDevice<int> setup;
+  return launch_resident(fn, kv_block_bounds_kernel<T>, setup, items, a, cols, kBoundsSmem, st,
+                         s);
 }
 
 }  // namespace
@@ -414,15 +509,9 @@ extern "C" int rc_kv_append(const rc_kv_append_args* a, void* stream) {
                "%s: pointers and strides must be multiples of 16 bytes", fn);
   int* st = rc::device_status_ptr();
   if (!st) return rc::fail(RC_ERR_CUDA, "%s: no device status word", fn);
-  int sms = 0;
-  const int e = rc::sm_count(fn, &sms);
-  if (e != RC_OK) return e;
-  if (a->dtype == RC_DTYPE_BF16)
-    rc::launch_append<__nv_bfloat16>(*a, sms, st, (cudaStream_t)stream);
-  else
-    rc::launch_append<float>(*a, sms, st, (cudaStream_t)stream);
-  rc::count_launches(1);
-  return rc::check_launch(fn);
+  return a->dtype == RC_DTYPE_BF16
+             ? rc::launch_append<__nv_bfloat16>(fn, *a, st, (cudaStream_t)stream)
+             : rc::launch_append<float>(fn, *a, st, (cudaStream_t)stream);
 }
 
 extern "C" int rc_kv_block_bounds(const rc_kv_block_bounds_args* a, void* stream) {
@@ -443,19 +532,7 @@ extern "C" int rc_kv_block_bounds(const rc_kv_block_bounds_args* a, void* stream
                "%s: k_pool and bounds must be 16-byte aligned", fn);
   int* st = rc::device_status_ptr();
   if (!st) return rc::fail(RC_ERR_CUDA, "%s: no device status word", fn);
-  int sms = 0;
-  const int e = rc::sm_count(fn, &sms);
-  if (e != RC_OK) return e;
-  const int chunks = a->num_kv_heads * a->head_dim * (a->dtype == RC_DTYPE_BF16 ? 2 : 4) / 16;
-  const int cpc = std::min(chunks, rc::kThreads);
-  const int cg = (chunks + cpc - 1) / cpc;
-  const int64_t most = (int64_t)a->num_layers * a->num_rows * a->max_blocks * cg;
-  const int grid = (int)std::min<int64_t>(most, (int64_t)sms * 8);
-  cudaStream_t s = (cudaStream_t)stream;
-  if (a->dtype == RC_DTYPE_BF16)
-    rc::kv_block_bounds_kernel<__nv_bfloat16><<<grid, rc::kThreads, 0, s>>>(*a, cpc, cg, st);
-  else
-    rc::kv_block_bounds_kernel<float><<<grid, rc::kThreads, 0, s>>>(*a, cpc, cg, st);
-  rc::count_launches(1);
-  return rc::check_launch(fn);
+  return a->dtype == RC_DTYPE_BF16
+             ? rc::launch_bounds<__nv_bfloat16>(fn, *a, st, (cudaStream_t)stream)
+             : rc::launch_bounds<float>(fn, *a, st, (cudaStream_t)stream);
 }
