@@ -7,7 +7,7 @@
 // and maximum with what it holds (which makes a repeated append of the same tokens change nothing).
 // Requests are taken in windows of kWindow, whose item offsets each CTA sums up in shared memory, so
 // neither their number nor their lengths need to be known on the host; the warps of the resident
-// CTAs then walk the items with a grid stride.
+// CTAs then take the items one by one.
 #include <algorithm>
 
 #include "host_common.h"
@@ -18,12 +18,13 @@ namespace rc {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kRun = 4;         // items a CTA takes beside one another
 constexpr int kWindow = 1024;   // requests whose item offsets a CTA holds at a time
 
 // off[k] = items of the window's requests before k (off[n] = all), each of n <= kWindow requests
-// having count(k) items. All threads of the CTA call it.
+// having count(k) items; none taken yet. All threads of the CTA call it.
 template <typename F>
-__device__ void window_offsets(int* off, int* warp_sums, int n, F count) {
+__device__ void window_offsets(int* off, int* warp_sums, int* taken, int n, F count) {
   constexpr int PER = kWindow / kThreads;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   int c[PER], sum = 0;
@@ -50,7 +51,20 @@ __device__ void window_offsets(int* off, int* warp_sums, int n, F count) {
     base += c[j];
   }
   if (threadIdx.x == kThreads - 1) off[kWindow] = base;
+  if (threadIdx.x == 0) *taken = 0;
   __syncthreads();
+}
+// The warp's next item of the window. A CTA has runs of kRun neighbouring items (the heads of a block:
+// its warps share the block's angles and write neighbouring rows) where there are plenty of items,
+// else single ones, spread over the SMs. Its warps take them as they come free, since blocks hold
+// unlike numbers of tokens.
+__device__ __forceinline__ int64_t next_item(int* taken, int64_t items) {
+  int k = 0;
+  if ((threadIdx.x & 31) == 0) k = atomicAdd(taken, 1);
+  k = __shfl_sync(0xffffffffu, k, 0);
+  return items < (int64_t)gridDim.x * kRun * 4
+             ? (int64_t)k * gridDim.x + blockIdx.x
+             : ((int64_t)(k / kRun) * gridDim.x + blockIdx.x) * kRun + k % kRun;
 }
 // the request k of the window with off[k] <= item < off[k + 1]
 __device__ __forceinline__ int find_request(const int* off, int n, int item) {
@@ -124,26 +138,25 @@ __device__ __forceinline__ uint4 shfl_xor4(const uint4& v, int o) {
 }
 __device__ __forceinline__ uint4 splat(uint32_t x) { return make_uint4(x, x, x, x); }
 
-// Each warp streams its tokens through a ring of kStages groups in shared memory by 16-byte
+// Each warp streams its tokens through a ring of a few groups in shared memory by 16-byte
 // asynchronous copies. A lane reads only what it copied itself, so the ring needs no barrier, and
 // the bytes in flight cost no registers.
-constexpr int kStages = 3;
+constexpr int kAppendStages = 2, kBoundsStages = 3;
 constexpr int kWarps = kThreads / 32;
 
 // A warp's lanes are 32 / L rows: `heads` KV heads beside one another (a power of two), the other
-// rows later tokens of the block. A group is TOK tokens of each row.
-template <typename T>
-constexpr int append_tokens() { return 4 / (int)sizeof(T); }
-template <typename T>
-constexpr int append_smem() { return kWarps * kStages * append_tokens<T>() * 4 * Raw<T>::N * 512; }
+// rows later tokens of the block. A group is TOK tokens of each row: 1 where there are warps enough to
+// hide a group's latency, more where there are few.
+template <typename T, int TOK>
+constexpr int append_smem() { return kWarps * kAppendStages * TOK * 4 * Raw<T>::N * 512; }
 
-template <typename T, int L>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a, int heads,
+template <typename T, int L, int TOK>
+__global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1) kv_append_kernel(rc_kv_append_args a, int heads,
                                                              int* status) {
-  constexpr int N = Raw<T>::N, TOK = append_tokens<T>();
+  constexpr int N = Raw<T>::N;
   extern __shared__ __align__(128) char ring[];
   __shared__ int off[kWindow + 1];
-  __shared__ int warp_sums[kWarps];
+  __shared__ int warp_sums[kWarps], taken;
   const int d = a.head_dim, r = a.rotary_dim;
   const bool inter = a.interleaved != 0;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -153,19 +166,17 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a
   const LaneChunks lc = lane_chunks(i, d, r, inter);
   const T* kw = (const T*)a.k_weight;
   // chunk c (K: 2 N, then V: 2 N) of token u of stage st of this lane
-  char* mine_ring = ring + wid * (kStages * TOK * 4 * N * 512) + lane * 16;
+  char* mine_ring = ring + wid * (kAppendStages * TOK * 4 * N * 512) + lane * 16;
   auto cell_of = [&](int st, int u, int c) { return mine_ring + ((st * TOK + u) * 4 * N + c) * 512; };
 
   for (int b0 = 0; b0 < a.num_reqs; b0 += kWindow) {
     const int nreq = min(kWindow, a.num_reqs - b0);
-    window_offsets(off, warp_sums, nreq, [&](int k) {
+    window_offsets(off, warp_sums, &taken, nreq, [&](int k) {
       const Span s = span_of(a, b0 + k, status, blockIdx.x == 0);
       return s.S ? (s.P + s.S - 1) / a.block - s.P / a.block + 1 : 0;
     });
     const int64_t items = (int64_t)off[kWindow] * head_groups;
-    // neighbouring items go to different CTAs: few items spread over the SMs
-    for (int64_t it = (int64_t)wid * gridDim.x + blockIdx.x; it < items;
-         it += (int64_t)gridDim.x * kWarps) {
+    for (int64_t it = next_item(&taken, items); it < items; it = next_item(&taken, items)) {
       const int job = (int)(it / head_groups), hg = (int)(it - (int64_t)job * head_groups);
       const int k = find_request(off, nreq, job);
       const Span s = span_of(a, b0 + k, status, false);
@@ -181,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a
       const int groups = (n + W * TOK - 1) / (W * TOK);
       auto issue = [&](int gr) {
         if (gr < groups) {
-          const int st = gr % kStages;
+          const int st = gr % kAppendStages;
 #pragma unroll
           for (int u = 0; u < TOK; ++u) {
             const int at = (gr * TOK + u) * W + w;
@@ -203,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a
         cp_async_commit();
       };
 #pragma unroll
-      for (int gr = 0; gr < kStages - 1; ++gr) issue(gr);
+      for (int gr = 0; gr < kAppendStages - 1; ++gr) issue(gr);
       T* cell = (T*)a.bounds +
                 ((((int64_t)s.row * a.max_blocks + blk) * a.num_kv_heads + h) * 2) * d;
       Raw<T> lo0, lo1, hi0, hi1;
@@ -223,18 +234,24 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a
         }
       }
       for (int gr = 0; gr < groups; ++gr) {   // the same count for every lane: shuffles inside
-        issue(gr + kStages - 1);
-        const int st = gr % kStages;
-        LaneAngles ang[TOK];
+        issue(gr + kAppendStages - 1);
+        const int st = gr % kAppendStages;
+        float cs[TOK][8], sn[TOK][8];
         int slot[TOK];
 #pragma unroll
         for (int u = 0; u < TOK; ++u) {
           const int at = (gr * TOK + u) * W + w;
           const bool in = mine && at < n;
           slot[u] = in ? a.out_loc[tok0 + at] : 0;
-          if (lc.rot && in) load_angles(a.rope + (int64_t)(p0 + at) * r, i, r, ang[u]);
+          if (lc.rot && in) {
+            const float* row = a.rope + (int64_t)(p0 + at) * r + 8 * i;
+            ((float4*)cs[u])[0] = ((const float4*)row)[0];
+            ((float4*)cs[u])[1] = ((const float4*)row)[1];
+            ((float4*)sn[u])[0] = ((const float4*)(row + (r >> 1)))[0];
+            ((float4*)sn[u])[1] = ((const float4*)(row + (r >> 1)))[1];
+          }
         }
-        cp_async_wait<kStages - 1>();
+        cp_async_wait<kAppendStages - 1>();
 #pragma unroll
         for (int u = 0; u < TOK; ++u) {
           bool live = mine && (gr * TOK + u) * W + w < n;
@@ -259,17 +276,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a
               ((uint4*)((T*)a.v_pool + dst + lc.c1 * 8))[c] = *(const uint4*)cell_of(st, u, 3 * N + c);
           }
           if (kw || r) {
-            float x[8], y[8];
-            x0.get(x);
-            x1.get(y);
-            if (kw) {
-              const float inv = norm_scale<L>(x, y, d, a.eps);
-              if (m0) scale8(x, inv, kw + lc.c0 * 8);
-              if (m1) scale8(y, inv, kw + lc.c1 * 8);
-            }
-            if (lc.rot) rotate_pairs(x, y, inter, ang[u]);
-            x0.set(x);
-            x1.set(y);
+            ScalarRow row;
+            row.get(x0, x1);
+            if (kw) row.scale(row.template norm_scale<L>(d, a.eps), kw, lc);
+            if (lc.rot) row.rotate(cs[u], sn[u], inter);
+            row.set(x0, x1);
           }
           if (m0 && live) x0.store((T*)a.k_pool + dst + lc.c0 * 8);
           if (m1 && live) x1.store((T*)a.k_pool + dst + lc.c1 * 8);
@@ -313,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(rc_kv_append_args a
 // block. A group is kFly tokens of each. The block's slots are loaded 32 at a time, coalesced, and
 // handed to the lanes by shuffles.
 constexpr int kFly = 8;
-constexpr int kBoundsSmem = kWarps * kStages * kFly * 512;
+constexpr int kBoundsSmem = kWarps * kBoundsStages * kFly * 512;
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_bounds_args a, int cols,
@@ -321,16 +332,16 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
   constexpr int V = 16 / (int)sizeof(T);   // elements of a chunk
   extern __shared__ __align__(128) char ring[];
   __shared__ int off[kWindow + 1];
-  __shared__ int warp_sums[kWarps];
+  __shared__ int warp_sums[kWarps], taken;
   const int d = a.head_dim;
   const int chunks = a.num_kv_heads * d / V;
   const int col_groups = (chunks + cols - 1) / cols;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int cl = lane & (cols - 1), w = lane / cols, W = 32 / cols;
-  char* mine_ring = ring + wid * (kStages * kFly * 512) + lane * 16;
+  char* mine_ring = ring + wid * (kBoundsStages * kFly * 512) + lane * 16;
   for (int b0 = 0; b0 < a.num_rows; b0 += kWindow) {
     const int nreq = min(kWindow, a.num_rows - b0);
-    window_offsets(off, warp_sums, nreq, [&](int k) {
+    window_offsets(off, warp_sums, &taken, nreq, [&](int k) {
       const int L = a.seq_len[b0 + k], row = a.req_idx[b0 + k];
       if (L < 0 || L > a.max_ctx || row < 0 || row >= a.max_reqs ||
           (L - 1) / a.block >= a.max_blocks) {
@@ -341,8 +352,7 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
     });
     const int64_t per_layer = (int64_t)off[kWindow] * col_groups;
     const int64_t items = per_layer * a.num_layers;
-    for (int64_t it = (int64_t)wid * gridDim.x + blockIdx.x; it < items;
-         it += (int64_t)gridDim.x * kWarps) {
+    for (int64_t it = next_item(&taken, items); it < items; it = next_item(&taken, items)) {
       const int64_t layer = it / per_layer;
       const int64_t rest = it - layer * per_layer;
       const int job = (int)(rest / col_groups), cg = (int)(rest - (int64_t)job * col_groups);
@@ -356,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
       const char* kp = (const char*)a.k_pool +
                        ((layer * a.num_slots * chunks) + (mine ? c : 0)) * 16;
       int slots = -1;   // of tokens 32 j + lane, -1: nothing to read
-      uint32_t have = 0;   // bit u of group gr at gr % kStages * kFly: this lane copied a token
+      uint32_t have = 0;   // bit u of group gr at gr % kBoundsStages * kFly: this lane copied a token
       const int groups = (n + W * kFly - 1) / (W * kFly);
       auto issue = [&](int gr) {
         if (gr < groups) {
@@ -368,7 +378,7 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
               slots = -1;
             }
           }
-          const int st = gr % kStages;
+          const int st = gr % kBoundsStages;
 #pragma unroll
           for (int u = 0; u < kFly; ++u) {
             const int at = (gr * kFly + u) * W + w;
@@ -385,12 +395,12 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
         cp_async_commit();
       };
 #pragma unroll
-      for (int gr = 0; gr < kStages - 1; ++gr) issue(gr);
+      for (int gr = 0; gr < kBoundsStages - 1; ++gr) issue(gr);
       uint4 lo = splat(Extremes<T>::kLo), hi = splat(Extremes<T>::kHi);
       for (int gr = 0; gr < groups; ++gr) {
-        issue(gr + kStages - 1);
-        cp_async_wait<kStages - 1>();
-        const int st = gr % kStages;
+        issue(gr + kBoundsStages - 1);
+        cp_async_wait<kBoundsStages - 1>();
+        const int st = gr % kBoundsStages;
 #pragma unroll
         for (int u = 0; u < kFly; ++u) {
           if (have >> (st * kFly + u) & 1) {
@@ -450,15 +460,27 @@ int pow2_at_least(int x) {
 }
 
 template <typename T, int L>
-int launch_append(const char* fn, const rc_kv_append_args& a, int* st, cudaStream_t s) {
-  // single tokens: every row of a warp a head; prompts: one head, tokens of its block beside one another
+int launch_append(const char* fn, const rc_kv_append_args& args, int* st, cudaStream_t s) {
+  rc_kv_append_args a = args;
+  int sms = 0;
+  const int e = sm_count(fn, &sms);
+  if (e != RC_OK) return e;
+  // single tokens: every row of a warp a head; prompts: one head, tokens of its block beside one
+  // another
   const bool prompts = a.num_tokens >= 16 * (int64_t)a.num_reqs;
   const int heads = std::min(pow2_at_least(a.num_kv_heads), prompts ? std::max(1, 8 / L) : 32 / L);
+  const int groups = (a.num_kv_heads + heads - 1) / heads;
+  const bool few = a.num_tokens / a.block * groups < (int64_t)sms * 8 * 2;
+  if (!a.bounds && few) a.block = 16;   // without bounds an item is any run of tokens
   // blocks the tokens can touch: each request begins and ends inside at most two more
-  const int64_t items = (a.num_tokens / a.block + 2 * (int64_t)a.num_reqs) *
-                        ((a.num_kv_heads + heads - 1) / heads);
-  static PerDevice<int> setup;
-  return launch_resident(fn, kv_append_kernel<T, L>, setup, items, a, heads, append_smem<T>(), st, s);
+  const int64_t items = (a.num_tokens / a.block + 2 * (int64_t)a.num_reqs) * groups;
+  static PerDevice<int> one, more;
+  constexpr int kMore = 8 / (int)sizeof(T);   // as many as the ring has room for
+  if (prompts && few)
+    return launch_resident(fn, kv_append_kernel<T, L, kMore>, more, items, a, heads,
+                           append_smem<T, kMore>(), st, s);
+  return launch_resident(fn, kv_append_kernel<T, L, 1>, one, items, a, heads, append_smem<T, 1>(), st,
+                         s);
 }
 
 template <typename T>

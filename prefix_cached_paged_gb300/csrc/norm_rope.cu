@@ -2,9 +2,10 @@
 //   y = x * rsqrt(mean(x^2) + eps) * w   per head row,   then (a, b) -> (a cos - b sin, b cos + a sin)
 // in fp32, rounded once at the store.
 //
-// One group of L lanes per (token, head) row (norm_rope.cuh). A CTA works on heads of one token, so
-// the token's cosines and sines are loaded once per lane and serve every head the lane works on;
-// the loads of kBatch heads are in flight together.
+// A warp works on the heads of one token, 32 / L head rows (norm_rope.cuh) at a time, so the token's
+// cosines and sines are loaded once per lane and serve every head. Rows stream through a ring in
+// shared memory by 16-byte asynchronous copies; a lane reads only what it copied itself, so the
+// ring needs no barrier.
 #include <algorithm>
 #include <cmath>
 
@@ -14,78 +15,100 @@
 namespace rc {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kBatch = 2;   // heads a lane group holds at a time
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kStages = 4;   // row groups of a warp in flight
 
-// splits CTAs per token, each with every splits-th group of kBatch * kThreads / L heads
-template <typename T, int L, int NB>
+// splits warps per token, each with consecutive groups of 32 / L heads (queries, then keys)
+template <typename T, int L>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(rc_qk_norm_rope_args a, int splits,
                                                                 int* status) {
-  constexpr int ROWS = kThreads / L;
-  const int64_t t = blockIdx.x / splits;
-  const int split = blockIdx.x - (int)t * splits;
-  const int i = threadIdx.x % L;
-  const int r = a.rotary_dim;
+  constexpr int ROWS = 32 / L, N = Raw<T>::N;
+  __shared__ uint4 ring[kWarps][kStages][2 * N][32];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int64_t gw = (int64_t)blockIdx.x * kWarps + wid;
+  const int64_t t = gw / splits;
+  if (t >= a.num_tokens) return;
+  const int i = lane % L, r = a.rotary_dim;
   const bool inter = a.interleaved != 0;
   const LaneChunks lc = lane_chunks(i, a.head_dim, r, inter);
-  const int pos = r ? a.positions[t] : 0;
   const int rows = a.num_q_heads + a.num_kv_heads;
-  LaneAngles ang;
-  bool have_angles = false;
-  for (int h0 = split * ROWS * NB + threadIdx.x / L; h0 - (int)threadIdx.x / L < rows;
-       h0 += splits * ROWS * NB) {
-    Raw<T> x[NB], y[NB];
+  const int groups = (rows + ROWS - 1) / ROWS, per = (groups + splits - 1) / splits;
+  const int g0 = (int)(gw - t * splits) * per, g1 = min(groups, g0 + per);
+  const T* q = (const T*)a.q + t * a.q_token_stride;
+  const T* k = (const T*)a.k + t * a.k_token_stride;
+  T* qo = (T*)a.q_out + t * a.q_out_token_stride;
+  T* ko = (T*)a.k_out + t * a.k_out_token_stride;
+  auto issue = [&](int g) {
+    const int h = g * ROWS + lane / L;
+    if (g < g1 && h < rows) {
+      const T* src = h < a.num_q_heads ? q + h * a.q_head_stride
+                                       : k + (h - a.num_q_heads) * a.k_head_stride;
+      uint4(*st)[32] = ring[wid][g % kStages];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int h = h0 + b * ROWS;
-      const bool is_q = h < a.num_q_heads;
-      const int64_t hh = is_q ? h : h - a.num_q_heads;
-      const T* src = is_q ? (const T*)a.q + t * a.q_token_stride + hh * a.q_head_stride
-                          : (const T*)a.k + t * a.k_token_stride + hh * a.k_head_stride;
-      x[b].clear();
-      y[b].clear();
-      if (h < rows && lc.c0 >= 0) x[b].load(src + lc.c0 * 8);
-      if (h < rows && lc.c1 >= 0) y[b].load(src + lc.c1 * 8);
-    }
-    if (r && !have_angles) {
-      if (pos < 0 || pos >= a.max_position) {   // the same for the whole CTA
-        if (threadIdx.x == 0) set_status(status, kStatusPosRange);
-        return;
+      for (int c = 0; c < N; ++c) {
+        if (lc.c0 >= 0) cp_async16(smem_u32(&st[c][lane]), (const uint4*)(src + lc.c0 * 8) + c);
+        if (lc.c1 >= 0) cp_async16(smem_u32(&st[N + c][lane]), (const uint4*)(src + lc.c1 * 8) + c);
       }
-      if (lc.rot) load_angles(a.rope + (int64_t)pos * r, i, r, ang);
-      have_angles = true;
     }
+    cp_async_commit();
+  };
+  const int pos = r ? a.positions[t] : 0;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int h = h0 + b * ROWS;
-      const bool is_q = h < a.num_q_heads;
-      const int64_t hh = is_q ? h : h - a.num_q_heads;
-      T* dst = is_q ? (T*)a.q_out + t * a.q_out_token_stride + hh * a.q_out_head_stride
-                    : (T*)a.k_out + t * a.k_out_token_stride + hh * a.k_out_head_stride;
-      const T* w = (const T*)(is_q ? a.q_weight : a.k_weight);
-      const bool v0 = h < rows && lc.c0 >= 0, v1 = h < rows && lc.c1 >= 0;
-      float u[8], v[8];
-      x[b].get(u);
-      y[b].get(v);
-      const float inv = norm_scale<L>(u, v, a.head_dim, a.eps);
-      if (w && v0) scale8(u, inv, w + lc.c0 * 8);
-      if (w && v1) scale8(v, inv, w + lc.c1 * 8);
-      if (lc.rot) rotate_pairs(u, v, inter, ang);
-      if (v0) store8(dst + lc.c0 * 8, u);
-      if (v1) store8(dst + lc.c1 * 8, v);
+  for (int s = 0; s < kStages - 1; ++s) issue(g0 + s);
+  LaneAngles ang;
+  if (r) {
+    if (pos < 0 || pos >= a.max_position) {   // the same for the whole warp
+      if (lane == 0) set_status(status, kStatusPosRange);
+      cp_async_wait<0>();
+      return;
     }
+    if (lc.rot) ang.load(a.rope + (int64_t)pos * r, i, r);
   }
+  LaneRow w;
+  int part = -1;   // whose weights w holds: 0 queries', 1 keys'
+  for (int g = g0; g < g1; ++g) {
+    issue(g + kStages - 1);
+    cp_async_wait<kStages - 1>();
+    const int h = g * ROWS + lane / L;
+    const int mine = h < a.num_q_heads ? 0 : 1;
+    const bool v0 = h < rows && lc.c0 >= 0, v1 = h < rows && lc.c1 >= 0;
+    const T* weights = (const T*)(mine ? a.k_weight : a.q_weight);
+    if (mine != part && weights) load_weights(weights, lc, w);
+    part = mine;
+    Raw<T> x, y;
+    x.clear();
+    y.clear();
+    uint4(*st)[32] = ring[wid][g % kStages];
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      if (v0) x.v[c] = st[c][lane];
+      if (v1) y.v[c] = st[N + c][lane];
+    }
+    LaneRow row;
+    x.get(row.x);
+    y.get(row.y);
+    const float inv = row.template norm_scale<L>(a.head_dim, a.eps);
+    if (weights) row.scale(inv, w);
+    if (lc.rot) row.rotate(ang, inter);
+    x.set(row.x);
+    y.set(row.y);
+    T* dst = mine ? ko + (h - a.num_q_heads) * a.k_out_head_stride : qo + h * a.q_out_head_stride;
+    if (v0) x.store(dst + lc.c0 * 8);
+    if (v1) y.store(dst + lc.c1 * 8);
+  }
+  cp_async_wait<0>();
 }
 
 template <typename T, int L>
 void launch_l(const rc_qk_norm_rope_args& a, int sms, int* st, cudaStream_t s) {
-  // with few tokens the heads of one go to several CTAs, one batch of one head each
-  const int rows = a.num_q_heads + a.num_kv_heads;
-  const int groups = (rows + kThreads / L - 1) / (kThreads / L);
-  if (a.num_tokens * groups <= (int64_t)sms * 8)
-    qk_norm_rope_kernel<T, L, 1><<<(unsigned)(a.num_tokens * groups), kThreads, 0, s>>>(a, groups, st);
-  else
-    qk_norm_rope_kernel<T, L, kBatch><<<(unsigned)a.num_tokens, kThreads, 0, s>>>(a, 1, st);
+  // one warp per token where that fills the GPU eight times over; with fewer tokens their heads go
+  // to more warps, down to one group of heads each
+  const int groups = (a.num_q_heads + a.num_kv_heads + 32 / L - 1) / (32 / L);
+  int splits = 1;
+  while (splits < groups && a.num_tokens * splits < (int64_t)sms * kWarps * 16) splits *= 2;
+  splits = std::min(splits, groups);
+  const int64_t ctas = (a.num_tokens * splits + kWarps - 1) / kWarps;
+  qk_norm_rope_kernel<T, L><<<(unsigned)ctas, kThreads, 0, s>>>(a, splits, st);
 }
 
 template <typename T>
@@ -133,7 +156,7 @@ extern "C" int rc_qk_norm_rope(const rc_qk_norm_rope_args* a, void* stream) {
   static const char* fn = "rc_qk_norm_rope";
   RC_CHECK_ARG(a != nullptr, "%s: args is NULL", fn);
   RC_CHECK_ARG(a->dtype == RC_DTYPE_BF16 || a->dtype == RC_DTYPE_F32, "%s: dtype %d", fn, a->dtype);
-  RC_CHECK_ARG(a->num_tokens >= 0 && a->num_tokens <= 0x7fffffff && a->num_q_heads >= 0 &&
+  RC_CHECK_ARG(a->num_tokens >= 0 && a->num_tokens <= (1 << 24) && a->num_q_heads >= 0 &&
                    a->num_kv_heads >= 0 && a->num_q_heads <= 65536 && a->num_kv_heads <= 65536,
                "%s: bad sizes", fn);
   const int c = rc::check_norm_rope(fn, a->head_dim, a->rotary_dim, a->max_position, a->rope, a->eps,
