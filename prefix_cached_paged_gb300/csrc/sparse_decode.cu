@@ -67,9 +67,9 @@ constexpr int kBins = 2048;        // counters of the selection's radix steps
 template <typename T, int D, int GM>
 struct Cfg {
   static constexpr bool kBf16 = sizeof(T) == 2;
-  static constexpr int TOK = 16, STAGES = 2;                  // a warp's ring: stages of 16 tokens
+  static constexpr int TOK = 16, STAGES = 3;                  // a warp's ring: K or V of 16 tokens
   static constexpr int RB = D * 2, RS = RB + 16;              // bytes of a row, padded
-  static constexpr int STAGE = TOK * 2 * RS;
+  static constexpr int STAGE = TOK * RS;
   static constexpr int STATE = GM * D * 4;                    // o of one state
   static constexpr int RING = kBf16 ? kWarps * STAGES * STAGE : (kWarps + 1) * STATE;
   static constexpr int BASE = RING > 36864 ? RING : 36864;
@@ -605,6 +605,9 @@ struct AttendMma {
   uint32_t qb[NT][KS][2];
   float acc[NT][KS][4], m[NT][2], l[NT][2];
 
+  static __device__ __forceinline__ int next1(int b) { return b == 2 ? 0 : b + 1; }
+  static __device__ __forceinline__ int next2(int b) { return b == 0 ? 2 : b - 1; }
+
   __device__ __forceinline__ void begin(const Params& p, int64_t n, int g) {
     const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
 #pragma unroll
@@ -633,30 +636,35 @@ struct AttendMma {
     const int64_t slot_bytes = (int64_t)p.a.num_kv_heads * C::RB;
     constexpr int CPR = C::RB / 16, RPI = 32 / CPR;   // copies per row, rows per copy step
     const int cc = (lane % CPR) * 16, rsub = lane / CPR;
-    auto issue = [&](int s, int buf) {
-      const uint32_t kd = ring + buf * C::STAGE + cc;
+    // the stream of a warp: K of its first tokens, their V, K of the next ones, .. (half h: stage
+    // wid + 4 (h / 2), K or V), three halves in flight or in use
+    const int stages = (n + C::TOK - 1) / C::TOK;
+    auto issue = [&](int h, int buf) {
+      const int s = wid + (h >> 1) * kWarps;
+      if (s < stages) {
+        const char* src = h & 1 ? vp : kp;
+        const uint32_t dst = ring + buf * C::STAGE + cc;
 #pragma unroll
-      for (int i = 0; i < C::TOK / RPI; ++i) {
-        const int t = i * RPI + rsub, at = s * C::TOK + t;
-        const int slot = at < n ? slots[at] : -1;
-        const int64_t off = (int64_t)max(slot, 0) * slot_bytes + cc;
-        cp_async16_or_zero(kd + t * C::RS, kp + off, slot >= 0);
-        cp_async16_or_zero(kd + (C::TOK + t) * C::RS, vp + off, slot >= 0);
+        for (int i = 0; i < C::TOK / RPI; ++i) {
+          const int t = i * RPI + rsub, at = s * C::TOK + t;
+          const int slot = at < n ? slots[at] : -1;
+          cp_async16_or_zero(dst + t * C::RS, src + (int64_t)max(slot, 0) * slot_bytes + cc,
+                             slot >= 0);
+        }
       }
+      cp_async_commit();
     };
     const float qscale = p.a.sm_scale * kLog2e;
     const int k_row = (lane & 7) + ((lane >> 3) & 1) * 8, k_col = (lane >> 4) * 8;
     const int v_row = (lane & 7) + (lane >> 4) * 8, v_col = ((lane >> 3) & 1) * 8;
-    const int stages = (n + C::TOK - 1) / C::TOK;
-    if (wid < stages) issue(wid, 0);
-    cp_async_commit();
-    int buf = 0;
-    for (int s = wid; s < stages; s += kWarps, buf ^= 1) {
-      if (s + kWarps < stages) issue(s + kWarps, buf ^ 1);
-      cp_async_commit();
-      cp_async_wait<1>();
+    issue(0, 0);
+    issue(1, 1);
+    int buf = 0;   // of K; V is in the next one
+    for (int s = wid, h = 0; s < stages; s += kWarps, h += 2, buf = next2(buf)) {
+      issue(h + 2, next2(buf));
+      cp_async_wait<2>();
       __syncwarp();
-      const uint32_t kb = ring + buf * C::STAGE, vb = kb + C::TOK * C::RS;
+      const uint32_t kb = ring + buf * C::STAGE, vb = ring + next1(buf) * C::STAGE;
       float sc[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
@@ -668,6 +676,8 @@ struct AttendMma {
         for (int t = 0; t < NT; ++t)
           mma_bf16(sc[t], r[0], r[1], r[2], r[3], qb[t][k][0], qb[t][k][1]);
       }
+      __syncwarp();   // K is used up: its place takes the next V
+      issue(h + 3, buf);
       const int at = s * C::TOK + gid;
       const bool ok0 = at < n && slots[at] >= 0, ok1 = at + 8 < n && slots[at + 8] >= 0;
       uint32_t ph[NT][2], pl[NT][2];
@@ -704,6 +714,8 @@ struct AttendMma {
         pl[t][0] = movmatrix_trans(pack2_bf16(sc[t][0] - bf16lo(hx), sc[t][1] - bf16hi(hx)));
         pl[t][1] = movmatrix_trans(pack2_bf16(sc[t][2] - bf16lo(hy), sc[t][3] - bf16hi(hy)));
       }
+      cp_async_wait<2>();
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         uint32_t r[4];
@@ -1014,12 +1026,12 @@ Params params_of(const rc_sparse_decode_args* a) {
   p.G = a->num_q_heads / a->num_kv_heads;
   p.nb = std::max(1, (a->max_seq_len + a->block - 1) / a->block);
   // CTAs per unit: until the GPU is full, while each still has a stage for every warp; with more
-  // units, until a CTA's part is at most 1024 tokens, so that the last wave of CTAs stays short
+  // units, until a CTA's part is at most 2048 tokens, so that the last wave of CTAs stays short
   const int64_t units = (int64_t)a->num_rows * a->num_kv_heads;
   const int64_t tokens = (int64_t)std::min(p.nb, a->top_blocks) * a->block;
   p.cluster = 1;
   while (p.cluster < kMaxCluster && tokens >= 128 * p.cluster &&
-         (units * p.cluster < kEnoughCtas || tokens > 1024 * p.cluster))
+         (units * p.cluster < kEnoughCtas || tokens > 2048 * p.cluster))
     p.cluster *= 2;
   return p;
 }
