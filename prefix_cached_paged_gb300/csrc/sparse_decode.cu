@@ -96,6 +96,9 @@ __device__ __forceinline__ uint32_t order32(float s) {
   const int b = __float_as_int(s + 0.f);   // -0 ranks as 0
   return (uint32_t)(b < 0 ? ~b : (b | (1 << 31)));
 }
+__device__ __forceinline__ float unorder32(uint32_t o) {
+  return __uint_as_float(o & (1u << 31) ? o & ~(1u << 31) : ~o);
+}
 __device__ __forceinline__ unsigned long long order64(double s) {
   if (!(s < 1.7976931348623157e308)) s = 1.7976931348623157e308;   // NaN, +inf
   if (s < -1.7976931348623157e308) s = -1.7976931348623157e308;
@@ -268,6 +271,24 @@ __device__ __forceinline__ void block_sum2(SelectShared& s, int& x, int& y) {
   }
 }
 
+// put(place, i) for every i < n for which is(i), in no particular order; `count` places are taken
+// after. The whole CTA; few i are expected, so a warp asks for places only where it has one.
+template <typename Is, typename Put>
+__device__ __forceinline__ void list_those(int& count, int n, Is is, Put put) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int i0 = threadIdx.x & ~31; i0 < n; i0 += kThreads) {
+    const bool yes = i0 + lane < n && is(i0 + lane);
+    const unsigned all = __ballot_sync(0xffffffffu, yes);
+    if (all) {
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&count, __popc(all));
+      at = __shfl_sync(0xffffffffu, at, 0);
+      if (yes) put(at + __popc(all & ((1u << lane) - 1)), i0 + lane);
+    }
+  }
+}
+
 // The k-th largest (k >= 1) of the values key(i), i < n, for which ok(i), all between lo and hi;
 // there are at least k, and `left` at most. Radix steps of 11 bits, beginning below the digits that
 // lo and hi share, until at most one key per thread is left, whose ranks are counted: one step,
@@ -283,13 +304,12 @@ __device__ K kth_largest(SelectShared& s, int* hist, int n, int left, int k, K l
     if (left <= kThreads) {
       if (tid == 0) s.listed = 0;
       __syncthreads();
-#pragma unroll 4
-      for (int i = tid; i < n; i += kThreads) {
-        if (!ok(i)) continue;
-        const K x = key(i);
-        if (shift == kBits || (x >> shift) == (prefix >> shift))
-          s.list[atomicAdd(&s.listed, 1)] = x;
-      }
+      list_those(
+          s.listed, n,
+          [&](int i) {
+            return ok(i) && (shift == kBits || (key(i) >> shift) == (prefix >> shift));
+          },
+          [&](int at, int i) { s.list[at] = key(i); });
       __syncthreads();
       const int c = s.listed;
       if (tid < c) {
@@ -397,15 +417,16 @@ __device__ __noinline__ unsigned long long exact_rank(const Params& p, int64_t n
 // in Ogita, Rump and Oishi, "Accurate sum and dot product", 2005). The errors' own sum is fp32: at
 // most 512 addends, each at most 2^-24 of the partial sums of a tree of depth 13, so what is lost is
 // below 512 * 13 * 2^-48 * t < 2^-35 * t. Far cheaper than doubles, of which an SM adds two a clock.
-constexpr double kFineError = 0x1p-34;
+constexpr float kFineError = 0x1p-34f;
 __device__ __forceinline__ void two_sum(float& s, float& err, float b) {
   const float a = s;
   s = __fadd_rn(a, b);
   const float bb = __fsub_rn(s, a);
   err = __fadd_rn(err, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb)));
 }
+// Returned as an integer of the same order: the sum's fp32 value, then what that lacks.
 template <typename T, int D>
-__device__ __forceinline__ double fine_score(const Params& p, int64_t n, int g, int b) {
+__device__ __forceinline__ unsigned long long fine_score(const Params& p, int64_t n, int g, int b) {
   constexpr int E = D / 32, H = 4;
   const rc_sparse_decode_args& a = p.a;
   const int lane = threadIdx.x & 31;
@@ -418,7 +439,7 @@ __device__ __forceinline__ double fine_score(const Params& p, int64_t n, int g, 
     lo[e] = Elem<T>::to_f(box[e * 32]);
     hi[e] = Elem<T>::to_f(box[D + e * 32]);
   }
-  double best = -INFINITY;
+  unsigned long long best = 0;
   for (int h0 = 0; h0 < p.G; h0 += H) {
     float s[H], c[H];
 #pragma unroll
@@ -443,8 +464,12 @@ __device__ __forceinline__ double fine_score(const Params& p, int64_t n, int g, 
       }
     }
 #pragma unroll
-    for (int h = 0; h < H; ++h)
-      if (h0 + h < p.G) best = fmax(best, (double)s[h] + (double)c[h]);
+    for (int h = 0; h < H; ++h) {
+      float err = 0.f;
+      two_sum(s[h], err, c[h]);
+      if (h0 + h < p.G)
+        best = max(best, (unsigned long long)order32(s[h]) << 32 | order32(err));
+    }
   }
   return best;
 }
@@ -513,7 +538,7 @@ __device__ __forceinline__ void select_blocks(const Params& p, SelectShared& sh,
     const uint32_t thr = kth_largest<uint32_t>(
         sh, hist, m, m, k, sh.lo, sh.hi, [&](int i) { return order32(score[i]); },
         [](int) { return true; });
-    const float ts = __uint_as_float(thr & (1u << 31) ? thr & ~(1u << 31) : ~thr);
+    const float ts = unorder32(thr);
     // (1 % for the roundings of these lines; products below the smallest normal number may be lost)
     const float e2 = 2.02f * kScoreError * tmax + 0x1p-110f;
     hi_s = ts + e2;
@@ -533,31 +558,29 @@ __device__ __forceinline__ void select_blocks(const Params& p, SelectShared& sh,
   if (kOwn && !clear && close <= kThreads && !all64) {
     if (tid == 0) sh.listed = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int i = tid; i < m; i += kThreads)
-      if (near(i)) sh.index[atomicAdd(&sh.listed, 1)] = i;
+    list_those(sh.listed, m, near, [&](int at, int i) { sh.index[at] = i; });
     __syncthreads();
     for (int c = wid; c < close; c += kWarps) {
-      const double f = fine_score<T, D>(p, n, g, f0 + sh.index[c]);
-      if (lane == 0) sh.list[c] = (unsigned long long)__double_as_longlong(f);
+      const unsigned long long f = fine_score<T, D>(p, n, g, f0 + sh.index[c]);
+      if (lane == 0) sh.list[c] = f;
     }
     __syncthreads();
-    const double f = tid < close ? __longlong_as_double((long long)sh.list[tid]) : 0.0;
+    const unsigned long long f = tid < close ? sh.list[tid] : 0;
     if (tid < close) {
       int above = 0, equal = 0;
       for (int c = 0; c < close; ++c) {
-        const double x = __longlong_as_double((long long)sh.list[c]);
-        above += x > f;
-        equal += x == f;
+        above += sh.list[c] > f;
+        equal += sh.list[c] == f;
       }
-      if (above < rest && above + equal >= rest) sh.kth = (unsigned long long)__double_as_longlong(f);
+      if (above < rest && above + equal >= rest) sh.kth = f;
     }
     __syncthreads();
-    const double t = __longlong_as_double((long long)sh.kth);
-    const double w = 2.0 * kFineError * tmax + 0x1p-120;
-    int take = tid < close && f >= t - w, unused = 0;
-    const bool mine = take;
-    block_sum2(sh, take, unused);
+    // how far above the least one taken
+    const float d = __fadd_rn(__fsub_rn(unorder32(f >> 32), unorder32(sh.kth >> 32)),
+                              __fsub_rn(unorder32((uint32_t)f), unorder32((uint32_t)sh.kth)));
+    const float w = 2.02f * kFineError * tmax + 0x1p-120f;
+    const bool mine = tid < close && d >= -w;
+    const int take = __syncthreads_count(mine);
     if (take == rest) {   // no block left out is as near as the error bound
       if (tid < close) score[sh.index[tid]] = mine ? INFINITY : -INFINITY;
       __syncthreads();
