@@ -552,7 +552,8 @@ int rc_rope_table(const double* inv_freq, int32_t num_pairs, int64_t first_posit
  * block of positions that the new tokens begin gets the bounds of their stored keys, a block that
  * tokens before prefix_len[b] began takes the minimum and maximum with what it holds. Rows of one
  * call are distinct. A request outside the arrays, its row's blocks or the table sets the device
- * status word and is skipped; so is a token whose slot is outside the pool.
+ * status word and is skipped; so is a token whose slot is outside the pool. A request without new
+ * tokens is passed over, whatever its prefix_len and req_idx.
  * k, v [T, Hkv, d] with strides in elements, heads' elements contiguous; head_dim, rotary_dim and
  * alignment as for rc_qk_norm_rope. */
 typedef struct rc_kv_append_args {
@@ -591,7 +592,8 @@ int rc_kv_append(const rc_kv_append_args* args, void* stream);
  *   bounds[layer][req_idx[n]][blk][h][0][e] = min_p k_pool[layer][req_to_token[req_idx[n]][p]][h][e]
  *   bounds[..][1][e]                        = max_p ...
  * bounds [num_layers, max_reqs, max_blocks, Hkv, 2, d] in dtype; other entries are not written.
- * k_pool [num_layers, num_slots, Hkv, d]. A row outside the table or the bounds sets the device
+ * k_pool [num_layers, num_slots, Hkv, d]. A req_idx given twice has one seq_len. A row of length 0 is
+ * passed over, whatever its req_idx. A row outside the table or the bounds sets the device
  * status word and is skipped; so is a token whose slot is outside the pool. max_ctx <= 2^24. */
 typedef struct rc_kv_block_bounds_args {
   int32_t dtype;
@@ -628,9 +630,10 @@ int rc_kv_block_bounds(const rc_kv_block_bounds_args* args, void* stream);
  *             (optional); selected [num_rows, Hkv, top_blocks] int32 (optional): block numbers in
  *             ascending order, then -1.
  * A request may have several rows (a chunk of new tokens: rows of growing seq_len). A row with
- * seq_len 0 gets o = 0, lse = -inf, selected = -1; so does a row whose seq_len or req_idx is out of
+ * seq_len 0 (its req_idx is not read) gets o = 0, lse = -inf, selected = -1; so does a row whose seq_len or req_idx is out of
  * range, which also sets the device status word. A slot outside the pool sets it and that token
- * weighs nothing. sm_scale > 0; Hq / Hkv <= 16; head_dim 64 or 128; tensors 16-byte aligned. */
+ * weighs nothing. sm_scale > 0; Hq / Hkv <= 16; head_dim 64 or 128; max_seq_len <= 2^24, top_blocks
+ * <= 8192; tensors 16-byte aligned. */
 typedef struct rc_sparse_decode_args {
   int32_t dtype;
   int32_t num_rows;
@@ -658,8 +661,9 @@ typedef struct rc_sparse_decode_args {
   float* lse;
   int32_t* selected;
 } rc_sparse_decode_args;
-/* Workspace bytes for these sizes (device memory, 16-byte aligned, no initialisation needed). Calls
- * that may overlap on the GPU need a workspace each. */
+/* Workspace bytes for these sizes (device memory, 16-byte aligned, no initialisation needed): 0, and
+ * no workspace, unless max_seq_len is more than 2304 blocks. Calls that may overlap on the GPU need a
+ * workspace each. */
 int rc_sparse_decode_workspace_bytes(const rc_sparse_decode_args* args, size_t* out_bytes);
 int rc_sparse_decode_attention(const rc_sparse_decode_args* args, void* workspace,
                                size_t workspace_bytes, void* stream);

@@ -89,9 +89,10 @@ __device__ __forceinline__ Span span_of(const rc_kv_append_args& a, int b, int* 
   s.S = a.qo_indptr[b + 1] - s.t0;
   s.P = a.prefix_len[b];
   s.row = a.bounds ? a.req_idx[b] : 0;
+  if (s.S == 0) return s;   // nothing to do, whatever the rest says (a padded batch)
   bool ok = s.t0 >= 0 && s.S >= 0 && (int64_t)s.t0 + s.S <= a.num_tokens && s.P >= 0 &&
             (int64_t)s.P + s.S <= 0x7fffffff;
-  if (ok && s.S > 0) {
+  if (ok) {
     const int64_t last = (int64_t)s.P + s.S - 1;
     if (a.rotary_dim && last >= a.max_position) ok = false;
     if (a.bounds && (s.row < 0 || s.row >= a.max_reqs || last / a.block >= a.max_blocks)) ok = false;
@@ -343,6 +344,7 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
     const int nreq = min(kWindow, a.num_rows - b0);
     window_offsets(off, warp_sums, &taken, nreq, [&](int k) {
       const int L = a.seq_len[b0 + k], row = a.req_idx[b0 + k];
+      if (L == 0) return 0;
       if (L < 0 || L > a.max_ctx || row < 0 || row >= a.max_reqs ||
           (L - 1) / a.block >= a.max_blocks) {
         if (blockIdx.x == 0) set_status(status, kStatusPosRange);

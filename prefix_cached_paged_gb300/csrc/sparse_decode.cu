@@ -50,9 +50,11 @@ struct Params {
   int* status;
 };
 
-// Visible tokens of row n; 0 for an empty row, and for one with bad data (recorded).
+// Visible tokens of row n; 0 for an empty row (whatever its req_idx: a padded batch), and for one
+// with bad data (recorded).
 __device__ __forceinline__ int row_len(const Params& p, int64_t n, bool report) {
   const int L = p.a.seq_len[n], row = p.a.req_idx[n];
+  if (L == 0) return 0;
   if (L < 0 || L > p.a.max_seq_len || row < 0 || row >= p.a.max_reqs) {
     if (report) set_status(p.status, kStatusPosRange);
     return 0;
@@ -1145,6 +1147,8 @@ extern "C" int rc_sparse_decode_attention(const rc_sparse_decode_args* a, void* 
                        (uintptr_t)a->bounds | (uintptr_t)a->o | (uintptr_t)workspace;
   RC_CHECK_ARG((al & 15) == 0, "%s: tensors and workspace must be 16-byte aligned", fn);
   rc::Params p = rc::params_of(a);
+  RC_CHECK_ARG((int64_t)a->num_rows * a->num_kv_heads * p.cluster < (1ll << 31), "%s: too many rows",
+               fn);
   size_t need = 0;
   p.w = rc::carve(workspace, p, &need);
   RC_CHECK_ARG(need == 0 || (workspace && workspace_bytes >= need),

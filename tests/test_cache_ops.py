@@ -343,6 +343,9 @@ def test_append_skips_bad_requests_and_slots():
         assert (vp[4:8] == 0).all() and (kp[4:8] == 0).all() and (bd[1] == 9.0).all(), kind
         for s in (slice(0, 4), slice(8, 12)):
             assert torch.equal(kp[s], good[0][s]) and torch.equal(vp[s], good[1][s]), kind
+    # a request without new tokens is passed over, whatever the rest of it says
+    kp, vp, bd, st = run(loc, [0, 4, 4, 12], [0, -7, 0], [0, 99, 2])
+    assert st == 0 and torch.equal(vp[4:12], x[4:12].cpu())
     # offsets that run backwards or past the tokens
     kp, vp, bd, st = run(loc, [0, 4, 2, 12], [0, 0, 0], [0, 1, 2])
     assert st == 2 and (bd[1] == 9.0).all()
@@ -389,6 +392,46 @@ def test_append_strides_graph_and_refusals():
     for bad in (dict(k=k.float()), dict(out_loc=loc.long()), dict(bounds=bd.float(), req_idx=pl)):
         with pytest.raises(TypeError):
             rc.kv_append(**{**ok, **bad})
+
+
+@pytest.mark.gpu
+def test_first_calls_of_a_process_may_be_captured():
+    """A fresh process whose first call of each operator is inside a graph capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, prefix_cached_paged_gb300 as rc
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+T, hkv, d = 40, 2, 128
+q = torch.randn((T, 4, d), device="cuda").bfloat16(); k = torch.randn((T, hkv, d), device="cuda").bfloat16()
+w = torch.ones(d, device="cuda").bfloat16()
+t = torch.from_numpy(rc.rope_table([0.5] * 64, 64)).cuda()
+kp = torch.zeros((64, hkv, d), device="cuda").bfloat16(); vp = torch.zeros_like(kp)
+bd = torch.zeros((1, 4, hkv, 2, d), device="cuda").bfloat16(); b2 = torch.zeros_like(bd)
+table = torch.arange(64, dtype=torch.int32, device="cuda")[None].contiguous()
+pos, ip, pl, zero, n = i32(list(range(T))), i32([0, T]), i32([0]), i32([0]), i32([T])
+qo, ko, o = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q[:1])
+ws = torch.empty(16, dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    rc.qk_norm_rope(q, k, pos, t, q_weight=w, q_out=qo, k_out=ko)
+    rc.kv_append(ko, k, pos, ip, pl, kp, vp, bounds=bd, req_idx=zero, block=16)
+    rc.kv_block_bounds(kp, table, zero, n, b2, block=16)
+    rc.sparse_decode_attention(qo[-1:], n, zero, table, kp, vp, bd, o, ws, sm_scale=0.1,
+                               max_seq_len=T, block=16, top_blocks=2)
+for _ in range(2):
+    g.replay()
+torch.cuda.synchronize()
+assert torch.equal(kp[:T], ko) and torch.equal(vp[:T], k) and torch.equal(bd[:, :3], b2[:, :3])
+assert o.float().abs().sum() > 0 and rc.device_status() == 0
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 # ---------------------------------------------------------------------------------- bounds
@@ -445,6 +488,8 @@ def test_block_bounds_nan_bad_rows_and_slots():
         assert (bd[1] == 3.0).all()
         assert torch.equal(bd[2].cpu().nan_to_num(99.0), R.bounds_of(kp[:33].cpu(), 16)
                            .nan_to_num(99.0))
+    rc.kv_block_bounds(kp, table, i32([-1, 99]), i32([0, 0]), bd, block=16)   # padded rows
+    assert rc.device_status() == 0
     table[3, 1], table[3, 2] = 40, -1
     rc.kv_block_bounds(kp, table, i32([3]), i32([8]), bd, block=16)
     assert rc.device_status() == 1

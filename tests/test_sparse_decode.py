@@ -49,7 +49,9 @@ def test_sparse_decode_rejects_bad_arguments_before_any_device_work():
                dict(sm_scale=0.0), dict(sm_scale=-1.0), dict(sm_scale=float("nan")),
                dict(sm_scale=float("inf")), dict(q=0), dict(bounds=0), dict(o=fake(7) + 8),
                dict(k_pool=fake(4) + 2), dict(ws=0, **long), dict(ws=fake(20) + 4),
-               dict(ws_bytes=need.value - 1, **long)):
+               dict(ws_bytes=need.value - 1, **long),
+               # 2^27 - 1 units of 16 CTAs each
+               dict(num_rows=(1 << 27) - 1, num_q_heads=1, num_kv_heads=1, top_blocks=1024, **long)):
         assert call(**kw) == rc.RC_ERR_INVALID, kw
     assert call(num_rows=0) == rc.RC_OK
     assert lib().rc_sparse_decode_attention(None, fake(20), 1 << 20, None) == rc.RC_ERR_INVALID
@@ -252,6 +254,29 @@ def test_scores_a_hair_apart_are_told_apart(dtype, step, nb):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("q2", [1.0, 2.0 ** -2, 2.0 ** -4, 2.0 ** -7])
+def test_scores_closer_than_fp32_sums_are_ranked_exactly(dtype, q2):
+    """Hundreds of blocks whose scores agree to 2^-11 .. 2^-20 of the sum of their terms'
+    magnitudes, some to the last bit: around and within what fp32 sums of such terms may be off, so
+    whatever they say near the border has to be looked at again."""
+    d, block, nb, rows = 128, 16, 600, 8
+    c = Case(dtype, [nb * block], [(0, nb * block)] * rows, 2, 2, d, block)
+    g = torch.Generator().manual_seed(11)
+    r = int(c.req[0])
+    q = torch.randn(d, generator=g).bfloat16().double()
+    q[d - 1], q[d - 2] = 1.0, q2
+    x = torch.randn((nb, d), generator=g).bfloat16().double()
+    x[:, d - 2:] = 0
+    for i in (d - 1, d - 2):     # the last dimensions bring every score near 40, ever nearer
+        x[:, i] = ((40.0 - x @ q) / q[i]).bfloat16().double()
+    c.q[:] = q.to(c.dt)
+    c.q[1::2] *= 0.5             # rows of two scales
+    c.bounds[r, :nb] = x[:, None, None].expand(nb, 2, 2, d).to(c.dt)
+    c.call(40, sink=0).check()
+
+
+@pytest.mark.gpu
 def test_scores_that_overflow_or_are_no_numbers():
     """Infinite and NaN bounds and finite ones whose fp32 products overflow: NaN and +inf count as
     the largest finite number (lowest block first), -inf as the smallest."""
@@ -325,6 +350,14 @@ def test_bad_rows_and_slots_are_reported_and_skipped():
         assert (c.o[0] == 0).all() and (c.sel[0] == -1).all()
         c.req = keep
         c.check(only=[1])
+    # an empty row of a padded batch may name any request
+    c = Case("bf16", [300, 100], [(0, 0), (1, 100)], 8, 2, 128, 32)
+    keep = c.req.clone()
+    c.req[0] = -1
+    c.call(4)
+    assert rc.device_status() == 0 and (c.o[0] == 0).all() and (c.sel[0] == -1).all()
+    c.req = keep
+    c.check(only=[1])
     c = Case("bf16", [300, 100], [(0, -4), (1, 100)], 8, 2, 128, 32).call(4)
     assert rc.device_status() == 2 and (c.o[0] == 0).all()
     c.check(only=[1])
