@@ -593,17 +593,24 @@ __device__ __forceinline__ void select_blocks(const Params& p, SelectShared& sh,
     compact<false>(sh, m, f0, 0, list, [&](int i) { return score[i] >= lo_s ? 2 : 0; });
     return;
   }
-  for (int i0 = wid * 32; i0 < m; i0 += kThreads) {
+  // many blocks: the cluster's CTAs, which all stand here, share them
+  const cg::cluster_group cl = cg::this_cluster();
+  const int P = p.cluster, rank = (int)(blockIdx.x % P);
+  for (int i0 = (rank * kWarps + wid) * 32; i0 < m; i0 += P * kThreads) {
     const int i = i0 + lane;
     unsigned todo = __ballot_sync(0xffffffffu, i < m && near(i));
     while (todo) {
       const int j = __ffs(todo) - 1;
       todo &= todo - 1;
       const unsigned long long r = exact_rank<T, D>(p, n, g, f0 + i0 + j);
-      if (lane == 0) r64[i0 + j] = r;
+      if (kOwn && P > 1) {
+        if (lane < P) cl.map_shared_rank(r64, lane)[i0 + j] = r;
+      } else if (lane == 0) {
+        r64[i0 + j] = r;
+      }
     }
   }
-  __syncthreads();
+  if (P > 1) cl.sync(); else __syncthreads();
   const unsigned long long thr64 = kth_largest<unsigned long long>(
       sh, hist, m, close, rest, 0ull, ~0ull, [&](int i) { return r64[i]; }, near);
   int c = 0, unused = 0;
