@@ -148,8 +148,12 @@ constexpr int kWarps = kThreads / 32;
 // A warp's lanes are 32 / L rows: `heads` KV heads beside one another (a power of two), the other
 // rows later tokens of the block. A group is TOK tokens of each row: 1 where there are warps enough to
 // hide a group's latency, more where there are few.
+// What a lane keeps of a token in the ring: 16-byte chunks of K (2 N) and V (2 N), four of its
+// angles, and the token's slot.
+template <typename T>
+constexpr int kTokenBytes = (4 * Raw<T>::N + 4) * 512 + 128;
 template <typename T, int TOK>
-constexpr int append_smem() { return kWarps * kAppendStages * TOK * 4 * Raw<T>::N * 512; }
+constexpr int append_smem() { return kWarps * kAppendStages * TOK * kTokenBytes<T>; }
 
 template <typename T, int L, int TOK>
 __global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1) kv_append_kernel(rc_kv_append_args a, int heads,
@@ -166,9 +170,14 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1) kv_append_kernel(r
   const int head_groups = (a.num_kv_heads + heads - 1) / heads;
   const LaneChunks lc = lane_chunks(i, d, r, inter);
   const T* kw = (const T*)a.k_weight;
-  // chunk c (K: 2 N, then V: 2 N) of token u of stage st of this lane
-  char* mine_ring = ring + wid * (kAppendStages * TOK * 4 * N * 512) + lane * 16;
-  auto cell_of = [&](int st, int u, int c) { return mine_ring + ((st * TOK + u) * 4 * N + c) * 512; };
+  // chunk c (K, V, angles) of token u of stage st of this lane, and the token's slot
+  char* warp_ring = ring + wid * (kAppendStages * TOK * kTokenBytes<T>);
+  auto cell_of = [&](int st, int u, int c) {
+    return warp_ring + (st * TOK + u) * kTokenBytes<T> + c * 512 + lane * 16;
+  };
+  auto slot_of = [&](int st, int u) {
+    return (int*)(warp_ring + (st * TOK + u + 1) * kTokenBytes<T> - 128 + lane * 4);
+  };
 
   for (int b0 = 0; b0 < a.num_reqs; b0 += kWindow) {
     const int nreq = min(kWindow, a.num_reqs - b0);
@@ -199,6 +208,16 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1) kv_append_kernel(r
             const int at = (gr * TOK + u) * W + w;
             const T* ks = ksrc + at * a.k_token_stride;
             const T* vs = vsrc + at * a.v_token_stride;
+            if (mine && at < n) {
+              cp_async4(smem_u32(slot_of(st, u)), a.out_loc + tok0 + at);
+              if (lc.rot) {
+                const float* row = a.rope + (int64_t)(p0 + at) * r + 8 * i;
+                cp_async16_l1(smem_u32(cell_of(st, u, 4 * N)), row);
+                cp_async16_l1(smem_u32(cell_of(st, u, 4 * N + 1)), row + 4);
+                cp_async16_l1(smem_u32(cell_of(st, u, 4 * N + 2)), row + (r >> 1));
+                cp_async16_l1(smem_u32(cell_of(st, u, 4 * N + 3)), row + (r >> 1) + 4);
+              }
+            }
 #pragma unroll
             for (int c = 0; c < N; ++c) {
               if (m0 && at < n) {
@@ -237,26 +256,12 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1) kv_append_kernel(r
       for (int gr = 0; gr < groups; ++gr) {   // the same count for every lane: shuffles inside
         issue(gr + kAppendStages - 1);
         const int st = gr % kAppendStages;
-        float cs[TOK][8], sn[TOK][8];
-        int slot[TOK];
-#pragma unroll
-        for (int u = 0; u < TOK; ++u) {
-          const int at = (gr * TOK + u) * W + w;
-          const bool in = mine && at < n;
-          slot[u] = in ? a.out_loc[tok0 + at] : 0;
-          if (lc.rot && in) {
-            const float* row = a.rope + (int64_t)(p0 + at) * r + 8 * i;
-            ((float4*)cs[u])[0] = ((const float4*)row)[0];
-            ((float4*)cs[u])[1] = ((const float4*)row)[1];
-            ((float4*)sn[u])[0] = ((const float4*)(row + (r >> 1)))[0];
-            ((float4*)sn[u])[1] = ((const float4*)(row + (r >> 1)))[1];
-          }
-        }
         cp_async_wait<kAppendStages - 1>();
 #pragma unroll
         for (int u = 0; u < TOK; ++u) {
           bool live = mine && (gr * TOK + u) * W + w < n;
-          if (live && (slot[u] < 0 || slot[u] >= a.num_slots)) {
+          const int slot = live ? *slot_of(st, u) : 0;
+          if (live && (slot < 0 || slot >= a.num_slots)) {
             if (i == 0) set_status(status, kStatusSlotRange);
             live = false;
           }
@@ -268,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1) kv_append_kernel(r
             if (m0 && live) x0.v[c] = *(const uint4*)cell_of(st, u, c);
             if (m1 && live) x1.v[c] = *(const uint4*)cell_of(st, u, N + c);
           }
-          const int64_t dst = ((int64_t)slot[u] * a.num_kv_heads + h) * d;
+          const int64_t dst = ((int64_t)slot * a.num_kv_heads + h) * d;
 #pragma unroll
           for (int c = 0; c < N; ++c) {
             if (m0 && live)
@@ -280,7 +285,14 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1) kv_append_kernel(r
             ScalarRow row;
             row.get(x0, x1);
             if (kw) row.scale(row.template norm_scale<L>(d, a.eps), kw, lc);
-            if (lc.rot) row.rotate(cs[u], sn[u], inter);
+            if (lc.rot) {
+              float cs[8], sn[8];
+              *(float4*)cs = *(const float4*)cell_of(st, u, 4 * N);
+              *(float4*)(cs + 4) = *(const float4*)cell_of(st, u, 4 * N + 1);
+              *(float4*)sn = *(const float4*)cell_of(st, u, 4 * N + 2);
+              *(float4*)(sn + 4) = *(const float4*)cell_of(st, u, 4 * N + 3);
+              row.rotate(cs, sn, inter);
+            }
             row.set(x0, x1);
           }
           if (m0 && live) x0.store((T*)a.k_pool + dst + lc.c0 * 8);
@@ -477,7 +489,7 @@ int launch_append(const char* fn, const rc_kv_append_args& args, int* st, cudaSt
   // blocks the tokens can touch: each request begins and ends inside at most two more
   const int64_t items = (a.num_tokens / a.block + 2 * (int64_t)a.num_reqs) * groups;
   static PerDevice<int> one, more;
-  constexpr int kMore = 8 / (int)sizeof(T);   // as many as the ring has room for
+  constexpr int kMore = 2;
   if (prompts && few)
     return launch_resident(fn, kv_append_kernel<T, L, kMore>, more, items, a, heads,
                            append_smem<T, kMore>(), st, s);
