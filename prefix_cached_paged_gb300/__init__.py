@@ -531,12 +531,15 @@ def _heads(fn, dev, name, t, dtype, shape, out=False):
         raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    T, H, d = shape
+    if t.is_contiguous():
+        return H * d, d
     st, sh, se = t.stride()
-    if se != 1 and shape[2] > 1:
+    if se != 1 and d > 1:
         raise ValueError(f"{fn}: the heads of {name} must be contiguous")
     # the stride of a dimension of size 1 says nothing
-    st, sh = st if shape[0] > 1 else 0, sh if shape[1] > 1 else 0
-    if out and ((st == 0 and shape[0] > 1) or (sh == 0 and shape[1] > 1)):
+    st, sh = st if T > 1 else 0, sh if H > 1 else 0
+    if out and ((st == 0 and T > 1) or (sh == 0 and H > 1)):
         raise ValueError(f"{fn}: {name} is expanded: its rows share memory")
     return st, sh
 
@@ -575,42 +578,42 @@ def qk_norm_rope(q, k, positions=None, rope=None, *, q_weight=None, k_weight=Non
         raise ValueError(f"{fn}: neither a rotation nor a norm is given")
     T, _, d = _dims(fn, "q" if q is not None else "k", x, 3)
     dt = x.dtype
-    a = RcQkNormRopeArgs(_dtype_code(x), 0, 0, d, 0, 1 if interleaved else 0, eps, T)
+    rot = max_pos = p_rope = p_pos = Hq = Hkv = p_q = p_k = p_wq = p_wk = p_qo = p_ko = 0
+    qt = qh = kt = kh = qot = qoh = kot = koh = 0
     if rope is not None:
         if positions is None:
             raise ValueError(f"{fn}: the rotation needs positions")
-        a.max_position, a.rotary_dim = _dims(fn, "rope", rope, 2)
-        _require(fn, dev, (("rope", rope, torch.float32, rope.shape),
+        max_pos, rot = _dims(fn, "rope", rope, 2)
+        _require(fn, dev, (("rope", rope, torch.float32, (max_pos, rot)),
                            ("positions", positions, torch.int32, (T,))))
-        a.rope, a.positions = rope.data_ptr(), positions.data_ptr()
+        p_rope, p_pos = rope.data_ptr(), positions.data_ptr()
     if q is not None:
-        shape = (T, q.shape[1], d)
-        a.num_q_heads, a.q = shape[1], q.data_ptr()
-        a.q_token_stride, a.q_head_stride = _heads(fn, dev, "q", q, dt, shape, q_out is None)
-        if q_out is None:
-            a.q_out, a.q_out_token_stride, a.q_out_head_stride = a.q, a.q_token_stride, \
-                a.q_head_stride
-        else:
-            a.q_out = q_out.data_ptr()
-            a.q_out_token_stride, a.q_out_head_stride = _heads(fn, dev, "q_out", q_out, dt, shape,
-                                                               True)
+        Hq = q.shape[1]
+        shape = (T, Hq, d)
+        qt, qh = _heads(fn, dev, "q", q, dt, shape, q_out is None)
+        p_q = p_qo = q.data_ptr()
+        qot, qoh = qt, qh
+        if q_out is not None:
+            p_qo = q_out.data_ptr()
+            qot, qoh = _heads(fn, dev, "q_out", q_out, dt, shape, True)
         if q_weight is not None:
             _require(fn, dev, (("q_weight", q_weight, dt, (d,)),))
-            a.q_weight = q_weight.data_ptr()
+            p_wq = q_weight.data_ptr()
     if k is not None:
-        shape = (T, _dims(fn, "k", k, 3)[1], d)
-        a.num_kv_heads, a.k = shape[1], k.data_ptr()
-        a.k_token_stride, a.k_head_stride = _heads(fn, dev, "k", k, dt, shape, k_out is None)
-        if k_out is None:
-            a.k_out, a.k_out_token_stride, a.k_out_head_stride = a.k, a.k_token_stride, \
-                a.k_head_stride
-        else:
-            a.k_out = k_out.data_ptr()
-            a.k_out_token_stride, a.k_out_head_stride = _heads(fn, dev, "k_out", k_out, dt, shape,
-                                                               True)
+        Hkv = _dims(fn, "k", k, 3)[1]
+        shape = (T, Hkv, d)
+        kt, kh = _heads(fn, dev, "k", k, dt, shape, k_out is None)
+        p_k = p_ko = k.data_ptr()
+        kot, koh = kt, kh
+        if k_out is not None:
+            p_ko = k_out.data_ptr()
+            kot, koh = _heads(fn, dev, "k_out", k_out, dt, shape, True)
         if k_weight is not None:
             _require(fn, dev, (("k_weight", k_weight, dt, (d,)),))
-            a.k_weight = k_weight.data_ptr()
+            p_wk = k_weight.data_ptr()
+    a = RcQkNormRopeArgs(_dtype_code(x), Hq, Hkv, d, rot, 1 if interleaved else 0, eps, T, max_pos,
+                         p_q, qt, qh, p_k, kt, kh, p_wq, p_wk, p_pos, p_rope, p_qo, qot, qoh, p_ko,
+                         kot, koh)
     check(lib().rc_qk_norm_rope(ctypes.byref(a), _raw_stream(dev, stream)), "rc_qk_norm_rope")
 
 
@@ -632,25 +635,25 @@ def kv_append(k, v, out_loc, qo_indptr, prefix_len, k_pool, v_pool, *, rope=None
     _require(fn, dev, (("k_pool", k_pool, dt, (S, Hkv, d)), ("v_pool", v_pool, dt, (S, Hkv, d)),
                        ("out_loc", out_loc, i32, (T,)), ("qo_indptr", qo_indptr, i32, (B + 1,)),
                        ("prefix_len", prefix_len, i32, (B,))))
-    a = RcKvAppendArgs(_dtype_code(k_pool), B, Hkv, d, 0, 1 if interleaved else 0, eps, block, T, S,
-                       0, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, out_loc.data_ptr(),
-                       qo_indptr.data_ptr(), prefix_len.data_ptr(), 0, 0, k_pool.data_ptr(),
-                       v_pool.data_ptr())
+    rot = max_pos = p_rope = p_w = p_b = p_req = R = nb = 0
     if rope is not None:
-        a.max_position, a.rotary_dim = _dims(fn, "rope", rope, 2)
-        _require(fn, dev, (("rope", rope, torch.float32, rope.shape),))
-        a.rope = rope.data_ptr()
+        max_pos, rot = _dims(fn, "rope", rope, 2)
+        _require(fn, dev, (("rope", rope, torch.float32, (max_pos, rot)),))
+        p_rope = rope.data_ptr()
     if k_weight is not None:
         _require(fn, dev, (("k_weight", k_weight, dt, (d,)),))
-        a.k_weight = k_weight.data_ptr()
+        p_w = k_weight.data_ptr()
     if bounds is not None:
         if req_idx is None:
             raise ValueError(f"{fn}: bounds need req_idx")
         R, nb = _dims(fn, "bounds", bounds, 5)[:2]
         _require(fn, dev, (("bounds", bounds, dt, (R, nb, Hkv, 2, d)),
                            ("req_idx", req_idx, i32, (B,))))
-        a.max_reqs, a.max_blocks = R, nb
-        a.bounds, a.req_idx = bounds.data_ptr(), req_idx.data_ptr()
+        p_b, p_req = bounds.data_ptr(), req_idx.data_ptr()
+    a = RcKvAppendArgs(_dtype_code(k_pool), B, Hkv, d, rot, 1 if interleaved else 0, eps, block, T, S,
+                       max_pos, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, out_loc.data_ptr(),
+                       qo_indptr.data_ptr(), prefix_len.data_ptr(), p_w, p_rope, k_pool.data_ptr(),
+                       v_pool.data_ptr(), p_b, p_req, R, nb)
     check(lib().rc_kv_append(ctypes.byref(a), _raw_stream(dev, stream)), "rc_kv_append")
 
 
