@@ -630,8 +630,8 @@ int rc_kv_block_bounds(const rc_kv_block_bounds_args* args, void* stream);
  *             (optional); selected [num_rows, Hkv, top_blocks] int32 (optional): block numbers in
  *             ascending order, then -1.
  * A request may have several rows (a chunk of new tokens: rows of growing seq_len). A row with
- * seq_len 0 (its req_idx is not read) gets o = 0, lse = -inf, selected = -1; so does a row whose seq_len or req_idx is out of
- * range, which also sets the device status word. A slot outside the pool sets it and that token
+ * seq_len 0 (its req_idx is not read) gets o = 0, lse = -inf, selected = -1; so does a row whose
+ * seq_len or req_idx is out of range, which also sets the device status word. A slot outside the pool sets it and that token
  * weighs nothing. sm_scale > 0; Hq / Hkv <= 16; head_dim 64 or 128; max_seq_len <= 2^24, top_blocks
  * <= 8192; tensors 16-byte aligned. */
 typedef struct rc_sparse_decode_args {

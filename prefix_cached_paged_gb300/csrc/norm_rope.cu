@@ -2,10 +2,17 @@
 //   y = x * rsqrt(mean(x^2) + eps) * w   per head row,   then (a, b) -> (a cos - b sin, b cos + a sin)
 // in fp32, rounded once at the store.
 //
-// A warp works on the heads of one token, 32 / L head rows (norm_rope.cuh) at a time, so the token's
-// cosines and sines are loaded once per lane and serve every head. Rows stream through a ring in
-// shared memory by 16-byte asynchronous copies; a lane reads only what it copied itself, so the
-// ring needs no barrier.
+// Bound by HBM: every element is read and written once, the table row once per token. A warp works
+// on the heads of one token, 32 / L head rows (norm_rope.cuh) at a time, so the token's cosines and
+// sines are loaded once per lane and serve every head. Rows stream through a ring in shared memory
+// by 16-byte asynchronous copies; a lane reads only what it copied itself, so the ring needs no
+// barrier, and the arithmetic runs on packed fp32 pairs.
+//
+// Measured, 16 000 tokens of 32 + 32 heads of 128, bf16, sliced from a fused projection: 84 us,
+// 6.29 TB/s, 94 % of the copy rate (issue slots 68 % busy, DRAM 74 % of its nominal peak). On the way:
+// one CTA per token and scalar arithmetic 94 us (267 warp instructions per 4 rows, a third of them
+// per-CTA set-up); four rows per lane in registers 152 us (115 registers, too few warps); one head
+// group per warp, the angles loaded anew for each, 121 us; three ring stages instead of four 87 us.
 #include <algorithm>
 #include <cmath>
 
@@ -101,8 +108,9 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(rc_qk_norm_rope_
 
 template <typename T, int L>
 void launch_l(const rc_qk_norm_rope_args& a, int sms, int* st, cudaStream_t s) {
-  // one warp per token where that fills the GPU eight times over; with fewer tokens their heads go
-  // to more warps, down to one group of heads each
+  // One warp per token where there are tokens enough; with fewer, their heads go to more warps, down
+  // to one group of heads each. 16 000 tokens: 84 us with one warp each, 90 with two, 104 with four;
+  // 8 tokens of 40 heads: 3.7 us with ten warps each, 6.3 with a CTA of four.
   const int groups = (a.num_q_heads + a.num_kv_heads + 32 / L - 1) / (32 / L);
   int splits = 1;
   while (splits < groups && a.num_tokens * splits < (int64_t)sms * kWarps * 16) splits *= 2;

@@ -14,6 +14,18 @@
 //           maximum and sum;
 //   join:   the CTAs' states are joined through distributed shared memory, each CTA finishing a
 //           share of the outputs.
+//
+// Bound by HBM (boxes of a row once, K and V of the selected tokens once per KV head) with many rows,
+// by the chain of dependent steps with few. Measured, bf16, heads of 128, inputs beyond L2:
+//   128 rows, 32 + 32 heads, contexts 512 .. 8192, 16 blocks of 64: 334 us, 6.5 TB/s, 97 % of the
+//     copy rate; 64 rows, 32 + 8 heads, contexts 4096 .. 32768, 64 blocks: 200 us, 5.7 TB/s, 85 % (a
+//     CTA scores, waits and selects for ~8 us of its ~60; four of them share an SM).
+//   1 row, 64 + 8 heads, 131071 tokens, 64 blocks: 26 us: score 4, cluster barriers 5, select 4 to
+//     11 (the longer where finer scores are needed), slots 1, 256 tokens 4, join 2.
+// On the way, for the three: separate kernels for scores, selection, attention and merge, all scores
+// in 64 bits and attention on CUDA cores 1093, 1399, 334 us; scores on matrix instructions 710, 728,
+// 141; attention too, the last CTA of a row merging 417, 263, 126 (the merge of 64 parts alone 80);
+// one kernel 341, 227, 39; K and V halves in one ring of three (four CTAs per SM, not three) 334, 200.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -33,7 +45,7 @@ constexpr int kMaxGroup = 16;      // query heads per KV head
 constexpr int kMaxTop = 8192;      // the list of chosen blocks is kept in shared memory
 constexpr int kMaxCluster = 16;
 constexpr int kSegment = 512;      // tokens whose slots are resolved at a time
-constexpr int kEnoughCtas = 456;   // three per SM
+constexpr int kEnoughCtas = 456;   // three per SM: more of them do not come sooner to their tokens
 
 struct Workspace {                 // used only when a unit's scores outgrow shared memory
   float* score;                    // [units * nb]
@@ -127,8 +139,8 @@ struct ScoreSink {
   }
 };
 
-// Scores of 16 blocks at a time against the query heads of a KV head by one warp, boxes and queries straight
-// from global memory into matrix fragments: the dot product does not care in which order the
+// Scores of 16 blocks at a time against the query heads of a KV head by one warp, boxes and queries
+// straight from global memory into matrix fragments: the dot product does not care in which order the
 // dimensions come, so lane (gid, tig) takes 16 contiguous bytes of a row where the instruction
 // wants four pairs, the same ones for both operands. [q-, q+] . [lo, hi] needs no comparison:
 // one of q+ = max(q, 0) and q- = min(q, 0) is zero. (0 * inf gives a NaN that the definition has
@@ -375,6 +387,9 @@ __device__ K kth_largest(SelectShared& s, int* hist, int n, int left, int k, K l
   return prefix;
 }
 
+// Where many blocks tie (all keys alike, a query of zeros) every one of them is ranked so, and the
+// adders of a GB300 SM for doubles are few: one row of 2048 tied blocks takes 0.44 ms, 512 units of
+// 64 .. 512 tied blocks 1.4 ms.
 // The 64-bit rank of block b: the largest score over the KV head's queries. One warp, four queries
 // at a time so that their loads and sums overlap.
 template <typename T, int D>
@@ -1057,8 +1072,11 @@ Params params_of(const rc_sparse_decode_args* a) {
   p.a = *a;
   p.G = a->num_q_heads / a->num_kv_heads;
   p.nb = std::max(1, (a->max_seq_len + a->block - 1) / a->block);
-  // CTAs per unit: until the GPU is full, while each still has a stage for every warp; with more
-  // units, until a CTA's part is at most 2048 tokens, so that the last wave of CTAs stays short
+  // CTAs per unit: until the GPU is full, while each still has two stages for every warp; with more
+  // units, until a CTA's part is at most 2048 tokens, so that the last wave of CTAs stays short.
+  // One row of 4096 selected tokens and 8 heads: 26 us with 16 CTAs per unit, 31 with 8, 46 with 4.
+  // 110 units of 288 tokens: 16.7 us with 4, 22.5 with 2, 20.6 with 8. 512 units of 4096 tokens:
+  // 200 us with 2, 245 with 1, 214 with 4, 240 with 8; 4096 units of 1024: 334 us with 1, 389 with 2.
   const int64_t units = (int64_t)a->num_rows * a->num_kv_heads;
   const int64_t tokens = (int64_t)std::min(p.nb, a->top_blocks) * a->block;
   p.cluster = 1;
