@@ -470,6 +470,25 @@ def test_block_bounds_are_the_extremes_of_the_cached_keys(dtype, lens, hkv, d, b
 
 
 @pytest.mark.gpu
+def test_block_bounds_of_more_rows_than_one_window():
+    n = 2300
+    lens = np.random.default_rng(3).integers(0, 40, n)
+    lens[7] = 0
+    g = _gen(12)
+    kp = torch.randn((500, 1, 64), generator=g)
+    table = torch.randint(0, 500, (n, 40), generator=g, dtype=torch.int32)
+    bd = torch.full((n, 3, 1, 2, 64), 3.0)
+    want = bd.clone()
+    for r in range(n):
+        b = R.bounds_of(kp[table[r, :int(lens[r])].long()], 16)
+        want[r, :b.shape[0]] = b
+    db = bd.cuda()
+    rc.kv_block_bounds(kp.cuda(), table.cuda(), torch.arange(n, dtype=torch.int32, device="cuda"),
+                       torch.from_numpy(lens.astype(np.int32)).cuda(), db, block=16)
+    assert rc.device_status() == 0 and torch.equal(db.cpu(), want)
+
+
+@pytest.mark.gpu
 def test_block_bounds_nan_bad_rows_and_slots():
     g = _gen(2)
     i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731

@@ -181,6 +181,52 @@ def test_more_blocks_than_shared_memory_holds(dtype):
 
 
 @pytest.mark.gpu
+def test_largest_selection():
+    """8192 blocks selected of 12 500: the longest list, and the most tokens of a CTA."""
+    g = torch.Generator().manual_seed(8)
+    n, block = 200_000, 16
+    c = Case("bf16", [600], [(0, n)], 2, 1, 64, block)
+    c.max_ctx = n
+    c.table = torch.randint(0, 600, (c.table.shape[0], n), generator=g, dtype=torch.int32)
+    x = torch.randn((c.table.shape[0], n // block, 1, 2, 64), generator=g).to(c.dt)
+    c.bounds = torch.cat([x.amin(3, True), x.amax(3, True)], 3).contiguous()
+    c.call(8192).check()
+    assert rc.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_many_short_rows_and_calls_on_two_streams_at_once():
+    """5000 rows of one short request, and two different calls that may overlap (sizes that need no
+    workspace share nothing)."""
+    n = 5000
+    c = Case("bf16", [90], [(0, 1 + i % 90) for i in range(n)], 4, 2, 64, 16)
+    c.call(3).check(only=list(range(0, n, 499)) + [n - 1])
+    a = Case("bf16", [2000, 333], [(0, 2000), (1, 333)], 16, 4, 128, 64)
+    b = Case("f32", [1500], [(0, 1500), (0, 1490)], 4, 2, 64, 32)
+    want = [(x.call(6).o.clone(), x.sel.clone()) for x in (a, b)]
+    args = []
+    for x in (a, b):
+        seq = torch.tensor([m for _, m in x.rows], dtype=torch.int32).cuda()
+        req = x.req[torch.tensor([i for i, _ in x.rows])].to(torch.int32).cuda()
+        q = x.q.cuda()
+        o = [torch.empty_like(q) for _ in range(20)]
+        sel = torch.empty((len(x.rows), x.hkv, 6), dtype=torch.int32, device="cuda")
+        args.append((x, q, seq, req, x.table.cuda(), x.k.cuda(), x.v.cuda(), x.bounds.cuda(), o, sel))
+    ws = torch.empty(0, dtype=torch.uint8, device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s, (x, q, seq, req, t, k, v, bd, o, sel) in zip(streams, args):
+            rc.sparse_decode_attention(q, seq, req, t, k, v, bd, o[i], ws, sm_scale=x.scale,
+                                       max_seq_len=x.max_seq, block=x.block, top_blocks=6,
+                                       selected=sel, stream=s)
+    torch.cuda.synchronize()
+    for (w, ws_), (*_, o, sel) in zip(want, args):
+        assert all(torch.equal(x, w) for x in o) and torch.equal(sel, ws_)
+    assert rc.device_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("units,top", [(1, 4), (1, 40), (3, 40), (40, 12), (150, 12), (460, 3)])
 def test_every_number_of_parts_per_row(units, top):
     """From 16 CTAs per row to one, rows of unlike lengths among them."""
