@@ -81,12 +81,16 @@ constexpr int kBins = 2048;        // counters of the selection's radix steps
 template <typename T, int D, int GM>
 struct Cfg {
   static constexpr bool kBf16 = sizeof(T) == 2;
-  static constexpr int TOK = 16, STAGES = 3;                  // a warp's ring: K or V of 16 tokens
+  static constexpr int STAGES = 3;
+  static constexpr int TOK = 16;                              // bf16: a stage is K or V of 16 tokens
   static constexpr int RB = D * 2, RS = RB + 16;              // bytes of a row, padded
-  static constexpr int STAGE = TOK * RS;
+  static constexpr int TB = GM == 16 ? 2 : 4;                 // fp32: K and V of TB tokens
+  static constexpr int STAGE = kBf16 ? TOK * RS : 2 * TB * D * 4;
   static constexpr int STATE = GM * D * 4;                    // o of one state
-  static constexpr int RING = kBf16 ? kWarps * STAGES * STAGE : (kWarps + 1) * STATE;
-  static constexpr int BASE = RING > 36864 ? RING : 36864;
+  static constexpr int WEIGHTS = kWarps * STAGES * STAGE;     // fp32: 64 words per warp
+  static constexpr int RING = WEIGHTS + (kBf16 ? 0 : kWarps * 256);
+  static constexpr int NEED = RING > (kWarps + 1) * STATE ? RING : (kWarps + 1) * STATE;
+  static constexpr int BASE = NEED > 36864 ? NEED : 36864;
   static constexpr int BLOCKS = BASE / 16;                    // a rank and a score take 12 bytes
   static_assert(BASE >= (kWarps + 1) * STATE, "the states fit");
   static constexpr int HIST = BLOCKS * 12;
@@ -217,42 +221,71 @@ __device__ __forceinline__ void score_tiles(const Params& p, int64_t n, int g, i
   }
 }
 
-// The fp32 form: one warp per block, lanes over the dimensions.
-template <int D>
+// The sums over a warp of V values per lane (a power of two up to 32), V - 1 exchanges instead of
+// 5 V: every step hands half of the values to the other half of the lanes. Lane l gets the sum of
+// value l / (32 / V).
+template <int V>
+__device__ __forceinline__ float sum_values(float (&a)[V]) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int n = V / 2; n >= 1; n /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? a[i] : a[i + n];
+      a[i] = (up ? a[i + n] : a[i]) + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+#pragma unroll
+  for (; o >= 1; o /= 2) a[0] += __shfl_xor_sync(0xffffffffu, a[0], o);
+  return a[0];
+}
+
+// The fp32 form: one warp per block, lanes over the dimensions, GM >= G query heads. t is taken as the
+// sum over the lanes of the largest head's part, which is no less.
+template <int D, int GM>
 __device__ __forceinline__ void score_blocks_f32(const Params& p, int64_t n, int g, int first,
                                                  int step, ScoreSink& out) {
   constexpr int E = D / 32;
   const rc_sparse_decode_args& a = p.a;
   const int lane = threadIdx.x & 31;
-  const float* q = (const float*)a.q + (n * a.num_q_heads + (int64_t)g * p.G) * D + lane * E;
+  const float* src = (const float*)a.q + (n * a.num_q_heads + (int64_t)g * p.G) * D + lane * E;
+  float q[GM][E];
+#pragma unroll
+  for (int h = 0; h < GM; ++h)
+#pragma unroll
+    for (int e = 0; e < E; ++e) q[h][e] = h < p.G ? src[h * D + e] : 0.f;
   const float* boxes = (const float*)a.bounds +
                        ((int64_t)a.req_idx[n] * a.max_blocks * a.num_kv_heads + g) * 2 * D + lane * E;
   for (int b = out.f0 + first; b < out.f1; b += step) {
     const float* box = boxes + (int64_t)b * a.num_kv_heads * 2 * D;
-    float lo[E], hi[E];
+    float lo[E], hi[E], s[GM], t = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       lo[e] = box[e];
       hi[e] = box[D + e];
     }
-    float best = -INFINITY;
-    for (int h = 0; h < p.G; ++h) {
-      float s = 0.f, t = 0.f;
+#pragma unroll
+    for (int h = 0; h < GM; ++h) {
+      s[h] = 0.f;
+      float th = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float x = q[h * D + e];
-        const float y = x >= 0.f ? hi[e] : lo[e];
-        s = fmaf(x, y, s);
-        t = fmaf(fabsf(x), fabsf(y), t);
+        const float x = q[h][e], y = x >= 0.f ? hi[e] : lo[e];
+        s[h] = fmaf(x, y, s[h]);
+        th = fmaf(fabsf(x), fabsf(y), th);
       }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        t += __shfl_xor_sync(0xffffffffu, t, o);
-      }
-      best = max_nan(best, s);
-      out.tmax = max_nan(out.tmax, t);
+      t = max_nan(t, h < p.G ? th : 0.f);
     }
+    float best = sum_values<GM>(s);
+    if (lane / (32 / GM) >= p.G) best = -INFINITY;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (o >= 32 / GM) best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, o));
+    }
+    out.tmax = max_nan(out.tmax, t);
     if (lane == 0) out.put(b, best);
   }
 }
@@ -805,90 +838,136 @@ struct AttendMma {
   }
 };
 
-// The fp32 form: a warp takes every 4th group of TB tokens (their loads and sums overlap), lanes
-// over the dimensions (D / 32 consecutive ones each), GM >= G query heads.
+// The fp32 form: a warp takes every 4th group of TB tokens, lanes over the dimensions (D / 32
+// consecutive ones each), GM >= G query heads. Groups stream through a ring in shared memory; a lane
+// reads only what it copied itself. The V = GM * TB scores of a group are summed over the lanes
+// together (sum_values), so each lane ends with one score, of head h = its place / TB, takes one
+// exponential, and hands its weight to the others through shared memory.
 template <int D, int GM>
 struct AttendF32 {
-  static constexpr int E = D / 32, TB = 4;
-  float q[GM][E], acc[GM][E], m[GM], l[GM];
+  using C = Cfg<float, D, GM>;
+  static constexpr int E = D / 32, TB = C::TB, V = GM * TB, SPAN = 32 / V;   // lanes per score
+  float q[GM][E], acc[GM][E], m, l;   // m, l: of this lane's head (l: of its token alone)
 
   __device__ __forceinline__ void begin(const Params& p, int64_t n, int g) {
     const float scale = p.a.sm_scale * kLog2e;
     const float* src = (const float*)p.a.q + (n * p.a.num_q_heads + (int64_t)g * p.G) * D +
                        (threadIdx.x & 31) * E;
+    m = -INFINITY;
+    l = 0.f;
 #pragma unroll
-    for (int h = 0; h < GM; ++h) {
-      m[h] = -INFINITY;
-      l[h] = 0.f;
+    for (int h = 0; h < GM; ++h)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         q[h][e] = h < p.G ? src[h * D + e] * scale : 0.f;
         acc[h][e] = 0.f;
       }
-    }
   }
 
-  __device__ __forceinline__ void tokens(const Params& p, char*, int g, const int* slots, int n) {
+  __device__ __forceinline__ void tokens(const Params& p, char* smem, int g, const int* slots,
+                                         int n) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int64_t base = (int64_t)g * D + lane * E, step = (int64_t)p.a.num_kv_heads * D;
-    for (int t0 = wid * TB; t0 < n; t0 += kWarps * TB) {
-      float k[TB][E], v[TB][E];
-      bool ok[TB];
+    float* ring = (float*)(smem + wid * C::STAGES * C::STAGE) + lane * E;
+    float* weights = (float*)(smem + C::WEIGHTS) + wid * 64;   // then what the heads are scaled by
+    const int groups = (n + TB - 1) / TB;
+    auto at = [&](int st, int b, int v) { return ring + (st * 2 * TB + 2 * b + v) * D; };
+    auto issue = [&](int s, int st) {
+      if (s < groups) {
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+          const int slot = s * TB + b < n ? slots[s * TB + b] : -1;
+          const int64_t off = (int64_t)max(slot, 0) * step + base;
+          cp_async_or_zero<4 * E>(smem_u32(at(st, b, 0)), (const float*)p.a.k_pool + off, slot >= 0);
+          cp_async_or_zero<4 * E>(smem_u32(at(st, b, 1)), (const float*)p.a.v_pool + off, slot >= 0);
+        }
+      }
+      cp_async_commit();
+    };
+    int head = 0;
+#pragma unroll
+    for (; head < C::STAGES - 1; ++head) issue(wid + head * kWarps, head);
+    int st = 0;
+    for (int s = wid; s < groups; s += kWarps) {
+      issue(s + (C::STAGES - 1) * kWarps, st == 0 ? C::STAGES - 1 : st - 1);
+      cp_async_wait<C::STAGES - 1>();
+      float sc[V];
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
-        const int slot = t0 + b < n ? slots[t0 + b] : -1;
-        ok[b] = slot >= 0;
+        float k[E];
+        load_e(at(st, b, 0), k);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          k[b][e] = ok[b] ? ((const float*)p.a.k_pool)[slot * step + base + e] : 0.f;
-          v[b][e] = ok[b] ? ((const float*)p.a.v_pool)[slot * step + base + e] : 0.f;
+        for (int h = 0; h < GM; ++h) {
+          float x = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) x = fmaf(q[h][e], k[e], x);
+          sc[h * TB + b] = x;
         }
       }
+      const int mine = s * TB + (lane / SPAN) % TB;
+      float x = sum_values<V>(sc);
+      x = mine < n && slots[mine] >= 0 ? x : -INFINITY;
+      float mx = x;
+#pragma unroll
+      for (int o = SPAN; o < SPAN * TB; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      // the running maximum moves only when it grows by more than 2^8
+      const float top = fmaxf(m, mx);
+      const bool grow = top > m + 8.f;
+      const float al = grow && m != -INFINITY ? exp2f(m - top) : 1.f;
+      if (grow) m = top;
+      const float w = exp2f(x - (m == -INFINITY ? 0.f : m));   // 0 for a score of -inf, NaN for one
+      l = l * al + w;
+      __syncwarp();   // the last group's weights are used up
+      if (lane % SPAN == 0) weights[lane / SPAN] = w;
+      const bool rescale = __any_sync(0xffffffffu, al != 1.f);
+      if (rescale && lane % (SPAN * TB) == 0) weights[32 + lane / (SPAN * TB)] = al;
+      __syncwarp();
+      if (rescale) {
+#pragma unroll
+        for (int h = 0; h < GM; ++h)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[h][e] *= weights[32 + h];
+      }
+      float v[TB][E];
+#pragma unroll
+      for (int b = 0; b < TB; ++b) load_e(at(st, b, 1), v[b]);
 #pragma unroll
       for (int h = 0; h < GM; ++h) {
-        if (h >= p.G) break;
-        float s[TB], mn = m[h];
+        float wt[TB];
+        if constexpr (TB == 4)
+          *(float4*)wt = *(const float4*)(weights + h * TB);
+        else
+          *(float2*)wt = *(const float2*)(weights + h * TB);
 #pragma unroll
-        for (int b = 0; b < TB; ++b) {
-          s[b] = 0.f;
+        for (int b = 0; b < TB; ++b)
 #pragma unroll
-          for (int e = 0; e < E; ++e) s[b] = fmaf(q[h][e], k[b][e], s[b]);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-#pragma unroll
-          for (int b = 0; b < TB; ++b) s[b] += __shfl_xor_sync(0xffffffffu, s[b], o);
-#pragma unroll
-        for (int b = 0; b < TB; ++b) {
-          s[b] = ok[b] ? s[b] : -INFINITY;
-          mn = fmaxf(mn, s[b]);
-        }
-        const float al = mn == -INFINITY ? 1.f : exp2f(m[h] - mn);
-        m[h] = mn;
-        l[h] *= al;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[h][e] *= al;
-#pragma unroll
-        for (int b = 0; b < TB; ++b) {
-          // a score of -inf weighs nothing; a NaN reaches the output as it would in a dense softmax
-          const float pr = s[b] == -INFINITY ? 0.f : exp2f(s[b] - mn);
-          l[h] += pr;
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[h][e] = fmaf(pr, v[b][e], acc[h][e]);
-        }
+          for (int e = 0; e < E; ++e) acc[h][e] = fmaf(wt[b], v[b][e], acc[h][e]);
       }
+      st = st == C::STAGES - 1 ? 0 : st + 1;
     }
+    cp_async_wait<0>();
+  }
+
+  static __device__ __forceinline__ void load_e(const float* p, float (&v)[E]) {
+    if constexpr (E == 4)
+      *(float4*)v = *(const float4*)p;
+    else
+      *(float2*)v = *(const float2*)p;
   }
 
   __device__ __forceinline__ void end(int G, float* sm, float* sl, float* so) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    float sum = l;
+#pragma unroll
+    for (int o = SPAN; o < SPAN * TB; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int mine = lane / (SPAN * TB);
+    if (lane % (SPAN * TB) == 0 && mine < G) {
+      sm[wid * G + mine] = m;
+      sl[wid * G + mine] = sum;
+    }
 #pragma unroll
     for (int h = 0; h < GM; ++h) {
       if (h >= G) break;
-      if (lane == 0) {
-        sm[wid * G + h] = m[h];
-        sl[wid * G + h] = l[h];
-      }
 #pragma unroll
       for (int e = 0; e < E; ++e) so[(wid * G + h) * D + lane * E + e] = acc[h][e];
     }
@@ -949,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads) sparse_decode_kernel(Params p) {
       if constexpr (C::kBf16)
         score_tiles<D, GM / 8>(p, n, g, rank * kWarps + wid, P * kWarps, sink);
       else
-        score_blocks_f32<D>(p, n, g, rank * kWarps + wid, P * kWarps, sink);
+        score_blocks_f32<D, GM>(p, n, g, rank * kWarps + wid, P * kWarps, sink);
       const uint32_t lo = __reduce_min_sync(0xffffffffu, sink.lo);
       const uint32_t hi = __reduce_max_sync(0xffffffffu, sink.hi);
       const uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(sink.tmax) & 0x7fffffffu);

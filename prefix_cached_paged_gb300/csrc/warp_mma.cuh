@@ -31,6 +31,18 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
 }
+// the same for 8 or 16 bytes
+template <int N>
+__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, bool live) {
+  static_assert(N == 8 || N == 16, "");
+  if constexpr (N == 16) {
+    cp_async16_or_zero(dst, src, live);
+  } else {
+    const int n = live ? 8 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+  }
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
