@@ -132,13 +132,15 @@ struct ScoreSink {
   int cluster, f0, f1;
   float tmax = 0.f;   // largest t this lane saw; least and greatest score it put
   uint32_t lo = 0xffffffffu, hi = 0;
-  __device__ __forceinline__ void put(int b, float s) {
+  // `parts` lanes that all have the score share the CTAs it goes to; this one is number `part`
+  __device__ __forceinline__ void put(int b, float s, int part, int parts) {
     lo = min(lo, order32(s));
     hi = max(hi, order32(s));
     if (!shared || cluster == 1) {
-      local[b - f0] = s;
+      if (part == 0) local[b - f0] = s;
     } else {
-      for (int r = 0; r < cluster; ++r) cg::this_cluster().map_shared_rank(local, r)[b - f0] = s;
+      for (int r = part; r < cluster; r += parts)
+        cg::this_cluster().map_shared_rank(local, r)[b - f0] = s;
     }
   }
 };
@@ -216,8 +218,8 @@ __device__ __forceinline__ void score_tiles(const Params& p, int64_t n, int g, i
       best0 = max_nan(best0, __shfl_xor_sync(0xffffffffu, best0, o));
       best1 = max_nan(best1, __shfl_xor_sync(0xffffffffu, best1, o));
     }
-    if (tig == 0 && r0 < out.f1) out.put(r0, best0);
-    if (tig == 0 && r1 < out.f1) out.put(r1, best1);
+    if (r0 < out.f1) out.put(r0, best0, tig, 4);
+    if (r1 < out.f1) out.put(r1, best1, tig, 4);
   }
 }
 
@@ -258,35 +260,44 @@ __device__ __forceinline__ void score_blocks_f32(const Params& p, int64_t n, int
     for (int e = 0; e < E; ++e) q[h][e] = h < p.G ? src[h * D + e] : 0.f;
   const float* boxes = (const float*)a.bounds +
                        ((int64_t)a.req_idx[n] * a.max_blocks * a.num_kv_heads + g) * 2 * D + lane * E;
-  for (int b = out.f0 + first; b < out.f1; b += step) {
-    const float* box = boxes + (int64_t)b * a.num_kv_heads * 2 * D;
-    float lo[E], hi[E], s[GM], t = 0.f;
+  constexpr int NB = GM * E >= 32 ? 2 : 4;   // boxes in flight, as registers allow
+  for (int b0 = out.f0 + first; b0 < out.f1; b0 += NB * step) {
+    float lo[NB][E], hi[NB][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      lo[e] = box[e];
-      hi[e] = box[D + e];
-    }
-#pragma unroll
-    for (int h = 0; h < GM; ++h) {
-      s[h] = 0.f;
-      float th = 0.f;
+    for (int u = 0; u < NB; ++u) {
+      const float* box = boxes + (int64_t)min(b0 + u * step, out.f1 - 1) * a.num_kv_heads * 2 * D;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float x = q[h][e], y = x >= 0.f ? hi[e] : lo[e];
-        s[h] = fmaf(x, y, s[h]);
-        th = fmaf(fabsf(x), fabsf(y), th);
+        lo[u][e] = box[e];
+        hi[u][e] = box[D + e];
       }
-      t = max_nan(t, h < p.G ? th : 0.f);
     }
-    float best = sum_values<GM>(s);
-    if (lane / (32 / GM) >= p.G) best = -INFINITY;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      t += __shfl_xor_sync(0xffffffffu, t, o);
-      if (o >= 32 / GM) best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, o));
+    for (int u = 0; u < NB; ++u) {
+      if (b0 + u * step >= out.f1) break;
+      float s[GM], t = 0.f;
+#pragma unroll
+      for (int h = 0; h < GM; ++h) {
+        s[h] = 0.f;
+        float th = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float x = q[h][e], y = x >= 0.f ? hi[u][e] : lo[u][e];
+          s[h] = fmaf(x, y, s[h]);
+          th = fmaf(fabsf(x), fabsf(y), th);
+        }
+        t = max_nan(t, h < p.G ? th : 0.f);
+      }
+      float best = sum_values<GM>(s);
+      if (lane / (32 / GM) >= p.G) best = -INFINITY;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (o >= 32 / GM) best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, o));
+      }
+      out.tmax = max_nan(out.tmax, t);
+      out.put(b0 + u * step, best, lane, 32);
     }
-    out.tmax = max_nan(out.tmax, t);
-    if (lane == 0) out.put(b, best);
   }
 }
 
