@@ -662,7 +662,7 @@ typedef struct rc_sparse_decode_args {
   int32_t* selected;
 } rc_sparse_decode_args;
 /* Workspace bytes for these sizes (device memory, 16-byte aligned, no initialisation needed): 0, and
- * no workspace, unless max_seq_len is more than 2304 blocks. Calls that may overlap on the GPU need a
+ * no workspace, unless max_seq_len is more than 7500 blocks. Calls that may overlap on the GPU need a
  * workspace each. */
 int rc_sparse_decode_workspace_bytes(const rc_sparse_decode_args* args, size_t* out_bytes);
 int rc_sparse_decode_attention(const rc_sparse_decode_args* args, void* workspace,

@@ -45,6 +45,7 @@ constexpr int kMaxGroup = 16;      // query heads per KV head
 constexpr int kMaxTop = 8192;      // the list of chosen blocks is kept in shared memory
 constexpr int kMaxCluster = 16;
 constexpr int kSegment = 512;      // tokens whose slots are resolved at a time
+constexpr int kSmemBlocks = 7500;  // blocks whose scores and ranks are kept in shared memory (90 KB)
 constexpr int kEnoughCtas = 456;   // three per SM: more of them do not come sooner to their tokens
 
 struct Workspace {                 // used only when a unit's scores outgrow shared memory
@@ -60,6 +61,8 @@ struct Params {
   int G;         // query heads per KV head
   int cluster;   // CTAs per unit
   int* status;
+  // dynamic shared memory (see Cfg): where the scores, the histogram, the slots and the list begin
+  int score_at, hist_at, slots_at, list_at;
 };
 
 // Visible tokens of row n; 0 for an empty row (whatever its req_idx: a padded batch), and for one
@@ -74,8 +77,9 @@ __device__ __forceinline__ int row_len(const Params& p, int64_t n, bool report) 
   return L;
 }
 
-// Dynamic shared memory of a CTA: the copy rings (bf16), which first hold the unit's scores and
-// ranks and in the end the states to join; then the slots of a segment; then the chosen blocks.
+// Dynamic shared memory of a CTA: the copy rings, in whose place first the unit's 64-bit ranks, scores
+// and the selection's histogram stand and in the end the states to join; then the slots of a segment;
+// then the chosen blocks. With many blocks the first part outgrows the rings.
 constexpr int kBins = 2048;        // counters of the selection's radix steps
 
 template <typename T, int D, int GM>
@@ -89,15 +93,19 @@ struct Cfg {
   static constexpr int STATE = GM * D * 4;                    // o of one state
   static constexpr int WEIGHTS = kWarps * STAGES * STAGE;     // fp32: 64 words per warp
   static constexpr int RING = WEIGHTS + (kBf16 ? 0 : kWarps * 256);
-  static constexpr int NEED = RING > (kWarps + 1) * STATE ? RING : (kWarps + 1) * STATE;
-  static constexpr int BASE = NEED > 36864 ? NEED : 36864;
-  static constexpr int BLOCKS = BASE / 16;                    // a rank and a score take 12 bytes
-  static_assert(BASE >= (kWarps + 1) * STATE, "the states fit");
-  static constexpr int HIST = BLOCKS * 12;
-  static_assert(HIST % 4 == 0 && BASE - HIST >= kBins * 4, "the histogram fits beside them");
-  static constexpr int SLOTS = BASE;
-  static constexpr int LIST = BASE + kSegment * 4;
-  static int bytes(int top) { return LIST + top * 4; }
+  static constexpr int BASE = RING > (kWarps + 1) * STATE ? RING : (kWarps + 1) * STATE;
+
+  // Lays it out for p; returns its size.
+  static int layout(Params& p) {
+    const int blocks = p.nb <= kSmemBlocks ? (p.nb + 1) / 2 * 2 : 0;
+    p.score_at = blocks * 8;
+    p.hist_at = blocks * 12;
+    p.slots_at = (std::max(BASE, p.hist_at + kBins * 4) + 127) / 128 * 128;
+    p.list_at = p.slots_at + kSegment * 4;
+    return p.list_at + std::min(p.nb, p.a.top_blocks) * 4;
+  }
+  static constexpr int MOST = (BASE > kSmemBlocks * 12 + kBins * 4 ? BASE : kSmemBlocks * 12 +
+                               kBins * 4) + 128 + kSegment * 4 + kMaxTop * 4;
 };
 
 // ---------------------------------------------------------------- scores
@@ -260,43 +268,51 @@ __device__ __forceinline__ void score_blocks_f32(const Params& p, int64_t n, int
     for (int e = 0; e < E; ++e) q[h][e] = h < p.G ? src[h * D + e] : 0.f;
   const float* boxes = (const float*)a.bounds +
                        ((int64_t)a.req_idx[n] * a.max_blocks * a.num_kv_heads + g) * 2 * D + lane * E;
-  constexpr int NB = GM * E >= 32 ? 2 : 4;   // boxes in flight, as registers allow
+  constexpr int NB = GM >= 8 ? 2 : 4;   // boxes at a time: one warp per scheduler has to overlap itself
   for (int b0 = out.f0 + first; b0 < out.f1; b0 += NB * step) {
-    float lo[NB][E], hi[NB][E];
+    float lo[NB][E], hi[NB][E], s[NB][GM], t[NB], best[NB];
 #pragma unroll
-    for (int u = 0; u < NB; ++u) {
+    for (int u = 0; u < NB; ++u) {   // past the end: the last box again
       const float* box = boxes + (int64_t)min(b0 + u * step, out.f1 - 1) * a.num_kv_heads * 2 * D;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         lo[u][e] = box[e];
         hi[u][e] = box[D + e];
       }
+      t[u] = 0.f;
+    }
+#pragma unroll
+    for (int h = 0; h < GM; ++h) {
+#pragma unroll
+      for (int u = 0; u < NB; ++u) {
+        float x = 0.f, th = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float y = q[h][e] >= 0.f ? hi[u][e] : lo[u][e];
+          x = fmaf(q[h][e], y, x);
+          th = fmaf(fabsf(q[h][e]), fabsf(y), th);
+        }
+        s[u][h] = x;
+        t[u] = max_nan(t[u], h < p.G ? th : 0.f);
+      }
     }
 #pragma unroll
     for (int u = 0; u < NB; ++u) {
-      if (b0 + u * step >= out.f1) break;
-      float s[GM], t = 0.f;
+      best[u] = sum_values<GM>(s[u]);
+      if (lane / (32 / GM) >= p.G) best[u] = -INFINITY;
+    }
 #pragma unroll
-      for (int h = 0; h < GM; ++h) {
-        s[h] = 0.f;
-        float th = 0.f;
+    for (int o = 16; o; o >>= 1) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float x = q[h][e], y = x >= 0.f ? hi[u][e] : lo[u][e];
-          s[h] = fmaf(x, y, s[h]);
-          th = fmaf(fabsf(x), fabsf(y), th);
-        }
-        t = max_nan(t, h < p.G ? th : 0.f);
+      for (int u = 0; u < NB; ++u) {
+        t[u] += __shfl_xor_sync(0xffffffffu, t[u], o);
+        if (o >= 32 / GM) best[u] = max_nan(best[u], __shfl_xor_sync(0xffffffffu, best[u], o));
       }
-      float best = sum_values<GM>(s);
-      if (lane / (32 / GM) >= p.G) best = -INFINITY;
+    }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        t += __shfl_xor_sync(0xffffffffu, t, o);
-        if (o >= 32 / GM) best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, o));
-      }
-      out.tmax = max_nan(out.tmax, t);
-      out.put(b0 + u * step, best, lane, 32);
+    for (int u = 0; u < NB; ++u) {
+      out.tmax = max_nan(out.tmax, t[u]);
+      if (b0 + u * step < out.f1) out.put(b0 + u * step, best[u], lane, 32);
     }
   }
 }
@@ -1000,8 +1016,10 @@ __device__ __forceinline__ void join(int count, M m, L l, O o, float& mx, float&
   }
 }
 
+// (fp32 is held to the registers of four CTAs per SM, but for 16 heads of 128)
 template <typename T, int D, int GM>
-__global__ void __launch_bounds__(kThreads) sparse_decode_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 0 : D * GM > 1024 ? 2 : 4)
+    sparse_decode_kernel(Params p) {
   using C = Cfg<T, D, GM>;
   extern __shared__ __align__(128) char smem[];
   __shared__ SelectShared sh;
@@ -1018,8 +1036,8 @@ __global__ void __launch_bounds__(kThreads) sparse_decode_kernel(Params p) {
   const int shift = __ffs(a.block) - 1;
   const int have = (L + a.block - 1) >> shift;
   const int take = min(have, a.top_blocks);
-  int* slots = (int*)(smem + C::SLOTS);
-  int* list = (int*)(smem + C::LIST);
+  int* slots = (int*)(smem + p.slots_at);
+  int* list = (int*)(smem + p.list_at);
   const bool choose = take < have;   // else every block is taken and none is scored
   if (choose) {
     const int f0 = min(a.sink_blocks, have), f1 = max(f0, have - a.recent_blocks);
@@ -1027,9 +1045,9 @@ __global__ void __launch_bounds__(kThreads) sparse_decode_kernel(Params p) {
     for (int i = tid; i < f0; i += kThreads) list[i] = i;
     for (int i = tid; i < have - f1; i += kThreads) list[f0 + k + i] = f1 + i;
     if (k > 0) {
-      const bool own = p.nb <= C::BLOCKS;
+      const bool own = p.nb <= kSmemBlocks;
       unsigned long long* r64_s = (unsigned long long*)smem;
-      float* score_s = (float*)(r64_s + C::BLOCKS);
+      float* score_s = (float*)(smem + p.score_at);
       if (tid == 0) {
         sh.lo = 0xffffffffu;
         sh.hi = sh.tmax = 0;
@@ -1050,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads) sparse_decode_kernel(Params p) {
         atomicMax(&to->tmax, tb);
       }
       if (P > 1) cl.sync(); else __syncthreads();
-      int* hist = (int*)(smem + C::HIST);
+      int* hist = (int*)(smem + p.hist_at);
       if (own)
         select_blocks<T, D, true>(p, sh, hist, n, g, f0, m, k, score_s, r64_s, list + f0);
       else
@@ -1176,11 +1194,8 @@ Params params_of(const rc_sparse_decode_args* a) {
   return p;
 }
 
-// Whether a unit's scores and ranks stay in shared memory (see Cfg::BLOCKS, the smallest of them).
-bool needs_workspace(const Params& p) { return p.nb > 36864 / 16; }
-
 Workspace carve(void* base, const Params& p, size_t* total) {
-  const size_t cells = needs_workspace(p) ? (size_t)p.a.num_rows * p.a.num_kv_heads * p.nb : 0;
+  const size_t cells = p.nb > kSmemBlocks ? (size_t)p.a.num_rows * p.a.num_kv_heads * p.nb : 0;
   Workspace w{};
   char* b = (char*)base;
   w.rank = (unsigned long long*)b;
@@ -1198,17 +1213,18 @@ cudaError_t launch_t(const Params& p, cudaStream_t s) {
   cudaError_t e = setup.get(
       [&](int&) {
         cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             C::bytes(kMaxTop));
+                                             C::MOST);
         if (r == cudaSuccess)
           r = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         return r;
       },
       &unused);
   if (e != cudaSuccess) return e;
+  Params q = p;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)p.a.num_rows * p.a.num_kv_heads * p.cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::bytes(std::min(p.nb, p.a.top_blocks));
+  cfg.dynamicSmemBytes = C::layout(q);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1216,7 +1232,7 @@ cudaError_t launch_t(const Params& p, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  e = cudaLaunchKernelEx(&cfg, kernel, q);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

@@ -161,10 +161,10 @@ def test_sparse_decode_matches_the_definition(dtype, ctx, hq, hkv, d, block, top
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_more_blocks_than_shared_memory_holds(dtype):
-    """Contexts of 120 000 and 70 000 tokens in blocks of 16: the scores live in the workspace. The
+    """Contexts of 130 000 and 70 000 tokens in blocks of 16: the scores live in the workspace. The
     pool is small (slots repeat), the selection is checked over all blocks."""
     g = torch.Generator().manual_seed(7)
-    hq, hkv, d, block, n = 2, 1, 64, 16, (120_000, 70_001)
+    hq, hkv, d, block, n = 2, 1, 64, 16, (130_000, 70_001)
     c = Case(dtype, [600, 300], [(0, n[0]), (1, n[1])], hq, hkv, d, block)
     c.max_ctx = n[0]
     c.table = torch.randint(0, 900, (c.table.shape[0], n[0]), generator=g, dtype=torch.int32)
@@ -178,6 +178,13 @@ def test_more_blocks_than_shared_memory_holds(dtype):
     c.bounds[:, 77, 0, 1] = float("inf")
     c.call(90).check()
     assert 77 in c.sel[0, 0].tolist() and rc.device_status() == 0
+    # the most blocks that shared memory holds: no workspace
+    c.rows = [(0, 120_000), (1, 70_001)]
+    assert rc.sparse_decode_workspace_bytes(q, k, max_seq_len=120_000, block=block,
+                                            top_blocks=90) == 0
+    c.call(90).check()
+    c.bounds[:, 77, 0, 1] = 1.0
+    c.call(90).check()
 
 
 @pytest.mark.gpu
