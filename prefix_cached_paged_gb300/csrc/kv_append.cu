@@ -155,18 +155,18 @@ __device__ __forceinline__ uint4 splat(uint32_t x) { return make_uint4(x, x, x, 
 constexpr int kAppendStages = 2, kBoundsStages = 3;
 constexpr int kWarps = kThreads / 32;
 
-// A warp's lanes are 32 / L rows: `heads` KV heads beside one another (a power of two), the other
-// rows later tokens of the block. A group is TOK tokens of each row: 1 where there are warps enough to
-// hide a group's latency, 2 where there are few.
 // What a lane keeps of a token in the ring: 16-byte chunks of K (2 N) and V (2 N), four of its
 // angles, and the token's slot.
 template <typename T>
 constexpr int kTokenBytes = (4 * Raw<T>::N + 4) * 512 + 128;
-template <typename T, int TOK>
-constexpr int append_smem() { return kWarps * kAppendStages * TOK * kTokenBytes<T>; }
+template <typename T>
+constexpr int append_smem() { return kWarps * kAppendStages * kTokenBytes<T>; }
 
-template <typename T, int L, int TOK>
-__global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1)
+// A warp's lanes are 32 / L rows: `heads` KV heads beside one another (a power of two), the other
+// rows later tokens of the block; one token of each row is a group. kShare: an item is a whole CTA's,
+// its warps taking groups in turn and joining their extremes at the end.
+template <typename T, int L, bool kShare>
+__global__ void __launch_bounds__(kThreads, 3)
     kv_append_kernel(rc_kv_append_args a, int heads, int* status) {
   constexpr int N = Raw<T>::N;
   extern __shared__ __align__(128) char ring[];
@@ -176,17 +176,20 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1)
   const bool inter = a.interleaved != 0;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int i = lane % L, row_in = lane / L;
-  const int hl = row_in & (heads - 1), w = row_in / heads, W = 32 / L / heads;
+  const int hl = row_in & (heads - 1), w = row_in / heads;
+  // this row has every W-th token, from its w0-th on
+  const int W = 32 / L / heads * (kShare ? kWarps : 1);
+  const int w0 = kShare ? wid * (32 / L / heads) + w : w;
   const int head_groups = (a.num_kv_heads + heads - 1) / heads;
   const LaneChunks lc = lane_chunks(i, d, r, inter);
   const T* kw = (const T*)a.k_weight;
-  // chunk c (K, V, angles) of token u of stage st of this lane, and the token's slot
-  char* warp_ring = ring + wid * (kAppendStages * TOK * kTokenBytes<T>);
-  auto cell_of = [&](int st, int u, int c) {
-    return warp_ring + (st * TOK + u) * kTokenBytes<T> + c * 512 + lane * 16;
+  // chunk c (K, V, angles) of the token in stage st of this lane, and the token's slot
+  char* warp_ring = ring + wid * (kAppendStages * kTokenBytes<T>);
+  auto cell_of = [&](int st, int c) {
+    return warp_ring + st * kTokenBytes<T> + c * 512 + lane * 16;
   };
-  auto slot_of = [&](int st, int u) {
-    return (int*)(warp_ring + (st * TOK + u + 1) * kTokenBytes<T> - 128 + lane * 4);
+  auto slot_of = [&](int st) {
+    return (int*)(warp_ring + (st + 1) * kTokenBytes<T> - 128 + lane * 4);
   };
 
   for (int b0 = 0; b0 < a.num_reqs; b0 += kWindow) {
@@ -196,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1)
       return s.S ? (s.P + s.S - 1) / a.block - s.P / a.block + 1 : 0;
     });
     const int64_t items = (int64_t)off[kWindow] * head_groups;
-    for (int64_t it = next_item(&taken, items); it < items; it = next_item(&taken, items)) {
+    int64_t it = kShare ? blockIdx.x : next_item(&taken, items);
+    for (; it < items; it = kShare ? it + gridDim.x : next_item(&taken, items)) {
       const int job = (int)(it / head_groups), hg = (int)(it - (int64_t)job * head_groups);
       const int k = find_request(off, nreq, job);
       const Span s = span_of(a, b0 + k, status, false);
@@ -209,35 +213,30 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1)
       const bool m0 = mine && lc.c0 >= 0, m1 = mine && lc.c1 >= 0;
       const T* ksrc = (const T*)a.k + tok0 * a.k_token_stride + (int64_t)h * a.k_head_stride;
       const T* vsrc = (const T*)a.v + tok0 * a.v_token_stride + (int64_t)h * a.v_head_stride;
-      const int groups = (n + W * TOK - 1) / (W * TOK);
+      const int groups = (n + W - 1) / W;
       auto issue = [&](int gr) {
-        if (gr < groups) {
+        const int at = gr * W + w0;
+        if (gr < groups && mine && at < n) {
           const int st = gr % kAppendStages;
+          cp_async4(smem_u32(slot_of(st)), a.out_loc + tok0 + at);
+          if (lc.rot) {
+            const float* row = a.rope + (int64_t)(p0 + at) * r + 8 * i;
+            cp_async16_l1(smem_u32(cell_of(st, 4 * N)), row);
+            cp_async16_l1(smem_u32(cell_of(st, 4 * N + 1)), row + 4);
+            cp_async16_l1(smem_u32(cell_of(st, 4 * N + 2)), row + (r >> 1));
+            cp_async16_l1(smem_u32(cell_of(st, 4 * N + 3)), row + (r >> 1) + 4);
+          }
+          const T* ks = ksrc + at * a.k_token_stride;
+          const T* vs = vsrc + at * a.v_token_stride;
 #pragma unroll
-          for (int u = 0; u < TOK; ++u) {
-            const int at = (gr * TOK + u) * W + w;
-            const T* ks = ksrc + at * a.k_token_stride;
-            const T* vs = vsrc + at * a.v_token_stride;
-            if (mine && at < n) {
-              cp_async4(smem_u32(slot_of(st, u)), a.out_loc + tok0 + at);
-              if (lc.rot) {
-                const float* row = a.rope + (int64_t)(p0 + at) * r + 8 * i;
-                cp_async16_l1(smem_u32(cell_of(st, u, 4 * N)), row);
-                cp_async16_l1(smem_u32(cell_of(st, u, 4 * N + 1)), row + 4);
-                cp_async16_l1(smem_u32(cell_of(st, u, 4 * N + 2)), row + (r >> 1));
-                cp_async16_l1(smem_u32(cell_of(st, u, 4 * N + 3)), row + (r >> 1) + 4);
-              }
+          for (int c = 0; c < N; ++c) {
+            if (m0) {
+              cp_async16(smem_u32(cell_of(st, c)), (const uint4*)(ks + lc.c0 * 8) + c);
+              cp_async16(smem_u32(cell_of(st, 2 * N + c)), (const uint4*)(vs + lc.c0 * 8) + c);
             }
-#pragma unroll
-            for (int c = 0; c < N; ++c) {
-              if (m0 && at < n) {
-                cp_async16(smem_u32(cell_of(st, u, c)), (const uint4*)(ks + lc.c0 * 8) + c);
-                cp_async16(smem_u32(cell_of(st, u, 2 * N + c)), (const uint4*)(vs + lc.c0 * 8) + c);
-              }
-              if (m1 && at < n) {
-                cp_async16(smem_u32(cell_of(st, u, N + c)), (const uint4*)(ks + lc.c1 * 8) + c);
-                cp_async16(smem_u32(cell_of(st, u, 3 * N + c)), (const uint4*)(vs + lc.c1 * 8) + c);
-              }
+            if (m1) {
+              cp_async16(smem_u32(cell_of(st, N + c)), (const uint4*)(ks + lc.c1 * 8) + c);
+              cp_async16(smem_u32(cell_of(st, 3 * N + c)), (const uint4*)(vs + lc.c1 * 8) + c);
             }
           }
         }
@@ -253,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1)
         lo0.v[c] = lo1.v[c] = splat(Extremes<T>::kLo);
         hi0.v[c] = hi1.v[c] = splat(Extremes<T>::kHi);
       }
-      if (a.bounds && w == 0 && blk * a.block < s.P) {   // cached tokens began the block
+      if (a.bounds && w0 == 0 && blk * a.block < s.P) {   // cached tokens began the block
         if (m0) {
           lo0.load(cell + lc.c0 * 8);
           hi0.load(cell + d + lc.c0 * 8);
@@ -267,54 +266,51 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1)
         issue(gr + kAppendStages - 1);
         const int st = gr % kAppendStages;
         cp_async_wait<kAppendStages - 1>();
+        bool live = mine && gr * W + w0 < n;
+        const int slot = live ? *slot_of(st) : 0;
+        if (live && (slot < 0 || slot >= a.num_slots)) {
+          if (i == 0) set_status(status, kStatusSlotRange);
+          live = false;
+        }
+        Raw<T> x0, x1;
+        x0.clear();
+        x1.clear();
 #pragma unroll
-        for (int u = 0; u < TOK; ++u) {
-          bool live = mine && (gr * TOK + u) * W + w < n;
-          const int slot = live ? *slot_of(st, u) : 0;
-          if (live && (slot < 0 || slot >= a.num_slots)) {
-            if (i == 0) set_status(status, kStatusSlotRange);
-            live = false;
+        for (int c = 0; c < N; ++c) {
+          if (m0 && live) x0.v[c] = *(const uint4*)cell_of(st, c);
+          if (m1 && live) x1.v[c] = *(const uint4*)cell_of(st, N + c);
+        }
+        const int64_t dst = ((int64_t)slot * a.num_kv_heads + h) * d;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          if (m0 && live)
+            ((uint4*)((T*)a.v_pool + dst + lc.c0 * 8))[c] = *(const uint4*)cell_of(st, 2 * N + c);
+          if (m1 && live)
+            ((uint4*)((T*)a.v_pool + dst + lc.c1 * 8))[c] = *(const uint4*)cell_of(st, 3 * N + c);
+        }
+        if (kw || r) {
+          ScalarRow row;
+          row.get(x0, x1);
+          if (kw) row.scale(row.template norm_scale<L>(d, a.eps), kw, lc);
+          if (lc.rot) {
+            float cs[8], sn[8];
+            *(float4*)cs = *(const float4*)cell_of(st, 4 * N);
+            *(float4*)(cs + 4) = *(const float4*)cell_of(st, 4 * N + 1);
+            *(float4*)sn = *(const float4*)cell_of(st, 4 * N + 2);
+            *(float4*)(sn + 4) = *(const float4*)cell_of(st, 4 * N + 3);
+            row.rotate(cs, sn, inter);
           }
-          Raw<T> x0, x1;
-          x0.clear();
-          x1.clear();
+          row.set(x0, x1);
+        }
+        if (m0 && live) x0.store((T*)a.k_pool + dst + lc.c0 * 8);
+        if (m1 && live) x1.store((T*)a.k_pool + dst + lc.c1 * 8);
+        if (a.bounds && live) {   // the extremes of the stored (rounded) keys
 #pragma unroll
           for (int c = 0; c < N; ++c) {
-            if (m0 && live) x0.v[c] = *(const uint4*)cell_of(st, u, c);
-            if (m1 && live) x1.v[c] = *(const uint4*)cell_of(st, u, N + c);
-          }
-          const int64_t dst = ((int64_t)slot * a.num_kv_heads + h) * d;
-#pragma unroll
-          for (int c = 0; c < N; ++c) {
-            if (m0 && live)
-              ((uint4*)((T*)a.v_pool + dst + lc.c0 * 8))[c] = *(const uint4*)cell_of(st, u, 2 * N + c);
-            if (m1 && live)
-              ((uint4*)((T*)a.v_pool + dst + lc.c1 * 8))[c] = *(const uint4*)cell_of(st, u, 3 * N + c);
-          }
-          if (kw || r) {
-            ScalarRow row;
-            row.get(x0, x1);
-            if (kw) row.scale(row.template norm_scale<L>(d, a.eps), kw, lc);
-            if (lc.rot) {
-              float cs[8], sn[8];
-              *(float4*)cs = *(const float4*)cell_of(st, u, 4 * N);
-              *(float4*)(cs + 4) = *(const float4*)cell_of(st, u, 4 * N + 1);
-              *(float4*)sn = *(const float4*)cell_of(st, u, 4 * N + 2);
-              *(float4*)(sn + 4) = *(const float4*)cell_of(st, u, 4 * N + 3);
-              row.rotate(cs, sn, inter);
-            }
-            row.set(x0, x1);
-          }
-          if (m0 && live) x0.store((T*)a.k_pool + dst + lc.c0 * 8);
-          if (m1 && live) x1.store((T*)a.k_pool + dst + lc.c1 * 8);
-          if (a.bounds && live) {   // the extremes of the stored (rounded) keys
-#pragma unroll
-            for (int c = 0; c < N; ++c) {
-              lower<T>(lo0.v[c], x0.v[c]);
-              raise<T>(hi0.v[c], x0.v[c]);
-              lower<T>(lo1.v[c], x1.v[c]);
-              raise<T>(hi1.v[c], x1.v[c]);
-            }
+            lower<T>(lo0.v[c], x0.v[c]);
+            raise<T>(hi0.v[c], x0.v[c]);
+            lower<T>(lo1.v[c], x1.v[c]);
+            raise<T>(hi1.v[c], x1.v[c]);
           }
         }
       }
@@ -329,11 +325,32 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 3 : 1)
           raise<T>(hi1.v[c], shfl_xor4(hi1.v[c], o));
         }
       }
-      if (w == 0 && m0) {
+      if (kShare) {   // join the warps, through their rings
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          *(uint4*)cell_of(0, c) = lo0.v[c];
+          *(uint4*)cell_of(0, N + c) = lo1.v[c];
+          *(uint4*)cell_of(0, 2 * N + c) = hi0.v[c];
+          *(uint4*)cell_of(0, 3 * N + c) = hi1.v[c];
+        }
+        __syncthreads();
+        for (int v = 1; v < kWarps && wid == 0; ++v) {
+          const char* theirs = cell_of(0, 0) + v * (kAppendStages * kTokenBytes<T>);
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            lower<T>(lo0.v[c], *(const uint4*)(theirs + c * 512));
+            lower<T>(lo1.v[c], *(const uint4*)(theirs + (N + c) * 512));
+            raise<T>(hi0.v[c], *(const uint4*)(theirs + (2 * N + c) * 512));
+            raise<T>(hi1.v[c], *(const uint4*)(theirs + (3 * N + c) * 512));
+          }
+        }
+        __syncthreads();
+      }
+      if (w0 == 0 && m0) {
         lo0.store(cell + lc.c0 * 8);
         hi0.store(cell + d + lc.c0 * 8);
       }
-      if (w == 0 && m1) {
+      if (w0 == 0 && m1) {
         lo1.store(cell + lc.c1 * 8);
         hi1.store(cell + d + lc.c1 * 8);
       }
@@ -495,19 +512,21 @@ int launch_append(const char* fn, const rc_kv_append_args& args, int* st, cudaSt
   const bool prompts = a.num_tokens >= 16 * (int64_t)a.num_reqs;
   const int heads = std::min(pow2_at_least(a.num_kv_heads), prompts ? std::max(1, 8 / L) : 32 / L);
   const int groups = (a.num_kv_heads + heads - 1) / heads;
-  // Few items: two tokens of a row in flight, which takes registers and so CTAs from the SM (the
-  // 80 x 200 tokens 114 us so, 93 without; 2 000 fp32 tokens of 2 heads 11 us so, 16 without).
-  const bool few = a.num_tokens / a.block * groups < (int64_t)sms * 8 * 2;
-  if (!a.bounds && few) a.block = 16;   // without bounds an item is any run of tokens
+  // Few items: without bounds an item is any run of tokens, so it is made a short one (2 000 fp32
+  // tokens of 2 heads: 11 us so, 24 with 64 tokens each); with bounds the warps of a CTA share a block
+  // (8 requests x 300 .. 600 tokens, 2 heads: 10.5 us so, 16.6 with a warp each and two tokens in
+  // flight; 5 x 1 .. 46 tokens in blocks of 128: 9.1 against 14.4; 40 x 200 tokens of 8 heads, near the
+  // rule's border: 23.9 against 22.7).
+  const bool few = prompts && a.num_tokens / a.block * groups < (int64_t)sms * kWarps * 2;
+  if (few && !a.bounds) a.block = 16;
   // blocks the tokens can touch: each request begins and ends inside at most two more
   const int64_t items = (a.num_tokens / a.block + 2 * (int64_t)a.num_reqs) * groups;
-  static PerDevice<int> one, more;
-  constexpr int kMore = 2;
-  if (prompts && few)
-    return launch_resident(fn, kv_append_kernel<T, L, kMore>, more, items, a, heads,
-                           append_smem<T, kMore>(), st, s);
-  return launch_resident(fn, kv_append_kernel<T, L, 1>, one, items, a, heads, append_smem<T, 1>(), st,
-                         s);
+  static PerDevice<int> alone, shared;
+  if (few && a.bounds)
+    return launch_resident(fn, kv_append_kernel<T, L, true>, shared, items, a, heads,
+                           append_smem<T>(), st, s);
+  return launch_resident(fn, kv_append_kernel<T, L, false>, alone, items, a, heads, append_smem<T>(),
+                         st, s);
 }
 
 template <typename T>

@@ -20,8 +20,12 @@
 //   128 rows, 32 + 32 heads, contexts 512 .. 8192, 16 blocks of 64: 334 us, 6.5 TB/s, 97 % of the
 //     copy rate; 64 rows, 32 + 8 heads, contexts 4096 .. 32768, 64 blocks: 200 us, 5.7 TB/s, 85 % (a
 //     CTA scores, waits and selects for ~8 us of its ~60; four of them share an SM).
-//   1 row, 64 + 8 heads, 131071 tokens, 64 blocks: 26 us: score 4, cluster barriers 5, select 4 to
-//     11 (the longer where finer scores are needed), slots 1, 256 tokens 4, join 2.
+//   1 row, 64 + 8 heads, 131071 tokens, 64 blocks: 27 us: score 4, cluster barriers 5, select 4 to
+//     11 (the longer where finer scores are needed), slots 1, 256 tokens 4, join 2. A fifth of the
+//     stalls there is instruction fetch: every step runs once.
+//   fp32, heads of 128, 4096 or 2048 selected tokens: 32 rows, 8 + 8 heads 117 us of a floor of 90; 64
+//     rows, 32 + 4 heads 127 of 86; 64 rows, 32 + 2 heads 258 of 86, bound by its 16 products per key
+//     element on the CUDA cores (scores summed one by one over the lanes: 146, 436, 817 us).
 // On the way, for the three: separate kernels for scores, selection, attention and merge, all scores
 // in 64 bits and attention on CUDA cores 1093, 1399, 334 us; scores on matrix instructions 710, 728,
 // 141; attention too, the last CTA of a row merging 417, 263, 126 (the merge of 64 parts alone 80);
@@ -450,6 +454,7 @@ __device__ K kth_largest(SelectShared& s, int* hist, int n, int left, int k, K l
 // Where many blocks tie (all keys alike, a query of zeros) every one of them is ranked so, and the
 // adders of a GB300 SM for doubles are few: one row of 2048 tied blocks takes 0.44 ms, 512 units of
 // 64 .. 512 tied blocks 1.4 ms.
+//
 // The 64-bit rank of block b: the largest score over the KV head's queries. One warp, four queries
 // at a time so that their loads and sums overlap.
 template <typename T, int D>
