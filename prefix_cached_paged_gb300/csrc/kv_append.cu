@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       const int blk = s.P / a.block + (job - off[k]);
       const int p0 = max(s.P, blk * a.block);
       const int n = (int)(min((int64_t)s.P + s.S, (int64_t)(blk + 1) * a.block) - p0);
+      if (n <= 0) continue;   // offsets so wrong that their items cannot be counted
       const int64_t tok0 = (int64_t)s.t0 + (p0 - s.P);
       const int h = hg * heads + hl;
       const bool mine = h < a.num_kv_heads;

@@ -122,7 +122,8 @@ class Engine:
                     self.rope.shape[0] < max_ctx:
                 raise ValueError(f"rope must be an fp32 table of at least {max_ctx} positions")
         # sparse_block: positions per block of the bounds that sparse_layer selects blocks by
-        # (16, 32, 64 or 128; 0: no bounds are kept)
+        # (16, 32, 64 or 128; 0: no bounds are kept). They take two elements per block, KV head and
+        # dimension of every slot-table row: 2 / sparse_block of the keys that full rows would hold
         self.sparse_block = int(sparse_block)
         if self.sparse_block:
             if self.sparse_block not in (16, 32, 64, 128):
