@@ -18,13 +18,13 @@
 // Bound by HBM (boxes of a row once, K and V of the selected tokens once per KV head) with many rows,
 // by the chain of dependent steps with few. Measured, bf16, heads of 128, inputs beyond L2:
 //   128 rows, 32 + 32 heads, contexts 512 .. 8192, 16 blocks of 64: 334 us, 6.5 TB/s, 97 % of the
-//     copy rate; 64 rows, 32 + 8 heads, contexts 4096 .. 32768, 64 blocks: 200 us, 5.7 TB/s, 85 % (a
+//     copy rate; 64 rows, 32 + 8 heads, contexts 4096 .. 32768, 64 blocks: 204 us, 5.6 TB/s, 83 % (a
 //     CTA scores, waits and selects for ~8 us of its ~60; four of them share an SM).
 //   1 row, 64 + 8 heads, 131071 tokens, 64 blocks: 27 us: score 4, cluster barriers 5, select 4 to
 //     11 (the longer where finer scores are needed), slots 1, 256 tokens 4, join 2. A fifth of the
 //     stalls there is instruction fetch: every step runs once.
-//   fp32, heads of 128, 4096 or 2048 selected tokens: 32 rows, 8 + 8 heads 117 us of a floor of 90; 64
-//     rows, 32 + 4 heads 127 of 86; 64 rows, 32 + 2 heads 258 of 86, bound by its 16 products per key
+//   fp32, heads of 128, 4096 or 2048 selected tokens: 32 rows, 8 + 8 heads 115 us of a floor of 90; 64
+//     rows, 32 + 4 heads 127 of 86; 64 rows, 32 + 2 heads 244 of 86, bound by its 16 products per key
 //     element on the CUDA cores (scores summed one by one over the lanes: 146, 436, 817 us).
 // On the way, for the three: separate kernels for scores, selection, attention and merge, all scores
 // in 64 bits and attention on CUDA cores 1093, 1399, 334 us; scores on matrix instructions 710, 728,
@@ -50,7 +50,7 @@ constexpr int kMaxTop = 8192;      // the list of chosen blocks is kept in share
 constexpr int kMaxCluster = 16;
 constexpr int kSegment = 512;      // tokens whose slots are resolved at a time
 constexpr int kSmemBlocks = 7500;  // blocks whose scores and ranks are kept in shared memory (90 KB)
-constexpr int kEnoughCtas = 456;   // three per SM: more of them do not come sooner to their tokens
+constexpr int kResident = 608;     // CTAs on the GPU at once: four per SM, but two with 16 heads of 128
 
 struct Workspace {                 // used only when a unit's scores outgrow shared memory
   float* score;                    // [units * nb]
@@ -1185,16 +1185,19 @@ Params params_of(const rc_sparse_decode_args* a) {
   p.a = *a;
   p.G = a->num_q_heads / a->num_kv_heads;
   p.nb = std::max(1, (a->max_seq_len + a->block - 1) / a->block);
-  // CTAs per unit: until the GPU is full, while each still has two stages for every warp; with more
-  // units, until a CTA's part is at most 2048 tokens, so that the last wave of CTAs stays short.
-  // One row of 4096 selected tokens and 8 heads: 26 us with 16 CTAs per unit, 31 with 8, 46 with 4.
-  // 110 units of 288 tokens: 16.7 us with 4, 22.5 with 2, 20.6 with 8. 512 units of 4096 tokens:
-  // 200 us with 2, 245 with 1, 214 with 4, 240 with 8; 4096 units of 1024: 334 us with 1, 389 with 2.
+  // CTAs per unit (us, contexts of 8192 in blocks of 64). Few units are split while the CTAs stay
+  // resident at once and each has two stages for every warp: beyond that a split only adds joins (bf16,
+  // 32+8 heads of 128, 16 blocks read: 40 units 16.0 in one wave, 30.3 with twice the CTAs, 96 units
+  // 20.0 and 32.5, 320 units 50.0 and 68.7; fp32, 8+8 heads, 40 units 17.1 and 32.8). More units than
+  // are resident are split where a CTA would read over 2048 tokens, which shortens the last wave (640
+  // units of 64 blocks: bf16 266 split, 307 whole; fp32 475 and 550); fewer are not (320 units of 64
+  // blocks: 135 whole, 174 split).
   const int64_t units = (int64_t)a->num_rows * a->num_kv_heads;
   const int64_t tokens = (int64_t)std::min(p.nb, a->top_blocks) * a->block;
+  const int64_t resident = a->head_dim == 128 && p.G > 8 ? kResident / 2 : kResident;
   p.cluster = 1;
   while (p.cluster < kMaxCluster && tokens >= 128 * p.cluster &&
-         (units * p.cluster < kEnoughCtas || tokens > 2048 * p.cluster))
+         (2 * units * p.cluster <= resident || (units > resident && tokens > 2048 * p.cluster)))
     p.cluster *= 2;
   return p;
 }
