@@ -510,7 +510,7 @@ int rc_decode_attention_noalloc(const rc_decode_args* args, void* stream);
  * num_kv_heads 0: that part is left out. positions [T] device int32; a token whose position is
  * outside [0, max_position) sets the device status word and its rows are not written.
  * head_dim a multiple of 8 up to 256, rotary_dim a multiple of 16; pointers and strides multiples
- * of 16 bytes. */
+ * of 16 bytes; num_tokens <= 2^24. */
 typedef struct rc_qk_norm_rope_args {
   int32_t dtype;
   int32_t num_q_heads;
@@ -555,7 +555,7 @@ int rc_rope_table(const double* inv_freq, int32_t num_pairs, int64_t first_posit
  * status word and is skipped; so is a token whose slot is outside the pool. A request without new
  * tokens is passed over, whatever its prefix_len and req_idx.
  * k, v [T, Hkv, d] with strides in elements, heads' elements contiguous; head_dim, rotary_dim and
- * alignment as for rc_qk_norm_rope. */
+ * alignment as for rc_qk_norm_rope; num_tokens <= 2^24. */
 typedef struct rc_kv_append_args {
   int32_t dtype;
   int32_t num_reqs;

@@ -30,6 +30,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRun = 4;         // items a CTA takes beside one another
 constexpr int kWindow = 1024;   // requests whose item offsets a CTA holds at a time
+// Tokens of a call: a window's items can then be counted in 32 bits whatever the offsets hold (each
+// request passed on is within the tokens, so has at most kMaxAppend / 16 + 1 items).
+constexpr int kMaxAppend = 1 << 24;
 
 // off[k] = items of the window's requests before k (off[n] = all), each of n <= kWindow requests
 // having count(k) items; none taken yet. All threads of the CTA call it.
@@ -207,7 +210,6 @@ __global__ void __launch_bounds__(kThreads, 3)
       const int blk = s.P / a.block + (job - off[k]);
       const int p0 = max(s.P, blk * a.block);
       const int n = (int)(min((int64_t)s.P + s.S, (int64_t)(blk + 1) * a.block) - p0);
-      if (n <= 0) continue;   // offsets so wrong that their items cannot be counted
       const int64_t tok0 = (int64_t)s.t0 + (p0 - s.P);
       const int h = hg * heads + hl;
       const bool mine = h < a.num_kv_heads;
@@ -557,7 +559,7 @@ extern "C" int rc_kv_append(const rc_kv_append_args* a, void* stream) {
   static const char* fn = "rc_kv_append";
   RC_CHECK_ARG(a != nullptr, "%s: args is NULL", fn);
   RC_CHECK_ARG(a->dtype == RC_DTYPE_BF16 || a->dtype == RC_DTYPE_F32, "%s: dtype %d", fn, a->dtype);
-  RC_CHECK_ARG(a->num_reqs >= 0 && a->num_tokens >= 0 && a->num_tokens <= 0x7fffffff &&
+  RC_CHECK_ARG(a->num_reqs >= 0 && a->num_tokens >= 0 && a->num_tokens <= rc::kMaxAppend &&
                    a->num_kv_heads > 0 && a->num_kv_heads <= 65536 && a->num_slots > 0,
                "%s: bad sizes", fn);
   const int c = rc::check_norm_rope(fn, a->head_dim, a->rotary_dim, a->max_position, a->rope, a->eps,

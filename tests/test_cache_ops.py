@@ -104,6 +104,19 @@ def test_append_and_bounds_reject_bad_arguments_before_any_device_work():
     assert bounds(num_rows=0) == rc.RC_OK
 
 
+def test_calls_of_more_than_2_24_tokens_are_refused():
+    """Items of an append are counted in 32 bits, 1024 requests together."""
+    from prefix_cached_paged_gb300._lib import RcKvAppendArgs, RcQkNormRopeArgs, lib
+    a = RcKvAppendArgs(dtype=rc.RC_DTYPE_BF16, num_reqs=2000, num_kv_heads=1, head_dim=64, block=16,
+                       num_tokens=(1 << 24) + 1, num_slots=1 << 26,
+                       **{n: _fake(i) for i, n in enumerate(["k", "v", "out_loc", "qo_indptr",
+                                                             "prefix_len", "k_pool", "v_pool"])})
+    assert lib().rc_kv_append(ctypes.byref(a), None) == rc.RC_ERR_INVALID
+    a = RcQkNormRopeArgs(dtype=rc.RC_DTYPE_BF16, num_q_heads=1, head_dim=64, eps=1e-6,
+                         num_tokens=(1 << 24) + 1, q=_fake(0), q_out=_fake(0), q_weight=_fake(1))
+    assert lib().rc_qk_norm_rope(ctypes.byref(a), None) == rc.RC_ERR_INVALID
+
+
 # ---------------------------------------------------------------------------------- norms, rotation
 CASES = [  # dtype, T, hq, hkv, d, rot, interleaved, norm
     ("bf16", 1, 1, 1, 128, 128, False, True),
