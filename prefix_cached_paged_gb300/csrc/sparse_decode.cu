@@ -50,7 +50,7 @@ constexpr int kMaxTop = 8192;      // the list of chosen blocks is kept in share
 constexpr int kMaxCluster = 16;
 constexpr int kSegment = 512;      // tokens whose slots are resolved at a time
 constexpr int kSmemBlocks = 7500;  // blocks whose scores and ranks are kept in shared memory (90 KB)
-constexpr int kResident = 608;     // CTAs on the GPU at once: four per SM, but two with 16 heads of 128
+constexpr int kSms = 152;
 
 struct Workspace {                 // used only when a unit's scores outgrow shared memory
   float* score;                    // [units * nb]
@@ -94,6 +94,10 @@ struct Cfg {
   static constexpr int RB = D * 2, RS = RB + 16;              // bytes of a row, padded
   static constexpr int TB = GM == 16 ? 2 : 4;                 // fp32: K and V of TB tokens
   static constexpr int STAGE = kBf16 ? TOK * RS : 2 * TB * D * 4;
+  // 16 heads of 128 keep their queries in shared memory: 168 registers and three CTAs per SM, not 181
+  // and two (64 blocks of 64 read, 160, 320 and 640 units: 92, 157, 281 us, and 131, 226, 379)
+  static constexpr bool Q_SHARED = kBf16 && GM * D > 1024;
+  static constexpr int QUERIES = Q_SHARED ? GM * RS : 0;
   static constexpr int STATE = GM * D * 4;                    // o of one state
   static constexpr int WEIGHTS = kWarps * STAGES * STAGE;     // fp32: 64 words per warp
   static constexpr int RING = WEIGHTS + (kBf16 ? 0 : kWarps * 256);
@@ -105,11 +109,11 @@ struct Cfg {
     p.score_at = blocks * 8;
     p.hist_at = blocks * 12;
     p.slots_at = (std::max(BASE, p.hist_at + kBins * 4) + 127) / 128 * 128;
-    p.list_at = p.slots_at + kSegment * 4;
+    p.list_at = p.slots_at + kSegment * 4 + QUERIES;   // (the queries lie after the slots)
     return p.list_at + std::min(p.nb, p.a.top_blocks) * 4;
   }
   static constexpr int MOST = (BASE > kSmemBlocks * 12 + kBins * 4 ? BASE : kSmemBlocks * 12 +
-                               kBins * 4) + 128 + kSegment * 4 + kMaxTop * 4;
+                               kBins * 4) + 128 + kSegment * 4 + QUERIES + kMaxTop * 4;
 };
 
 // ---------------------------------------------------------------- scores
@@ -707,30 +711,42 @@ __device__ __forceinline__ void select_blocks(const Params& p, SelectShared& sh,
 // its own ring: 16-byte copies of the tokens' K and V rows, completion by copy groups. The two
 // contractions run on warp-level matrix instructions with the tokens as M and the KV head's query
 // heads as N (NT tiles of 8): S^T = K Q^T, O^T += V^T P^T. K fragments by ldmatrix, V^T by its
-// transposing form (rows padded by 16 bytes: no bank conflicts), Q^T in registers, P^T from the
-// accumulators by movmatrix. P goes in as a bf16 part and its bf16 remainder, so P.V keeps 16 bits
+// transposing form (rows padded by 16 bytes: no bank conflicts), Q^T in registers (16 heads of 128: shared memory), P^T
+// from the accumulators by movmatrix. P goes in as a bf16 part and its bf16 remainder, so P.V keeps 16 bits
 // of the weights.
 template <int D, int NT>
 struct AttendMma {
   using C = Cfg<__nv_bfloat16, D, 8 * NT>;
   static constexpr int KS = D / 16;
-  uint32_t qb[NT][KS][2];
+  uint32_t qb[C::Q_SHARED ? 1 : NT][C::Q_SHARED ? 1 : KS][2];
   float acc[NT][KS][4], m[NT][2], l[NT][2];
 
   static __device__ __forceinline__ int next1(int b) { return b == 2 ? 0 : b + 1; }
   static __device__ __forceinline__ int next2(int b) { return b == 0 ? 2 : b - 1; }
 
-  __device__ __forceinline__ void begin(const Params& p, int64_t n, int g) {
+  // (the queries in shared memory: before the CTA's next barrier)
+  __device__ __forceinline__ void begin(const Params& p, char* smem, int64_t n, int g) {
     const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    const __nv_bfloat16* q0 = (const __nv_bfloat16*)p.a.q +
+                              (n * p.a.num_q_heads + (int64_t)g * p.G) * D;
+    if constexpr (C::Q_SHARED) {
+      char* to = smem + p.slots_at + kSegment * 4;
+      for (int x = threadIdx.x; x < NT * 8 * (D / 8); x += kThreads) {
+        const int h = x / (D / 8), c = x % (D / 8);
+        *(uint4*)(to + h * C::RS + c * 16) =
+            h < p.G ? ((const uint4*)(q0 + h * D))[c] : make_uint4(0, 0, 0, 0);
+      }
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int h = t * 8 + gid;
-      const __nv_bfloat16* q = (const __nv_bfloat16*)p.a.q +
-                               (n * p.a.num_q_heads + (int64_t)g * p.G + (h < p.G ? h : 0)) * D;
+      if constexpr (!C::Q_SHARED) {
+        const int h = t * 8 + gid;
+        const __nv_bfloat16* q = q0 + (h < p.G ? h : 0) * D;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        qb[t][k][0] = h < p.G ? *(const uint32_t*)(q + k * 16 + tig * 2) : 0u;
-        qb[t][k][1] = h < p.G ? *(const uint32_t*)(q + k * 16 + tig * 2 + 8) : 0u;
+        for (int k = 0; k < KS; ++k) {
+          qb[t][k][0] = h < p.G ? *(const uint32_t*)(q + k * 16 + tig * 2) : 0u;
+          qb[t][k][1] = h < p.G ? *(const uint32_t*)(q + k * 16 + tig * 2 + 8) : 0u;
+        }
       }
       m[t][0] = m[t][1] = -INFINITY;
       l[t][0] = l[t][1] = 0.f;
@@ -767,6 +783,7 @@ struct AttendMma {
       cp_async_commit();
     };
     const float qscale = p.a.sm_scale * kLog2e;
+    const uint32_t qs = smem_u32(smem) + p.slots_at + kSegment * 4;
     const int k_row = (lane & 7) + ((lane >> 3) & 1) * 8, k_col = (lane >> 4) * 8;
     const int v_row = (lane & 7) + (lane >> 4) * 8, v_col = ((lane >> 3) & 1) * 8;
     issue(0, 0);
@@ -784,9 +801,16 @@ struct AttendMma {
       for (int k = 0; k < KS; ++k) {
         uint32_t r[4];
         ldmatrix_x4(kb + k_row * C::RS + (k * 16 + k_col) * 2, r);
+        if constexpr (C::Q_SHARED) {
+          uint32_t b[4];   // two tiles of heads
+          ldmatrix_x4(qs + v_row * C::RS + (k * 16 + v_col) * 2, b);
+          mma_bf16(sc[0], r[0], r[1], r[2], r[3], b[0], b[1]);
+          mma_bf16(sc[1], r[0], r[1], r[2], r[3], b[2], b[3]);
+        } else {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          mma_bf16(sc[t], r[0], r[1], r[2], r[3], qb[t][k][0], qb[t][k][1]);
+          for (int t = 0; t < NT; ++t)
+            mma_bf16(sc[t], r[0], r[1], r[2], r[3], qb[t][k][0], qb[t][k][1]);
+        }
       }
       __syncwarp();   // K is used up: its place takes the next V
       issue(h + 3, buf);
@@ -881,7 +905,7 @@ struct AttendF32 {
   static constexpr int E = D / 32, TB = C::TB, V = GM * TB, SPAN = 32 / V;   // lanes per score
   float q[GM][E], acc[GM][E], m, l;   // m, l: of this lane's head (l: of its token alone)
 
-  __device__ __forceinline__ void begin(const Params& p, int64_t n, int g) {
+  __device__ __forceinline__ void begin(const Params& p, char*, int64_t n, int g) {
     const float scale = p.a.sm_scale * kLog2e;
     const float* src = (const float*)p.a.q + (n * p.a.num_q_heads + (int64_t)g * p.G) * D +
                        (threadIdx.x & 31) * E;
@@ -1021,9 +1045,9 @@ __device__ __forceinline__ void join(int count, M m, L l, O o, float& mx, float&
   }
 }
 
-// (fp32 is held to the registers of four CTAs per SM, but for 16 heads of 128)
+// (fp32 is held to the registers of four CTAs per SM, 16 heads of 128 to those of two, in bf16 three)
 template <typename T, int D, int GM>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 0 : D * GM > 1024 ? 2 : 4)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (D * GM > 1024 ? 3 : 0) : D * GM > 1024 ? 2 : 4)
     sparse_decode_kernel(Params p) {
   using C = Cfg<T, D, GM>;
   extern __shared__ __align__(128) char smem[];
@@ -1096,7 +1120,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 0 : D * GM > 1024 ?
   const int share = ((count + P - 1) / P + 15) & ~15;
   const int t0 = min(count, rank * share), t1 = min(count, t0 + share);
   std::conditional_t<C::kBf16, AttendMma<D, (GM + 7) / 8>, AttendF32<D, GM>> at;
-  at.begin(p, n, g);
+  at.begin(p, smem, n, g);
   for (int seg = t0; seg < t1; seg += kSegment) {
     const int len = min(kSegment, t1 - seg);
     const int32_t* rt = a.req_to_token + (int64_t)a.req_idx[n] * a.max_ctx;
@@ -1194,7 +1218,8 @@ Params params_of(const rc_sparse_decode_args* a) {
   // blocks: 135 whole, 174 split).
   const int64_t units = (int64_t)a->num_rows * a->num_kv_heads;
   const int64_t tokens = (int64_t)std::min(p.nb, a->top_blocks) * a->block;
-  const int64_t resident = a->head_dim == 128 && p.G > 8 ? kResident / 2 : kResident;
+  const int per_sm = a->head_dim < 128 || p.G <= 8 ? 4 : a->dtype == RC_DTYPE_BF16 ? 3 : 2;
+  const int64_t resident = kSms * per_sm;
   p.cluster = 1;
   while (p.cluster < kMaxCluster && tokens >= 128 * p.cluster &&
          (2 * units * p.cluster <= resident || (units > resident && tokens > 2048 * p.cluster)))
