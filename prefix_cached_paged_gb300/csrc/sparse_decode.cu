@@ -50,7 +50,6 @@ constexpr int kMaxTop = 8192;      // the list of chosen blocks is kept in share
 constexpr int kMaxCluster = 16;
 constexpr int kSegment = 512;      // tokens whose slots are resolved at a time
 constexpr int kSmemBlocks = 7500;  // blocks whose scores and ranks are kept in shared memory (90 KB)
-constexpr int kSms = 152;
 
 struct Workspace {                 // used only when a unit's scores outgrow shared memory
   float* score;                    // [units * nb]
@@ -1209,21 +1208,6 @@ Params params_of(const rc_sparse_decode_args* a) {
   p.a = *a;
   p.G = a->num_q_heads / a->num_kv_heads;
   p.nb = std::max(1, (a->max_seq_len + a->block - 1) / a->block);
-  // CTAs per unit (us, contexts of 8192 in blocks of 64). Few units are split while the CTAs stay
-  // resident at once and each has two stages for every warp: beyond that a split only adds joins (bf16,
-  // 32+8 heads of 128, 16 blocks read: 40 units 16.0 in one wave, 30.3 with twice the CTAs, 96 units
-  // 20.0 and 32.5, 320 units 50.0 and 68.7; fp32, 8+8 heads, 40 units 17.1 and 32.8). More units than
-  // are resident are split where a CTA would read over 2048 tokens, which shortens the last wave (640
-  // units of 64 blocks: bf16 266 split, 307 whole; fp32 475 and 550); fewer are not (320 units of 64
-  // blocks: 135 whole, 174 split).
-  const int64_t units = (int64_t)a->num_rows * a->num_kv_heads;
-  const int64_t tokens = (int64_t)std::min(p.nb, a->top_blocks) * a->block;
-  const int per_sm = a->head_dim < 128 || p.G <= 8 ? 4 : a->dtype == RC_DTYPE_BF16 ? 3 : 2;
-  const int64_t resident = kSms * per_sm;
-  p.cluster = 1;
-  while (p.cluster < kMaxCluster && tokens >= 128 * p.cluster &&
-         (2 * units * p.cluster <= resident || (units > resident && tokens > 2048 * p.cluster)))
-    p.cluster *= 2;
   return p;
 }
 
@@ -1237,35 +1221,90 @@ Workspace carve(void* base, const Params& p, size_t* total) {
   return w;
 }
 
-template <typename T, int D, int GM>
-cudaError_t launch_t(const Params& p, cudaStream_t s) {
-  using C = Cfg<T, D, GM>;
-  const auto kernel = sparse_decode_kernel<T, D, GM>;
-  static PerDevice<int> setup;
-  const int* unused = nullptr;
-  cudaError_t e = setup.get(
-      [&](int&) {
-        cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             C::MOST);
-        if (r == cudaSuccess)
-          r = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        return r;
-      },
-      &unused);
-  if (e != cudaSuccess) return e;
-  Params q = p;
+// What fits on the GPU at once: clusters of 2^i CTAs when shared memory lets c CTAs on an SM
+// (clusters stay within a group of SMs, so there are fewer than the SMs' room divided by 2^i: of the 608
+// places for bf16 heads of 128, 152 units take 37 us with 4 CTAs each and 30 with 2, 36 units 33 with 16
+// and 16.5 with 8; contexts of 8192, 16 blocks of 64 read).
+constexpr int kMaxPerSm = 8;
+struct Room {
+  int per_sm;               // CTAs per SM by registers and threads, at most kMaxPerSm
+  int sm_bytes, cta_bytes;  // shared memory of an SM; what a CTA takes beside its dynamic part
+  int clusters[kMaxPerSm + 1][5];
+  int of(int smem, int i) const {
+    return clusters[std::min(per_sm, std::max(1, sm_bytes / (smem + cta_bytes)))][i];
+  }
+};
+
+cudaLaunchConfig_t launch_config(int64_t ctas, int smem, int cluster, cudaLaunchAttribute* at) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.a.num_rows * p.a.num_kv_heads * p.cluster));
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::layout(q);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = p.cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.dynamicSmemBytes = smem;
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = cluster;
+  at->val.clusterDim.y = at->val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, q);
+  return cfg;
+}
+
+template <typename T, int D, int GM>
+cudaError_t room_of(Room& m) {
+  const auto kernel = sparse_decode_kernel<T, D, GM>;
+  const int most = Cfg<T, D, GM>::MOST;
+  cudaFuncAttributes fa = {};
+  int dev = 0, reserved = 0;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess)
+    e = cudaDeviceGetAttribute(&m.sm_bytes, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
+  if (e == cudaSuccess)
+    e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev);
+  if (e == cudaSuccess)
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&m.per_sm, kernel, kThreads, 0);
+  m.per_sm = std::min(std::max(m.per_sm, 1), kMaxPerSm);
+  m.cta_bytes = (int)fa.sharedSizeBytes + reserved;
+  for (int c = 1; c <= m.per_sm && e == cudaSuccess; ++c) {
+    const int smem = std::min(most, (m.sm_bytes / c - m.cta_bytes) / 128 * 128);
+    for (int i = 0; i < 5 && e == cudaSuccess; ++i) {
+      cudaLaunchAttribute at;
+      const cudaLaunchConfig_t cfg = launch_config(1 << i, smem, 1 << i, &at);
+      e = cudaOccupancyMaxActiveClusters(&m.clusters[c][i], kernel, &cfg);
+    }
+  }
+  return e;
+}
+
+template <typename T, int D, int GM>
+cudaError_t launch_t(Params p, cudaStream_t s) {
+  static PerDevice<Room> setup;
+  const Room* room = nullptr;
+  cudaError_t e = setup.get(room_of<T, D, GM>, &room);
+  if (e != cudaSuccess) return e;
+  const int smem = Cfg<T, D, GM>::layout(p);
+  // CTAs per unit (us, contexts of 8192 in blocks of 64). Few units are split while all clusters fit
+  // at once and each CTA has two stages for every warp: beyond that a split only adds joins (bf16,
+  // 32+8 heads of 128, 16 blocks read: 40 units 16.0 in one wave, 30.3 with twice the CTAs, 96 units
+  // 20.0 and 32.5, 320 units 50.0 and 68.7; fp32, 8+8 heads, 40 units 17.1 and 32.8). More units than
+  // fit whole are split where a CTA would read over 2048 tokens, which shortens the last wave (640
+  // units of 64 blocks: bf16 266 split, 307 whole; fp32 475 and 550); fewer are not (320 units of 64
+  // blocks: 135 whole, 174 split).
+  const int64_t units = (int64_t)p.a.num_rows * p.a.num_kv_heads;
+  const int64_t tokens = (int64_t)std::min(p.nb, p.a.top_blocks) * p.a.block;
+  p.cluster = 1;
+  for (int i = 1; 2 * p.cluster <= kMaxCluster && tokens >= 128 * p.cluster &&
+                  2 * p.cluster * units < (1ll << 31) &&
+                  (units <= room->of(smem, i) ||
+                   (units > room->of(smem, 0) && tokens > 2048 * p.cluster));
+       ++i)
+    p.cluster *= 2;
+  cudaLaunchAttribute at;
+  cudaLaunchConfig_t cfg = launch_config(units * p.cluster, smem, p.cluster, &at);
+  cfg.stream = s;
+  e = cudaLaunchKernelEx(&cfg, sparse_decode_kernel<T, D, GM>, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
@@ -1311,8 +1350,6 @@ extern "C" int rc_sparse_decode_attention(const rc_sparse_decode_args* a, void* 
                        (uintptr_t)a->bounds | (uintptr_t)a->o | (uintptr_t)workspace;
   RC_CHECK_ARG((al & 15) == 0, "%s: tensors and workspace must be 16-byte aligned", fn);
   rc::Params p = rc::params_of(a);
-  RC_CHECK_ARG((int64_t)a->num_rows * a->num_kv_heads * p.cluster < (1ll << 31), "%s: too many rows",
-               fn);
   size_t need = 0;
   p.w = rc::carve(workspace, p, &need);
   RC_CHECK_ARG(need == 0 || (workspace && workspace_bytes >= need),
