@@ -364,8 +364,9 @@ __global__ void __launch_bounds__(kThreads, 3)
 // ---------------------------------------------------------------- bounds of cached keys
 // Work items are (layer, row, block, group of at most 32 16-byte chunks of a token's keys), one warp
 // each: `cols` chunks (a power of two) beside one another, the other lanes later tokens of the
-// block. A group is kFly tokens of each. The block's slots are loaded 32 at a time, coalesced, and
-// handed to the lanes by shuffles.
+// block. A group is kFly tokens of each, or fewer where the keys are narrower than 8 chunks: the
+// block's slots are loaded 32 at a time, coalesced, and handed to the lanes by shuffles, so a group
+// has at most 32 tokens.
 constexpr int kFly = 8;
 constexpr int kBoundsSmem = kWarps * kBoundsStages * kFly * 512;
 
@@ -381,6 +382,7 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
   const int col_groups = (chunks + cols - 1) / cols;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int cl = lane & (cols - 1), w = lane / cols, W = 32 / cols;
+  const int fly = min(kFly, cols), group = W * fly;
   char* mine_ring = ring + wid * (kBoundsStages * kFly * 512) + lane * 16;
   for (int b0 = 0; b0 < a.num_rows; b0 += kWindow) {
     const int nreq = min(kWindow, a.num_rows - b0);
@@ -411,11 +413,11 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
                        ((layer * a.num_slots * chunks) + (mine ? c : 0)) * 16;
       int slots = -1;   // of tokens 32 j + lane, -1: nothing to read
       uint32_t have = 0;   // bit u of group gr at gr % kBoundsStages * kFly: this lane copied a token
-      const int groups = (n + W * kFly - 1) / (W * kFly);
+      const int groups = (n + group - 1) / group;
       auto issue = [&](int gr) {
         if (gr < groups) {
-          if (gr * W * kFly % 32 == 0) {
-            const int t = gr * W * kFly + lane;
+          if (gr * group % 32 == 0) {
+            const int t = gr * group + lane;
             slots = t < n ? rt[t] : -1;
             if (t < n && (slots < 0 || slots >= a.num_slots)) {
               set_status(status, kStatusSlotRange);
@@ -425,10 +427,10 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
           const int st = gr % kBoundsStages;
 #pragma unroll
           for (int u = 0; u < kFly; ++u) {
-            const int at = (gr * kFly + u) * W + w;
+            const int at = (gr * fly + u) * W + w;
             const int slot = __shfl_sync(0xffffffffu, slots, at & 31);
             const uint32_t bit = 1u << (st * kFly + u);
-            if (mine && at < n && slot >= 0) {
+            if (u < fly && mine && at < n && slot >= 0) {
               cp_async16(smem_u32(mine_ring + (st * kFly + u) * 512), kp + (int64_t)slot * chunks * 16);
               have |= bit;
             } else {

@@ -483,6 +483,49 @@ def test_block_bounds_are_the_extremes_of_the_cached_keys(dtype, lens, hkv, d, b
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,hkv,d", [  # keys of 1, 2, 3, 4, 5, 7 and 8 chunks of 16 bytes
+    ("bf16", 1, 8), ("bf16", 2, 8), ("bf16", 1, 16), ("bf16", 3, 8), ("bf16", 1, 24),
+    ("bf16", 1, 32), ("bf16", 2, 16), ("bf16", 4, 8), ("bf16", 5, 8), ("bf16", 7, 8),
+    ("bf16", 1, 64), ("f32", 1, 8), ("f32", 1, 16), ("f32", 2, 8), ("f32", 1, 24), ("f32", 1, 32)])
+@pytest.mark.parametrize("block", [16, 32, 64, 128])
+def test_block_bounds_of_narrow_tokens(dtype, hkv, d, block):
+    """Tokens whose keys are narrower than a warp's copies: several tokens stand beside one another,
+    and every one of them has to be read. Lengths end inside a block and on its border; slots
+    outside the pool late in a block are left out and reported."""
+    lens = [1, 31, 33, 63, 64, 65, 97, 127, 128, 129, 200, 256, 0, 300]
+    g = _gen(hkv * 1000 + d + block)
+    dt, ctx = DT[dtype], 310
+    n = sum(lens) + 3
+    kp = torch.randn((n, hkv, d), generator=g).to(dt)
+    perm, at = torch.randperm(n, generator=g).to(torch.int32), 0
+    table = torch.full((len(lens), ctx), -7, dtype=torch.int32)
+    for r, m in enumerate(lens):
+        table[r, :m] = perm[at:at + m]
+        at += m
+    nb = -(-ctx // block)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def check():
+        bd = torch.full((len(lens), nb, hkv, 2, d), 3.0, dtype=dt)
+        want = bd.clone()
+        for r, m in enumerate(lens):
+            for b in range(-(-m // block)):
+                s = table[r, b * block:min(m, (b + 1) * block)].long()
+                s = s[(s >= 0) & (s < n)]
+                want[r, b, :, 0], want[r, b, :, 1] = kp[s].amin(0), kp[s].amax(0)
+        bd = bd.cuda()
+        rc.kv_block_bounds(kp.cuda(), table.cuda(), i32(list(range(len(lens)))), i32(lens), bd,
+                           block=block)
+        assert torch.equal(bd.cpu(), want)
+
+    check()
+    assert rc.device_status() == 0
+    table[13, 45], table[13, 110], table[13, 255] = -1, n, 2 ** 31 - 1
+    check()
+    assert rc.device_status() == 1
+
+
+@pytest.mark.gpu
 def test_block_bounds_of_more_rows_than_one_window():
     n = 2300
     lens = np.random.default_rng(3).integers(0, 40, n)
