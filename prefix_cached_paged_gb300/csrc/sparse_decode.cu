@@ -17,14 +17,14 @@
 //
 // Bound by HBM (boxes of a row once, K and V of the selected tokens once per KV head) with many rows,
 // by the chain of dependent steps with few. Measured, bf16, heads of 128, inputs beyond L2:
-//   128 rows, 32 + 32 heads, contexts 512 .. 8192, 16 blocks of 64: 334 us, 6.5 TB/s, 97 % of the
-//     copy rate; 64 rows, 32 + 8 heads, contexts 4096 .. 32768, 64 blocks: 204 us, 5.6 TB/s, 83 % (a
+//   128 rows, 32 + 32 heads, contexts 512 .. 8192, 16 blocks of 64: 339 us, 6.4 TB/s, 95 % of the
+//     copy rate; 64 rows, 32 + 8 heads, contexts 4096 .. 32768, 64 blocks: 208 us, 5.5 TB/s, 82 % (a
 //     CTA scores, waits and selects for ~8 us of its ~60; four of them share an SM).
-//   1 row, 64 + 8 heads, 131071 tokens, 64 blocks: 27 us: score 4, cluster barriers 5, select 4 to
+//   1 row, 64 + 8 heads, 131071 tokens, 64 blocks: 30 us: score 4, cluster barriers 5, select 4 to
 //     11 (the longer where finer scores are needed), slots 1, 256 tokens 4, join 2. A fifth of the
 //     stalls there is instruction fetch: every step runs once.
-//   fp32, heads of 128, 4096 or 2048 selected tokens: 32 rows, 8 + 8 heads 115 us of a floor of 90; 64
-//     rows, 32 + 4 heads 127 of 86; 64 rows, 32 + 2 heads 244 of 86, bound by its 16 products per key
+//   fp32, heads of 128, 4096 or 2048 selected tokens: 32 rows, 8 + 8 heads 117 us of a floor of 90; 64
+//     rows, 32 + 4 heads 130 of 86; 64 rows, 32 + 2 heads 245 of 86, bound by its 16 products per key
 //     element on the CUDA cores (scores summed one by one over the lanes: 146, 436, 817 us).
 // On the way, for the three: separate kernels for scores, selection, attention and merge, all scores
 // in 64 bits and attention on CUDA cores 1093, 1399, 334 us; scores on matrix instructions 710, 728,
@@ -94,7 +94,8 @@ struct Cfg {
   static constexpr int TB = GM == 16 ? 2 : 4;                 // fp32: K and V of TB tokens
   static constexpr int STAGE = kBf16 ? TOK * RS : 2 * TB * D * 4;
   // 16 heads of 128 keep their queries in shared memory: 168 registers and three CTAs per SM, not 181
-  // and two (64 blocks of 64 read, 160, 320 and 640 units: 92, 157, 281 us, and 131, 226, 379)
+  // and two (64 blocks of 64 read, 160, 320 and 640 units: 104, 176, 299 us; before the weights had
+  // three parts 92, 157, 281, and 131, 226, 379)
   static constexpr bool Q_SHARED = kBf16 && GM * D > 1024;
   static constexpr int QUERIES = Q_SHARED ? GM * RS : 0;
   static constexpr int STATE = GM * D * 4;                    // o of one state
@@ -706,13 +707,31 @@ __device__ __forceinline__ void select_blocks(const Params& p, SelectShared& sh,
 }
 
 // ---------------------------------------------------------------- attention
+// A weight x >= 0 goes to the matrix units as three bf16 parts that make it up exactly:
+// h = head_part(x), m = head_part(x - h) and x - h - m. head_part takes the top 8 of the 24 bits of
+// the number just below x, so what it leaves is above 0, at most 2^-7 of x and a multiple of x's last
+// bit; two steps leave at most 8 bits. With every part of a positive weight above 0 an infinite value
+// stays infinite (a part of 0 or of the other sign would make a NaN of it), down to weights of 2^-117,
+// whose least part may be the least number there is.
+__device__ __forceinline__ float head_part(float x) {
+  return __uint_as_float((max(__float_as_uint(x), 1u) - 1) & 0xffff0000u);
+}
+// two numbers of 8 bits as bf16
+__device__ __forceinline__ uint32_t pack2_cut(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+
 // One warp's running state over its tokens, bf16: every 4th stage of 16 tokens of a segment through
 // its own ring: 16-byte copies of the tokens' K and V rows, completion by copy groups. The two
 // contractions run on warp-level matrix instructions with the tokens as M and the KV head's query
 // heads as N (NT tiles of 8): S^T = K Q^T, O^T += V^T P^T. K fragments by ldmatrix, V^T by its
 // transposing form (rows padded by 16 bytes: no bank conflicts), Q^T in registers (16 heads of 128: shared memory), P^T
-// from the accumulators by movmatrix. P goes in as a bf16 part and its bf16 remainder, so P.V keeps 16 bits
-// of the weights.
+// from the accumulators by movmatrix, in three parts (head_part). The products of 16 tokens are summed
+// from zero and added to O^T in fp32: a matrix instruction cuts its sums off, which over thousands of
+// tokens in one accumulator goes one way. bf16 outputs unlike those of 64 bits, per 100 000: 64 rows of
+// 64 blocks of 64 265 with two parts and one accumulator, 198 with three parts, 241 from zero, 24 with
+// both (fp32 sums over fp32 weights: 77); 128 rows of 16 blocks 244, 64, 243, 24 (43). It takes 1 to 3 % of
+// the time of the batches above, 6 to 10 % with 16 heads (96, 160, 283 us before).
 template <int D, int NT>
 struct AttendMma {
   using C = Cfg<__nv_bfloat16, D, 8 * NT>;
@@ -815,7 +834,7 @@ struct AttendMma {
       issue(h + 3, buf);
       const int at = s * C::TOK + gid;
       const bool ok0 = at < n && slots[at] >= 0, ok1 = at + 8 < n && slots[at + 8] >= 0;
-      uint32_t ph[NT][2], pl[NT][2];
+      uint32_t w[NT][3][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -843,11 +862,17 @@ struct AttendMma {
             }
           }
         }
-        const uint32_t hx = pack2_bf16(sc[t][0], sc[t][1]), hy = pack2_bf16(sc[t][2], sc[t][3]);
-        ph[t][0] = movmatrix_trans(hx);
-        ph[t][1] = movmatrix_trans(hy);
-        pl[t][0] = movmatrix_trans(pack2_bf16(sc[t][0] - bf16lo(hx), sc[t][1] - bf16hi(hx)));
-        pl[t][1] = movmatrix_trans(pack2_bf16(sc[t][2] - bf16lo(hy), sc[t][3] - bf16hi(hy)));
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {   // the rest of each weight: its next part is split off
+          float a[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[e] = j < 2 ? head_part(sc[t][e]) : sc[t][e];
+            sc[t][e] -= a[e];
+          }
+          w[t][j][0] = movmatrix_trans(pack2_cut(a[0], a[1]));
+          w[t][j][1] = movmatrix_trans(pack2_cut(a[2], a[3]));
+        }
       }
       cp_async_wait<2>();
       __syncwarp();
@@ -857,8 +882,11 @@ struct AttendMma {
         ldmatrix_x4_trans(vb + v_row * C::RS + (i * 16 + v_col) * 2, r);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          mma_bf16(acc[t][i], r[0], r[1], r[2], r[3], ph[t][0], ph[t][1]);
-          mma_bf16(acc[t][i], r[0], r[1], r[2], r[3], pl[t][0], pl[t][1]);
+          float z[4] = {};   // the least parts first
+#pragma unroll
+          for (int j = 2; j >= 0; --j) mma_bf16(z, r[0], r[1], r[2], r[3], w[t][j][0], w[t][j][1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[t][i][e] += z[e];
         }
       }
       __syncwarp();   // the buffer may be filled again

@@ -381,6 +381,77 @@ def test_keys_with_infinities_and_nan_behave_as_in_a_dense_softmax():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,hq,d", [("bf16", 1, 64), ("bf16", 8, 128), ("bf16", 12, 64),
+                                        ("bf16", 16, 128), ("f32", 1, 128), ("f32", 3, 64),
+                                        ("f32", 16, 128)])
+def test_softmax_weights_keep_all_bits_of_fp32(dtype, hq, d):
+    """Element i of an output is the difference of the weights of tokens 2 i and 2 i + 1, whose
+    scores are near one another or not: what is lost of a weight shows undivided.
+
+    The products q k and their two-term sums are exact in any order (18 bits), so a weight is off
+    by: the scale to base 2 (constant, product and, where q is scaled first, the sum: three half
+    steps of at most 2.2), the difference from the maximum (half a step of a number below 4: 2^-23),
+    0.7 * 8.6 * 2^-24 together by the logarithm's base; exp2f, 2 ulp: 4 * 2^-24. That is 10 * 2^-24
+    of it, and half a step more in the sum with its neighbour. Normalisation and the output's
+    rounding are relative."""
+    n, block = 2 * d + 1, 16
+    c = Case(dtype, [n], [(0, n)], hq, 1, d, block, extra=0)
+    g = torch.Generator().manual_seed(hq + d)
+    slots = c.table[int(c.req[0]), :n].long()
+    k, v = torch.zeros((n, d)), torch.zeros((n, d))
+    k[:n - 1, 0] = -torch.randint(1, 96, (n - 1,), generator=g) / 64
+    k[1:n - 1:2, 0] = k[0:n - 1:2, 0]
+    k[:n - 1, 1] = -torch.randint(0, 128, (n - 1,), generator=g) / 64
+    i = torch.arange(d)
+    v[2 * i, i], v[2 * i + 1, i] = 1.0, -1.0
+    c.k[slots, 0], c.v[slots, 0] = k.to(c.dt), v.to(c.dt)
+    c.q[:] = 0.0
+    c.q[0, :, 0] = 1.0
+    c.q[0, :, 1] = 2.0 ** -8 * 2.0 ** -torch.arange(hq).remainder(3).float()
+    c.call(n, scale=1.0)
+    assert rc.device_status() == 0
+    for h in range(hq):
+        s = k[:, 0].double() + k[:, 1].double() * c.q[0, h, 1].double()
+        p = s.softmax(0)
+        ref = p[2 * i] - p[2 * i + 1]
+        tol = 11 * R.U32 * (p[2 * i] + p[2 * i + 1]) + (n + 64) * R.U32 * ref.abs()
+        tol = tol + R.half_step(c.dt) * (ref.abs() + tol)
+        err = (c.o[0, h].double().cpu() - ref).abs()
+        assert (err <= tol).all(), (h, float((err / tol).max()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,hq,d", [("bf16", 2, 64), ("bf16", 12, 128), ("f32", 2, 64),
+                                        ("f32", 16, 128)])
+def test_values_with_infinities_and_nan(dtype, hq, d):
+    """An infinite value gives an infinite output, values of both signs or a NaN give a NaN, in
+    their element alone; values past a row's length stay unseen."""
+    n = 70
+    c = Case(dtype, [n], [(0, n), (0, 33)], hq, 1, d, 16)
+    r = int(c.req[0])
+    slots = c.table[r, :n].long()
+    inf = float("inf")
+    c.v[slots[5], 0, 7] = inf
+    c.v[slots[31], 0, 8] = -inf
+    c.v[slots[6], 0, 9], c.v[slots[7], 0, 9] = inf, -inf
+    c.v[slots[8], 0, 10] = float("nan")
+    c.v[slots[33:], 0, 11] = inf          # the second row ends before them
+    c.call(8)
+    for i, m in enumerate((n, 33)):
+        ro, rl, to, tl = R.attend(c.q[i], R.select(c.q[i], c.bounds[r], m, 16, 8, 1, 1), m,
+                                  c.table[r], c.k, c.v, 16, c.scale)
+        o = c.o[i].double().cpu()
+        assert (o[:, 7] == inf).all() and (o[:, 8] == -inf).all()
+        assert o[:, 9:11].isnan().all()
+        assert (o[:, 11] == inf).all() if m > 33 else o[:, 11].isfinite().all()
+        fin = ro.isfinite()
+        assert torch.equal(fin, o.isfinite())
+        tol = to + R.half_step(c.dt) * (ro.abs() + to)
+        assert ((o - ro).abs()[fin] <= tol[fin]).all()
+    assert rc.device_status() == 0
+
+
+@pytest.mark.gpu
 def test_bad_rows_and_slots_are_reported_and_skipped():
     c = Case("bf16", [300, 100], [(0, 300), (1, 100)], 8, 2, 128, 32)
     r = int(c.req[0])
