@@ -707,6 +707,15 @@ __device__ __forceinline__ void select_blocks(const Params& p, SelectShared& sh,
 }
 
 // ---------------------------------------------------------------- attention
+// Weights are 2^(score - running maximum) times 2^-32: the maximum may lag by 2^8 and a unit has at most
+// 2^20 tokens (kMaxTop blocks of 128), so their sum times the largest value there is stays below 2^124
+// and the mean of any finite values is finite. (Subtracted in the exponent, 32 would cost the scores
+// five bits.)
+constexpr float kWeightScale = 0x1p-32f;
+__device__ __forceinline__ float log_sum(float mx, float den) {   // natural
+  return (mx + log2f(den * 0x1p32f)) * kLn2;
+}
+
 // A weight x >= 0 goes to the matrix units as three bf16 parts that make it up exactly:
 // h = head_part(x), m = head_part(x - h) and x - h - m. head_part takes the top 8 of the 24 bits of
 // the number just below x, so what it leaves is above 0, at most 2^-7 of x and a multiple of x's last
@@ -851,8 +860,8 @@ struct AttendMma {
           const float al = grow && mo != -INFINITY ? exp2f(mo - mn) : 1.f;
           m[t][e] = mn;
           const float u = mn == -INFINITY ? 0.f : mn;   // nothing but masked tokens so far
-          sc[t][e] = exp2f(sc[t][e] - u);
-          sc[t][2 + e] = exp2f(sc[t][2 + e] - u);
+          sc[t][e] = exp2f(sc[t][e] - u) * kWeightScale;
+          sc[t][2 + e] = exp2f(sc[t][2 + e] - u) * kWeightScale;
           l[t][e] = l[t][e] * al + sc[t][e] + sc[t][2 + e];
           if (__any_sync(0xffffffffu, al != 1.f)) {
 #pragma unroll
@@ -998,7 +1007,8 @@ struct AttendF32 {
       const bool grow = top > m + 8.f;
       const float al = grow && m != -INFINITY ? exp2f(m - top) : 1.f;
       if (grow) m = top;
-      const float w = exp2f(x - (m == -INFINITY ? 0.f : m));   // 0 for a score of -inf, NaN for one
+      // 0 for a score of -inf, NaN for one
+      const float w = exp2f(x - (m == -INFINITY ? 0.f : m)) * kWeightScale;
       l = l * al + w;
       __syncwarp();   // the last group's weights are used up
       if (lane % SPAN == 0) weights[lane / SPAN] = w;
@@ -1175,7 +1185,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (D * GM > 1024 ? 3 
       join(kWarps, [&](int c) { return sm[c * G + h]; }, [&](int c) { return sl[c * G + h]; },
            [&](int c) { return so[c * G * D + x]; }, mx, den, num);
       ((T*)a.o)[o0 + x] = Elem<T>::from_f(den == 0.f ? 0.f : num / den);
-      if (a.lse && x % D == 0) a.lse[l0 + h] = den == 0.f ? -INFINITY : (mx + log2f(den)) * kLn2;
+      if (a.lse && x % D == 0) a.lse[l0 + h] = den == 0.f ? -INFINITY : log_sum(mx, den);
     }
     return;
   }
@@ -1202,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (D * GM > 1024 ? 3 
          [&](int c) { return cl.map_shared_rank(ml, c)[h]; },
          [&](int c) { return cl.map_shared_rank(mo, c)[x]; }, mx, den, num);
     ((T*)a.o)[o0 + x] = Elem<T>::from_f(den == 0.f ? 0.f : num / den);
-    if (a.lse && x % D == 0) a.lse[l0 + h] = den == 0.f ? -INFINITY : (mx + log2f(den)) * kLn2;
+    if (a.lse && x % D == 0) a.lse[l0 + h] = den == 0.f ? -INFINITY : log_sum(mx, den);
   }
   cl.sync();   // no CTA leaves while another reads its shared memory
 }

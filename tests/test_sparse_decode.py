@@ -452,6 +452,28 @@ def test_values_with_infinities_and_nan(dtype, hq, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,hq,hkv,d,n", [("bf16", 2, 1, 64, 700), ("bf16", 16, 1, 128, 300),
+                                              ("f32", 4, 2, 64, 700), ("f32", 16, 1, 128, 300)])
+def test_values_near_the_largest_number(dtype, hq, hkv, d, n):
+    """Values up to the type's largest, of one sign per dimension and of both: their weighted mean
+    is finite, whatever the sum of unnormalised weights would be. Scores grow along the context, so
+    that a running maximum lags behind."""
+    c = Case(dtype, [n], [(0, n)], hq, hkv, d, 16)
+    r = int(c.req[0])
+    slots = c.table[r, :n].long()
+    c.k[slots, :, 0] = (torch.arange(n) / n * 40)[:, None].to(c.dt)
+    c.q[:, :, 0] = 1.0
+    for b in range(-(-n // 16)):
+        c.bounds[r, b] = R.bounds_of(c.k[slots[16 * b:16 * b + 16]], 16)[0]
+    big = torch.rand((n, hkv, d), generator=c.g) * 3e38
+    big[:, :, 1::2] *= torch.randn((n, hkv, d // 2), generator=c.g).sign()
+    big[3, 0, 0] = torch.finfo(c.dt).max
+    c.v[slots] = big.to(c.dt)
+    c.call(-(-n // 16)).check()
+    assert c.o.isfinite().all() and rc.device_status() == 0
+
+
+@pytest.mark.gpu
 def test_bad_rows_and_slots_are_reported_and_skipped():
     c = Case("bf16", [300, 100], [(0, 300), (1, 100)], 8, 2, 128, 32)
     r = int(c.req[0])
