@@ -552,8 +552,9 @@ int rc_rope_table(const double* inv_freq, int32_t num_pairs, int64_t first_posit
  * block of positions that the new tokens begin gets the bounds of their stored keys, a block that
  * tokens before prefix_len[b] began takes the minimum and maximum with what it holds. Rows of one
  * call are distinct. A request outside the arrays, its row's blocks or the table sets the device
- * status word and is skipped; so is a token whose slot is outside the pool. A request without new
- * tokens is passed over, whatever its prefix_len and req_idx.
+ * status word and is skipped; so is a token whose slot is outside the pool (a block that such tokens
+ * alone begin gets bounds as rc_kv_block_bounds gives it). A request without new tokens is passed
+ * over, whatever its prefix_len and req_idx.
  * k, v [T, Hkv, d] with strides in elements, heads' elements contiguous; head_dim, rotary_dim and
  * alignment as for rc_qk_norm_rope; num_tokens <= 2^24. */
 typedef struct rc_kv_append_args {
@@ -594,7 +595,10 @@ int rc_kv_append(const rc_kv_append_args* args, void* stream);
  * bounds [num_layers, max_reqs, max_blocks, Hkv, 2, d] in dtype; other entries are not written.
  * k_pool [num_layers, num_slots, Hkv, d]. A req_idx given twice has one seq_len. A row of length 0 is
  * passed over, whatever its req_idx. A row outside the table or the bounds sets the device
- * status word and is skipped; so is a token whose slot is outside the pool. max_ctx <= 2^24. */
+ * status word and is skipped; so is a token whose slot is outside the pool. A block without any other
+ * token has the largest finite number as its least and the lowest as its greatest element: bounds
+ * that later keys replace and that rank below every finite block's for a query that is not all
+ * zeros. max_ctx <= 2^24. */
 typedef struct rc_kv_block_bounds_args {
   int32_t dtype;
   int32_t num_layers;

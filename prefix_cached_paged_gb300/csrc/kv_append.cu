@@ -122,13 +122,15 @@ template <typename T>
 struct Extremes;
 template <>
 struct Extremes<__nv_bfloat16> {
-  static constexpr uint32_t kLo = 0x7f807f80u, kHi = 0xff80ff80u;   // inf, -inf
+  static constexpr uint32_t kLo = 0x7f807f80u, kHi = 0xff80ff80u;        // inf, -inf
+  static constexpr uint32_t kMost = 0x7f7f7f7fu, kLeast = 0xff7fff7fu;   // finite
   static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) { return min_nan_bf16x2(a, b); }
   static __device__ __forceinline__ uint32_t hi(uint32_t a, uint32_t b) { return max_nan_bf16x2(a, b); }
 };
 template <>
 struct Extremes<float> {
   static constexpr uint32_t kLo = 0x7f800000u, kHi = 0xff800000u;
+  static constexpr uint32_t kMost = 0x7f7fffffu, kLeast = 0xff7fffffu;
   static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) {
     return __float_as_uint(min_nan(__uint_as_float(a), __uint_as_float(b)));
   }
@@ -151,6 +153,16 @@ __device__ __forceinline__ uint4 shfl_xor4(const uint4& v, int o) {
                     __shfl_xor_sync(0xffffffffu, v.z, o), __shfl_xor_sync(0xffffffffu, v.w, o));
 }
 __device__ __forceinline__ uint4 splat(uint32_t x) { return make_uint4(x, x, x, x); }
+// Extremes of no key at all (every slot outside the pool; any key would make them meet) become the
+// largest and the lowest finite number: infinities would give NaN with a query element of 0, which
+// ranks a block first, and these rank it last.
+template <typename T>
+__device__ __forceinline__ void settle(uint4& lo, uint4& hi) {
+  if (lo.x == Extremes<T>::kLo && hi.x == Extremes<T>::kHi) {
+    lo = splat(Extremes<T>::kMost);
+    hi = splat(Extremes<T>::kLeast);
+  }
+}
 
 // Each warp streams its tokens through a ring of a few groups in shared memory by 16-byte
 // asynchronous copies. A lane reads only what it copied itself, so the ring needs no barrier, and
@@ -349,6 +361,11 @@ __global__ void __launch_bounds__(kThreads, 3)
         }
         __syncthreads();
       }
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        settle<T>(lo0.v[c], hi0.v[c]);
+        settle<T>(lo1.v[c], hi1.v[c]);
+      }
       if (w0 == 0 && m0) {
         lo0.store(cell + lc.c0 * 8);
         hi0.store(cell + d + lc.c0 * 8);
@@ -465,6 +482,7 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(rc_kv_block_b
         const int h = c * V / d, e0 = c * V - h * d;
         T* cell = (T*)a.bounds +
                   ((((layer * a.max_reqs + row) * a.max_blocks + blk) * a.num_kv_heads + h) * 2) * d;
+        settle<T>(lo, hi);
         *(uint4*)(cell + e0) = lo;
         *(uint4*)(cell + d + e0) = hi;
       }

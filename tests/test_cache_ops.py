@@ -580,3 +580,58 @@ def test_block_bounds_nan_bad_rows_and_slots():
         rc.kv_block_bounds(**{**ok, "bounds": bd.float()})
     with pytest.raises(rc.RcError):
         rc.kv_block_bounds(**ok, block=24)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_block_without_a_valid_token_ranks_last(dtype):
+    """Slots outside the pool for every token of a block, in a short append, one whose blocks the
+    warps of a CTA share, and a build: the block's bounds are the largest and the lowest finite
+    number, which no query takes for a good block, and which later tokens replace."""
+    dt, d, hkv, block = DT[dtype], 64, 2, 16
+    big = torch.finfo(dt).max
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    for n in (3, 100):
+        x = torch.randn((n, hkv, d), generator=_gen(n)).to(dt).cuda()
+        kp = torch.zeros((300, hkv, d), dtype=dt, device="cuda")
+        vp, bd = torch.zeros_like(kp), torch.full((1, 8, hkv, 2, d), 9.0, dtype=dt, device="cuda")
+        loc = torch.arange(n, dtype=torch.int32, device="cuda")
+        loc[-(n % block or block):] = -1
+        last = (n - 1) // block
+        rc.kv_append(x, x, loc, i32([0, n]), i32([0]), kp, vp, bounds=bd, req_idx=i32([0]),
+                     block=block)
+        assert rc.device_status() == 1
+        assert (bd[0, last, :, 0] == big).all() and (bd[0, last, :, 1] == -big).all()
+        assert (bd[0, last + 1:] == 9.0).all()
+        if last:
+            assert torch.equal(bd[0, :last], R.bounds_of(x[:last * block], block))
+        # a build of the same row says the same
+        table = torch.full((1, 128), 300, dtype=torch.int32, device="cuda")
+        table[0, :n] = loc
+        b2 = torch.full_like(bd, 9.0)
+        rc.kv_block_bounds(kp, table, i32([0]), i32([n]), b2, block=block)
+        assert rc.device_status() == 1 and torch.equal(b2, bd)
+        # the block's next token is its only one
+        rc.kv_append(x[:1], x[:1], i32([250]), i32([0, 1]), i32([n]), kp, vp, bounds=bd,
+                     req_idx=i32([0]), block=block)
+        assert rc.device_status() == 0
+        assert torch.equal(bd[0, last, :, 0], x[0]) and torch.equal(bd[0, last, :, 1], x[0])
+    # selection: zeros in the query, the empty block among real ones of negative scores
+    nb = 8
+    q = torch.zeros((1, hkv, d), dtype=dt, device="cuda")
+    q[:, :, 5] = 1.0
+    kp = -torch.rand((200, hkv, d), generator=_gen(1)).add(0.1).to(dt).cuda()
+    vp = torch.randn((200, hkv, d), generator=_gen(2)).to(dt).cuda()
+    table = torch.arange(nb * block, dtype=torch.int32, device="cuda")[None].contiguous()
+    table[0, 3 * block:4 * block] = 999
+    bd = torch.zeros((1, nb, hkv, 2, d), dtype=dt, device="cuda")
+    rc.kv_block_bounds(kp, table, i32([0]), i32([nb * block]), bd, block=block)
+    assert rc.device_status() == 1
+    o = torch.empty_like(q)
+    sel = torch.empty((1, hkv, nb - 1), dtype=torch.int32, device="cuda")
+    ws = torch.empty(0, dtype=torch.uint8, device="cuda")
+    rc.sparse_decode_attention(q, i32([nb * block]), i32([0]), table, kp, vp, bd, o, ws,
+                               sm_scale=0.1, max_seq_len=nb * block, block=block,
+                               top_blocks=nb - 1, sink_blocks=0, selected=sel)
+    assert rc.device_status() == 0
+    assert sel[0].tolist() == [[0, 1, 2, 4, 5, 6, 7]] * hkv
