@@ -505,8 +505,10 @@ int rc_decode_attention_noalloc(const rc_decode_args* args, void* stream);
  * in fp32, rounded once to dtype. Pair i is (n_i, n_{i + rotary_dim/2}), or (n_{2i}, n_{2i+1}) when
  * `interleaved`; its cosine and sine are rope[position][i] and rope[position][rotary_dim/2 + i]
  * (rc_rope_table). rotary_dim 0: norms only. q [T, Hq, d] and k [T, Hkv, d] with strides in
- * elements (slices of a fused projection); elements of a head are contiguous. Outputs may be the
- * inputs themselves (same pointer and strides), else they must not overlap them. num_q_heads or
+ * elements (slices of a fused projection); elements of a head are contiguous. An output may be its
+ * input itself (same pointer and strides); any other overlap of an output with an input, the other
+ * output or itself is refused, and so are views of one address range with unlike token strides,
+ * which are not told apart. num_q_heads or
  * num_kv_heads 0: that part is left out. positions [T] device int32; a token whose position is
  * outside [0, max_position) sets the device status word and its rows are not written.
  * head_dim a multiple of 8 up to 256, rotary_dim a multiple of 16; pointers and strides multiples

@@ -564,7 +564,8 @@ def qk_norm_rope(q, k, positions=None, rope=None, *, q_weight=None, k_weight=Non
     rc_qk_norm_rope). q [T, Hq, d] and k [T, Hkv, d]: CUDA tensors whose heads are contiguous, any
     token and head strides (slices of a fused projection); either may be None. positions: int32
     [T]; rope: fp32 [max_position, rotary_dim] (rope_table) or None for norms only; q_weight /
-    k_weight: [d] or None for no norm. q_out / k_out: where the results go, in place when None."""
+    k_weight: [d] or None for no norm. q_out / k_out: where the results go, in place when None; any
+    other overlap with an input or with one another is refused."""
     fn = "qk_norm_rope"
     torch = _torch()
     dev = torch.cuda.current_device()

@@ -18,6 +18,7 @@
 
 #include "host_common.h"
 #include "norm_rope.cuh"
+#include "views.h"
 
 namespace rc {
 namespace {
@@ -158,6 +159,30 @@ int sm_count(const char* fn, int* out) {
   return RC_OK;
 }
 
+namespace {
+bool same_rows(const RowsView& a, const RowsView& b) {
+  return a.p == b.p && (a.tokens == 1 || a.token_stride == b.token_stride) &&
+         (a.heads == 1 || a.head_stride == b.head_stride);
+}
+// Rows are read up to three groups of heads ahead of what is written, by other warps too: an output
+// is its input, row for row, or shares nothing with any input and the other output.
+bool outputs_clear(const rc_qk_norm_rope_args& a, int es) {
+  const int64_t T = a.num_tokens, w = (int64_t)a.head_dim * es;
+  const int64_t hq = a.num_q_heads, hk = a.num_kv_heads;
+  const RowsView q{a.q, a.q_token_stride * es, a.q_head_stride * es, T, hq, w};
+  const RowsView k{a.k, a.k_token_stride * es, a.k_head_stride * es, T, hk, w};
+  const RowsView qo{a.q_out, a.q_out_token_stride * es, a.q_out_head_stride * es, T, hq, w};
+  const RowsView ko{a.k_out, a.k_out_token_stride * es, a.k_out_head_stride * es, T, hk, w};
+  const bool q_in_place = hq == 0 || same_rows(q, qo), k_in_place = hk == 0 || same_rows(k, ko);
+  if ((hq && rows_overlap(qo)) || (hk && rows_overlap(ko))) return false;
+  if (!q_in_place && views_overlap(qo, q)) return false;
+  if (!k_in_place && views_overlap(ko, k)) return false;
+  if (hq == 0 || hk == 0) return true;
+  if (views_overlap(qo, ko)) return false;
+  return (k_in_place || !views_overlap(qo, k)) && (q_in_place || !views_overlap(ko, q));
+}
+}  // namespace
+
 }  // namespace rc
 
 extern "C" int rc_qk_norm_rope(const rc_qk_norm_rope_args* a, void* stream) {
@@ -180,6 +205,9 @@ extern "C" int rc_qk_norm_rope(const rc_qk_norm_rope_args* a, void* stream) {
                           a->k_head_stride | a->q_out_token_stride | a->q_out_head_stride |
                           a->k_out_token_stride | a->k_out_head_stride;
   const int es = a->dtype == RC_DTYPE_BF16 ? 2 : 4;
+  RC_CHECK_ARG(rc::outputs_clear(*a, es),
+               "%s: an output overlaps an input it is not the same rows of, the other output or "
+               "itself", fn);
   RC_CHECK_ARG((ptrs & 15) == 0 && (strides * es & 15) == 0,
                "%s: pointers and strides must be multiples of 16 bytes", fn);
   int* st = rc::device_status_ptr();

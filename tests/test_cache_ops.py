@@ -68,6 +68,85 @@ def test_norm_rope_rejects_bad_arguments_before_any_device_work():
     assert lib().rc_qk_norm_rope(None, None) == rc.RC_ERR_INVALID
 
 
+def test_norm_rope_refuses_outputs_that_overlap():
+    """Outputs that share a byte with an input other than their own rows, with the other output or
+    with themselves, against all bytes counted out; views of one fused tensor that share none are
+    taken. (The weight is misaligned: no call of this test gets past the checks.)"""
+    from prefix_cached_paged_gb300._lib import RcQkNormRopeArgs, lib
+    base, d, es = 1 << 20, 16, 2
+
+    def refused(T, hq, hk, q, k, qo, ko):
+        """Views as (offset, token stride, head stride) in elements."""
+        a = RcQkNormRopeArgs(dtype=rc.RC_DTYPE_BF16, num_q_heads=hq, num_kv_heads=hk, head_dim=d,
+                             eps=1e-6, num_tokens=T, q_weight=_fake(1) + 8)
+        for name, v in (("q", q), ("k", k), ("q_out", qo), ("k_out", ko)):
+            setattr(a, name, base + es * v[0])
+            setattr(a, name + "_token_stride", v[1])
+            setattr(a, name + "_head_stride", v[2])
+        assert lib().rc_qk_norm_rope(ctypes.byref(a), None) == rc.RC_ERR_INVALID
+        msg = lib().rc_last_error().decode()
+        assert "overlaps" in msg or "multiples of 16" in msg, msg
+        return "overlaps" in msg
+
+    def rows(T, h, v):
+        return [v[0] + t * v[1] + i * v[2] for t in range(T) for i in range(h)]
+
+    def share(x, y):
+        return bool({e + j for e in x for j in range(d)} & {e + j for e in y for j in range(d)})
+
+    def wrong(T, hq, hk, q, k, qo, ko):
+        r = [rows(T, h, v) for h, v in ((hq, q), (hk, k), (hq, qo), (hk, ko))]
+        own = [len({e + j for e in x for j in range(d)}) < len(x) * d for x in r]
+        return own[2] or own[3] or (r[2] != r[0] and share(r[2], r[0])) or \
+            (r[3] != r[1] and share(r[3], r[1])) or share(r[2], r[1]) or share(r[3], r[0]) or \
+            share(r[2], r[3])
+
+    T, hq, hk = 5, 6, 2
+    w = (hq + 2 * hk) * d
+    far = 1 << 16
+    fused_q, fused_k, fused_v = (0, w, d), (hq * d, w, d), ((hq + hk) * d, w, d)
+    out_q, out_k = (far, hq * d, d), (2 * far, hk * d, d)
+    for q, k, qo, ko in (
+            (fused_q, fused_k, fused_q, fused_k), (fused_q, fused_k, out_q, out_k),
+            (fused_q, fused_k, fused_q, out_k), (fused_q, fused_k, out_q, fused_v),
+            # heads first: one buffer [hq + hk, T, d]
+            ((0, d, T * d), (hq * T * d, d, T * d), (0, d, T * d), (hq * T * d, d, T * d)),
+            # every KV head's queries beside its key and value: [T, hk, 5, d] with 3 queries a head
+            # has no view of all queries; one query a head has
+            ((0, hq * 3 * d, 3 * d), (d, hq * 3 * d, 3 * d), (0, hq * 3 * d, 3 * d),
+             (2 * d, hq * 3 * d, 3 * d))):
+        assert not wrong(T, hq, hk, q, k, qo, ko)
+        assert not refused(T, hq, hk, q, k, qo, ko), (q, k, qo, ko)
+    for q, k, qo, ko in (
+            (fused_q, fused_k, (d, w, d), out_k), (fused_q, fused_k, (8, w, d), out_k),
+            (fused_q, fused_k, (w, w, d), out_k), (fused_q, fused_k, out_q, (hq * d - 8, w, d)),
+            (fused_q, fused_k, out_q, (far + 3 * d, hk * d, d)),
+            (fused_q, fused_k, (far, 0, d), out_k), (fused_q, fused_k, (far, w, 0), out_k),
+            (fused_q, fused_k, (far, d, d), out_k), (fused_q, fused_k, (far, w, 8), out_k)):
+        assert wrong(T, hq, hk, q, k, qo, ko)
+        assert refused(T, hq, hk, q, k, qo, ko), (q, k, qo, ko)
+    # tokens and heads of one have no strides to speak of
+    assert not refused(1, hq, 1, (0, 0, d), (hq * d, 7, 3), (0, 5 * w, d), (hq * d, 0, 0))
+    g = np.random.default_rng(1)
+    seen = [0, 0, 0]
+    for _ in range(4000):
+        T, hq, hk = (int(g.integers(1, 5)) for _ in range(3))
+        ts = 8 * int(g.integers(-6, 40))
+
+        def view():
+            return (8 * int(g.integers(0, 60)), ts if g.random() < 0.8 else 8 * int(g.integers(0, 40)),
+                    8 * int(g.integers(-4, 14)))
+
+        q, k, qo, ko = (view() for _ in range(4))
+        qo, ko = (q if g.random() < 0.5 else qo), (k if g.random() < 0.5 else ko)
+        bad, got = wrong(T, hq, hk, q, k, qo, ko), refused(T, hq, hk, q, k, qo, ko)
+        assert got or not bad, (T, hq, hk, q, k, qo, ko)
+        alike = T == 1 or len({v[1] for v in (q, k, qo, ko)}) == 1
+        assert bad or not got or not alike, (T, hq, hk, q, k, qo, ko)
+        seen[bad + (got and not bad)] += got == bad
+    assert min(seen[:2]) > 200, seen
+
+
 def test_append_and_bounds_reject_bad_arguments_before_any_device_work():
     from prefix_cached_paged_gb300._lib import RcKvAppendArgs, RcKvBlockBoundsArgs, lib
     ptrs = ["k", "v", "out_loc", "qo_indptr", "prefix_len", "k_weight", "rope", "k_pool",
