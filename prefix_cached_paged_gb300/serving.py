@@ -131,7 +131,6 @@ class Engine:
             nb = -(-max_ctx // self.sparse_block)
             self.bounds = self.dev.torch.empty((layers, max_reqs, nb, n_kv_heads, 2, head_dim),
                                                dtype=dtype, device=self.dev.device)
-        self._sparse_ws = None
         self.max_ctx = max_ctx
         self.kv_chunk = kv_chunk
         # decode reads a context prefix that several requests share once for all of them
@@ -375,11 +374,11 @@ class Engine:
             raise ValueError(f"sparse_layer: append_layer of layer {layer} comes first")
         need = sparse_decode_workspace_bytes(q, self.dev.k[layer], max_seq_len=longest,
                                              block=self.sparse_block, top_blocks=top_blocks)
-        if self._sparse_ws is None or self._sparse_ws.numel() < need:
-            self._sparse_ws = self.dev.torch.empty(need, dtype=self.dev.torch.uint8,
-                                                   device=self.dev.device)
+        # of this call alone: a captured call keeps the memory it was captured with, and calls on
+        # other streams may overlap
+        ws = self.dev.torch.empty(need, dtype=self.dev.torch.uint8, device=self.dev.device)
         sparse_decode_attention(q, length, row, self.dev.req_to_token, self.dev.k[layer],
-                                self.dev.v[layer], self.bounds[layer], o, self._sparse_ws,
+                                self.dev.v[layer], self.bounds[layer], o, ws,
                                 sm_scale=self.sm_scale, max_seq_len=longest,
                                 block=self.sparse_block, top_blocks=top_blocks,
                                 sink_blocks=sink_blocks, recent_blocks=recent_blocks, lse=lse,

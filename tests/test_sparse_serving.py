@@ -195,3 +195,63 @@ def test_engine_without_rope_or_bounds():
     eng.sparse_layer(b, 0, q, o, top_blocks=2)
     assert torch.equal(eng.dev.k[0][torch.from_numpy(b.plan.out_loc).long().cuda()], k)
     assert math.isfinite(float(o.sum())) and rc.device_status() == 0
+
+
+def test_a_captured_long_step_keeps_its_workspace():
+    """Contexts beyond the blocks whose scores shared memory holds: a captured call replayed after
+    a call that needs more workspace, with memory taken in between, gives what it gave and touches
+    nothing else."""
+    lens = (121_000, 130_000)
+    m = Model("bf16", 1, 4, 1, 64, 32, False, 16, max_ctx=131_072)
+    from prefix_cached_paged_gb300.serving import Engine
+    n = sum(lens) + 64
+    eng = Engine(1, 4, 1, 64, m.dt, n, 4, 131_072, synth.permutation(5, n), rope=m.table,
+                 sparse_block=16)
+    seqs = [synth.tokens(9, 20 + i, x) for i, x in enumerate(lens)]
+    for i, s in enumerate(seqs):
+        b = eng.extend_begin([s])
+        _, k, v = m.split(m.qkv(30 + i, 0, len(s)).cuda())
+        eng.append_layer(b, 0, k, v)
+        eng.extend_end(b)
+    db = eng.decode_begin([seqs[0]])
+    both = eng.decode_begin(seqs)
+    top = 9
+    out = {}
+    for name, batch in (("one", db), ("both", both)):
+        eng.decode_step(batch)
+        B = len(batch.row_ids)
+        q, k, v = (t.contiguous() for t in m.split(m.qkv(40 + B, 0, B).cuda()))
+        eng.append_layer(batch, 0, k, v)
+        out[name] = (q, torch.empty_like(q), torch.empty((B, 4), device="cuda"),
+                     torch.empty((B, 1, top), dtype=torch.int32, device="cuda"))
+
+    def run(name, batch):
+        q, o, lse, sel = out[name]
+        eng.sparse_layer(batch, 0, q, o, top_blocks=top, lse=lse, selected=sel)
+
+    run("one", db)
+    want = [t.clone() for t in out["one"][1:]]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        run("one", db)
+    need = rc.sparse_decode_workspace_bytes(out["one"][0], eng.dev.k[0], max_seq_len=lens[0] + 1,
+                                            block=16, top_blocks=top)
+    assert need > 0
+    run("both", both)
+    taken = [torch.full((need,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    want2 = [t.clone() for t in out["both"][1:]]
+    for t in out["one"][1:]:
+        t.zero_()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, w) for x, w in zip(out["one"][1:], want))
+    assert all((t == 7).all() for t in taken)
+    run("both", both)
+    assert all(torch.equal(x, w) for x, w in zip(out["both"][1:], want2))
+    for name, batch in (("one", db), ("both", both)):
+        q, o, lse, sel = out[name]
+        _check_rows(m, eng, 0, q, o, lse, sel,
+                    [(int(r), int(s)) for r, s in zip(batch.row_ids, batch.seq_len)], top)
+    assert rc.device_status() == 0

@@ -108,3 +108,24 @@ def test_empty_batches_have_metadata():
     b = eng.extend_begin([])
     assert b.num_tokens == 0 and b.token_pos.tolist() == [] and b.max_len == 0
     eng.extend_end(b)
+
+
+def test_every_sparse_call_has_a_workspace_of_its_own(monkeypatch):
+    """A captured call goes on using the workspace it was captured with, so no later call may have
+    the same one, or have it replaced by a larger one and freed."""
+    import torch
+    need, used = [64], []
+    monkeypatch.setattr(serving, "kv_block_bounds", lambda *a, **kw: None)
+    monkeypatch.setattr(serving, "kv_append", lambda *a, **kw: None)
+    monkeypatch.setattr(serving, "sparse_decode_workspace_bytes", lambda *a, **kw: need[0])
+    monkeypatch.setattr(serving, "sparse_decode_attention", lambda *a, **kw: used.append(a[8]))
+    eng = _engine()
+    eng.dev.torch, eng.dev.device = torch, torch.device("cpu")
+    eng.sm_scale = 1.0
+    b = eng.extend_begin([synth.tokens(3, 1, 20)])
+    eng.append_layer(b, 0, None, None)
+    for n in (64, 64, 32, 128, 0):
+        need[0] = n
+        eng.sparse_layer(b, 0, None, None, top_blocks=4)
+        assert used[-1].dtype == torch.uint8 and used[-1].numel() >= n
+    assert len({w.data_ptr() for w in used[:4]}) == 4
