@@ -555,6 +555,63 @@ def test_workspace_reused_by_other_shapes_graphs_and_streams():
 
 
 @pytest.mark.gpu
+def test_workspace_of_long_rows_reused_by_other_shapes_and_graphs():
+    """Two calls whose scores outgrow shared memory, of unlike rows, heads and types, on one
+    workspace filled with NaN patterns: in turn, and as two graphs replayed one after the other
+    with lengths and queries changed in between. Outputs as of a fresh workspace, bit for bit."""
+    def long(dtype, rows, hq, hkv, seed):
+        g = torch.Generator().manual_seed(seed)
+        n, block, d = max(m for _, m in rows), 16, 64
+        c = Case(dtype, [600], rows, hq, hkv, d, block)
+        c.max_ctx = n
+        c.table = torch.randint(0, 600, (c.table.shape[0], n), generator=g, dtype=torch.int32)
+        x = torch.randn((c.table.shape[0], -(-n // block), hkv, 2, d), generator=g).to(c.dt)
+        x[:, 100:140, 0] = x[:, 100:101, 0]          # some scores tie
+        c.bounds = torch.cat([x.amin(3, True), x.amax(3, True)], 3).contiguous()
+        return c
+
+    a = long("bf16", [(0, 125_000), (0, 700), (0, 120_017)], 4, 2, 1)
+    b = long("f32", [(0, 140_001), (0, 0)], 3, 1, 2)
+    top, cases = 12, (a, b)
+    need = [rc.sparse_decode_workspace_bytes(x.q, x.k, max_seq_len=max(m for _, m in x.rows),
+                                             block=16, top_blocks=top) for x in cases]
+    assert min(need) > 0 and need[0] != need[1]
+    ws = torch.full((max(need),), 255, dtype=torch.uint8, device="cuda")
+    want = [x.call(top).check() and (x.o.clone(), x.lse.clone(), x.sel.clone()) for x in cases]
+    for _ in range(2):
+        for x, w in zip(cases, want):
+            x.call(top, ws=ws)
+            assert all(torch.equal(u, v) for u, v in zip((x.o, x.lse, x.sel), w))
+    graphs = []
+    for x in cases:
+        keep = [t.cuda() for t in (x.q, x.table, x.k, x.v, x.bounds)]
+        q, t, k, v, bd = keep
+        seq = torch.tensor([m for _, m in x.rows], dtype=torch.int32, device="cuda")
+        req = x.req[torch.zeros(len(x.rows), dtype=torch.long)].to(torch.int32).cuda()
+        o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        sel = torch.empty((q.shape[0], x.hkv, top), dtype=torch.int32, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            rc.sparse_decode_attention(q, seq, req, t, k, v, bd, o, ws, sm_scale=x.scale,
+                                       max_seq_len=x.max_seq, block=16, top_blocks=top, lse=lse,
+                                       selected=sel)
+        graphs.append((g, keep, seq, req, o, lse, sel))
+    for _ in range(2):
+        for g, *_ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for x, (_, keep, seq, _, o, lse, sel) in zip(cases, graphs):
+            x.o, x.lse, x.sel = o, lse, sel
+            x.check()
+            x.rows = [(i, max(0, m - 3333)) for i, m in x.rows]
+            seq.copy_(torch.tensor([m for _, m in x.rows], dtype=torch.int32))
+            x.q = torch.randn(x.q.shape, generator=x.g).to(x.dt)
+            keep[0].copy_(x.q)
+    assert rc.device_status() == 0
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits():
     """A pool plane of more than 2^31 elements and a bounds table of more than 2^31 elements; the
     request uses their far ends."""
