@@ -714,3 +714,33 @@ def test_a_block_without_a_valid_token_ranks_last(dtype):
                                top_blocks=nb - 1, sink_blocks=0, selected=sel)
     assert rc.device_status() == 0
     assert sel[0].tolist() == [[0, 1, 2, 4, 5, 6, 7]] * hkv
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("hkv,d,rot", [(5, 64, 64), (2, 128, 96), (3, 80, 32), (1, 256, 256)])
+def test_a_key_has_the_same_bits_whichever_call_rotates_it(dtype, inter, norm, hkv, d, rot):
+    """qk_norm_rope and kv_append have kernels, and arithmetic, of their own; requests of one token,
+    whose warps take heads beside one another, and of many, whose warps take tokens."""
+    g, dt = _gen(d + hkv), DT[dtype]
+    new = [1] * 9 if d == 80 else [70, 1, 45]
+    pre = [7 * i for i in range(len(new))]
+    T = sum(new)
+    k = (3 * torch.randn((T, hkv, d), generator=g)).to(dt).cuda()
+    w = (1 + 0.3 * torch.randn(d, generator=g)).to(dt).cuda() if norm else None
+    table = R.rope_table(rot, 200).cuda()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    pos = i32([p + i for n, p in zip(new, pre) for i in range(n)])
+    ko = torch.empty_like(k)
+    rc.qk_norm_rope(None, k, pos, table, k_weight=w, interleaved=inter, k_out=ko)
+    kp, vp = torch.zeros((T, hkv, d), dtype=dt, device="cuda"), torch.zeros_like(k)
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    for bounds in (False, True):
+        kp.zero_()
+        kw = dict(bounds=torch.zeros((len(new), 16, hkv, 2, d), dtype=dt, device="cuda"),
+                  req_idx=i32(list(range(len(new)))), block=16) if bounds else {}
+        rc.kv_append(k, k, i32(list(range(T))), i32([sum(new[:i]) for i in range(len(new) + 1)]),
+                     i32(pre), kp, vp, rope=table, k_weight=w, interleaved=inter, **kw)
+        assert torch.equal(kp.view(bits), ko.view(bits)) and rc.device_status() == 0
