@@ -630,15 +630,19 @@ int rc_kv_block_bounds(const rc_kv_block_bounds_args* args, void* stream);
  *   selected          = of the have = ceil(seq_len[n] / block) blocks the first sink_blocks, the last
  *                       recent_blocks (recent_blocks >= 1: the block of the newest token), and those
  *                       with the largest scores up to top_blocks in all; of equal scores the lower
- *                       block number. Decided as by 64-bit scores, so it depends on no summation
- *                       order.
+ *                       block number. Decided as by 64-bit scores, whose products are exact and whose
+ *                       sums round as any 64-bit sum does: scores nearer than 2^-49 of their terms'
+ *                       magnitudes may rank either way, unless the sums are exact (bf16 products
+ *                       within a factor of 2^29 of one another; terms that are alike).
  *   o[n, h] = softmax(sm_scale * <q, k>) v over the selected tokens; lse [Hq] fp32 natural log
  *             (optional); selected [num_rows, Hkv, top_blocks] int32 (optional): block numbers in
- *             ascending order, then -1.
+ *             ascending order, then -1. Weights and sums are fp32. Means of finite values are
+ *             finite; an infinite value gives an infinite output (NaN if its weight is below 2^-80
+ *             of the row's largest, which 32 bits may lose).
  * A request may have several rows (a chunk of new tokens: rows of growing seq_len). A row with
- * seq_len 0 (its req_idx is not read) gets o = 0, lse = -inf, selected = -1; so does a row whose
- * seq_len or req_idx is out of range, which also sets the device status word. A slot outside the pool sets it and that token
- * weighs nothing. sm_scale > 0; Hq / Hkv <= 16; head_dim 64 or 128; max_seq_len <= 2^24, top_blocks
+ * seq_len 0 (whatever its req_idx holds) gets o = 0, lse = -inf, selected = -1; so does a row whose
+ * seq_len or req_idx is out of range, which also sets the device status word. A slot outside the
+ * pool sets it and that token weighs nothing. sm_scale > 0; Hq / Hkv <= 16; head_dim 64 or 128; max_seq_len <= 2^24, top_blocks
  * <= 8192; tensors 16-byte aligned. */
 typedef struct rc_sparse_decode_args {
   int32_t dtype;

@@ -7,7 +7,8 @@
 //   half-split pairs (e, e + r/2):  lane i < r/16 holds chunks i and i + r/16;
 //   interleaved pairs (2e, 2e + 1): lane i holds chunks 2i and 2i + 1;
 // either way lane i < r/16 rotates the pairs 8i .. 8i + 7. Chunks past the rotated dims follow two
-// by two. A warp's loads of one chunk index are contiguous over its lanes.
+// by two. Where pairs are half-split, a warp's loads of one chunk index are contiguous over the lanes
+// that rotate; elsewhere they take every second chunk, and the other index takes the rest.
 #pragma once
 #include "device_common.cuh"
 #include "warp_mma.cuh"
