@@ -10,12 +10,12 @@
 // CTAs then take the items one by one.
 //
 // Both kernels are bound by HBM. Measured (bf16, heads of 128, inputs beyond L2):
-//   append, 80 requests x 200 tokens x 32 heads, with bounds: 93 us, 5.7 TB/s, 85 % of the copy rate
+//   append, 80 requests x 200 tokens x 32 heads, with bounds: 94 us, 5.7 TB/s, 85 % of the copy rate
 //     (half of it writes of 256-byte rows to scattered slots). A CTA per block with the tokens in
 //     turn took 208 us, warps with a fixed share of the items 121 (blocks hold 36 or 64 tokens),
 //     angles loaded as they are needed 98, angles copied past L1 180: every head reads them.
 //   append, 256 requests x 1 token x 8 heads: 8 us, launch and dependent loads.
-//   bounds, 256 contexts of 128 .. 16384 tokens, 8 heads: 260 us, 6.55 TB/s, 98 % of the copy rate.
+//   bounds, 256 contexts of 128 .. 16384 tokens, 8 heads: 262 us, 6.53 TB/s, 97 % of the copy rate.
 //     With the keys loaded into registers 316 us (64 KB in flight per SM instead of 192), joined by
 //     a CTA 336; two ring stages 267, four 308 (one CTA less per SM).
 #include <algorithm>

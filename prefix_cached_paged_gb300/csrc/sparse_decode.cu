@@ -20,7 +20,7 @@
 //   128 rows, 32 + 32 heads, contexts 512 .. 8192, 16 blocks of 64: 339 us, 6.4 TB/s, 95 % of the
 //     copy rate; 64 rows, 32 + 8 heads, contexts 4096 .. 32768, 64 blocks: 208 us, 5.5 TB/s, 82 % (a
 //     CTA scores, waits and selects for ~8 us of its ~60; four of them share an SM).
-//   1 row, 64 + 8 heads, 131071 tokens, 64 blocks: 30 us: score 4, cluster barriers 5, select 4 to
+//   1 row, 64 + 8 heads, 131071 tokens, 64 blocks: 28 us: score 4, cluster barriers 5, select 4 to
 //     11 (the longer where finer scores are needed), slots 1, 256 tokens 4, join 2. A fifth of the
 //     stalls there is instruction fetch: every step runs once.
 //   fp32, heads of 128, 4096 or 2048 selected tokens: 32 rows, 8 + 8 heads 117 us of a floor of 90; 64
@@ -94,8 +94,7 @@ struct Cfg {
   static constexpr int TB = GM == 16 ? 2 : 4;                 // fp32: K and V of TB tokens
   static constexpr int STAGE = kBf16 ? TOK * RS : 2 * TB * D * 4;
   // 16 heads of 128 keep their queries in shared memory: 168 registers and three CTAs per SM, not 181
-  // and two (64 blocks of 64 read, 160, 320 and 640 units: 104, 176, 299 us; before the weights had
-  // three parts 92, 157, 281, and 131, 226, 379)
+  // and two (64 blocks of 64 read, 160, 320 and 640 units: 101, 173, 296 us, and 140, 232, 395)
   static constexpr bool Q_SHARED = kBf16 && GM * D > 1024;
   static constexpr int QUERIES = Q_SHARED ? GM * RS : 0;
   static constexpr int STATE = GM * D * 4;                    // o of one state
@@ -456,8 +455,8 @@ __device__ K kth_largest(SelectShared& s, int* hist, int n, int left, int k, K l
 }
 
 // Where many blocks tie (all keys alike, a query of zeros) every one of them is ranked so, and the
-// adders of a GB300 SM for doubles are few: one row of 2048 tied blocks takes 0.44 ms, 512 units of
-// 64 .. 512 tied blocks 1.4 ms.
+// adders of a GB300 SM for doubles are few: one row of 2048 tied blocks takes 0.45 ms, 512 units of
+// 64 .. 512 tied blocks 1.2 ms.
 //
 // The 64-bit rank of block b: the largest score over the KV head's queries. One warp, four queries
 // at a time so that their loads and sums overlap.
@@ -740,7 +739,8 @@ __device__ __forceinline__ uint32_t pack2_cut(float lo, float hi) {
 // tokens in one accumulator goes one way. bf16 outputs unlike those of 64 bits, per 100 000: 64 rows of
 // 64 blocks of 64 265 with two parts and one accumulator, 198 with three parts, 241 from zero, 24 with
 // both (fp32 sums over fp32 weights: 77); 128 rows of 16 blocks 244, 64, 243, 24 (43). It takes 1 to 3 % of
-// the time of the batches above, 6 to 10 % with 16 heads (96, 160, 283 us before).
+// the time of the batches above, 6 to 10 % with 16 heads of 128 or several rows of a request, which
+// read from L2 (64 rows of 4 requests 162 us, 148 before).
 template <int D, int NT>
 struct AttendMma {
   using C = Cfg<__nv_bfloat16, D, 8 * NT>;
@@ -1261,8 +1261,8 @@ Workspace carve(void* base, const Params& p, size_t* total) {
 
 // What fits on the GPU at once: clusters of 2^i CTAs when shared memory lets c CTAs on an SM
 // (clusters stay within a group of SMs, so there are fewer than the SMs' room divided by 2^i: of the 608
-// places for bf16 heads of 128, 152 units take 37 us with 4 CTAs each and 30 with 2, 36 units 33 with 16
-// and 16.5 with 8; contexts of 8192, 16 blocks of 64 read).
+// places for bf16 heads of 128, 152 units take 39 us with 4 CTAs each and 27 with 2, 36 units 29 with 16
+// and 15 with 8; contexts of 8192, 16 blocks of 64 read).
 constexpr int kMaxPerSm = 8;
 struct Room {
   int per_sm;               // CTAs per SM by registers and threads, at most kMaxPerSm
@@ -1325,11 +1325,11 @@ cudaError_t launch_t(Params p, cudaStream_t s) {
   const int smem = Cfg<T, D, GM>::layout(p);
   // CTAs per unit (us, contexts of 8192 in blocks of 64). Few units are split while all clusters fit
   // at once and each CTA has two stages for every warp: beyond that a split only adds joins (bf16,
-  // 32+8 heads of 128, 16 blocks read: 40 units 16.0 in one wave, 30.3 with twice the CTAs, 96 units
-  // 20.0 and 32.5, 320 units 50.0 and 68.7; fp32, 8+8 heads, 40 units 17.1 and 32.8). More units than
+  // 32+8 heads of 128, 16 blocks read: 40 units 16.5 in one wave, 31.0 with twice the CTAs, 96 units
+  // 20.4 and 33.3, 320 units 50.6 and 67.5; fp32, 8+8 heads, 40 units 17.0 and 32.8). More units than
   // fit whole are split where a CTA would read over 2048 tokens, which shortens the last wave (640
-  // units of 64 blocks: bf16 266 split, 307 whole; fp32 475 and 550); fewer are not (320 units of 64
-  // blocks: 135 whole, 174 split).
+  // units of 64 blocks: bf16 273 split, 315 whole; fp32 475 and 550); fewer are not (320 units of 64
+  // blocks: 141 whole, 180 split).
   const int64_t units = (int64_t)p.a.num_rows * p.a.num_kv_heads;
   const int64_t tokens = (int64_t)std::min(p.nb, p.a.top_blocks) * p.a.block;
   p.cluster = 1;

@@ -123,7 +123,9 @@ class Engine:
                 raise ValueError(f"rope must be an fp32 table of at least {max_ctx} positions")
         # sparse_block: positions per block of the bounds that sparse_layer selects blocks by
         # (16, 32, 64 or 128; 0: no bounds are kept). They take two elements per block, KV head and
-        # dimension of every slot-table row: 2 / sparse_block of the keys that full rows would hold
+        # dimension of every slot-table row, used or not: 2 / sparse_block of the keys that full rows
+        # would hold (32 layers, 256 rows of 131072 positions, 8 KV heads of 128 in bf16, blocks of
+        # 64: 64 GiB). A prefix that rows share has its bounds in each of them, built per batch.
         self.sparse_block = int(sparse_block)
         if self.sparse_block:
             if self.sparse_block not in (16, 32, 64, 128):
