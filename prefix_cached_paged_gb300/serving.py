@@ -90,6 +90,7 @@ class Engine:
     rope = None        # fp32 table [positions, rotary_dim] on the device, or None
     sparse_block = 0   # positions per block of the bounds, 0: none are kept
     bounds = None      # [layers, max_reqs, blocks, Hkv, 2, d]
+    _no_workspace = None
 
     def __init__(self, layers, n_q_heads, n_kv_heads, head_dim, dtype, num_slots, max_reqs,
                  max_ctx, initial_order=None, device="cuda", kv_chunk=0, share_decode=True,
@@ -378,7 +379,11 @@ class Engine:
                                              block=self.sparse_block, top_blocks=top_blocks)
         # of this call alone: a captured call keeps the memory it was captured with, and calls on
         # other streams may overlap
-        ws = self.dev.torch.empty(need, dtype=self.dev.torch.uint8, device=self.dev.device)
+        ws = self._no_workspace
+        if need or ws is None:
+            ws = self.dev.torch.empty(need, dtype=self.dev.torch.uint8, device=self.dev.device)
+        if need == 0:
+            self._no_workspace = ws   # of 0 bytes: most calls need none
         sparse_decode_attention(q, length, row, self.dev.req_to_token, self.dev.k[layer],
                                 self.dev.v[layer], self.bounds[layer], o, ws,
                                 sm_scale=self.sm_scale, max_seq_len=longest,
