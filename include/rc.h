@@ -678,6 +678,105 @@ int rc_sparse_decode_workspace_bytes(const rc_sparse_decode_args* args, size_t* 
 int rc_sparse_decode_attention(const rc_sparse_decode_args* args, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* A cache held in 4 bits. Planes [num_slots, Hkv, d * 5 / 8] bytes for K and for V; of a head's d
+ * elements 32 neighbours make a group j with a scale and a minimum, and an element stands for
+ *   code * scale_j + minimum_j,   code 0 .. 15.
+ * A head's d * 5 / 8 bytes: d / 2 of codes, element 32 j + 8 t + n in nibble n of the little-endian
+ * 32-bit word t * d / 32 + j; then scale and minimum of each group, bf16. As written by rc_kv4_append
+ * (lo, hi the group's least and greatest element; differences, quotients and products in fp32):
+ *   minimum = lo rounded down to bf16 (+0 for -0)
+ *   scale   = (hi - minimum) / 15 rounded up to four significant bits, at least 2^-80
+ *   code    = the integer nearest to (x - minimum) * (1 / scale), ties to even
+ * so an element is at most half a scale (and a relative 2^-20 of it) from what it stands for. A group that
+ * holds a NaN or a magnitude of 2^30 and more has NaN as scale and minimum: all its elements read as
+ * NaN.
+ *
+ * Writes new keys and values into their slots: token t's k[t], v[t] to k_pool[out_loc[t]],
+ * v_pool[out_loc[t]]. Tokens at and past qo_indptr[num_reqs] (a padded batch) are not read, nor is
+ * their out_loc. Slots of out_loc are distinct; a slot outside the pool sets the device status word
+ * and that token is skipped. k, v [T, Hkv, d] with strides in elements, heads' elements contiguous;
+ * head_dim 64, 128, 192 or 256; num_tokens <= 2^24; k, v and strides multiples of 16 bytes, planes
+ * of 16 (head_dim 64 and 192: of 8). Planes that overlap one another or an input are refused. */
+typedef struct rc_kv4_append_args {
+  int32_t dtype;             /* of k and v */
+  int32_t num_reqs;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int64_t num_tokens;        /* rows of k, v and out_loc, >= qo_indptr[num_reqs] */
+  int64_t num_slots;
+  const void* k;
+  int64_t k_token_stride, k_head_stride;
+  const void* v;
+  int64_t v_token_stride, v_head_stride;
+  const int32_t* out_loc;    /* [T] */
+  const int32_t* qo_indptr;  /* [num_reqs + 1] */
+  void* k_pool;
+  void* v_pool;
+} rc_kv4_append_args;
+int rc_kv4_append(const rc_kv4_append_args* args, void* stream);
+
+/* Reads cached tokens back: row i of the outputs (row out_loc[i] with out_loc) gets what k_pool[slots[i]]
+ * and v_pool[slots[i]] stand for, code * scale + minimum in fp32, rounded to dtype. Other rows are not
+ * written. A slot may be read by several rows; rows of out_loc are distinct. A slot outside the pool or a
+ * row outside the outputs sets the device status word and is skipped. k_out, v_out [out_rows, Hkv, d]
+ * with strides in elements, heads' elements contiguous: rows for rc_extend_attention to attend to, for
+ * instance. Outputs that overlap themselves, one another or a plane are refused. head_dim, num_tokens and
+ * alignment as for rc_kv4_append; out_rows < 2^31. */
+typedef struct rc_kv4_read_args {
+  int32_t dtype;             /* of k_out and v_out */
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int64_t num_tokens;        /* entries of slots and out_loc */
+  int64_t num_slots;
+  int64_t out_rows;
+  const void* k_pool;
+  const void* v_pool;
+  const int32_t* slots;      /* [num_tokens] */
+  const int32_t* out_loc;    /* [num_tokens], or NULL: row i */
+  void* k_out;
+  int64_t k_token_stride, k_head_stride;
+  void* v_out;
+  int64_t v_token_stride, v_head_stride;
+} rc_kv4_read_args;
+int rc_kv4_read(const rc_kv4_read_args* args, void* stream);
+
+/* Decode attention over the cache held in 4 bits, as it is held. Query row n attends to the cached
+ * tokens of its request's row req_idx[n] at positions below seq_len[n] (its own token included,
+ * already in the pool: rc_kv4_append):
+ *   o[n, h] = softmax(sm_scale * <q, k>) v,   k and v what the codes stand for, not rounded;
+ * lse [num_rows, Hq] fp32 natural log (optional). Scores, weights and sums are fp32. A request may have
+ * several rows (a chunk of new tokens: rows of growing seq_len). A row with seq_len 0 (whatever its
+ * req_idx holds) gets o = 0, lse = -inf; so does a row whose seq_len or req_idx is out of range, which
+ * also sets the device status word. A slot outside the pool sets it and that token weighs nothing; a row
+ * of such tokens alone is as one of length 0. dtype is q's and o's; sm_scale > 0; Hq / Hkv <= 16;
+ * head_dim 64 or 128; max_seq_len <= 2^24; num_rows <= 2^20; q and o
+ * 16-byte aligned, planes as for rc_kv4_append. */
+typedef struct rc_kv4_decode_args {
+  int32_t dtype;
+  int32_t num_rows;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t max_reqs;          /* rows of req_to_token */
+  int32_t max_ctx;           /* columns of req_to_token */
+  int32_t max_seq_len;       /* >= every seq_len (host-known; sizes grid and workspace) */
+  int64_t num_slots;
+  float sm_scale;
+  const void* q;             /* [num_rows, Hq, d] */
+  const int32_t* seq_len;    /* [num_rows] */
+  const int32_t* req_idx;    /* [num_rows] */
+  const int32_t* req_to_token;
+  const void* k_pool;        /* this layer's planes [num_slots, Hkv, d * 5 / 8] */
+  const void* v_pool;
+  void* o;                   /* [num_rows, Hq, d] */
+  float* lse;
+} rc_kv4_decode_args;
+/* Workspace bytes for these sizes (device memory, 16-byte aligned, no initialisation needed). Calls
+ * that may overlap on the GPU need a workspace each. */
+int rc_kv4_decode_workspace_bytes(const rc_kv4_decode_args* args, size_t* out_bytes);
+int rc_kv4_decode_attention(const rc_kv4_decode_args* args, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
 /* Test hook; the pages have no counterpart. Bound, in nanoseconds, of every wait inside the
  * extend kernel (0 restores the default, 2 s). With a short bound waits give up: the kernel
  * records code 3 in the device status word, stops issuing work and returns without hanging; its

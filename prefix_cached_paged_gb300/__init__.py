@@ -17,14 +17,16 @@ import numpy as np
 
 from ._lib import (RC_DTYPE_BF16, RC_DTYPE_F32, RC_ERR_CUDA, RC_ERR_DEVICE, RC_ERR_INSUFFICIENT,
                    RC_ERR_INVALID, RC_ERR_OOM, RC_OK, RC_SCHED_FCFS, RC_SCHED_LSPF, RcDecodeArgs,
-                   RcError, RcExtendArgs, RcKvAppendArgs, RcKvBlockBoundsArgs, RcKvCopyArgs,
-                   RcQkNormRopeArgs, RcSlotWriteArgs, RcSparseDecodeArgs, RcStackPlan,
-                   RcStackPlanArgs, RcStats, check, lib)
+                   RcError, RcExtendArgs, RcKv4AppendArgs, RcKv4DecodeArgs, RcKv4ReadArgs,
+                   RcKvAppendArgs, RcKvBlockBoundsArgs, RcKvCopyArgs, RcQkNormRopeArgs,
+                   RcSlotWriteArgs, RcSparseDecodeArgs, RcStackPlan, RcStackPlanArgs, RcStats, check,
+                   lib)
 
 __all__ = [
     "Pool", "RadixTree", "RcError", "slot_table_write", "extend_attention", "decode_attention",
     "rope_table", "qk_norm_rope", "kv_append", "kv_block_bounds", "sparse_decode_attention",
-    "sparse_decode_workspace_bytes",
+    "sparse_decode_workspace_bytes", "kv4_row_bytes", "kv4_append", "kv4_read",
+    "kv4_decode_attention", "kv4_decode_workspace_bytes",
     "decode_workspace_bytes", "decode_attention_noalloc", "device_status", "launch_count", "RC_OK", "RC_ERR_INVALID",
     "RC_ERR_OOM", "RC_ERR_INSUFFICIENT", "RC_ERR_CUDA", "RC_ERR_DEVICE", "RC_SCHED_LSPF",
     "RC_SCHED_FCFS",
@@ -729,6 +731,108 @@ def sparse_decode_attention(q, seq_len, req_idx, req_to_token, k_pool, v_pool, b
         a.selected = selected.data_ptr()
     check(lib().rc_sparse_decode_attention(ctypes.byref(a), workspace.data_ptr(), workspace.numel(),
                                            _raw_stream(dev, stream)), "rc_sparse_decode_attention")
+
+
+# ------------------------------------------------------------------ the cache held in 4 bits
+def kv4_row_bytes(head_dim: int) -> int:
+    """Bytes of one head's row in a plane of the 4-bit cache (uint8 [num_slots, Hkv, kv4_row_bytes]):
+    half a byte per element, a scale and a minimum per 32 elements (rc_kv4_append)."""
+    if head_dim not in (64, 128, 192, 256):
+        raise ValueError(f"kv4_row_bytes: head_dim {head_dim} (64, 128, 192 or 256)")
+    return head_dim * 5 // 8
+
+
+def _kv4_planes(fn, dev, k_pool, v_pool, Hkv, d):
+    """Slots of the planes of a 4-bit cache, which must be [S, Hkv, kv4_row_bytes(d)]."""
+    u8 = _torch().uint8
+    shape = (_dims(fn, "k_pool", k_pool, 3)[0], Hkv, kv4_row_bytes(d))
+    _require(fn, dev, (("k_pool", k_pool, u8, shape), ("v_pool", v_pool, u8, shape)))
+    return shape[0]
+
+
+def kv4_append(k, v, out_loc, qo_indptr, k_pool, v_pool, *, stream=None):
+    """Quantise the new tokens' keys and values into their slots of one layer's planes of the 4-bit
+    cache, uint8 [num_slots, Hkv, kv4_row_bytes(d)] (see rc_kv4_append). k, v [T, Hkv, d] with any
+    token and head strides, bf16 or fp32; out_loc [T], qo_indptr [B + 1] int32: tokens from
+    qo_indptr[B] on are padding. Keys are held as given: qk_norm_rope comes first."""
+    fn = "kv4_append"
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    dt, i32 = k.dtype, torch.int32
+    T, Hkv, d = _dims(fn, "k", k, 3)
+    B = _dims(fn, "qo_indptr", qo_indptr, 1)[0] - 1
+    kt, kh = _heads(fn, dev, "k", k, dt, (T, Hkv, d))
+    vt, vh = _heads(fn, dev, "v", v, dt, (T, Hkv, d))
+    S = _kv4_planes(fn, dev, k_pool, v_pool, Hkv, d)
+    _require(fn, dev, (("out_loc", out_loc, i32, (T,)), ("qo_indptr", qo_indptr, i32, (B + 1,))))
+    a = RcKv4AppendArgs(_dtype_code(k), B, Hkv, d, T, S, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                        out_loc.data_ptr(), qo_indptr.data_ptr(), k_pool.data_ptr(),
+                        v_pool.data_ptr())
+    check(lib().rc_kv4_append(ctypes.byref(a), _raw_stream(dev, stream)), "rc_kv4_append")
+
+
+def kv4_read(k_pool, v_pool, slots, k_out, v_out, *, out_loc=None, stream=None):
+    """Read cached tokens of the 4-bit cache back as numbers (see rc_kv4_read): row i of k_out and
+    v_out [rows, Hkv, d] (row out_loc[i] with out_loc) gets the key and value in slot slots[i], in
+    the outputs' type; other rows stay. slots, out_loc int32; outputs with any token and head
+    strides."""
+    fn = "kv4_read"
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    dt, i32 = k_out.dtype, torch.int32
+    R, Hkv, d = _dims(fn, "k_out", k_out, 3)
+    T = _dims(fn, "slots", slots, 1)[0]
+    kt, kh = _heads(fn, dev, "k_out", k_out, dt, (R, Hkv, d), True)
+    vt, vh = _heads(fn, dev, "v_out", v_out, dt, (R, Hkv, d), True)
+    S = _kv4_planes(fn, dev, k_pool, v_pool, Hkv, d)
+    _require(fn, dev, (("slots", slots, i32, (T,)),))
+    p_loc = 0
+    if out_loc is not None:
+        _require(fn, dev, (("out_loc", out_loc, i32, (T,)),))
+        p_loc = out_loc.data_ptr()
+    a = RcKv4ReadArgs(_dtype_code(k_out), Hkv, d, T, S, R, k_pool.data_ptr(), v_pool.data_ptr(),
+                      slots.data_ptr(), p_loc, k_out.data_ptr(), kt, kh, v_out.data_ptr(), vt, vh)
+    check(lib().rc_kv4_read(ctypes.byref(a), _raw_stream(dev, stream)), "rc_kv4_read")
+
+
+def kv4_decode_workspace_bytes(q, k_pool, *, max_seq_len) -> int:
+    """Workspace of kv4_decode_attention for these sizes (rc_kv4_decode_workspace_bytes)."""
+    N, Hq, d = q.shape
+    a = RcKv4DecodeArgs(dtype=_dtype_code(q), num_rows=N, num_q_heads=Hq,
+                        num_kv_heads=k_pool.shape[1], head_dim=d, max_seq_len=max_seq_len)
+    n = ctypes.c_size_t()
+    check(lib().rc_kv4_decode_workspace_bytes(ctypes.byref(a), ctypes.byref(n)),
+          "rc_kv4_decode_workspace_bytes")
+    return int(n.value)
+
+
+def kv4_decode_attention(q, seq_len, req_idx, req_to_token, k_pool, v_pool, o, workspace, *,
+                         sm_scale, max_seq_len, lse=None, stream=None):
+    """Decode attention of one layer over the 4-bit cache as it is held (see
+    rc_kv4_decode_attention). q, o [N, Hq, d] bf16 or fp32; seq_len, req_idx [N] int32, a row's own
+    token already in the pool (kv4_append); k_pool, v_pool uint8 [num_slots, Hkv,
+    kv4_row_bytes(d)]; workspace: a uint8 CUDA tensor of at least kv4_decode_workspace_bytes(...)
+    bytes; lse fp32 [N, Hq] optional."""
+    fn = "kv4_decode_attention"
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    dt, i32 = q.dtype, torch.int32
+    N, Hq, d = _dims(fn, "q", q, 3)
+    Hkv = _dims(fn, "k_pool", k_pool, 3)[1]
+    R, C = _dims(fn, "req_to_token", req_to_token, 2)
+    S = _kv4_planes(fn, dev, k_pool, v_pool, Hkv, d)
+    _require(fn, dev, (("q", q, dt, (N, Hq, d)), ("o", o, dt, (N, Hq, d)),
+                       ("req_to_token", req_to_token, i32, (R, C)),
+                       ("seq_len", seq_len, i32, (N,)), ("req_idx", req_idx, i32, (N,)),
+                       ("workspace", workspace, torch.uint8, workspace.shape)))
+    a = RcKv4DecodeArgs(_dtype_code(q), N, Hq, Hkv, d, R, C, max_seq_len, S, sm_scale, q.data_ptr(),
+                        seq_len.data_ptr(), req_idx.data_ptr(), req_to_token.data_ptr(),
+                        k_pool.data_ptr(), v_pool.data_ptr(), o.data_ptr())
+    if lse is not None:
+        _require(fn, dev, (("lse", lse, torch.float32, (N, Hq)),))
+        a.lse = lse.data_ptr()
+    check(lib().rc_kv4_decode_attention(ctypes.byref(a), workspace.data_ptr(), workspace.numel(),
+                                        _raw_stream(dev, stream)), "rc_kv4_decode_attention")
 
 
 def device_status(stream=None) -> int:

@@ -74,6 +74,10 @@ SIGNATURES = {
     "rc_kv_block_bounds": (ctypes.c_int, [_P, _P]),
     "rc_sparse_decode_workspace_bytes": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_size_t)]),
     "rc_sparse_decode_attention": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
+    "rc_kv4_append": (ctypes.c_int, [_P, _P]),
+    "rc_kv4_read": (ctypes.c_int, [_P, _P]),
+    "rc_kv4_decode_workspace_bytes": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_size_t)]),
+    "rc_kv4_decode_attention": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
     "rc_device_status": (ctypes.c_int, [ctypes.POINTER(_I32), _P]),
     "rc_debug_set_wait_limit_ns": (ctypes.c_int, [_U64]),
     "rc_plan_extend_stacking": (ctypes.c_int, [_P, _P]),
@@ -178,6 +182,30 @@ class RcSparseDecodeArgs(ctypes.Structure):
                 ("num_slots", _I64), ("sm_scale", ctypes.c_float), ("q", _P), ("seq_len", _P),
                 ("req_idx", _P), ("req_to_token", _P), ("k_pool", _P), ("v_pool", _P),
                 ("bounds", _P), ("o", _P), ("lse", _P), ("selected", _P)]
+
+
+class RcKv4AppendArgs(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("num_reqs", _I32), ("num_kv_heads", _I32), ("head_dim", _I32),
+                ("num_tokens", _I64), ("num_slots", _I64), ("k", _P), ("k_token_stride", _I64),
+                ("k_head_stride", _I64), ("v", _P), ("v_token_stride", _I64),
+                ("v_head_stride", _I64), ("out_loc", _P), ("qo_indptr", _P), ("k_pool", _P),
+                ("v_pool", _P)]
+
+
+class RcKv4ReadArgs(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("num_kv_heads", _I32), ("head_dim", _I32), ("num_tokens", _I64),
+                ("num_slots", _I64), ("out_rows", _I64), ("k_pool", _P), ("v_pool", _P),
+                ("slots", _P), ("out_loc", _P), ("k_out", _P), ("k_token_stride", _I64),
+                ("k_head_stride", _I64), ("v_out", _P), ("v_token_stride", _I64),
+                ("v_head_stride", _I64)]
+
+
+class RcKv4DecodeArgs(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("num_rows", _I32), ("num_q_heads", _I32),
+                ("num_kv_heads", _I32), ("head_dim", _I32), ("max_reqs", _I32),
+                ("max_ctx", _I32), ("max_seq_len", _I32), ("num_slots", _I64),
+                ("sm_scale", ctypes.c_float), ("q", _P), ("seq_len", _P), ("req_idx", _P),
+                ("req_to_token", _P), ("k_pool", _P), ("v_pool", _P), ("o", _P), ("lse", _P)]
 
 
 _lib = None

@@ -1,0 +1,261 @@
+// Writes keys and values into a cache held in 4 bits (format: kv4.cuh) and reads them back.
+//
+// Both are bound by HBM: a head of 128 in bf16 is 256 bytes on one side and 80 on the other. One warp
+// per (token, K or V); a lane takes 8 neighbouring elements (one 16- or two 16-byte accesses on the wide
+// side, one 32-bit word of codes on the other), the four lanes of a group find its extremes by two
+// shuffles, and a warp keeps several chunks of 32 lanes in flight.
+#include <algorithm>
+
+#include "host_common.h"
+#include "kv4.cuh"
+#include "norm_rope.cuh"
+#include "views.h"
+
+namespace rc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kAhead = 4;   // chunks of a warp in flight
+
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const void* p) { r = __ldcs((const uint4*)p); }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = bf16lo(r.x), x[1] = bf16hi(r.x), x[2] = bf16lo(r.y), x[3] = bf16hi(r.y);
+    x[4] = bf16lo(r.z), x[5] = bf16hi(r.z), x[6] = bf16lo(r.w), x[7] = bf16hi(r.w);
+  }
+  static __device__ __forceinline__ void store(void* p, const float* x) {
+    *(uint4*)p = make_uint4(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]),
+                            pack2_bf16(x[4], x[5]), pack2_bf16(x[6], x[7]));
+  }
+};
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* p) {
+    a = __ldcs((const float4*)p), b = __ldcs((const float4*)p + 1);
+  }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(void* p, const float* x) {
+    ((float4*)p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    ((float4*)p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
+
+template <typename T, int NG>
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(rc_kv4_append_args a, int* status) {
+  constexpr int D = 32 * NG, C = D / 8, RB = kv4_row_bytes(D);
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * kWarps;
+  const int64_t items = 2 * min(max((int64_t)a.qo_indptr[a.num_reqs], (int64_t)0), a.num_tokens);
+  const int chunks = a.num_kv_heads * C;
+  for (int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); i < items; i += warps) {
+    const int64_t t = i >> 1;
+    const bool is_v = i & 1;
+    const int slot = a.out_loc[t];
+    if (slot < 0 || slot >= a.num_slots) {
+      if (lane == 0) set_status(status, kStatusSlotRange);
+      continue;
+    }
+    const T* x = is_v ? (const T*)a.v + t * a.v_token_stride : (const T*)a.k + t * a.k_token_stride;
+    const int64_t hs = is_v ? a.v_head_stride : a.k_head_stride;
+    char* row = (char*)(is_v ? a.v_pool : a.k_pool) + (int64_t)slot * a.num_kv_heads * RB;
+    for (int c0 = 0; c0 < chunks; c0 += 32 * kAhead) {
+      Eight<T> e[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int c = c0 + 32 * u + lane;
+        e[u] = Eight<T>();
+        if (c < chunks) e[u].load(x + c / C * hs + c % C * 8);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int c = c0 + 32 * u + lane;
+        float v[8];
+        e[u].get(v);
+        float lo = v[0], hi = v[0];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) lo = min_nan(lo, v[k]), hi = max_nan(hi, v[k]);
+#pragma unroll
+        for (int s = 1; s < 4; s *= 2) {
+          lo = min_nan(lo, __shfl_xor_sync(~0u, lo, s));
+          hi = max_nan(hi, __shfl_xor_sync(~0u, hi, s));
+        }
+        const Kv4Group g = kv4_group(lo, hi);
+        uint32_t w = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w |= kv4_code(g, v[k]) << 4 * k;
+        if (g.lost) w = 0;
+        if (c >= chunks) continue;   // a multiple of 8: a group's lanes are all in or out
+        const int j = c % C / 4, q = c % 4;
+        uint32_t* head = (uint32_t*)(row + c / C * RB);
+        head[q * NG + j] = w;
+        if (q == 0) head[C + j] = g.pair;
+      }
+    }
+  }
+}
+
+template <typename T, int NG>
+__global__ void __launch_bounds__(kThreads) kv4_read_kernel(rc_kv4_read_args a, int* status) {
+  constexpr int D = 32 * NG, C = D / 8, RB = kv4_row_bytes(D);
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * kWarps;
+  const int64_t items = 2 * a.num_tokens;
+  const int chunks = a.num_kv_heads * C;
+  for (int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); i < items; i += warps) {
+    const int64_t t = i >> 1;
+    const bool is_v = i & 1;
+    const int slot = a.slots[t];
+    const int64_t to = a.out_loc ? a.out_loc[t] : t;
+    if (slot < 0 || slot >= a.num_slots || to < 0 || to >= a.out_rows) {
+      if (lane == 0) set_status(status, kStatusSlotRange);
+      continue;
+    }
+    const char* row = (const char*)(is_v ? a.v_pool : a.k_pool) + (int64_t)slot * a.num_kv_heads * RB;
+    T* out = is_v ? (T*)a.v_out + to * a.v_token_stride : (T*)a.k_out + to * a.k_token_stride;
+    const int64_t hs = is_v ? a.v_head_stride : a.k_head_stride;
+    for (int c0 = 0; c0 < chunks; c0 += 32 * kAhead) {
+      uint32_t w[kAhead], p[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int c = c0 + 32 * u + lane;
+        if (c < chunks) {
+          const uint32_t* head = (const uint32_t*)(row + c / C * RB);
+          w[u] = head[c % C];
+          p[u] = head[C + c % NG];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int c = c0 + 32 * u + lane;
+        if (c >= chunks) continue;
+        const float s = bf16lo(p[u]), m = bf16hi(p[u]);
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = fmaf((float)(w[u] >> 4 * k & 15u), s, m);
+        Eight<T>::store(out + c / C * hs + c % NG * 32 + c % C / NG * 8, v);
+      }
+    }
+  }
+}
+
+// Two warps of work per token, at most what fits on the GPU at once.
+unsigned grid_of(int64_t tokens, int sms) {
+  return (unsigned)std::min<int64_t>((2 * tokens + kWarps - 1) / kWarps, (int64_t)sms * 8);
+}
+
+template <typename T>
+void launch_append(const rc_kv4_append_args& a, unsigned grid, int* st, cudaStream_t s) {
+  switch (a.head_dim / 64) {
+    case 1: kv4_append_kernel<T, 2><<<grid, kThreads, 0, s>>>(a, st); break;
+    case 2: kv4_append_kernel<T, 4><<<grid, kThreads, 0, s>>>(a, st); break;
+    case 3: kv4_append_kernel<T, 6><<<grid, kThreads, 0, s>>>(a, st); break;
+    default: kv4_append_kernel<T, 8><<<grid, kThreads, 0, s>>>(a, st); break;
+  }
+}
+template <typename T>
+void launch_read(const rc_kv4_read_args& a, unsigned grid, int* st, cudaStream_t s) {
+  switch (a.head_dim / 64) {
+    case 1: kv4_read_kernel<T, 2><<<grid, kThreads, 0, s>>>(a, st); break;
+    case 2: kv4_read_kernel<T, 4><<<grid, kThreads, 0, s>>>(a, st); break;
+    case 3: kv4_read_kernel<T, 6><<<grid, kThreads, 0, s>>>(a, st); break;
+    default: kv4_read_kernel<T, 8><<<grid, kThreads, 0, s>>>(a, st); break;
+  }
+}
+
+int check_sizes(const char* fn, int dtype, int heads, int d, int64_t tokens, int64_t slots) {
+  RC_CHECK_ARG(dtype == RC_DTYPE_BF16 || dtype == RC_DTYPE_F32, "%s: dtype %d", fn, dtype);
+  RC_CHECK_ARG(d >= 64 && d <= kKv4MaxDim && d % 64 == 0, "%s: head_dim %d (64, 128, 192 or 256)", fn,
+               d);
+  RC_CHECK_ARG(heads > 0 && heads <= 65536 && tokens >= 0 && tokens <= (1 << 24) && slots > 0,
+               "%s: bad sizes", fn);
+  return RC_OK;
+}
+
+}  // namespace
+}  // namespace rc
+
+extern "C" int rc_kv4_append(const rc_kv4_append_args* a, void* stream) {
+  static const char* fn = "rc_kv4_append";
+  RC_CHECK_ARG(a != nullptr, "%s: args is NULL", fn);
+  const int c = rc::check_sizes(fn, a->dtype, a->num_kv_heads, a->head_dim, a->num_tokens,
+                                a->num_slots);
+  if (c != RC_OK) return c;
+  RC_CHECK_ARG(a->num_reqs >= 0, "%s: bad sizes", fn);
+  if (a->num_tokens == 0 || a->num_reqs == 0) return RC_OK;
+  RC_CHECK_ARG(a->k && a->v && a->out_loc && a->qo_indptr && a->k_pool && a->v_pool,
+               "%s: NULL pointer", fn);
+  const int es = a->dtype == RC_DTYPE_BF16 ? 2 : 4;
+  const int64_t strides = a->k_token_stride | a->k_head_stride | a->v_token_stride | a->v_head_stride;
+  RC_CHECK_ARG((((uintptr_t)a->k | (uintptr_t)a->v) & 15) == 0 && (strides * es & 15) == 0,
+               "%s: k, v and strides must be multiples of 16 bytes", fn);
+  RC_CHECK_ARG((((uintptr_t)a->k_pool | (uintptr_t)a->v_pool) & (rc::kv4_align(a->head_dim) - 1)) == 0,
+               "%s: planes must be multiples of %d bytes", fn, rc::kv4_align(a->head_dim));
+  const int64_t T = a->num_tokens, h = a->num_kv_heads, w = (int64_t)a->head_dim * es;
+  const int64_t plane = a->num_slots * h * rc::kv4_row_bytes(a->head_dim);
+  const rc::RowsView k{a->k, a->k_token_stride * es, a->k_head_stride * es, T, h, w};
+  const rc::RowsView v{a->v, a->v_token_stride * es, a->v_head_stride * es, T, h, w};
+  const rc::RowsView kp{a->k_pool, 0, 0, 1, 1, plane}, vp{a->v_pool, 0, 0, 1, 1, plane};
+  RC_CHECK_ARG(!rc::views_overlap(kp, vp) && !rc::views_overlap(kp, k) && !rc::views_overlap(kp, v) &&
+                   !rc::views_overlap(vp, k) && !rc::views_overlap(vp, v),
+               "%s: a plane overlaps the other or an input", fn);
+  int* st = rc::device_status_ptr();
+  if (!st) return rc::fail(RC_ERR_CUDA, "%s: no device status word", fn);
+  int sms = 0;
+  const int e = rc::sm_count(fn, &sms);
+  if (e != RC_OK) return e;
+  const unsigned grid = rc::grid_of(T, sms);
+  if (a->dtype == RC_DTYPE_BF16)
+    rc::launch_append<__nv_bfloat16>(*a, grid, st, (cudaStream_t)stream);
+  else
+    rc::launch_append<float>(*a, grid, st, (cudaStream_t)stream);
+  rc::count_launches(1);
+  return rc::check_launch(fn);
+}
+
+extern "C" int rc_kv4_read(const rc_kv4_read_args* a, void* stream) {
+  static const char* fn = "rc_kv4_read";
+  RC_CHECK_ARG(a != nullptr, "%s: args is NULL", fn);
+  const int c = rc::check_sizes(fn, a->dtype, a->num_kv_heads, a->head_dim, a->num_tokens,
+                                a->num_slots);
+  if (c != RC_OK) return c;
+  RC_CHECK_ARG(a->out_rows >= 0 && a->out_rows <= INT32_MAX &&
+                   (a->out_loc || a->out_rows >= a->num_tokens),
+               "%s: bad sizes", fn);
+  if (a->num_tokens == 0) return RC_OK;
+  RC_CHECK_ARG(a->k_pool && a->v_pool && a->slots && a->k_out && a->v_out, "%s: NULL pointer", fn);
+  const int es = a->dtype == RC_DTYPE_BF16 ? 2 : 4;
+  const int64_t strides = a->k_token_stride | a->k_head_stride | a->v_token_stride | a->v_head_stride;
+  RC_CHECK_ARG((((uintptr_t)a->k_out | (uintptr_t)a->v_out) & 15) == 0 && (strides * es & 15) == 0,
+               "%s: outputs and strides must be multiples of 16 bytes", fn);
+  RC_CHECK_ARG((((uintptr_t)a->k_pool | (uintptr_t)a->v_pool) & (rc::kv4_align(a->head_dim) - 1)) == 0,
+               "%s: planes must be multiples of %d bytes", fn, rc::kv4_align(a->head_dim));
+  const int64_t R = a->out_rows, h = a->num_kv_heads, w = (int64_t)a->head_dim * es;
+  const int64_t plane = a->num_slots * h * rc::kv4_row_bytes(a->head_dim);
+  const rc::RowsView k{a->k_out, a->k_token_stride * es, a->k_head_stride * es, R, h, w};
+  const rc::RowsView v{a->v_out, a->v_token_stride * es, a->v_head_stride * es, R, h, w};
+  const rc::RowsView kp{a->k_pool, 0, 0, 1, 1, plane}, vp{a->v_pool, 0, 0, 1, 1, plane};
+  RC_CHECK_ARG(!rc::rows_overlap(k) && !rc::rows_overlap(v) && !rc::views_overlap(k, v) &&
+                   !rc::views_overlap(kp, k) && !rc::views_overlap(kp, v) &&
+                   !rc::views_overlap(vp, k) && !rc::views_overlap(vp, v),
+               "%s: an output overlaps itself, the other or a plane", fn);
+  int* st = rc::device_status_ptr();
+  if (!st) return rc::fail(RC_ERR_CUDA, "%s: no device status word", fn);
+  int sms = 0;
+  const int e = rc::sm_count(fn, &sms);
+  if (e != RC_OK) return e;
+  const unsigned grid = rc::grid_of(a->num_tokens, sms);
+  if (a->dtype == RC_DTYPE_BF16)
+    rc::launch_read<__nv_bfloat16>(*a, grid, st, (cudaStream_t)stream);
+  else
+    rc::launch_read<float>(*a, grid, st, (cudaStream_t)stream);
+  rc::count_launches(1);
+  return rc::check_launch(fn);
+}
