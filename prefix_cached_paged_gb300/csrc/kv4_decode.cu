@@ -9,9 +9,9 @@
 // Work split: the steps of all (row, group of KV heads) pairs in one line, cut into as many equal ranges as
 // CTAs fit on the GPU at once, so long and short rows share them evenly; states of a pair that
 // ranges cut are joined by a second kernel, in the order of their tokens. In a CTA a warp takes one KV
-// head, so that neighbouring heads of a slot are read at the same time (their rows do not end on
-// sectors), and with few KV heads several warps share a head's tokens. A warp works alone on its ring
-// of cp.async stages of 32 tokens.
+// head; with few KV heads several warps share a head's tokens. A step's tokens (16 for each warp) are
+// copied whole, all heads of the CTA from neighbouring lanes, into a ring that the warps share: 640
+// bytes at once reach 6.7 TB/s on scattered slots, 80 bytes for each head 3.2 (8 heads of 128).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -23,11 +23,8 @@
 namespace rc {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxGroup = 16;
-constexpr int kMaxCtas = 304;   // two for each of 152 SMs
-constexpr int kTile = 32;       // tokens of a stage
+constexpr int kTile = 16;       // tokens of a step for each warp
 
 struct Range {     // of one CTA: the pairs it shares with others, -1: none
   int row0, hg0, start0, last0;   // begun before it: first and last CTA
@@ -52,23 +49,51 @@ struct Params {
 template <typename T, int D, int NT>
 struct Cfg {
   static constexpr int NG = D / 32, RB = kv4_row_bytes(D);
-  static constexpr int CH = 4 * NG;          // bytes of a chunk: what a lane reads of a token's codes
   static constexpr bool F32 = sizeof(T) == 4;
   static constexpr int QP = F32 ? 3 : 1;     // bf16 parts of a query element
   static constexpr int PP = F32 ? 3 : 2;     // of a weight
-  static constexpr int PER_SM = F32 || NT > 1 ? 1 : 2;
-  static constexpr int STAGES = PER_SM == 1 ? 4 : 2;
-  // a stage: codes of K, (scale, minimum) of K in rows of 16 bytes, the same of V
-  static constexpr int PAR = kTile * 4 * CH, VAL = PAR + kTile * 16, STAGE = 2 * VAL;
-  static constexpr int WARP = STAGES * STAGE, SMEM = kWarps * WARP;
-  static_assert(STAGE >= 8 * (D + 2) * 4, "a stage holds the state of 8 heads");
+  static constexpr int WARPS = NT > 1 || F32 ? 4 : 8;               // of a CTA, at most
+  static constexpr int PER_SM = F32 ? 2 : NT > 1 ? 3 : 2;           // CTAs of so many warps
+  static constexpr int CH = 4 * NG;          // bytes of a copy: a head's row is five
+  static constexpr int STAGES = 5, AHEAD = 3;
 };
+// The most warps of the kernels above on an SM.
+constexpr int kMaxWarpsPerSm = 16;
+constexpr int kSms = 152;
+constexpr int kMaxSmem = 112 << 10;   // of a CTA
 
-// chunk c of row r of a stage's codes lies at c ^ swizzle(r): conflict-free for K (8 rows x 4 chunks)
-// and V (rows 2t, chunk g / 2)
+// Row r of a tile lies at place(r) of its 16 tokens, so that rows whose addresses differ by an odd
+// number of 16 bytes for each place are read without conflicts: the lanes of K that go together take two
+// (heads of 64: four) rows of 64 (32) bytes, those of V four rows' pieces.
 template <int NG>
-__device__ __forceinline__ int swizzle(int r) {
-  return NG == 4 ? r >> 1 & 3 : (r >> 2 & 1) << 1;
+__device__ __forceinline__ int place(int r) {
+  return NG == 4 ? (r & 8) | (r & 1) << 2 | (r >> 1 & 3) : (r & 8) | (r & 3) << 1 | (r >> 2 & 1);
+}
+
+// Waits for the phase of that parity, at most about 2 s: then the thread sets the status word, waits
+// for its copies and leaves, as the others will. A wait that looks no more often than it has to, and in
+// few instructions: warps that wait share their scheduler with those that work.
+__device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, int* status) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+  if (done) return;
+  for (int i = 0; i < 100000; ++i) {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done) : "r"(bar), "r"(parity), "r"(20000) : "memory");   // 20 us
+    if (done) return;
+  }
+  set_status(status, kStatusWaitExpired);
+  asm volatile("cp.async.wait_all;\n exit;" ::: "memory");
+}
+
+// Bytes between tokens of a stage: an odd number of 16.
+__host__ __device__ constexpr int pitch_of(int heads, int row_bytes) {
+  return ((heads * row_bytes + 15) / 16 | 1) * 16;
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -79,28 +104,43 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+constexpr uint32_t pow2_bf16x2(int e) { return (uint32_t)(127 + e) << 7 | (uint32_t)(127 + e) << 23; }
+constexpr uint32_t kMinus = 0x80008000u;
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ void ldmatrix_x2_trans(uint32_t addr, uint32_t& r0, uint32_t& r1) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
-               : "=r"(r0), "=r"(r1) : "r"(addr) : "memory");
+// D (16 x 8) = A (16 x 16) B (16 x 8) + C
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 template <int N>
-__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&r)[N]) {
+__device__ __forceinline__ void load(const char* at, uint32_t (&r)[N]) {
   static_assert(N == 2 || N == 4, "");
-  if constexpr (N == 4)
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-  else
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ uint32_t lds1(uint32_t addr) {
-  uint32_t r;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
-  return r;
+  if constexpr (N == 4) {
+    const uint4 v = *(const uint4*)at;
+    r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+  } else {
+    const uint2 v = *(const uint2*)at;
+    r[0] = v.x, r[1] = v.y;
+  }
 }
 // the upper and lower halves' next bf16 part: packs and leaves the rest
 __device__ __forceinline__ uint32_t take_part(float& lo, float& hi) {
@@ -123,22 +163,27 @@ struct Cut {
   __device__ int of(int64_t x) const { return (int)(((x + 1) * ctas - 1) / total); }
 };
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, (Cfg<T, D, NT>::PER_SM))
+// FULL: a warp for each of C::WARPS KV heads; all distances in shared memory are constants then.
+template <typename T, int D, int NT, bool FULL>
+__global__ void __launch_bounds__(32 * Cfg<T, D, NT>::WARPS, (Cfg<T, D, NT>::PER_SM))
 kv4_decode_kernel(const __grid_constant__ Params p) {
   using C = Cfg<T, D, NT>;
-  constexpr int NG = C::NG, QP = C::QP, PP = C::PP, S = C::STAGES;
+  constexpr int NG = C::NG, RB = C::RB, QP = C::QP, PP = C::PP, S = C::STAGES;
   extern __shared__ __align__(16) char smem[];
-  __shared__ int64_t s_sum[kWarps];
+  __shared__ int64_t s_sum[C::WARPS];
   __shared__ int64_t s_before;
   __shared__ int s_row;
-  __shared__ uint4 s_meta[kWarps][S];
+  __shared__ __align__(16) uint8_t s_none[S][128];   // tokens that are not there
+  __shared__ uint64_t s_full[S], s_empty[S];
   const auto& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
+  const int HG = FULL ? C::WARPS : p.HG, TS = FULL ? 1 : p.TS, warps = HG * TS;
+  const int pitch = pitch_of(HG, RB);
+  const int tokens = kTile * TS, plane = tokens * pitch;   // of a stage
 
   // ---- the CTA's range: a scan of all rows' steps
-  const int each = (a.num_rows + kThreads - 1) / kThreads;
+  const int each = (a.num_rows + (int)blockDim.x - 1) / (int)blockDim.x;
   const int r0 = min(a.num_rows, (int)threadIdx.x * each), r1 = min(a.num_rows, r0 + each);
   int64_t mine = 0;
   for (int r = r0; r < r1; ++r) mine += steps_of(p, a.seq_len[r], a.req_idx[r]);
@@ -149,9 +194,14 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     if (lane >= x) upto += y;
   }
   if (lane == 31) s_sum[warp] = upto;
+  if (threadIdx.x < S) {
+    mbar_init(&s_full[threadIdx.x], 33 * warps);
+    mbar_init(&s_empty[threadIdx.x], warps);
+    fence_mbar_init();
+  }
   __syncthreads();
   int64_t total = 0;
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < warps; ++w) {
     if (w == warp) upto += total;
     total += s_sum[w];
   }
@@ -180,19 +230,12 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     const int len = a.seq_len[r];
     if (steps_of(p, len, a.req_idx[r])) continue;
     if (len != 0 && threadIdx.x == 0) set_status(p.status, kStatusPosRange);
-    for (int x = threadIdx.x; x < a.num_q_heads * D; x += kThreads)
+    for (int x = threadIdx.x; x < a.num_q_heads * D; x += blockDim.x)
       ((T*)a.o)[(int64_t)r * a.num_q_heads * D + x] = Elem<T>::from_f(0.f);
     if (a.lse)
-      for (int x = threadIdx.x; x < a.num_q_heads; x += kThreads)
+      for (int x = threadIdx.x; x < a.num_q_heads; x += blockDim.x)
         a.lse[(int64_t)r * a.num_q_heads + x] = -INFINITY;
   }
-  // the unused half of the rows of (scale, minimum) takes part in matrix products
-  const uint32_t ring = smem_u32(smem) + warp * C::WARP;
-  if (NG == 2)
-    for (int s = 0; s < S; ++s)
-      for (int v = 0; v < 2; ++v)
-        *(uint2*)(smem + warp * C::WARP + s * C::STAGE + v * C::VAL + C::PAR + lane * 16 + 8) =
-            make_uint2(0, 0);
   __syncthreads();
   if (threadIdx.x == 0) {
     Range rg = {-1, 0, 0, 0, -1, 0, 0, 0};
@@ -210,86 +253,110 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     p.w.range[blockIdx.x] = rg;   // row1 follows where the pair is met
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int hw = warp % p.HG, ts = warp / p.HG;
-  if (idle || ts >= p.TS) return;
+  if (idle) return;
 
-  // ---- the producer's place: pair (row, hg), step of it
-  const int64_t stride = (int64_t)a.num_kv_heads * C::RB;
-  int row = s_row, req = a.req_idx[row], len = a.seq_len[row], steps = max(1, steps_of(p, len, req));
-  int hg = min(p.groups - 1, (int)((begin - s_before) / steps)), step = (int)((begin - s_before) % steps);
-  int64_t left = end - begin;   // steps to issue
-  const int64_t count = left;
-  int len1 = 0, req1 = 0;       // of the next row
-  auto peek = [&] {
-    if (row + 1 < a.num_rows) len1 = a.seq_len[row + 1], req1 = a.req_idx[row + 1];
+  // ---- copies: of a step's rows (K and V of its tokens in turn) a warp takes 32 / HG at a time, HG
+  // lanes for each; with head counts that are no power of two some warps take as many again
+  const int rows_each = 32 / HG, piece = lane % HG;
+  const int mine0 = warp * rows_each + lane / HG, mine1 = mine0 + warps * rows_each;
+  const bool part0 = FULL || (lane / HG < rows_each && mine0 < 2 * tokens);
+  const bool part1 = !FULL && part0 && mine1 < 2 * tokens;
+  const bool twice = !FULL && warps * rows_each < 2 * tokens;
+  const int further = (mine1 >> 1) - (mine0 >> 1);   // tokens from the first row's to the second's
+  // a place in the line: a pair, and its steps that are left to this CTA
+  struct Place {
+    int row, hg, steps, left;
+    int64_t total;   // of all pairs from this one on
   };
-  peek();
-  bool opened = true;           // first step of a pair in this CTA
-  int slot = 0;
-  auto load_slots = [&] {
-    const int pos = (step * p.TS + ts) * kTile + lane;
-    slot = pos < len ? a.req_to_token[(int64_t)req * a.max_ctx + pos] : 0;
-  };
-  // where the lane's 5 of a stage's 160 chunks (5 of a token: four of codes, (scale, minimum)) lie
-  int from[5], dst[5];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) {
-    const int tok = (i * 32 + lane) / 5, c = (i * 32 + lane) % 5;
-    from[i] = tok | c << 8;
-    dst[i] = c < 4 ? tok * 4 * C::CH + (c ^ swizzle<NG>(tok)) * C::CH : C::PAR + tok * 16;
-  }
-  auto issue = [&](int stage) {
-    if (left > 0) {
-      const int n = len - (step * p.TS + ts) * kTile;
-      const bool ok = lane < n && slot >= 0 && slot < a.num_slots;
-      if (lane < n && !ok) set_status(p.status, kStatusSlotRange);
-      const uint32_t live = __ballot_sync(~0u, ok);
-      const char* kb = (const char*)a.k_pool + (int64_t)(hg * p.HG + hw) * C::RB;
-      const char* vb = (const char*)a.v_pool + (int64_t)(hg * p.HG + hw) * C::RB;
-      const uint32_t base = ring + stage * C::STAGE;
-#pragma unroll
-      for (int i = 0; i < 5; ++i) {
-        const int tok = from[i] & 255;
-        const bool in = live >> tok & 1;
-        const int s = __shfl_sync(~0u, slot, tok);
-        const int64_t off = in ? s * stride + (from[i] >> 8) * C::CH : 0;
-        cp_async_or_zero<C::CH>(base + dst[i], kb + off, in);
-        cp_async_or_zero<C::CH>(base + C::VAL + dst[i], vb + off, in);
-      }
-      --left;
-      const bool ends = step + 1 == steps;
-      if (lane == 0)
-        s_meta[warp][stage] = make_uint4(row, hg << 4 | (opened ? 1 : 0) | (ends || left == 0 ? 2 : 0) |
-                                                  (ends ? 4 : 0) | (step == 0 ? 8 : 0),
-                                         live, steps);
-      opened = ends;
-      if (!ends) {
-        ++step;
-      } else if (left > 0) {
-        step = 0;
-        if (++hg == p.groups) {
-          hg = 0;
-          do {
-            ++row, len = len1, req = req1;
-            steps = steps_of(p, len, req);
-            peek();
-          } while (steps == 0 && row + 1 < a.num_rows);
-        }
-      }
-      if (left > 0) load_slots();
+  const int first_steps = max(1, steps_of(p, a.seq_len[s_row], a.req_idx[s_row]));
+  const int64_t within = begin - s_before;
+  const int first_step = (int)(within % first_steps);
+  Place from;
+  from.row = s_row, from.hg = min(p.groups - 1, (int)(within / first_steps));
+  from.steps = first_steps, from.total = end - begin;
+  from.left = (int)min((int64_t)(first_steps - first_step), from.total);
+  auto next_pair = [&](Place& x) {
+    if (x.total <= 0) return;   // its steps are counted off as they are taken
+    if (++x.hg == p.groups) {
+      x.hg = 0;
+      do {
+        ++x.row;
+        x.steps = steps_of(p, a.seq_len[x.row], a.req_idx[x.row]);
+      } while (x.steps == 0 && x.row + 1 < a.num_rows);
     }
-    cp_async_commit();
+    x.left = (int)min((int64_t)x.steps, x.total);
+  };
+  Place copied = from;
+  const int64_t stride = (int64_t)a.num_kv_heads * RB;
+  const char* src0 = nullptr;        // of the lane's first row in slot 0
+  const int32_t* table = nullptr;    // its token's slot
+  int rest = 0;                      // tokens of the row from it on
+  int slot0 = 0, slot1 = 0;
+  auto slots = [&] {
+    slot0 = part0 && rest > 0 ? *table : 0;
+    if (twice) slot1 = part1 && rest > further ? table[further] : 0;
+  };
+  auto open_copies = [&](int step) {
+    const int pos = step * tokens + (mine0 >> 1);
+    table = a.req_to_token + (int64_t)a.req_idx[copied.row] * a.max_ctx + pos;
+    rest = a.seq_len[copied.row] - pos;
+    src0 = (const char*)(mine0 & 1 ? a.v_pool : a.k_pool) + copied.hg * HG * RB + piece * C::CH;
+    slots();
+  };
+  int to = 0;                   // the stage that is copied to next
+  uint32_t to_phase = 1;        // and what its last use has ended; a new barrier counts as ended
+  const uint32_t dst0 = smem_u32(smem) + (mine0 & 1) * plane + (mine0 >> 1) * pitch + piece * C::CH;
+  const uint32_t none0 = smem_u32(&s_none[0][mine0 >> 1]);
+  const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
+  const uint32_t slots_in = (uint32_t)min(a.num_slots, (int64_t)1 << 31);
+  auto copy_row = [&](const char* src, uint32_t dst, uint32_t none, int slot, bool in) {
+    const bool good = in && (uint32_t)slot < slots_in;
+    if (in && !good) set_status(p.status, kStatusSlotRange);
+    src += (good ? slot : 0) * stride;
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+      cp_async_or_zero<C::CH>(dst + i * HG * C::CH, src + i * HG * C::CH, good);
+    if (piece == 0)
+      asm volatile("st.shared.u8 [%0], %1;" ::"r"(none), "r"(good ? 0 : 1) : "memory");
+  };
+  auto issue = [&] {
+    wait_for(empty0 + 8 * to, to_phase, p.status);
+    const uint32_t dst = dst0 + to * 2 * plane, none = none0 + to * 128;
+    if (part0) copy_row(src0, dst, none, slot0, rest > 0);
+    // the rows between the two are an even number: both K or both V
+    if (twice && part1)
+      copy_row(src0, dst + further * pitch, none + further, slot1, rest > further);
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full0 + 8 * to) : "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s_full[to]);
+    if (++to == S) to = 0, to_phase ^= 1;
+    --copied.total;
+    if (--copied.left == 0) {
+      next_pair(copied);
+      if (copied.left > 0) open_copies(0);
+    } else {
+      table += tokens, rest -= tokens;
+      slots();
+    }
   };
 
-  // ---- the consumer's state of one pair: queries, maxima and sums, outputs
+  // ---- the state of one pair: queries, maxima and sums, outputs
+  const int hw = FULL ? warp : warp % HG, ts = FULL ? 0 : warp / HG;
   uint32_t qf[QP][NT][NG][2][2];   // query elements of the matrix steps of each group
   uint32_t qm[NT][3];              // sums of a group's query elements, in three bf16 parts
+  float Q[C::F32 ? NT : 1][C::F32 ? NG : 1][2];   // the same in fp32, of heads 2t and 2t + 1
   float F[NT][2], mx[NT][2], l[NT][2];
-  float O[NT][NG][2][4], M[NT][4];
-  int whole = 0;                   // the pair began in this CTA
-  int64_t first = 0;               // its first step here
+  constexpr int NW = NG / 2;       // words of codes that a lane holds of a token's values
+  float O[NT][NW][2][2][4];
+  float M[NT][C::F32 ? 2 * NG : 4];
+  Place at = from;
+  int here = from.left;            // its steps in this CTA
+  bool whole = first_step == 0;    // the pair began in this CTA
+  bool ends = first_step + from.left == from.steps;
+  int64_t first = begin;           // its first step here
 
-  auto begin_pair = [&](int row, int h) {
+  auto begin_pair = [&] {
+    const int h = at.hg * HG + hw;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int qh = nt * 8 + g;
@@ -299,7 +366,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
         for (int n = 0; n < 8; ++n) x[j][n] = 0.f;
         if (qh < p.G) {
-          const T* src = (const T*)a.q + ((int64_t)row * a.num_q_heads + h * p.G + qh) * D + 32 * j +
+          const T* src = (const T*)a.q + ((int64_t)at.row * a.num_q_heads + h * p.G + qh) * D + 32 * j +
                          8 * t;
           if constexpr (C::F32) {
             const float4 u = ((const float4*)src)[0], v = ((const float4*)src)[1];
@@ -318,8 +385,8 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
       most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
       // the head's elements over 2^e, below 4 in magnitude: a power of two, exact. A code's pattern
       // is the bf16 number code * 2^-133 (or 16 times that), subnormal or next to it, which times
-      // an element * 2^125 is code * element * 2^-8
-      const int e = min(max((int)(__float_as_uint(most) >> 23) - 127, -100), 126);
+      // an element * 2^125 is code * element * 2^-8 (fp32: (code - 8) * 2^-33, times 2^25)
+      const int e = min(max((int)(__float_as_uint(most) >> 23) - 127, -40), 126);
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);
       float sum = 0.f;
 #pragma unroll
@@ -330,11 +397,14 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
         s += __shfl_xor_sync(~0u, s, 1);
         s += __shfl_xor_sync(~0u, s, 2);
         if (t == j) sum = s;
+        if constexpr (C::F32)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) Q[nt][j][k] = 0x1p-8f * __shfl_sync(~0u, s, (2 * t + k) * 4);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const float up = b ? 0x1p121f : 0x1p125f;
+            const float up = (C::F32 ? 0x1p25f : 0x1p125f) * (b ? 0.0625f : 1.f);
             float lo = x[j][2 * k + b] * up, hi = x[j][2 * k + b + 4] * up;
 #pragma unroll
             for (int q = 0; q < QP; ++q) qf[q][nt][j][k][b] = take_part(lo, hi);
@@ -351,58 +421,108 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
         mx[nt][k] = -FLT_MAX, l[nt][k] = 0.f;
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        M[nt][k] = 0.f;
+      for (int k = 0; k < (C::F32 ? 2 * NG : 4); ++k) M[nt][k] = 0.f;
 #pragma unroll
-        for (int j = 0; j < NG; ++j) O[nt][j][0][k] = O[nt][j][1][k] = 0.f;
-      }
+      for (int k = 0; k < 16 * NW; ++k) (&O[nt][0][0][0][0])[k] = 0.f;
     }
   };
 
-  // scores of 16 tokens (rows 16 u ..): x[nt] = tokens g, g + 8 x heads 2t, 2t + 1
-  auto scores = [&](uint32_t st, int u, float (&x)[NT][4]) {
-    const int r = u * 16 + g;
-    const uint32_t at = st + r * 4 * C::CH + (t ^ swizzle<NG>(r)) * C::CH;
-    const uint32_t par = st + C::PAR + r * 16;
+  // scores of the warp's 16 tokens at kt: x[nt] = rows g, g + 8 x heads 2t, 2t + 1
+  const int k_at = place<NG>(g) * pitch + 4 * NG * t;
+  const int kp_at = place<NG>(g) * pitch + D / 2;
+  const int eight = 8 * pitch;   // rows r and r + 8
+  auto scores = [&](const char* kt, float (&x)[NT][4]) {
     uint32_t wa[NG], wb[NG], pa[NG], pb[NG];
-    lds(at, wa);
-    lds(at + 32 * C::CH, wb);
-    lds(par, pa);
-    lds(par + 128, pb);
-    const uint32_t ma = lds1(par + 4 * t), mb = lds1(par + 128 + 4 * t);
+    load(kt + k_at, wa);
+    load(kt + k_at + eight, wb);
+    load(kt + kp_at, pa);
+    load(kt + kp_at + eight, pb);
+    if constexpr (C::F32) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
-      mma_bf16(x[nt], ma, mb, ma, mb, qm[nt][0], qm[nt][1]);
-      mma_bf16(x[nt], ma, mb, 0, 0, qm[nt][2], 0);
+      for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+    } else {
+      uint32_t ma = 0, mb = 0;
+      if (NG == 4 || t < NG) {
+        ma = *(const uint32_t*)(kt + kp_at + 4 * t);
+        mb = *(const uint32_t*)(kt + kp_at + 4 * t + eight);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_zero(x[nt], ma, mb, ma, mb, qm[nt][0], qm[nt][1]);
+        mma(x[nt], ma, mb, 0, 0, qm[nt][2], 0);
+      }
     }
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
-      float d[NT][4] = {};
+      float d[NT][4], rest[NT][4];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t va = wa[j] >> 8 * k, vb = wb[j] >> 8 * k;
-        const uint32_t a0 = va & 0x000F000Fu, a1 = vb & 0x000F000Fu;
-        const uint32_t a2 = va & 0x00F000F0u, a3 = vb & 0x00F000F0u;
+        uint32_t a0 = va & 0x000F000Fu, a1 = vb & 0x000F000Fu;
+        uint32_t a2 = va & 0x00F000F0u, a3 = vb & 0x00F000F0u;
+        if constexpr (C::F32) {   // (code - 8) * 2^-33, 16 times that: small sums lose less
+          a0 = fma2(a0, pow2_bf16x2(100), kMinus | pow2_bf16x2(-30));
+          a1 = fma2(a1, pow2_bf16x2(100), kMinus | pow2_bf16x2(-30));
+          a2 = fma2(a2, pow2_bf16x2(100), kMinus | pow2_bf16x2(-26));
+          a3 = fma2(a3, pow2_bf16x2(100), kMinus | pow2_bf16x2(-26));
+        }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int q = 0; q < QP; ++q)
-            mma_bf16(d[nt], a0, a1, a2, a3, qf[q][nt][j][k][0], qf[q][nt][j][k][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          if (k == 0)
+            mma_zero(d[nt], a0, a1, a2, a3, qf[0][nt][j][k][0], qf[0][nt][j][k][1]);
+          else
+            mma(d[nt], a0, a1, a2, a3, qf[0][nt][j][k][0], qf[0][nt][j][k][1]);
+          if constexpr (C::F32) {
+            if (k == 0)
+              mma_zero(rest[nt], a0, a1, a2, a3, qf[1][nt][j][k][0], qf[1][nt][j][k][1]);
+            else
+              mma(rest[nt], a0, a1, a2, a3, qf[1][nt][j][k][0], qf[1][nt][j][k][1]);
+            mma(rest[nt], a0, a1, a2, a3, qf[2][nt][j][k][0], qf[2][nt][j][k][1]);
+          }
+        }
       }
       const float sa = bf16lo(pa[j]), sb = bf16lo(pb[j]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        x[nt][0] = fmaf(sa, d[nt][0], x[nt][0]);
-        x[nt][1] = fmaf(sa, d[nt][1], x[nt][1]);
-        x[nt][2] = fmaf(sb, d[nt][2], x[nt][2]);
-        x[nt][3] = fmaf(sb, d[nt][3], x[nt][3]);
+        if constexpr (C::F32) {
+          const float ca = fmaf(8.f, sa, bf16hi(pa[j])), cb = fmaf(8.f, sb, bf16hi(pb[j]));
+          x[nt][0] += fmaf(sa, d[nt][0], fmaf(sa, rest[nt][0], ca * Q[nt][j][0]));
+          x[nt][1] += fmaf(sa, d[nt][1], fmaf(sa, rest[nt][1], ca * Q[nt][j][1]));
+          x[nt][2] += fmaf(sb, d[nt][2], fmaf(sb, rest[nt][2], cb * Q[nt][j][0]));
+          x[nt][3] += fmaf(sb, d[nt][3], fmaf(sb, rest[nt][3], cb * Q[nt][j][1]));
+        } else {
+          x[nt][0] = fmaf(sa, d[nt][0], x[nt][0]);
+          x[nt][1] = fmaf(sa, d[nt][1], x[nt][1]);
+          x[nt][2] = fmaf(sb, d[nt][2], x[nt][2]);
+          x[nt][3] = fmaf(sb, d[nt][3], x[nt][3]);
+        }
       }
     }
   };
 
-  // outputs += weights x of 16 tokens times their values
-  auto values = [&](uint32_t st, int u, float (&x)[NT][4]) {
+  // outputs += weights x of the 16 tokens at vt times their values. A lane has the elements
+  // 32 vj + 8 (vt0 + w) + n of tokens 2t, 2t + 1, 2t + 8, 2t + 9: all of one group
+  const int vj = g / (8 / NG), vt0 = g % (8 / NG) * NW;
+  const int v_at = place<NG>(2 * t) * pitch + 4 * (vt0 * NG + vj);
+  const int vp_at = place<NG>(2 * t) * pitch + D / 2 + 4 * vj;
+  const int odd = (place<NG>(1) - place<NG>(0)) * pitch;   // rows 2t and 2t + 1
+  auto word = [](const char* at) { return *(const uint32_t*)at; };
+  auto values = [&](const char* vt, float (&x)[NT][4]) {
+    if constexpr (C::F32) {   // the groups' middles in fp32
+      uint32_t pa[NG], pb[NG];
+      load(vt + kp_at, pa);
+      load(vt + kp_at + eight, pb);
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        const float ca = fmaf(8.f, bf16lo(pa[j]), bf16hi(pa[j]));
+        const float cb = fmaf(8.f, bf16lo(pb[j]), bf16hi(pb[j]));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            M[nt][2 * j + c] += fmaf(x[nt][c], ca, x[nt][2 + c] * cb);
+      }
+    }
     uint32_t b[NT][PP][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -411,71 +531,80 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
         b[nt][k][0] = movmatrix_trans(take_part(x[nt][0], x[nt][1]));
         b[nt][k][1] = movmatrix_trans(take_part(x[nt][2], x[nt][3]));
       }
-    const int r = u * 16 + 2 * t;
-    const uint32_t at = st + C::VAL + r * 4 * C::CH + ((g >> 1) ^ swizzle<NG>(r)) * C::CH;
-    const uint32_t par = st + C::VAL + C::PAR + u * 256;
-    uint32_t m0, m1;
-    ldmatrix_x2_trans(par + (lane & 15) * 16, m0, m1);
+    const uint32_t q0 = word(vt + vp_at), q1 = word(vt + vp_at + odd);
+    const uint32_t q2 = word(vt + vp_at + eight), q3 = word(vt + vp_at + odd + eight);
+    const uint32_t s01 = mul2(prmt(q0, q1, 0x5410), pow2_bf16x2(96));
+    const uint32_t s23 = mul2(prmt(q2, q3, 0x5410), pow2_bf16x2(96));
+    if constexpr (!C::F32) {   // row g: weights times minima of the lane's group
+      const uint32_t m01 = prmt(q0, q1, 0x7632), m23 = prmt(q2, q3, 0x7632);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k = 0; k < PP; ++k) mma_bf16(M[nt], m0, 0, m1, 0, b[nt][k][0], b[nt][k][1]);
-    uint32_t w0[NG], w1[NG], w2[NG], w3[NG], s01[NG], s23[NG];
-    {
-      uint32_t q0[NG], q1[NG];
-      lds(par + 2 * t * 16, q0);
-      lds(par + 2 * t * 16 + 16, q1);
-#pragma unroll
-      for (int j = 0; j < NG; ++j) s01[j] = mul2(prmt(q0[j], q1[j], 0x5410), 0x6F806F80u);   // 2^96
-      lds(par + 2 * t * 16 + 128, q0);
-      lds(par + 2 * t * 16 + 144, q1);
-#pragma unroll
-      for (int j = 0; j < NG; ++j) s23[j] = mul2(prmt(q0[j], q1[j], 0x5410), 0x6F806F80u);
+        for (int k = 0; k < PP; ++k) {
+          float (&m)[4] = *(float (*)[4])&M[nt][0];
+          mma(m, m01, 0, m23, 0, b[nt][k][0], b[nt][k][1]);
+        }
     }
-    lds(at, w0);
-    lds(at + 4 * C::CH, w1);
-    lds(at + 32 * C::CH, w2);
-    lds(at + 36 * C::CH, w3);
-    const uint32_t half = g & 1 ? 0x7632 : 0x5410;
+    uint32_t n01 = 0, n23 = 0, e01 = 0, e23 = 0;
+    if constexpr (C::F32) {   // -8 times the scale, and 16 times that
+      n01 = mul2(s01, kMinus | pow2_bf16x2(-126)), n23 = mul2(s23, kMinus | pow2_bf16x2(-126));
+      e01 = mul2(n01, pow2_bf16x2(-4)), e23 = mul2(n23, pow2_bf16x2(-4));
+    }
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      const uint32_t v01 = prmt(w0[j], w1[j], half), v23 = prmt(w2[j], w3[j], half);
+    for (int w = 0; w < NW; ++w) {
+      const char* at = vt + v_at + 4 * NG * w;
+      const uint32_t w0 = word(at), w1 = word(at + odd), w2 = word(at + eight);
+      const uint32_t w3 = word(at + odd + eight);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        // code * 2^-133 (16 times that) times scale * 2^96: eight bits, exact
-        const uint32_t va = v01 >> 8 * k, vb = v23 >> 8 * k;
-        const uint32_t a0 = mul2(va & 0x000F000Fu, s01[j]), a1 = mul2(va & 0x00F000F0u, s01[j]);
-        const uint32_t a2 = mul2(vb & 0x000F000Fu, s23[j]), a3 = mul2(vb & 0x00F000F0u, s23[j]);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t v01 = prmt(w0, w1, h ? 0x7632 : 0x5410), v23 = prmt(w2, w3, h ? 0x7632 : 0x5410);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if constexpr (C::F32) {   // sums in fp32, since a matrix instruction cuts its sums off
-            float d[4] = {};
-#pragma unroll
-            for (int q = 0; q < PP; ++q) mma_bf16(d, a0, a1, a2, a3, b[nt][q][0], b[nt][q][1]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) O[nt][j][k][q] += d[q];
+        for (int k = 0; k < 2; ++k) {
+          // code * 2^-133 (16 times that) times scale * 2^96: eight bits, exact
+          const uint32_t va = v01 >> 8 * k, vb = v23 >> 8 * k;
+          uint32_t a0, a1, a2, a3;
+          if constexpr (C::F32) {   // of code - 8
+            a0 = fma2(va & 0x000F000Fu, s01, e01), a1 = fma2(va & 0x00F000F0u, s01, n01);
+            a2 = fma2(vb & 0x000F000Fu, s23, e23), a3 = fma2(vb & 0x00F000F0u, s23, n23);
           } else {
+            a0 = mul2(va & 0x000F000Fu, s01), a1 = mul2(va & 0x00F000F0u, s01);
+            a2 = mul2(vb & 0x000F000Fu, s23), a3 = mul2(vb & 0x00F000F0u, s23);
+          }
 #pragma unroll
-            for (int q = 0; q < PP; ++q)
-              mma_bf16(O[nt][j][k], a0, a1, a2, a3, b[nt][q][0], b[nt][q][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (C::F32) {   // sums in fp32, since a matrix instruction cuts its sums off
+              float d[4];
+              mma_zero(d, a0, a1, a2, a3, b[nt][0][0], b[nt][0][1]);
+              mma(d, a0, a1, a2, a3, b[nt][1][0], b[nt][1][1]);
+              mma(d, a0, a1, a2, a3, b[nt][2][0], b[nt][2][1]);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) O[nt][w][h][k][q] += d[q];
+            } else {
+#pragma unroll
+              for (int q = 0; q < PP; ++q)
+                mma(O[nt][w][h][k], a0, a1, a2, a3, b[nt][q][0], b[nt][q][1]);
+            }
           }
         }
       }
     }
   };
 
-  // the state of head 2t + c of tile nt: dims 32 j + 4 g .. + 3
-  auto outputs = [&](int nt, int c, int j, float4& v) {
-    const float m = __shfl_sync(~0u, M[nt][c], (2 * j + 1) * 4 + t);
-    v.x = fmaf(O[nt][j][0][c], 0x1p37f, m);
-    v.y = fmaf(O[nt][j][0][2 + c], 0x1p33f, m);
-    v.z = fmaf(O[nt][j][1][c], 0x1p37f, m);
-    v.w = fmaf(O[nt][j][1][2 + c], 0x1p33f, m);
+  // the state of head 2t + c of tile nt: elements 32 vj + 8 (vt0 + w) + 4 h .. + 3
+  auto element = [&](int w, int h) { return 32 * vj + 8 * (vt0 + w) + 4 * h; };
+  auto outputs = [&](int nt, int c, int w, int h) {
+    float m = M[nt][c];
+    if constexpr (C::F32)
+#pragma unroll
+      for (int j = 1; j < NG; ++j) m = vj == j ? M[nt][2 * j + c] : m;
+    const auto& o = O[nt][w][h];
+    return make_float4(fmaf(o[0][c], 0x1p37f, m), fmaf(o[0][2 + c], 0x1p33f, m),
+                       fmaf(o[1][c], 0x1p37f, m), fmaf(o[1][2 + c], 0x1p33f, m));
   };
   // what a pair's head gave: the outputs, or a state in the workspace
-  auto store = [&](int row, int hg, int flags, int qh, int d, float4 v, float m, float den) {
-    const int64_t head = (int64_t)row * a.num_q_heads + (hg * p.HG + hw) * p.G + qh;
-    if (whole && (flags & 4)) {
+  auto store = [&](int qh, int d, float4 v, float m, float den) {
+    const int64_t head = (int64_t)at.row * a.num_q_heads + (at.hg * HG + hw) * p.G + qh;
+    if (whole && ends) {
       const float f = den == 0.f ? 0.f : 1.f / den;
       T* o = (T*)a.o + head * D + d;
       if constexpr (C::F32)
@@ -484,118 +613,112 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
         *(uint2*)o = make_uint2(pack2_bf16(v.x * f, v.y * f), pack2_bf16(v.z * f, v.w * f));
       if (a.lse && d == 0) a.lse[head] = den == 0.f ? -INFINITY : kLn2 * (m + log2f(den));
     } else {
-      const int64_t at = (((int64_t)blockIdx.x * 2 + (whole ? 1 : 0)) * p.HG + hw) * p.G + qh;
-      *(float4*)(p.w.o + at * D + d) = v;
-      if (d == 0) *(float2*)(p.w.ml + at * 2) = make_float2(m, den);
+      const int64_t i = (((int64_t)blockIdx.x * 2 + (whole ? 1 : 0)) * HG + hw) * p.G + qh;
+      *(float4*)(p.w.o + i * D + d) = v;
+      if (d == 0) *(float2*)(p.w.ml + i * 2) = make_float2(m, den);
     }
   };
-  auto end_pair = [&](int row, int hg, int flags, int steps, int stage) {
-    if (warp == 0 && lane == 0 && whole && !(flags & 4)) {
+  auto end_pair = [&](char* stage) {
+    if (threadIdx.x == 0 && whole && !ends) {
       Range* rg = p.w.range + blockIdx.x;
-      rg->row1 = row, rg->hg1 = hg, rg->last1 = cut.of(begin + first + steps - 1);
+      rg->row1 = at.row, rg->hg1 = at.hg, rg->last1 = cut.of(first + at.steps - 1);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int x = 4; x < 32; x *= 2) {
 #pragma unroll
-        for (int x = 4; x < 32; x *= 2) l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], x);
-      if (p.TS == 1) {
+        for (int c = 0; c < 2; ++c) l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], x);
+        if constexpr (C::F32)
+#pragma unroll
+          for (int k = 0; k < 2 * NG; ++k) M[nt][k] += __shfl_xor_sync(~0u, M[nt][k], x);
+      }
+    }
+    if (TS == 1) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int j = 0; j < NG; ++j) {
-            float4 v;
-            outputs(nt, c, j, v);
+          for (int w = 0; w < 2 * NW; ++w) {
+            const float4 v = outputs(nt, c, w >> 1, w & 1);
             const int qh = nt * 8 + 2 * t + c;
-            if (qh < p.G) store(row, hg, flags, qh, 32 * j + 4 * g, v, mx[nt][c], l[nt][c]);
+            if (qh < p.G) store(qh, element(w >> 1, w & 1), v, mx[nt][c], l[nt][c]);
           }
-        continue;
-      }
-      // warps that share a head join their states through the stage that each has just read
-      float* own = (float*)(smem + warp * C::WARP + stage * C::STAGE);
-      __syncwarp();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          float4 v;
-          outputs(nt, c, j, v);
-          *(float4*)(own + (2 * t + c) * D + 32 * j + 4 * g) = v;
-        }
-        if (g == 0) own[8 * D + 2 * t + c] = mx[nt][c], own[8 * D + 8 + 2 * t + c] = l[nt][c];
-      }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + hw), "r"(32 * p.TS) : "memory");
-      const int heads = min(8, p.G - nt * 8);
-      for (int x = ts * 32 + lane; x < heads * (D / 4); x += 32 * p.TS) {
-        const int qh = x / (D / 4), d = x % (D / 4) * 4;
-        float m = -FLT_MAX, den = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = 0; s < p.TS; ++s)
-          m = fmaxf(m, ((const float*)(smem + (s * p.HG + hw) * C::WARP + stage * C::STAGE))[8 * D + qh]);
-        for (int s = 0; s < p.TS; ++s) {
-          const float* other = (const float*)(smem + (s * p.HG + hw) * C::WARP + stage * C::STAGE);
-          const float f = ex2(other[8 * D + qh] - m);
-          const float4 w = *(const float4*)(other + qh * D + d);
-          den = fmaf(f, other[8 * D + 8 + qh], den);
-          v.x = fmaf(f, w.x, v.x), v.y = fmaf(f, w.y, v.y);
-          v.z = fmaf(f, w.z, v.z), v.w = fmaf(f, w.w, v.w);
-        }
-        store(row, hg, flags, nt * 8 + qh, d, v, m, den);
-      }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + hw), "r"(32 * p.TS) : "memory");
+      return;
     }
-    // the copies that come next write what the joins read and wrote; (scale, minimum) rows of two
-    // groups keep their zeros
-    if (NG == 2 && p.TS > 1) {
+    // warps that share a head join their states, four heads at a time, in the stage that all have read
+    constexpr int STATE = 4 * (D + 2);
+    float* own = (float*)stage + warp * STATE;
 #pragma unroll
-      for (int v = 0; v < 2; ++v)
-        *(uint2*)(smem + warp * C::WARP + stage * C::STAGE + v * C::VAL + C::PAR + lane * 16 + 8) =
-            make_uint2(0, 0);
-      __syncwarp();
-    }
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int q4 = (2 * t + c) & 3;
+#pragma unroll
+          for (int w = 0; w < 2 * NW; ++w) {
+            const float4 v = outputs(nt, c, w >> 1, w & 1);
+            if (t >> 1 == part) *(float4*)(own + q4 * D + element(w >> 1, w & 1)) = v;
+          }
+          if (g == 0 && t >> 1 == part)
+            own[4 * D + q4] = mx[nt][c], own[4 * D + 4 + q4] = l[nt][c];
+        }
+        __syncthreads();
+        const int heads = min(4, p.G - nt * 8 - part * 4);
+        for (int x = ts * 32 + lane; x < heads * (D / 4); x += 32 * TS) {
+          const int q4 = x / (D / 4), d = x % (D / 4) * 4;
+          float m = -FLT_MAX, den = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int s = 0; s < TS; ++s)
+            m = fmaxf(m, ((const float*)stage)[(s * HG + hw) * STATE + 4 * D + q4]);
+          for (int s = 0; s < TS; ++s) {
+            const float* other = (const float*)stage + (s * HG + hw) * STATE;
+            const float f = ex2(other[4 * D + q4] - m);
+            const float4 w = *(const float4*)(other + q4 * D + d);
+            den = fmaf(f, other[4 * D + 4 + q4], den);
+            v.x = fmaf(f, w.x, v.x), v.y = fmaf(f, w.y, v.y);
+            v.z = fmaf(f, w.z, v.z), v.w = fmaf(f, w.w, v.w);
+          }
+          store(nt * 8 + part * 4 + q4, d, v, m, den);
+        }
+      }
   };
 
-  load_slots();
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(i);
+  open_copies(first_step);
+  for (int i = 0; i < C::AHEAD && copied.left > 0; ++i) issue();
+  begin_pair();
   int stage = 0;
-  for (int64_t i = 0; i < count; ++i) {
-    issue(stage == 0 ? S - 1 : stage - 1);
-    cp_async_wait<S - 1>();
-    __syncwarp();
-    const uint4 meta = s_meta[warp][stage];
-    const int flags = meta.y & 15, pair = (int)meta.y >> 4;
-    if (flags & 1) {
-      whole = flags & 8;
-      first = i;
-      begin_pair((int)meta.x, pair * p.HG + hw);
+  uint32_t phase = 0;
+  while (true) {
+    if (copied.left > 0) issue();
+    wait_for(full0 + 8 * stage, phase, p.status);
+    char* st = smem + stage * 2 * plane;
+    const char* kt = st + ts * kTile * pitch + hw * RB;
+    float x[NT][4];
+    scores(kt, x);
+    // tokens that are not there weigh nothing
+    const uint4 none = *(const uint4*)&s_none[stage][ts * kTile];
+    if (none.x | none.y | none.z | none.w) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (s_none[stage][ts * kTile + place<NG>(g + 8 * k)])
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) x[nt][2 * k] = x[nt][2 * k + 1] = -INFINITY;
     }
-    const uint32_t st = ring + stage * C::STAGE;
-    float x[2][NT][4];
-    scores(st, 0, x[0]);
-    scores(st, 1, x[1]);
-    // scores to base 2; tokens that are not there weigh nothing. The reference of a head's weights
-    // is a running maximum that follows once a score is 2^8 times beyond it
-    const bool all = meta.z == ~0u;
+    // the reference of a head's weights (to base 2) is a running maximum that follows once a score is
+    // 2^8 times beyond it
     bool beyond = false;
     float top[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) top[nt][c] = -INFINITY;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float& y = x[u][nt][k];
-          y *= F[nt][k & 1];
-          if (!all && !(meta.z >> (u * 16 + (k >> 1) * 8 + g) & 1)) y = -INFINITY;
-          top[nt][k & 1] = fmaxf(top[nt][k & 1], y);
-        }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) beyond |= top[nt][c] > mx[nt][c] + 8.f;
-    }
+      for (int c = 0; c < 2; ++c) {
+        top[nt][c] = fmaxf(x[nt][c], x[nt][2 + c]) * F[nt][c];
+        beyond |= top[nt][c] > mx[nt][c] + 8.f;
+      }
     if (__any_sync(~0u, beyond)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -604,38 +727,50 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
           for (int s = 4; s < 32; s *= 2)
             top[nt][c] = fmaxf(top[nt][c], __shfl_xor_sync(~0u, top[nt][c], s));
-          const float now = fmaxf(mx[nt][c], top[nt][c]), f = ex2(mx[nt][c] - now);
-          mx[nt][c] = now;
+          const float to = fmaxf(mx[nt][c], top[nt][c]), f = ex2(mx[nt][c] - to);
+          mx[nt][c] = to;
           l[nt][c] *= f;
-          M[nt][c] *= f;
 #pragma unroll
-          for (int j = 0; j < NG; ++j)
+          for (int k = 0; k < (C::F32 ? NG : 1); ++k) M[nt][2 * k + c] *= f;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) O[nt][j][k][c] *= f, O[nt][j][k][2 + c] *= f;
+          for (int k = 0; k < 4 * NW; ++k) {
+            float* o = &O[nt][0][0][0][0] + 4 * k + c;
+            o[0] *= f, o[2] *= f;
+          }
         }
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x[u][nt][k] = ex2(x[u][nt][k] - mx[nt][k & 1]);
-          l[nt][k & 1] += x[u][nt][k];
-        }
-      values(st, u, x[u]);
-    }
+      for (int k = 0; k < 4; ++k) {
+        x[nt][k] = ex2(fmaf(x[nt][k], F[nt][k & 1], -mx[nt][k & 1]));
+        l[nt][k & 1] += x[nt][k];
+      }
+    values(kt + plane, x);
+    if (--at.left == 0) end_pair(st);
     __syncwarp();
-    if (flags & 2) end_pair((int)meta.x, pair, flags, (int)meta.w, stage);
-    stage = stage + 1 == S ? 0 : stage + 1;
+    if (lane == 0) mbar_arrive(&s_empty[stage]);
+    if (++stage == S) stage = 0, phase ^= 1;
+    if (at.left > 0) continue;
+    // the next pair of this CTA
+    at.total -= here;
+    first += here;
+    next_pair(at);
+    if (at.left == 0) return;
+    here = at.left;
+    whole = true, ends = here == at.steps;
+    begin_pair();
   }
 }
+
+constexpr int kMergeThreads = 256;
+constexpr int kMergeWarps = kMergeThreads / 32;
 
 // Joins the states of pairs that ranges cut. The CTAs that share a pair share its heads; few states: a
 // warp for each head, many: all warps.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const __grid_constant__ Params p) {
-  __shared__ float so[kWarps][D], sml[kWarps][2];
+__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const __grid_constant__ Params p) {
+  __shared__ float so[kMergeWarps][D], sml[kMergeWarps][2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int E = D / 32;
   const auto& a = p.a;
@@ -648,7 +783,7 @@ __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const __grid_consta
     const int start = side ? (int)blockIdx.x : rg.start0, last = side ? rg.last1 : rg.last0;
     const int n = last - start + 1;
     const bool many = n > 16;
-    const int team = many ? 1 : kWarps, i0 = many ? warp : 0, di = many ? kWarps : 1;
+    const int team = many ? 1 : kMergeWarps, i0 = many ? warp : 0, di = many ? kMergeWarps : 1;
     for (int h = (blockIdx.x - start) * team + (many ? 0 : warp); h < heads; h += n * team) {
       auto at = [&](int i) { return ((int64_t)(start + i) * 2 + (i == 0)) * heads + h; };
       float m = -FLT_MAX, den = 0.f, v[E] = {};
@@ -675,10 +810,10 @@ __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const __grid_consta
         if (lane == 0) sml[warp][0] = m, sml[warp][1] = den;
         __syncthreads();
         m = -FLT_MAX, den = 0.f;
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sml[w][0]);
+        for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, sml[w][0]);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = 0.f;
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < kMergeWarps; ++w) {
           const float f = ex2(sml[w][0] - m);
           den = fmaf(f, sml[w][1], den);
 #pragma unroll
@@ -719,23 +854,21 @@ Params params_of(const rc_kv4_decode_args* a) {
   Params p{};
   p.a = *a;
   p.G = a->num_q_heads / a->num_kv_heads;
-  // the divisor of the KV heads (up to 8) that leaves fewest warps idle, the largest of those
-  int best = 0;
-  for (int h = 1; h <= kWarps; ++h) {
-    if (a->num_kv_heads % h) continue;
-    const int busy = kWarps / h * h;
-    if (busy >= best) best = busy, p.HG = h, p.TS = kWarps / h;
-  }
+  const int warps = a->dtype == RC_DTYPE_F32 || p.G > 8 ? 4 : 8;   // Cfg::WARPS
+  for (int h = 1; h <= warps; ++h)
+    if (a->num_kv_heads % h == 0) p.HG = h;
+  p.TS = warps / p.HG;
   p.groups = a->num_kv_heads / p.HG;
-  p.min_steps = 2;
+  p.min_steps = 4;
   return p;
 }
 
 // CTAs that may have a range, whatever the rows hold.
 int64_t most_ctas(const Params& p) {
   const int64_t steps = (p.a.max_seq_len + kTile * p.TS - 1) / (kTile * p.TS);
+  const int64_t fit = kSms * std::max(1, kMaxWarpsPerSm / (p.HG * p.TS));
   return std::max<int64_t>(1, std::min<int64_t>(
-      kMaxCtas, (steps * p.a.num_rows * p.groups + p.min_steps - 1) / p.min_steps));
+      fit, (steps * p.a.num_rows * p.groups + p.min_steps - 1) / p.min_steps));
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -754,8 +887,15 @@ Workspace carve(void* base, const Params& p, size_t* total) {
   return w;
 }
 
+template <typename T, int D, int NT>
+int smem_of(int HG) {
+  using C = Cfg<T, D, NT>;
+  return C::STAGES * 2 * kTile * (C::WARPS / HG) * pitch_of(HG, C::RB);
+}
+
 struct Setup {
-  int ctas;
+  int sms;
+  int per_sm[9];   // CTAs, by KV heads of a CTA
 };
 
 template <typename T, int D, int NT>
@@ -765,29 +905,37 @@ cudaError_t launch_t(const Params& p, cudaStream_t s) {
   const Setup* st = nullptr;
   cudaError_t e = setup.get(
       [](Setup& x) {
-        int dev = 0, sms = 0, per = 0;
-        cudaError_t r = cudaFuncSetAttribute(kv4_decode_kernel<T, D, NT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-        if (r == cudaSuccess) r = cudaGetDevice(&dev);
+        int dev = 0;
+        cudaError_t r = cudaGetDevice(&dev);
         if (r == cudaSuccess)
-          r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (r == cudaSuccess)
-          r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kv4_decode_kernel<T, D, NT>,
-                                                            kThreads, C::SMEM);
-        x.ctas = std::max(1, std::min(kMaxCtas, sms * per));
+          r = cudaDeviceGetAttribute(&x.sms, cudaDevAttrMultiProcessorCount, dev);
+        for (int h = 1; h <= C::WARPS && r == cudaSuccess; ++h) {
+          const auto kernel = h == C::WARPS ? kv4_decode_kernel<T, D, NT, true>
+                                            : kv4_decode_kernel<T, D, NT, false>;
+          r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+          if (r == cudaSuccess)
+            r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                &x.per_sm[h], kernel, 32 * (C::WARPS / h * h), smem_of<T, D, NT>(h));
+        }
         return r;
       },
       &st);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)std::min<int64_t>(most_ctas(p), st->ctas);
-  kv4_decode_kernel<T, D, NT><<<grid, kThreads, C::SMEM, s>>>(p);
+  const int warps = p.HG * p.TS;
+  const unsigned grid = (unsigned)std::min<int64_t>(
+      most_ctas(p), (int64_t)st->sms * std::max(1, std::min(st->per_sm[p.HG], kMaxWarpsPerSm / warps)));
+  const int smem = smem_of<T, D, NT>(p.HG);
+  if (p.HG == C::WARPS)
+    kv4_decode_kernel<T, D, NT, true><<<grid, 32 * warps, smem, s>>>(p);
+  else
+    kv4_decode_kernel<T, D, NT, false><<<grid, 32 * warps, smem, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   count_launches(1);
   if (grid == 1 || p.a.max_seq_len <= kTile * p.TS) return cudaSuccess;   // no pair is cut
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
