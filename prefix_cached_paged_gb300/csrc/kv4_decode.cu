@@ -24,7 +24,6 @@ namespace rc {
 namespace {
 
 constexpr int kMaxGroup = 16;
-constexpr int kTile = 16;       // tokens of a step for each warp
 
 struct Range {     // of one CTA: the pairs it shares with others, -1: none
   int row0, hg0, start0, last0;   // begun before it: first and last CTA
@@ -42,6 +41,7 @@ struct Params {
   int* status;
   int G;          // query heads of a KV head
   int HG, TS;     // KV heads of a CTA, warps that share a head's tokens
+  int tokens;     // of a step
   int groups;     // KV heads / HG
   int min_steps;  // of a CTA
 };
@@ -55,7 +55,8 @@ struct Cfg {
   static constexpr int WARPS = NT > 1 || F32 ? 4 : 8;               // of a CTA, at most
   static constexpr int PER_SM = F32 ? 2 : NT > 1 ? 3 : 2;           // CTAs of so many warps
   static constexpr int CH = 4 * NG;          // bytes of a copy: a head's row is five
-  static constexpr int STAGES = 5, AHEAD = 3;
+  static constexpr int HALVES = 5, AHEAD = 4;   // of the ring, in flight
+  static constexpr int U = 2;                // tiles of 16 tokens of a warp's step
 };
 // The most warps of the kernels above on an SM.
 constexpr int kMaxWarpsPerSm = 16;
@@ -152,7 +153,7 @@ __device__ __forceinline__ uint32_t take_part(float& lo, float& hi) {
 
 __device__ __forceinline__ int steps_of(const Params& p, int len, int req) {
   if (len <= 0 || len > p.a.max_seq_len || req < 0 || req >= p.a.max_reqs) return 0;
-  return (len + kTile * p.TS - 1) / (kTile * p.TS);
+  return (len + p.tokens - 1) / p.tokens;
 }
 
 // How the line of steps is cut: range c is [total c / ctas, total (c + 1) / ctas).
@@ -168,19 +169,19 @@ template <typename T, int D, int NT, bool FULL>
 __global__ void __launch_bounds__(32 * Cfg<T, D, NT>::WARPS, (Cfg<T, D, NT>::PER_SM))
 kv4_decode_kernel(const __grid_constant__ Params p) {
   using C = Cfg<T, D, NT>;
-  constexpr int NG = C::NG, RB = C::RB, QP = C::QP, PP = C::PP, S = C::STAGES;
+  constexpr int NG = C::NG, RB = C::RB, QP = C::QP, PP = C::PP, S = C::HALVES, U = C::U;
   extern __shared__ __align__(16) char smem[];
   __shared__ int64_t s_sum[C::WARPS];
   __shared__ int64_t s_before;
   __shared__ int s_row;
-  __shared__ __align__(16) uint8_t s_none[S][128];   // tokens that are not there
+  __shared__ __align__(16) uint8_t s_none[S][16 * C::WARPS * U];   // tokens that are not there
   __shared__ uint64_t s_full[S], s_empty[S];
   const auto& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int HG = FULL ? C::WARPS : p.HG, TS = FULL ? 1 : p.TS, warps = HG * TS;
   const int pitch = pitch_of(HG, RB);
-  const int tokens = kTile * TS, plane = tokens * pitch;   // of a stage
+  const int tokens = 16 * U * TS, half = tokens * pitch;   // of K or V of a step
 
   // ---- the CTA's range: a scan of all rows' steps
   const int each = (a.num_rows + (int)blockDim.x - 1) / (int)blockDim.x;
@@ -255,14 +256,13 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (idle) return;
 
-  // ---- copies: of a step's rows (K and V of its tokens in turn) a warp takes 32 / HG at a time, HG
-  // lanes for each; with head counts that are no power of two some warps take as many again
+  // ---- copies: K and V of a step in turn. Of their tokens a warp takes 32 / HG at a time, HG lanes for
+  // each; with head counts that are no power of two some warps take as many again
   const int rows_each = 32 / HG, piece = lane % HG;
-  const int mine0 = warp * rows_each + lane / HG, mine1 = mine0 + warps * rows_each;
-  const bool part0 = FULL || (lane / HG < rows_each && mine0 < 2 * tokens);
-  const bool part1 = !FULL && part0 && mine1 < 2 * tokens;
-  const bool twice = !FULL && warps * rows_each < 2 * tokens;
-  const int further = (mine1 >> 1) - (mine0 >> 1);   // tokens from the first row's to the second's
+  const int tok0 = warp * rows_each + lane / HG;   // the lane's first
+  const bool copies = FULL || lane / HG < rows_each;
+  const int further = warps * rows_each;           // from one of its tokens to the next
+  constexpr int MOST = FULL ? U / 2 + U % 2 : U;   // tokens of a lane
   // a place in the line: a pair, and its steps that are left to this CTA
   struct Place {
     int row, hg, steps, left;
@@ -288,48 +288,51 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   };
   Place copied = from;
   const int64_t stride = (int64_t)a.num_kv_heads * RB;
-  const char* src0 = nullptr;        // of the lane's first row in slot 0
-  const int32_t* table = nullptr;    // its token's slot
+  int64_t column = 0;                // of the lane's piece in a slot
+  const int32_t* table = nullptr;    // the first token's slot
   int rest = 0;                      // tokens of the row from it on
-  int slot0 = 0, slot1 = 0;
+  int slot[MOST];
   auto slots = [&] {
-    slot0 = part0 && rest > 0 ? *table : 0;
-    if (twice) slot1 = part1 && rest > further ? table[further] : 0;
+#pragma unroll
+    for (int u = 0; u < MOST; ++u) slot[u] = rest > u * further ? table[u * further] : 0;
   };
   auto open_copies = [&](int step) {
-    const int pos = step * tokens + (mine0 >> 1);
+    const int pos = step * tokens + tok0;
     table = a.req_to_token + (int64_t)a.req_idx[copied.row] * a.max_ctx + pos;
     rest = a.seq_len[copied.row] - pos;
-    src0 = (const char*)(mine0 & 1 ? a.v_pool : a.k_pool) + copied.hg * HG * RB + piece * C::CH;
+    column = copied.hg * HG * RB + piece * C::CH;
     slots();
   };
-  int to = 0;                   // the stage that is copied to next
+  int to = 0;                   // the half that is copied to next
   uint32_t to_phase = 1;        // and what its last use has ended; a new barrier counts as ended
-  const uint32_t dst0 = smem_u32(smem) + (mine0 & 1) * plane + (mine0 >> 1) * pitch + piece * C::CH;
-  const uint32_t none0 = smem_u32(&s_none[0][mine0 >> 1]);
+  const uint32_t dst0 = smem_u32(smem) + tok0 * pitch + piece * C::CH;
+  const uint32_t none0 = smem_u32(&s_none[0][tok0]);
   const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
   const uint32_t slots_in = (uint32_t)min(a.num_slots, (int64_t)1 << 31);
-  auto copy_row = [&](const char* src, uint32_t dst, uint32_t none, int slot, bool in) {
-    const bool good = in && (uint32_t)slot < slots_in;
-    if (in && !good) set_status(p.status, kStatusSlotRange);
-    src += (good ? slot : 0) * stride;
-#pragma unroll
-    for (int i = 0; i < 5; ++i)
-      cp_async_or_zero<C::CH>(dst + i * HG * C::CH, src + i * HG * C::CH, good);
-    if (piece == 0)
-      asm volatile("st.shared.u8 [%0], %1;" ::"r"(none), "r"(good ? 0 : 1) : "memory");
-  };
-  auto issue = [&] {
+  auto issue = [&](bool is_v) {
     wait_for(empty0 + 8 * to, to_phase, p.status);
-    const uint32_t dst = dst0 + to * 2 * plane, none = none0 + to * 128;
-    if (part0) copy_row(src0, dst, none, slot0, rest > 0);
-    // the rows between the two are an even number: both K or both V
-    if (twice && part1)
-      copy_row(src0, dst + further * pitch, none + further, slot1, rest > further);
+    const char* pool = (const char*)(is_v ? a.v_pool : a.k_pool) + column;
+#pragma unroll
+    for (int u = 0; u < MOST; ++u) {
+      if (!(FULL && U % 2 == 0) && (!copies || tok0 + u * further >= tokens)) continue;
+      const bool in = rest > u * further, good = in && (uint32_t)slot[u] < slots_in;
+      const char* src = pool + (good ? slot[u] : 0) * stride;
+      const uint32_t dst = dst0 + to * half + u * further * pitch;
+#pragma unroll
+      for (int i = 0; i < 5; ++i)
+        cp_async_or_zero<C::CH>(dst + i * HG * C::CH, src + i * HG * C::CH, good);
+      if (!is_v) {
+        if (in && !good) set_status(p.status, kStatusSlotRange);
+        if (piece == 0)
+          asm volatile("st.shared.u8 [%0], %1;" ::"r"(none0 + to * (16 * C::WARPS * U) + u * further),
+                       "r"(good ? 0 : 1) : "memory");
+      }
+    }
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full0 + 8 * to) : "memory");
     __syncwarp();
     if (lane == 0) mbar_arrive(&s_full[to]);
     if (++to == S) to = 0, to_phase ^= 1;
+    if (!is_v) return;
     --copied.total;
     if (--copied.left == 0) {
       next_pair(copied);
@@ -647,67 +650,79 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
           }
       return;
     }
-    // warps that share a head join their states, four heads at a time, in the stage that all have read
-    constexpr int STATE = 4 * (D + 2);
+    // warps that share a head join their states, a few heads at a time, in the half that all have read
+    constexpr int H = U == 2 ? 4 : 2, STATE = H * (D + 2);
     float* own = (float*)stage + warp * STATE;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
+      for (int part = 0; part < 8 / H; ++part) {
         __syncthreads();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int q4 = (2 * t + c) & 3;
+          const int q8 = 2 * t + c, qh = q8 % H;
 #pragma unroll
           for (int w = 0; w < 2 * NW; ++w) {
             const float4 v = outputs(nt, c, w >> 1, w & 1);
-            if (t >> 1 == part) *(float4*)(own + q4 * D + element(w >> 1, w & 1)) = v;
+            if (q8 / H == part) *(float4*)(own + qh * D + element(w >> 1, w & 1)) = v;
           }
-          if (g == 0 && t >> 1 == part)
-            own[4 * D + q4] = mx[nt][c], own[4 * D + 4 + q4] = l[nt][c];
+          if (g == 0 && q8 / H == part) own[H * D + qh] = mx[nt][c], own[H * D + H + qh] = l[nt][c];
         }
         __syncthreads();
-        const int heads = min(4, p.G - nt * 8 - part * 4);
+        const int heads = min(H, p.G - nt * 8 - part * H);
         for (int x = ts * 32 + lane; x < heads * (D / 4); x += 32 * TS) {
-          const int q4 = x / (D / 4), d = x % (D / 4) * 4;
+          const int qh = x / (D / 4), d = x % (D / 4) * 4;
           float m = -FLT_MAX, den = 0.f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
           for (int s = 0; s < TS; ++s)
-            m = fmaxf(m, ((const float*)stage)[(s * HG + hw) * STATE + 4 * D + q4]);
+            m = fmaxf(m, ((const float*)stage)[(s * HG + hw) * STATE + H * D + qh]);
           for (int s = 0; s < TS; ++s) {
             const float* other = (const float*)stage + (s * HG + hw) * STATE;
-            const float f = ex2(other[4 * D + q4] - m);
-            const float4 w = *(const float4*)(other + q4 * D + d);
-            den = fmaf(f, other[4 * D + 4 + q4], den);
+            const float f = ex2(other[H * D + qh] - m);
+            const float4 w = *(const float4*)(other + qh * D + d);
+            den = fmaf(f, other[H * D + H + qh], den);
             v.x = fmaf(f, w.x, v.x), v.y = fmaf(f, w.y, v.y);
             v.z = fmaf(f, w.z, v.z), v.w = fmaf(f, w.w, v.w);
           }
-          store(nt * 8 + part * 4 + q4, d, v, m, den);
+          store(nt * 8 + part * H + qh, d, v, m, den);
         }
       }
   };
 
   open_copies(first_step);
-  for (int i = 0; i < C::AHEAD && copied.left > 0; ++i) issue();
+#pragma unroll
+  for (int i = 0; i < C::AHEAD; ++i)
+    if (copied.left > 0) issue(i & 1);
   begin_pair();
-  int stage = 0;
+  int now = 0;                  // the half that is read next
   uint32_t phase = 0;
+  auto release = [&] {          // and goes to the next
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s_empty[now]);
+    if (++now == S) now = 0, phase ^= 1;
+  };
+  const int mine_at = ts * 16 * U * pitch + hw * RB;
+  static_assert(C::AHEAD % 2 == 0, "K is copied after K is read, V after V");
   while (true) {
-    if (copied.left > 0) issue();
-    wait_for(full0 + 8 * stage, phase, p.status);
-    char* st = smem + stage * 2 * plane;
-    const char* kt = st + ts * kTile * pitch + hw * RB;
-    float x[NT][4];
-    scores(kt, x);
+    wait_for(full0 + 8 * now, phase, p.status);
+    float x[U][NT][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) scores(smem + now * half + mine_at + u * 16 * pitch, x[u]);
     // tokens that are not there weigh nothing
-    const uint4 none = *(const uint4*)&s_none[stage][ts * kTile];
-    if (none.x | none.y | none.z | none.w) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (s_none[stage][ts * kTile + place<NG>(g + 8 * k)])
+    for (int u = 0; u < U; ++u) {
+      const uint8_t* gone = &s_none[now][(ts * U + u) * 16];
+      const uint4 none = *(const uint4*)gone;
+      if (none.x | none.y | none.z | none.w) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) x[nt][2 * k] = x[nt][2 * k + 1] = -INFINITY;
+        for (int k = 0; k < 2; ++k)
+          if (gone[place<NG>(g + 8 * k)])
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) x[u][nt][2 * k] = x[u][nt][2 * k + 1] = -INFINITY;
+      }
     }
+    release();
+    if (copied.left > 0) issue(false);
     // the reference of a head's weights (to base 2) is a running maximum that follows once a score is
     // 2^8 times beyond it
     bool beyond = false;
@@ -716,7 +731,11 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        top[nt][c] = fmaxf(x[nt][c], x[nt][2 + c]) * F[nt][c];
+        top[nt][c] = fmaxf(x[0][nt][c], x[0][nt][2 + c]);
+#pragma unroll
+        for (int u = 1; u < U; ++u)
+          top[nt][c] = fmaxf(top[nt][c], fmaxf(x[u][nt][c], x[u][nt][2 + c]));
+        top[nt][c] *= F[nt][c];
         beyond |= top[nt][c] > mx[nt][c] + 8.f;
       }
     if (__any_sync(~0u, beyond)) {
@@ -740,17 +759,21 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
         }
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[nt][k] = ex2(fmaf(x[nt][k], F[nt][k & 1], -mx[nt][k & 1]));
-        l[nt][k & 1] += x[nt][k];
-      }
-    values(kt + plane, x);
-    if (--at.left == 0) end_pair(st);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s_empty[stage]);
-    if (++stage == S) stage = 0, phase ^= 1;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[u][nt][k] = ex2(fmaf(x[u][nt][k], F[nt][k & 1], -mx[nt][k & 1]));
+          l[nt][k & 1] += x[u][nt][k];
+        }
+    wait_for(full0 + 8 * now, phase, p.status);
+    char* vt = smem + now * half;
+#pragma unroll
+    for (int u = 0; u < U; ++u) values(vt + mine_at + u * 16 * pitch, x[u]);
+    if (--at.left == 0) end_pair(vt);
+    release();
+    if (copied.left > 0) issue(true);
     if (at.left > 0) continue;
     // the next pair of this CTA
     at.total -= here;
@@ -850,14 +873,26 @@ int validate(const rc_kv4_decode_args* a, const char* fn) {
   return RC_OK;
 }
 
+// What the configuration of the kernel that runs these sizes says.
+template <typename F>
+int by_kernel(const rc_kv4_decode_args& a, F f) {
+  const bool many = a.num_q_heads / a.num_kv_heads > 8, wide = a.head_dim == 128;
+  if (a.dtype == RC_DTYPE_F32)
+    return many ? wide ? f(Cfg<float, 128, 2>()) : f(Cfg<float, 64, 2>())
+                : wide ? f(Cfg<float, 128, 1>()) : f(Cfg<float, 64, 1>());
+  return many ? wide ? f(Cfg<__nv_bfloat16, 128, 2>()) : f(Cfg<__nv_bfloat16, 64, 2>())
+              : wide ? f(Cfg<__nv_bfloat16, 128, 1>()) : f(Cfg<__nv_bfloat16, 64, 1>());
+}
+
 Params params_of(const rc_kv4_decode_args* a) {
   Params p{};
   p.a = *a;
   p.G = a->num_q_heads / a->num_kv_heads;
-  const int warps = a->dtype == RC_DTYPE_F32 || p.G > 8 ? 4 : 8;   // Cfg::WARPS
+  const int warps = by_kernel(*a, [](auto c) { return decltype(c)::WARPS; });
   for (int h = 1; h <= warps; ++h)
     if (a->num_kv_heads % h == 0) p.HG = h;
   p.TS = warps / p.HG;
+  p.tokens = 16 * p.TS * by_kernel(*a, [](auto c) { return decltype(c)::U; });
   p.groups = a->num_kv_heads / p.HG;
   p.min_steps = 4;
   return p;
@@ -865,7 +900,7 @@ Params params_of(const rc_kv4_decode_args* a) {
 
 // CTAs that may have a range, whatever the rows hold.
 int64_t most_ctas(const Params& p) {
-  const int64_t steps = (p.a.max_seq_len + kTile * p.TS - 1) / (kTile * p.TS);
+  const int64_t steps = (p.a.max_seq_len + p.tokens - 1) / p.tokens;
   const int64_t fit = kSms * std::max(1, kMaxWarpsPerSm / (p.HG * p.TS));
   return std::max<int64_t>(1, std::min<int64_t>(
       fit, (steps * p.a.num_rows * p.groups + p.min_steps - 1) / p.min_steps));
@@ -890,7 +925,7 @@ Workspace carve(void* base, const Params& p, size_t* total) {
 template <typename T, int D, int NT>
 int smem_of(int HG) {
   using C = Cfg<T, D, NT>;
-  return C::STAGES * 2 * kTile * (C::WARPS / HG) * pitch_of(HG, C::RB);
+  return C::HALVES * 16 * C::U * (C::WARPS / HG) * pitch_of(HG, C::RB);
 }
 
 struct Setup {
@@ -932,7 +967,7 @@ cudaError_t launch_t(const Params& p, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   count_launches(1);
-  if (grid == 1 || p.a.max_seq_len <= kTile * p.TS) return cudaSuccess;   // no pair is cut
+  if (grid == 1 || p.a.max_seq_len <= p.tokens) return cudaSuccess;   // no pair is cut
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kMergeThreads);
