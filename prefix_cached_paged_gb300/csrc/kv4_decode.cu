@@ -42,6 +42,7 @@ struct Params {
   int G;          // query heads of a KV head
   int HG, TS;     // KV heads of a CTA, warps that share a head's tokens
   int tokens;     // of a step
+  int stride;     // bytes of a slot
   int groups;     // KV heads / HG
   int min_steps;  // of a CTA
 };
@@ -51,6 +52,7 @@ struct Cfg {
   static constexpr int NG = D / 32, RB = kv4_row_bytes(D);
   static constexpr bool F32 = sizeof(T) == 4;
   static constexpr int QP = F32 ? 3 : 1;     // bf16 parts of a query element
+  static constexpr int UNIT = F32 ? 2 : 7;   // scores are summed in 2^-UNIT
   static constexpr int PP = F32 ? 3 : 2;     // of a weight
   static constexpr int WARPS = NT > 1 || F32 ? 4 : 8;               // of a CTA, at most
   static constexpr int PER_SM = F32 ? 2 : NT > 1 ? 3 : 2;           // CTAs of so many warps
@@ -132,6 +134,10 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+__device__ __forceinline__ void ldmatrix_x2_trans(uint32_t at, uint32_t& r0, uint32_t& r1) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+               : "=r"(r0), "=r"(r1) : "r"(at) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void load(const char* at, uint32_t (&r)[N]) {
   static_assert(N == 2 || N == 4, "");
@@ -164,6 +170,13 @@ struct Cut {
   __device__ int of(int64_t x) const { return (int)(((x + 1) * ctas - 1) / total); }
 };
 
+// A pair in the line of steps and a CTA's part of it.
+struct Place {
+  int row, hg, steps, here;   // here: its steps in this CTA
+  int64_t begin, end;         // the first of them, and where the CTA's range ends
+  bool whole, ends;           // whether its first step is here, and its last
+};
+
 // FULL: a warp for each of C::WARPS KV heads; all distances in shared memory are constants then.
 template <typename T, int D, int NT, bool FULL>
 __global__ void __launch_bounds__(32 * Cfg<T, D, NT>::WARPS, (Cfg<T, D, NT>::PER_SM))
@@ -176,6 +189,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   __shared__ int s_row;
   __shared__ __align__(16) uint8_t s_none[S][16 * C::WARPS * U];   // tokens that are not there
   __shared__ uint64_t s_full[S], s_empty[S];
+  __shared__ Place s_place[C::WARPS][2];             // copied and read
   const auto& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -263,32 +277,45 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   const bool copies = FULL || lane / HG < rows_each;
   const int further = warps * rows_each;           // from one of its tokens to the next
   constexpr int MOST = FULL ? U / 2 + U % 2 : U;   // tokens of a lane
-  // a place in the line: a pair, and its steps that are left to this CTA
-  struct Place {
-    int row, hg, steps, left;
-    int64_t total;   // of all pairs from this one on
-  };
+  // Where a warp is in the line: what it needs when a pair ends is kept in shared memory, the steps left
+  // of the pairs that are copied and read in registers
   const int first_steps = max(1, steps_of(p, a.seq_len[s_row], a.req_idx[s_row]));
   const int64_t within = begin - s_before;
   const int first_step = (int)(within % first_steps);
-  Place from;
-  from.row = s_row, from.hg = min(p.groups - 1, (int)(within / first_steps));
-  from.steps = first_steps, from.total = end - begin;
-  from.left = (int)min((int64_t)(first_steps - first_step), from.total);
-  auto next_pair = [&](Place& x) {
-    if (x.total <= 0) return;   // its steps are counted off as they are taken
-    if (++x.hg == p.groups) {
-      x.hg = 0;
-      do {
-        ++x.row;
-        x.steps = steps_of(p, a.seq_len[x.row], a.req_idx[x.row]);
-      } while (x.steps == 0 && x.row + 1 < a.num_rows);
+  Place& copied = s_place[warp][0];
+  Place& at = s_place[warp][1];
+  int copy_left, left;
+  {
+    Place x;
+    x.row = s_row, x.hg = min(p.groups - 1, (int)(within / first_steps)), x.steps = first_steps;
+    x.begin = begin, x.end = end;
+    x.here = (int)min((int64_t)(first_steps - first_step), end - begin);
+    x.whole = first_step == 0, x.ends = first_step + x.here == first_steps;
+    copy_left = left = x.here;
+    if (lane == 0) copied = at = x;
+    __syncwarp();
+  }
+  auto next_pair = [&](Place& place) {   // the steps of the next pair, 0: there is none
+    Place x = place;
+    x.begin += x.here;
+    x.here = 0;
+    if (x.begin < x.end) {
+      if (++x.hg == p.groups) {
+        x.hg = 0;
+        do {
+          ++x.row;
+          x.steps = steps_of(p, a.seq_len[x.row], a.req_idx[x.row]);
+        } while (x.steps == 0 && x.row + 1 < a.num_rows);
+      }
+      x.here = (int)min((int64_t)x.steps, x.end - x.begin);
+      x.whole = true, x.ends = x.here == x.steps;
     }
-    x.left = (int)min((int64_t)x.steps, x.total);
+    __syncwarp();
+    if (lane == 0) place = x;
+    __syncwarp();
+    return x.here;
   };
-  Place copied = from;
-  const int64_t stride = (int64_t)a.num_kv_heads * RB;
-  int64_t column = 0;                // of the lane's piece in a slot
+  int column = 0;                    // of the lane's piece in a slot
   const int32_t* table = nullptr;    // the first token's slot
   int rest = 0;                      // tokens of the row from it on
   int slot[MOST];
@@ -297,9 +324,9 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     for (int u = 0; u < MOST; ++u) slot[u] = rest > u * further ? table[u * further] : 0;
   };
   auto open_copies = [&](int step) {
-    const int pos = step * tokens + tok0;
-    table = a.req_to_token + (int64_t)a.req_idx[copied.row] * a.max_ctx + pos;
-    rest = a.seq_len[copied.row] - pos;
+    const int row = copied.row, pos = step * tokens + tok0;
+    table = a.req_to_token + (int64_t)a.req_idx[row] * a.max_ctx + pos;
+    rest = a.seq_len[row] - pos;
     column = copied.hg * HG * RB + piece * C::CH;
     slots();
   };
@@ -316,7 +343,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     for (int u = 0; u < MOST; ++u) {
       if (!(FULL && U % 2 == 0) && (!copies || tok0 + u * further >= tokens)) continue;
       const bool in = rest > u * further, good = in && (uint32_t)slot[u] < slots_in;
-      const char* src = pool + (good ? slot[u] : 0) * stride;
+      const char* src = pool + (int64_t)(good ? slot[u] : 0) * p.stride;
       const uint32_t dst = dst0 + to * half + u * further * pitch;
 #pragma unroll
       for (int i = 0; i < 5; ++i)
@@ -333,10 +360,9 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     if (lane == 0) mbar_arrive(&s_full[to]);
     if (++to == S) to = 0, to_phase ^= 1;
     if (!is_v) return;
-    --copied.total;
-    if (--copied.left == 0) {
-      next_pair(copied);
-      if (copied.left > 0) open_copies(0);
+    if (--copy_left == 0) {
+      copy_left = next_pair(copied);
+      if (copy_left > 0) open_copies(0);
     } else {
       table += tokens, rest -= tokens;
       slots();
@@ -352,14 +378,8 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   constexpr int NW = NG / 2;       // words of codes that a lane holds of a token's values
   float O[NT][NW][2][2][4];
   float M[NT][C::F32 ? 2 * NG : 4];
-  Place at = from;
-  int here = from.left;            // its steps in this CTA
-  bool whole = first_step == 0;    // the pair began in this CTA
-  bool ends = first_step + from.left == from.steps;
-  int64_t first = begin;           // its first step here
-
   auto begin_pair = [&] {
-    const int h = at.hg * HG + hw;
+    const int row = at.row, h = at.hg * HG + hw;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int qh = nt * 8 + g;
@@ -369,7 +389,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
         for (int n = 0; n < 8; ++n) x[j][n] = 0.f;
         if (qh < p.G) {
-          const T* src = (const T*)a.q + ((int64_t)at.row * a.num_q_heads + h * p.G + qh) * D + 32 * j +
+          const T* src = (const T*)a.q + ((int64_t)row * a.num_q_heads + h * p.G + qh) * D + 32 * j +
                          8 * t;
           if constexpr (C::F32) {
             const float4 u = ((const float4*)src)[0], v = ((const float4*)src)[1];
@@ -386,11 +406,9 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
       }
       most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
       most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
-      // the head's elements over 2^e, below 4 in magnitude: a power of two, exact. A code's pattern
-      // is the bf16 number code * 2^-133 (or 16 times that), subnormal or next to it, which times
-      // an element * 2^125 is code * element * 2^-8 (fp32: (code - 8) * 2^-33, times 2^25)
-      const int e = min(max((int)(__float_as_uint(most) >> 23) - 127, -40), 126);
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      // the head's elements over 2^e: below 2 in magnitude, exact
+      const int e = min(max((int)(__float_as_uint(most) >> 23) - 127, -126), 127);
+      const float down = __uint_as_float(e == 127 ? 1u << 22 : (uint32_t)(127 - e) << 23);
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
@@ -402,25 +420,30 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
         if (t == j) sum = s;
         if constexpr (C::F32)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) Q[nt][j][k] = 0x1p-8f * __shfl_sync(~0u, s, (2 * t + k) * 4);
+          for (int k = 0; k < 2; ++k) Q[nt][j][k] = 0.25f * __shfl_sync(~0u, s, (2 * t + k) * 4);
+        // a code's pattern is the bf16 number code * 2^-133 (or 16 times that), subnormal or next to
+        // it, which times an element * 2^126 is code * element * 2^-7; fp32: (code - 8) * 2^-33 times
+        // an element * 2^31
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const float up = (C::F32 ? 0x1p25f : 0x1p125f) * (b ? 0.0625f : 1.f);
+            const float up = (C::F32 ? 0x1p31f : 0x1p126f) * (b ? 0.0625f : 1.f);
             float lo = x[j][2 * k + b] * up, hi = x[j][2 * k + b + 4] * up;
 #pragma unroll
             for (int q = 0; q < QP; ++q) qf[q][nt][j][k][b] = take_part(lo, hi);
           }
       }
+      constexpr float unit = 1 << C::UNIT;
       float none = 0.f;
-      sum *= 0x1p-8f;
+      sum /= unit;
 #pragma unroll
       for (int k = 0; k < 3; ++k) qm[nt][k] = take_part(none, sum);
-      const float f = a.sm_scale * (kLog2e * 256.f) * __uint_as_float((uint32_t)(127 + e) << 23);
+      const float f = a.sm_scale * (kLog2e * unit) * __uint_as_float((uint32_t)(127 + e) << 23);
+      const float factor = fminf(fmaxf(f, FLT_MIN), FLT_MAX);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        F[nt][k] = __shfl_sync(~0u, f, (2 * t + k) * 4);
+        F[nt][k] = __shfl_sync(~0u, factor, (2 * t + k) * 4);
         mx[nt][k] = -FLT_MAX, l[nt][k] = 0.f;
       }
 #pragma unroll
@@ -452,7 +475,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         mma_zero(x[nt], ma, mb, ma, mb, qm[nt][0], qm[nt][1]);
-        mma(x[nt], ma, mb, 0, 0, qm[nt][2], 0);
+        mma(x[nt], ma, mb, ma, mb, qm[nt][2], 0);
       }
     }
 #pragma unroll
@@ -471,16 +494,19 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          const auto& q0 = qf[0][nt][j][k];
           if (k == 0)
-            mma_zero(d[nt], a0, a1, a2, a3, qf[0][nt][j][k][0], qf[0][nt][j][k][1]);
+            mma_zero(d[nt], a0, a1, a2, a3, q0[0], q0[1]);
           else
-            mma(d[nt], a0, a1, a2, a3, qf[0][nt][j][k][0], qf[0][nt][j][k][1]);
+            mma(d[nt], a0, a1, a2, a3, q0[0], q0[1]);
           if constexpr (C::F32) {
+            const auto& q1 = qf[1][nt][j][k];
+            const auto& q2 = qf[2][nt][j][k];
             if (k == 0)
-              mma_zero(rest[nt], a0, a1, a2, a3, qf[1][nt][j][k][0], qf[1][nt][j][k][1]);
+              mma_zero(rest[nt], a0, a1, a2, a3, q1[0], q1[1]);
             else
-              mma(rest[nt], a0, a1, a2, a3, qf[1][nt][j][k][0], qf[1][nt][j][k][1]);
-            mma(rest[nt], a0, a1, a2, a3, qf[2][nt][j][k][0], qf[2][nt][j][k][1]);
+              mma(rest[nt], a0, a1, a2, a3, q1[0], q1[1]);
+            mma(rest[nt], a0, a1, a2, a3, q2[0], q2[1]);
           }
         }
       }
@@ -503,12 +529,14 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     }
   };
 
-  // outputs += weights x of the 16 tokens at vt times their values. A lane has the elements
-  // 32 vj + 8 (vt0 + w) + n of tokens 2t, 2t + 1, 2t + 8, 2t + 9: all of one group
+  // outputs += weights x of the 16 tokens at vt times their values. A lane has 2 NW times four
+  // elements, element(w, h) .., of tokens 2t, 2t + 1, 2t + 8, 2t + 9: all of group vj
+  constexpr bool PAIRS = NG == 4;    // pairs of tokens come transposed from shared memory
   const int vj = g / (8 / NG), vt0 = g % (8 / NG) * NW;
   const int v_at = place<NG>(2 * t) * pitch + 4 * (vt0 * NG + vj);
   const int vp_at = place<NG>(2 * t) * pitch + D / 2 + 4 * vj;
   const int odd = (place<NG>(1) - place<NG>(0)) * pitch;   // rows 2t and 2t + 1
+  const int row_at = place<NG>(lane & 15) * pitch + (lane >> 4) * 16;
   auto word = [](const char* at) { return *(const uint32_t*)at; };
   auto values = [&](const char* vt, float (&x)[NT][4]) {
     if constexpr (C::F32) {   // the groups' middles in fp32
@@ -534,18 +562,25 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
         b[nt][k][0] = movmatrix_trans(take_part(x[nt][0], x[nt][1]));
         b[nt][k][1] = movmatrix_trans(take_part(x[nt][2], x[nt][3]));
       }
-    const uint32_t q0 = word(vt + vp_at), q1 = word(vt + vp_at + odd);
-    const uint32_t q2 = word(vt + vp_at + eight), q3 = word(vt + vp_at + odd + eight);
-    const uint32_t s01 = mul2(prmt(q0, q1, 0x5410), pow2_bf16x2(96));
-    const uint32_t s23 = mul2(prmt(q2, q3, 0x5410), pow2_bf16x2(96));
-    if constexpr (!C::F32) {   // row g: weights times minima of the lane's group
-      const uint32_t m01 = prmt(q0, q1, 0x7632), m23 = prmt(q2, q3, 0x7632);
+    uint32_t r01, r23, m01, m23;
+    if constexpr (PAIRS) {   // column g of (scale, minimum) of all groups; the neighbour has the other
+      ldmatrix_x2_trans(smem_u32(vt + row_at + D / 2 - (lane >> 4) * 16), m01, m23);
+      const uint32_t o01 = __shfl_xor_sync(~0u, m01, 4), o23 = __shfl_xor_sync(~0u, m23, 4);
+      r01 = g & 1 ? o01 : m01, r23 = g & 1 ? o23 : m23;
+    } else {
+      const uint32_t q0 = word(vt + vp_at), q1 = word(vt + vp_at + odd);
+      const uint32_t q2 = word(vt + vp_at + eight), q3 = word(vt + vp_at + odd + eight);
+      r01 = prmt(q0, q1, 0x5410), r23 = prmt(q2, q3, 0x5410);
+      m01 = prmt(q0, q1, 0x7632), m23 = prmt(q2, q3, 0x7632);
+    }
+    const uint32_t s01 = mul2(r01, pow2_bf16x2(96)), s23 = mul2(r23, pow2_bf16x2(96));
+    if constexpr (!C::F32) {   // row g: weights times minima of the lane's group, with PAIRS in row g | 1
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < PP; ++k) {
           float (&m)[4] = *(float (*)[4])&M[nt][0];
-          mma(m, m01, 0, m23, 0, b[nt][k][0], b[nt][k][1]);
+          mma(m, m01, r01, m23, r23, b[nt][k][0], b[nt][k][1]);
         }
     }
     uint32_t n01 = 0, n23 = 0, e01 = 0, e23 = 0;
@@ -555,48 +590,69 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     }
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      const char* at = vt + v_at + 4 * NG * w;
-      const uint32_t w0 = word(at), w1 = word(at + odd), w2 = word(at + eight);
-      const uint32_t w3 = word(at + odd + eight);
+      uint32_t pairs[4];   // of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9: four elements, and four more
+      if constexpr (PAIRS) {
+        ldmatrix_x4_trans(smem_u32(vt + row_at) + 32 * w, pairs);
+      } else {
+        const char* at = vt + v_at + 4 * NG * w;
+        const uint32_t w0 = word(at), w1 = word(at + odd), w2 = word(at + eight);
+        const uint32_t w3 = word(at + odd + eight);
+        pairs[0] = prmt(w0, w1, 0x5410), pairs[1] = prmt(w2, w3, 0x5410);
+        pairs[2] = prmt(w0, w1, 0x7632), pairs[3] = prmt(w2, w3, 0x7632);
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t v01 = prmt(w0, w1, h ? 0x7632 : 0x5410), v23 = prmt(w2, w3, h ? 0x7632 : 0x5410);
+        const uint32_t v01 = pairs[2 * h], v23 = pairs[2 * h + 1];
+        uint32_t v[2][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           // code * 2^-133 (16 times that) times scale * 2^96: eight bits, exact
           const uint32_t va = v01 >> 8 * k, vb = v23 >> 8 * k;
-          uint32_t a0, a1, a2, a3;
+          const uint32_t a0 = va & 0x000F000Fu, a1 = va & 0x00F000F0u;
+          const uint32_t a2 = vb & 0x000F000Fu, a3 = vb & 0x00F000F0u;
           if constexpr (C::F32) {   // of code - 8
-            a0 = fma2(va & 0x000F000Fu, s01, e01), a1 = fma2(va & 0x00F000F0u, s01, n01);
-            a2 = fma2(vb & 0x000F000Fu, s23, e23), a3 = fma2(vb & 0x00F000F0u, s23, n23);
+            v[k][0] = fma2(a0, s01, e01), v[k][1] = fma2(a1, s01, n01);
+            v[k][2] = fma2(a2, s23, e23), v[k][3] = fma2(a3, s23, n23);
           } else {
-            a0 = mul2(va & 0x000F000Fu, s01), a1 = mul2(va & 0x00F000F0u, s01);
-            a2 = mul2(vb & 0x000F000Fu, s23), a3 = mul2(vb & 0x00F000F0u, s23);
+            v[k][0] = mul2(a0, s01), v[k][1] = mul2(a1, s01);
+            v[k][2] = mul2(a2, s23), v[k][3] = mul2(a3, s23);
           }
+        }
+        if constexpr (C::F32) {   // sums in fp32, since a matrix instruction cuts its sums off
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (C::F32) {   // sums in fp32, since a matrix instruction cuts its sums off
-              float d[4];
-              mma_zero(d, a0, a1, a2, a3, b[nt][0][0], b[nt][0][1]);
-              mma(d, a0, a1, a2, a3, b[nt][1][0], b[nt][1][1]);
-              mma(d, a0, a1, a2, a3, b[nt][2][0], b[nt][2][1]);
+            float d[2][4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) O[nt][w][h][k][q] += d[q];
-            } else {
+            for (int k = 0; k < 2; ++k)
+              mma_zero(d[k], v[k][0], v[k][1], v[k][2], v[k][3], b[nt][0][0], b[nt][0][1]);
 #pragma unroll
-              for (int q = 0; q < PP; ++q)
-                mma(O[nt][w][h][k], a0, a1, a2, a3, b[nt][q][0], b[nt][q][1]);
-            }
+            for (int q = 1; q < PP; ++q)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                mma(d[k], v[k][0], v[k][1], v[k][2], v[k][3], b[nt][q][0], b[nt][q][1]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) O[nt][w][h][k / 4][k % 4] += d[k / 4][k % 4];
           }
+        } else {
+#pragma unroll
+          for (int q = 0; q < PP; ++q)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                mma(O[nt][w][h][k], v[k][0], v[k][1], v[k][2], v[k][3], b[nt][q][0], b[nt][q][1]);
         }
       }
     }
   };
 
-  // the state of head 2t + c of tile nt: elements 32 vj + 8 (vt0 + w) + 4 h .. + 3
-  auto element = [&](int w, int h) { return 32 * vj + 8 * (vt0 + w) + 4 * h; };
+  // the state of head 2t + c of tile nt: elements element(w, h) .. + 3
+  auto element = [&](int w, int h) {
+    return PAIRS ? 32 * vj + 8 * (2 * w + h) + 4 * (g & 1) : 32 * vj + 8 * (vt0 + w) + 4 * h;
+  };
   auto outputs = [&](int nt, int c, int w, int h) {
     float m = M[nt][c];
+    if constexpr (!C::F32 && PAIRS) m = __shfl_sync(~0u, m, lane | 4);
     if constexpr (C::F32)
 #pragma unroll
       for (int j = 1; j < NG; ++j) m = vj == j ? M[nt][2 * j + c] : m;
@@ -607,7 +663,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   // what a pair's head gave: the outputs, or a state in the workspace
   auto store = [&](int qh, int d, float4 v, float m, float den) {
     const int64_t head = (int64_t)at.row * a.num_q_heads + (at.hg * HG + hw) * p.G + qh;
-    if (whole && ends) {
+    if (at.whole && at.ends) {
       const float f = den == 0.f ? 0.f : 1.f / den;
       T* o = (T*)a.o + head * D + d;
       if constexpr (C::F32)
@@ -616,15 +672,15 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
         *(uint2*)o = make_uint2(pack2_bf16(v.x * f, v.y * f), pack2_bf16(v.z * f, v.w * f));
       if (a.lse && d == 0) a.lse[head] = den == 0.f ? -INFINITY : kLn2 * (m + log2f(den));
     } else {
-      const int64_t i = (((int64_t)blockIdx.x * 2 + (whole ? 1 : 0)) * HG + hw) * p.G + qh;
+      const int64_t i = (((int64_t)blockIdx.x * 2 + (at.whole ? 1 : 0)) * HG + hw) * p.G + qh;
       *(float4*)(p.w.o + i * D + d) = v;
       if (d == 0) *(float2*)(p.w.ml + i * 2) = make_float2(m, den);
     }
   };
   auto end_pair = [&](char* stage) {
-    if (threadIdx.x == 0 && whole && !ends) {
+    if (threadIdx.x == 0 && at.whole && !at.ends) {
       Range* rg = p.w.range + blockIdx.x;
-      rg->row1 = at.row, rg->hg1 = at.hg, rg->last1 = cut.of(first + at.steps - 1);
+      rg->row1 = at.row, rg->hg1 = at.hg, rg->last1 = cut.of(at.begin + at.steps - 1);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -692,7 +748,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   open_copies(first_step);
 #pragma unroll
   for (int i = 0; i < C::AHEAD; ++i)
-    if (copied.left > 0) issue(i & 1);
+    if (copy_left > 0) issue(i & 1);
   begin_pair();
   int now = 0;                  // the half that is read next
   uint32_t phase = 0;
@@ -722,7 +778,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
       }
     }
     release();
-    if (copied.left > 0) issue(false);
+    if (copy_left > 0) issue(false);
     // the reference of a head's weights (to base 2) is a running maximum that follows once a score is
     // 2^8 times beyond it
     bool beyond = false;
@@ -771,17 +827,12 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     char* vt = smem + now * half;
 #pragma unroll
     for (int u = 0; u < U; ++u) values(vt + mine_at + u * 16 * pitch, x[u]);
-    if (--at.left == 0) end_pair(vt);
+    if (--left == 0) end_pair(vt);
     release();
-    if (copied.left > 0) issue(true);
-    if (at.left > 0) continue;
-    // the next pair of this CTA
-    at.total -= here;
-    first += here;
-    next_pair(at);
-    if (at.left == 0) return;
-    here = at.left;
-    whole = true, ends = here == at.steps;
+    if (copy_left > 0) issue(true);
+    if (left > 0) continue;
+    left = next_pair(at);
+    if (left == 0) return;
     begin_pair();
   }
 }
@@ -892,6 +943,7 @@ Params params_of(const rc_kv4_decode_args* a) {
   for (int h = 1; h <= warps; ++h)
     if (a->num_kv_heads % h == 0) p.HG = h;
   p.TS = warps / p.HG;
+  p.stride = a->num_kv_heads * kv4_row_bytes(a->head_dim);
   p.tokens = 16 * p.TS * by_kernel(*a, [](auto c) { return decltype(c)::U; });
   p.groups = a->num_kv_heads / p.HG;
   p.min_steps = 4;
