@@ -57,7 +57,7 @@ struct Cfg {
   static constexpr int WARPS = NT > 1 || F32 ? 4 : 8;               // of a CTA, at most
   static constexpr int PER_SM = F32 ? 2 : NT > 1 ? 3 : 2;           // CTAs of so many warps
   static constexpr int CH = 4 * NG;          // bytes of a copy: a head's row is five
-  static constexpr int HALVES = 5, AHEAD = 4;   // of the ring, in flight
+  static constexpr int HALVES = 5;           // of the ring: K or V of a step
   static constexpr int U = 2;                // tiles of 16 tokens of a warp's step
 };
 // The most warps of the kernels above on an SM.
@@ -182,13 +182,14 @@ template <typename T, int D, int NT, bool FULL>
 __global__ void __launch_bounds__(32 * Cfg<T, D, NT>::WARPS, (Cfg<T, D, NT>::PER_SM))
 kv4_decode_kernel(const __grid_constant__ Params p) {
   using C = Cfg<T, D, NT>;
-  constexpr int NG = C::NG, RB = C::RB, QP = C::QP, PP = C::PP, S = C::HALVES, U = C::U;
+  constexpr int NG = C::NG, RB = C::RB, QP = C::QP, PP = C::PP, U = C::U;
   extern __shared__ __align__(16) char smem[];
   __shared__ int64_t s_sum[C::WARPS];
   __shared__ int64_t s_before;
   __shared__ int s_row;
-  __shared__ __align__(16) uint8_t s_none[S][16 * C::WARPS * U];   // tokens that are not there
-  __shared__ uint64_t s_full[S], s_empty[S];
+  // by step, four in turn: tokens that are not there; K and V have been copied; K has been read
+  __shared__ __align__(16) uint8_t s_none[4][16 * C::WARPS * U];
+  __shared__ uint64_t s_full[4], s_read[4];
   __shared__ Place s_place[C::WARPS][2];             // copied and read
   const auto& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -209,9 +210,9 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     if (lane >= x) upto += y;
   }
   if (lane == 31) s_sum[warp] = upto;
-  if (threadIdx.x < S) {
+  if (threadIdx.x < 4) {
     mbar_init(&s_full[threadIdx.x], 33 * warps);
-    mbar_init(&s_empty[threadIdx.x], warps);
+    mbar_init(&s_read[threadIdx.x], warps);
     fence_mbar_init();
   }
   __syncthreads();
@@ -270,8 +271,10 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (idle) return;
 
-  // ---- copies: K and V of a step in turn. Of their tokens a warp takes 32 / HG at a time, HG lanes for
-  // each; with head counts that are no power of two some warps take as many again
+  // ---- copies: K and V of step n, each into the next half of the ring, are issued when step n - 2 has
+  // been read: the halves then held V of step n - 3 and K of step n - 2. Of the tokens a warp takes
+  // 32 / HG at a time, HG lanes for each; with head counts that are no power of two some warps take as
+  // many again
   const int rows_each = 32 / HG, piece = lane % HG;
   const int tok0 = warp * rows_each + lane / HG;   // the lane's first
   const bool copies = FULL || lane / HG < rows_each;
@@ -330,36 +333,38 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     column = copied.hg * HG * RB + piece * C::CH;
     slots();
   };
-  int to = 0;                   // the half that is copied to next
-  uint32_t to_phase = 1;        // and what its last use has ended; a new barrier counts as ended
+  const uint32_t full0 = smem_u32(&s_full[0]), read0 = smem_u32(&s_read[0]);
+  auto next_half = [](int h, int by) { return h + by >= C::HALVES ? h + by - C::HALVES : h + by; };
+  uint32_t to = 0;              // the step that is copied next
+  int to_half = 0;              // where K goes
   const uint32_t dst0 = smem_u32(smem) + tok0 * pitch + piece * C::CH;
   const uint32_t none0 = smem_u32(&s_none[0][tok0]);
-  const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
   const uint32_t slots_in = (uint32_t)min(a.num_slots, (int64_t)1 << 31);
-  auto issue = [&](bool is_v) {
-    wait_for(empty0 + 8 * to, to_phase, p.status);
-    const char* pool = (const char*)(is_v ? a.v_pool : a.k_pool) + column;
+  auto issue = [&] {
+    const uint32_t kd = dst0 + to_half * half, vd = dst0 + next_half(to_half, 1) * half;
 #pragma unroll
     for (int u = 0; u < MOST; ++u) {
       if (!(FULL && U % 2 == 0) && (!copies || tok0 + u * further >= tokens)) continue;
       const bool in = rest > u * further, good = in && (uint32_t)slot[u] < slots_in;
-      const char* src = pool + (int64_t)(good ? slot[u] : 0) * p.stride;
-      const uint32_t dst = dst0 + to * half + u * further * pitch;
+      if (in && !good) set_status(p.status, kStatusSlotRange);
+      const int64_t from = (int64_t)(good ? slot[u] : 0) * p.stride + column;
+      const char *ks = (const char*)a.k_pool + from, *vs = (const char*)a.v_pool + from;
 #pragma unroll
       for (int i = 0; i < 5; ++i)
-        cp_async_or_zero<C::CH>(dst + i * HG * C::CH, src + i * HG * C::CH, good);
-      if (!is_v) {
-        if (in && !good) set_status(p.status, kStatusSlotRange);
-        if (piece == 0)
-          asm volatile("st.shared.u8 [%0], %1;" ::"r"(none0 + to * (16 * C::WARPS * U) + u * further),
-                       "r"(good ? 0 : 1) : "memory");
-      }
+        cp_async_or_zero<C::CH>(kd + u * further * pitch + i * HG * C::CH, ks + i * HG * C::CH, good);
+#pragma unroll
+      for (int i = 0; i < 5; ++i)
+        cp_async_or_zero<C::CH>(vd + u * further * pitch + i * HG * C::CH, vs + i * HG * C::CH, good);
+      if (piece == 0)
+        asm volatile("st.shared.u8 [%0], %1;" ::"r"(none0 + (to & 3) * (16 * C::WARPS * U) + u * further),
+                     "r"(good ? 0 : 1) : "memory");
     }
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full0 + 8 * to) : "memory");
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full0 + 8 * (to & 3))
+                 : "memory");
     __syncwarp();
-    if (lane == 0) mbar_arrive(&s_full[to]);
-    if (++to == S) to = 0, to_phase ^= 1;
-    if (!is_v) return;
+    if (lane == 0) mbar_arrive(&s_full[to & 3]);
+    ++to;
+    to_half = next_half(to_half, 2);
     if (--copy_left == 0) {
       copy_left = next_pair(copied);
       if (copy_left > 0) open_copies(0);
@@ -746,28 +751,21 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   };
 
   open_copies(first_step);
-#pragma unroll
-  for (int i = 0; i < C::AHEAD; ++i)
-    if (copy_left > 0) issue(i & 1);
+  issue();
+  if (copy_left > 0) issue();
   begin_pair();
-  int now = 0;                  // the half that is read next
-  uint32_t phase = 0;
-  auto release = [&] {          // and goes to the next
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s_empty[now]);
-    if (++now == S) now = 0, phase ^= 1;
-  };
+  uint32_t now = 0;             // the step that is read
+  int now_half = 0;             // and its K
   const int mine_at = ts * 16 * U * pitch + hw * RB;
-  static_assert(C::AHEAD % 2 == 0, "K is copied after K is read, V after V");
   while (true) {
-    wait_for(full0 + 8 * now, phase, p.status);
+    wait_for(full0 + 8 * (now & 3), now >> 2 & 1, p.status);
     float x[U][NT][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) scores(smem + now * half + mine_at + u * 16 * pitch, x[u]);
+    for (int u = 0; u < U; ++u) scores(smem + now_half * half + mine_at + u * 16 * pitch, x[u]);
     // tokens that are not there weigh nothing
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint8_t* gone = &s_none[now][(ts * U + u) * 16];
+      const uint8_t* gone = &s_none[now & 3][(ts * U + u) * 16];
       const uint4 none = *(const uint4*)gone;
       if (none.x | none.y | none.z | none.w) {
 #pragma unroll
@@ -777,8 +775,8 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
             for (int nt = 0; nt < NT; ++nt) x[u][nt][2 * k] = x[u][nt][2 * k + 1] = -INFINITY;
       }
     }
-    release();
-    if (copy_left > 0) issue(false);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s_read[now & 3]);
     // the reference of a head's weights (to base 2) is a running maximum that follows once a score is
     // 2^8 times beyond it
     bool beyond = false;
@@ -823,13 +821,17 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
           x[u][nt][k] = ex2(fmaf(x[u][nt][k], F[nt][k & 1], -mx[nt][k & 1]));
           l[nt][k & 1] += x[u][nt][k];
         }
-    wait_for(full0 + 8 * now, phase, p.status);
-    char* vt = smem + now * half;
+    char* vt = smem + next_half(now_half, 1) * half;
 #pragma unroll
     for (int u = 0; u < U; ++u) values(vt + mine_at + u * 16 * pitch, x[u]);
     if (--left == 0) end_pair(vt);
-    release();
-    if (copy_left > 0) issue(true);
+    __syncwarp();
+    if (copy_left > 0) {
+      wait_for(read0 + 8 * (now & 3), now >> 2 & 1, p.status);
+      issue();
+    }
+    ++now;
+    now_half = next_half(now_half, 2);
     if (left > 0) continue;
     left = next_pair(at);
     if (left == 0) return;
