@@ -22,6 +22,11 @@ Between a model's projections and attention, at a batch's positions (an extend o
   sparse_layer   attention of one layer over the blocks that the bounds select for each query and
                  KV head, after append_layer: decode steps, and short chunks of new tokens.
 
+With kv_bits=4 the cache is held in 4 bits (kv4_append): the same steps, append_layer and norm_rope
+among them, on a pool of 5 / 16 of the bf16 bytes. New tokens of an extend attend to each other as
+given and to the cached prefix as it is held, read back once per layer into rows of the batch; later
+steps see them as they are held too.
+
 The model's projections (q, k_new, v_new per layer) are the caller's: this module never
 computes them.
 """
@@ -32,7 +37,8 @@ from dataclasses import dataclass, field
 import numpy as np
 
 from . import (DEFAULT_KV_CHUNK, decode_attention, decode_workspace_bytes, extend_attention,
-               extend_workspace_bytes, kv_append, kv_block_bounds, kv_copy, plan_extend_stacking,
+               extend_workspace_bytes, kv4_append, kv4_decode_attention, kv4_decode_workspace_bytes,
+               kv4_read, kv4_row_bytes, kv_append, kv_block_bounds, kv_copy, plan_extend_stacking,
                qk_norm_rope, shared_context_groups, sparse_decode_attention,
                sparse_decode_workspace_bytes, MAX_STACK_LEVELS)
 from .runtime import DeviceKV, HostCache, Plan
@@ -55,10 +61,23 @@ class ExtendBatch:
     token_row: object = None   # device int32 [T]: its request's slot-table row
     max_len: int = 0           # longest request
     bounded: set = field(default_factory=set)   # layers whose bounds hold the new tokens
+    prefix: object = None      # the cached tokens of a 4-bit cache, as numbers (Engine._stage)
 
     @property
     def num_tokens(self) -> int:
         return self.plan.num_tokens
+
+
+@dataclass
+class Prefix:
+    """The cached tokens that an extend batch over a 4-bit cache attends to, each once, in rows 0 ..;
+    behind them a row per new token."""
+    slots: object      # device int32 [U]: the cached tokens' slots
+    table: object      # device int32 [B, columns]: the rows' counterpart of the slot table
+    req_idx: object    # device int32 [B]: 0, 1, ..
+    out_loc: object    # device int32 [T]: U, U + 1, ..
+    k: object          # [U + T, Hkv, d], the layer in hand
+    v: object
 
 
 @dataclass
@@ -79,7 +98,8 @@ class DecodeBatch:
     steps: int = 0               # decode_steps taken
     token_pos: object = None     # device int32 [B]: position of the step's new tokens
     one_each: object = None      # device int32 [B + 1]: 0, 1, .. B
-    bounded: dict = field(default_factory=dict)   # layer -> steps whose tokens its bounds hold
+    bounded: dict = field(default_factory=dict)   # layer -> steps whose tokens its bounds hold (with
+                                                  # kv_bits=4: the last step appended)
 
 
 # shortest shared prefix worth a stacked pass: two key tiles
@@ -90,24 +110,39 @@ class Engine:
     rope = None        # fp32 table [positions, rotary_dim] on the device, or None
     sparse_block = 0   # positions per block of the bounds, 0: none are kept
     bounds = None      # [layers, max_reqs, blocks, Hkv, 2, d]
+    kv_bits = 16       # 4: the cache is held in 4 bits; 16: in the engine's dtype
     _no_workspace = None
 
     def __init__(self, layers, n_q_heads, n_kv_heads, head_dim, dtype, num_slots, max_reqs,
                  max_ctx, initial_order=None, device="cuda", kv_chunk=0, share_decode=True,
                  stack_extend=True, host_tier_slots=0, host_planes=None,
-                 stack_levels=MAX_STACK_LEVELS, fold_extend=True, rope=None, sparse_block=0):
+                 stack_levels=MAX_STACK_LEVELS, fold_extend=True, rope=None, sparse_block=0, kv_bits=16):
+        if kv_bits not in (4, 16):
+            raise ValueError("kv_bits must be 16 (the cache in dtype) or 4")
+        if kv_bits == 4 and head_dim not in (64, 128):
+            raise ValueError("kv_bits=4 attends to heads of 64 or 128")
+        if kv_bits == 4 and sparse_block:
+            raise ValueError("kv_bits=4 keeps no block bounds: sparse_block must be 0")
+        if kv_bits == 4 and host_tier_slots and n_kv_heads * kv4_row_bytes(head_dim) % 16:
+            raise ValueError("kv_bits=4 with a host tier needs slots of a multiple of 16 bytes: an "
+                             "even number of KV heads of 64")
+        self.kv_bits, self.dtype = int(kv_bits), dtype
         self.layers = layers
         self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
         self.sm_scale = 1.0 / float(np.sqrt(head_dim))
         self.host = HostCache(num_slots, max_ctx, initial_order, host_slots=host_tier_slots)
-        self.dev = DeviceKV(layers, num_slots, n_kv_heads, head_dim, dtype, max_reqs, max_ctx,
-                            device)
+        if self.kv_bits == 4:
+            import torch
+            row, dtype = kv4_row_bytes(head_dim), torch.uint8
+        else:
+            row = head_dim
+        self.dev = DeviceKV(layers, num_slots, n_kv_heads, row, dtype, max_reqs, max_ctx, device)
         self.host_k = self.host_v = None
         if host_tier_slots:
             # the host tier's KV planes: pinned host memory the kernels address directly
             # (host_planes: a caller's (k, v) pair of that shape, reused across engines)
             torch = self.dev.torch
-            shape = (layers, host_tier_slots, n_kv_heads, head_dim)
+            shape = (layers, host_tier_slots, n_kv_heads, row)
             if host_planes is not None:
                 self.host_k, self.host_v = host_planes
                 if tuple(self.host_k.shape) != shape or not self.host_k.is_pinned():
@@ -219,7 +254,39 @@ class Engine:
                 batch.workspace = self._ext_ws
         return batch
 
+    def _stage(self, batch: ExtendBatch) -> Prefix:
+        """Rows for a batch's cached tokens as numbers and its new tokens, and the slot table's
+        counterpart over them. Slots that requests share are one row, so stacking groups hold."""
+        plan = batch.plan
+        P, B, T = plan.prefix_len, len(plan.lengths), plan.num_tokens
+        slots = np.unique(np.concatenate([plan.rows[b, :P[b]] for b in range(B)] +
+                                         [np.zeros(0, np.int32)]))
+        U = len(slots)
+        cols = -(-max(batch.max_len, 1) // 4) * 4
+        table = np.zeros((max(B, 1), cols), np.int32)
+        for b in range(B):
+            table[b, :P[b]] = np.searchsorted(slots, plan.rows[b, :P[b]])
+            table[b, P[b]:plan.lengths[b]] = U + np.arange(plan.qo_indptr[b], plan.qo_indptr[b + 1])
+        d_slots, d_table, d_req, d_loc = self.dev.upload_i32(
+            [slots, table, np.arange(B), U + np.arange(T)])
+        shape = (max(U + T, 1), self.n_kv_heads, self.head_dim)
+        k, v = (self.dev.torch.empty(shape, dtype=self.dtype, device=self.dev.device)
+                for _ in range(2))
+        return Prefix(d_slots, d_table.reshape(table.shape), d_req, d_loc, k, v)
+
     def extend_layer(self, batch: ExtendBatch, layer: int, q, k_new, v_new, o, lse=None):
+        if self.kv_bits == 4:
+            if batch.prefix is None:
+                batch.prefix = self._stage(batch)
+            x = batch.prefix
+            kv4_read(self.dev.k[layer], self.dev.v[layer], x.slots, x.k, x.v)
+            extend_attention(q, k_new, v_new, x.out_loc, batch.qo_indptr, batch.prefix_len,
+                             x.req_idx, x.table, x.k, x.v, o, sm_scale=self.sm_scale,
+                             max_q_len=batch.max_q_len, max_prefix_len=batch.max_prefix_len, lse=lse,
+                             stack=batch.stack, workspace=batch.workspace)
+            kv4_append(k_new, v_new, batch.out_loc, batch.qo_indptr, self.dev.k[layer],
+                       self.dev.v[layer])
+            return
         extend_attention(q, k_new, v_new, batch.out_loc, batch.qo_indptr, batch.prefix_len,
                          batch.req_idx, self.dev.req_to_token, self.dev.k[layer],
                          self.dev.v[layer], o, sm_scale=self.sm_scale,
@@ -279,7 +346,7 @@ class Engine:
             batch.gen_slots.append(batch.new_slots.copy())
         batch.step_id = object()   # the lengths changed: the next layer plans again
         meta = [batch.seq_len, batch.row_ids, batch.new_slots]
-        if self.rope is not None or self.sparse_block:
+        if self.rope is not None or self.sparse_block or self.kv_bits == 4:
             meta += [cols, np.arange(B + 1)]
         batch.dev_seq_len, batch.dev_req_idx, batch.dev_out_loc, *more = self.dev.upload_i32(meta)
         if more:
@@ -297,6 +364,27 @@ class Engine:
 
     def decode_layer(self, batch: DecodeBatch, layer: int, q, k_new, v_new, o, lse=None,
                      max_total_tokens=None):
+        """Decode attention of one layer over each request's whole context, its new token's k_new
+        and v_new appended. With kv_bits=4 they may be None where append_layer of this layer and
+        step has written them; max_total_tokens says nothing there."""
+        if self.kv_bits == 4:
+            if batch.one_each is None:
+                raise ValueError("decode_layer: no decode_step has been taken")
+            if k_new is not None:
+                kv4_append(k_new, v_new, batch.dev_out_loc, batch.one_each, self.dev.k[layer],
+                           self.dev.v[layer])
+                batch.bounded[layer] = batch.steps
+            elif batch.bounded.get(layer, -1) != batch.steps:
+                raise ValueError(f"decode_layer: without keys and values, append_layer of layer "
+                                 f"{layer} comes first")
+            longest = int(batch.seq_len.max()) if len(batch.seq_len) else 0
+            need = kv4_decode_workspace_bytes(q, self.dev.k[layer], max_seq_len=longest)
+            # of this call alone, as sparse_layer's
+            ws = self.dev.torch.empty(need, dtype=self.dev.torch.uint8, device=self.dev.device)
+            kv4_decode_attention(q, batch.dev_seq_len, batch.dev_req_idx, self.dev.req_to_token,
+                                 self.dev.k[layer], self.dev.v[layer], o, ws, sm_scale=self.sm_scale,
+                                 max_seq_len=longest, lse=lse)
+            return
         mt = int(batch.seq_len.sum()) if max_total_tokens is None else max_total_tokens
         ws = self.workspace(q, k_new, mt)
         # every layer of a step has the same requests and lengths: the first plans, the others
@@ -333,7 +421,12 @@ class Engine:
         the keys are rotated by the engine's table on the way (False for keys that norm_rope has
         rotated already). With sparse_block the layer's block bounds follow; a batch's first append
         of a layer, and one after steps that only decode_layer has written, builds the bounds of
-        what is cached from the cache first."""
+        what is cached from the cache first. With kv_bits=4 the keys are normalised and rotated in a
+        pass of their own, rounded to their type and quantised with the values."""
+        if self.kv_bits == 4:
+            self._append4(batch, layer, k, v, rotate and self.rope is not None, k_weight, eps,
+                          interleaved)
+            return
         self._metadata(batch, "append_layer")
         if isinstance(batch, DecodeBatch):
             loc, ip, pre, req = batch.dev_out_loc, batch.one_each, batch.token_pos, \
@@ -356,6 +449,20 @@ class Engine:
             batch.bounded[layer] = batch.steps
         else:
             batch.bounded.add(layer)
+
+    def _append4(self, batch, layer, k, v, rotate, k_weight, eps, interleaved):
+        decode = isinstance(batch, DecodeBatch)
+        if decode and batch.one_each is None:
+            raise ValueError("append_layer: no decode_step has been taken")
+        if rotate or k_weight is not None:
+            given, k = k, self.dev.torch.empty(tuple(k.shape), dtype=k.dtype, device=k.device)
+            qk_norm_rope(None, given, batch.token_pos if rotate else None,
+                         self.rope if rotate else None, k_weight=k_weight, eps=eps,
+                         interleaved=interleaved, k_out=k)
+        loc, ip = (batch.dev_out_loc, batch.one_each) if decode else (batch.out_loc, batch.qo_indptr)
+        kv4_append(k, v, loc, ip, self.dev.k[layer], self.dev.v[layer])
+        if decode:
+            batch.bounded[layer] = batch.steps
 
     def sparse_layer(self, batch, layer: int, q, o, *, top_blocks, sink_blocks=1, recent_blocks=1,
                      lse=None, selected=None):
