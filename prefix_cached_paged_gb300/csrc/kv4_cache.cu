@@ -28,6 +28,17 @@ struct Eight<__nv_bfloat16> {
     x[0] = bf16lo(r.x), x[1] = bf16hi(r.x), x[2] = bf16lo(r.y), x[3] = bf16hi(r.y);
     x[4] = bf16lo(r.z), x[5] = bf16hi(r.z), x[6] = bf16lo(r.w), x[7] = bf16hi(r.w);
   }
+  // least and greatest of the four lanes' elements; a NaN stays
+  __device__ __forceinline__ void extremes(float& lo, float& hi) const {
+    uint32_t a = min_nan_bf16x2(min_nan_bf16x2(r.x, r.y), min_nan_bf16x2(r.z, r.w));
+    uint32_t b = max_nan_bf16x2(max_nan_bf16x2(r.x, r.y), max_nan_bf16x2(r.z, r.w));
+    // least and negated greatest side by side, so that a minimum finds both
+    b ^= 0x80008000u;
+    uint32_t m = min_nan_bf16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+    m = min_nan_bf16x2(m, __shfl_xor_sync(~0u, m, 1));
+    m = min_nan_bf16x2(m, __shfl_xor_sync(~0u, m, 2));
+    lo = bf16lo(m), hi = -bf16hi(m);
+  }
   static __device__ __forceinline__ void store(void* p, const float* x) {
     *(uint4*)p = make_uint4(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]),
                             pack2_bf16(x[4], x[5]), pack2_bf16(x[6], x[7]));
@@ -42,19 +53,72 @@ struct Eight<float> {
   __device__ __forceinline__ void get(float* x) const {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   }
+  __device__ __forceinline__ void extremes(float& lo, float& hi) const {
+    lo = min_nan(min_nan(min_nan(a.x, a.y), min_nan(a.z, a.w)),
+                 min_nan(min_nan(b.x, b.y), min_nan(b.z, b.w)));
+    hi = max_nan(max_nan(max_nan(a.x, a.y), max_nan(a.z, a.w)),
+                 max_nan(max_nan(b.x, b.y), max_nan(b.z, b.w)));
+#pragma unroll
+    for (int s = 1; s < 4; s *= 2) {
+      lo = min_nan(lo, __shfl_xor_sync(~0u, lo, s));
+      hi = max_nan(hi, __shfl_xor_sync(~0u, hi, s));
+    }
+  }
   static __device__ __forceinline__ void store(void* p, const float* x) {
     ((float4*)p)[0] = make_float4(x[0], x[1], x[2], x[3]);
     ((float4*)p)[1] = make_float4(x[4], x[5], x[6], x[7]);
   }
 };
 
+// Where a lane's chunk of eight elements (of codes: its word) lies in a token's heads. Chunks that are 32
+// apart are a whole number of heads apart where a head's chunks divide a warp: distances are then
+// constants and one stride.
+template <int NG>
+struct Chunks {
+  static constexpr int C = 4 * NG, RB = kv4_row_bytes(32 * NG);
+  static constexpr bool EVEN = 32 % C == 0;
+  // the head and the chunk of it of number c0 + 32 u + lane, c0 a multiple of 32
+  static __device__ __forceinline__ int head(int c0, int u, int lane) {
+    return EVEN ? c0 / C + u * (32 / C) + lane / C : (c0 + 32 * u + lane) / C;
+  }
+  static __device__ __forceinline__ int of_head(int c0, int u, int lane) {
+    return EVEN ? lane % C : (c0 + 32 * u + lane) % C;
+  }
+};
+
+// FULL: all of the kAhead chunks exist.
+template <typename T, int NG, bool FULL>
+__device__ __forceinline__ void append_chunks(const T* x, int64_t hs, char* row, int c0, int chunks,
+                                              int lane) {
+  using K = Chunks<NG>;
+  Eight<T> e[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    if (!FULL) e[u] = Eight<T>();
+    if (FULL || c0 + 32 * u + lane < chunks)
+      e[u].load(x + K::head(c0, u, lane) * hs + K::of_head(c0, u, lane) * 8);
+  }
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    float v[8], lo, hi;
+    e[u].get(v);
+    e[u].extremes(lo, hi);
+    const Kv4Group g = kv4_group<sizeof(T) == 4>(lo, hi);
+    const uint32_t w = kv4_codes(g, v);
+    if (!FULL && c0 + 32 * u + lane >= chunks) continue;   // a group's lanes are all in or out
+    const int c = K::of_head(c0, u, lane), j = c / 4, q = c % 4;
+    uint32_t* head = (uint32_t*)(row + K::head(c0, u, lane) * K::RB);
+    head[q * NG + j] = w;
+    if (q == 0) head[K::C + j] = g.pair;
+  }
+}
+
 template <typename T, int NG>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(rc_kv4_append_args a, int* status) {
-  constexpr int D = 32 * NG, C = D / 8, RB = kv4_row_bytes(D);
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * kWarps;
   const int64_t items = 2 * min(max((int64_t)a.qo_indptr[a.num_reqs], (int64_t)0), a.num_tokens);
-  const int chunks = a.num_kv_heads * C;
+  const int chunks = a.num_kv_heads * Chunks<NG>::C;
   for (int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); i < items; i += warps) {
     const int64_t t = i >> 1;
     const bool is_v = i & 1;
@@ -65,50 +129,45 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(rc_kv4_append_args
     }
     const T* x = is_v ? (const T*)a.v + t * a.v_token_stride : (const T*)a.k + t * a.k_token_stride;
     const int64_t hs = is_v ? a.v_head_stride : a.k_head_stride;
-    char* row = (char*)(is_v ? a.v_pool : a.k_pool) + (int64_t)slot * a.num_kv_heads * RB;
-    for (int c0 = 0; c0 < chunks; c0 += 32 * kAhead) {
-      Eight<T> e[kAhead];
+    char* row = (char*)(is_v ? a.v_pool : a.k_pool) + (int64_t)slot * a.num_kv_heads * Chunks<NG>::RB;
+    int c0 = 0;
+    for (; c0 + 32 * kAhead <= chunks; c0 += 32 * kAhead)
+      append_chunks<T, NG, true>(x, hs, row, c0, chunks, lane);
+    if (c0 < chunks) append_chunks<T, NG, false>(x, hs, row, c0, chunks, lane);
+  }
+}
+
+template <typename T, int NG, bool FULL>
+__device__ __forceinline__ void read_chunks(const char* row, T* out, int64_t hs, int c0, int chunks,
+                                            int lane) {
+  using K = Chunks<NG>;
+  uint32_t w[kAhead], p[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int c = c0 + 32 * u + lane;
-        e[u] = Eight<T>();
-        if (c < chunks) e[u].load(x + c / C * hs + c % C * 8);
-      }
+  for (int u = 0; u < kAhead; ++u) {
+    if (!FULL && c0 + 32 * u + lane >= chunks) continue;
+    const uint32_t* head = (const uint32_t*)(row + K::head(c0, u, lane) * K::RB);
+    const int c = K::of_head(c0, u, lane);
+    w[u] = head[c];
+    p[u] = head[K::C + c % NG];
+  }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int c = c0 + 32 * u + lane;
-        float v[8];
-        e[u].get(v);
-        float lo = v[0], hi = v[0];
+  for (int u = 0; u < kAhead; ++u) {
+    if (!FULL && c0 + 32 * u + lane >= chunks) continue;
+    const float s = bf16lo(p[u]), m = bf16hi(p[u]);
+    const int c = K::of_head(c0, u, lane);
+    float v[8];
 #pragma unroll
-        for (int k = 1; k < 8; ++k) lo = min_nan(lo, v[k]), hi = max_nan(hi, v[k]);
-#pragma unroll
-        for (int s = 1; s < 4; s *= 2) {
-          lo = min_nan(lo, __shfl_xor_sync(~0u, lo, s));
-          hi = max_nan(hi, __shfl_xor_sync(~0u, hi, s));
-        }
-        const Kv4Group g = kv4_group(lo, hi);
-        uint32_t w = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w |= kv4_code(g, v[k]) << 4 * k;
-        if (g.lost) w = 0;
-        if (c >= chunks) continue;   // a multiple of 8: a group's lanes are all in or out
-        const int j = c % C / 4, q = c % 4;
-        uint32_t* head = (uint32_t*)(row + c / C * RB);
-        head[q * NG + j] = w;
-        if (q == 0) head[C + j] = g.pair;
-      }
-    }
+    for (int k = 0; k < 8; ++k) v[k] = fmaf((float)(w[u] >> 4 * k & 15u), s, m);
+    Eight<T>::store(out + K::head(c0, u, lane) * hs + c % NG * 32 + c / NG * 8, v);
   }
 }
 
 template <typename T, int NG>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(rc_kv4_read_args a, int* status) {
-  constexpr int D = 32 * NG, C = D / 8, RB = kv4_row_bytes(D);
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * kWarps;
   const int64_t items = 2 * a.num_tokens;
-  const int chunks = a.num_kv_heads * C;
+  const int chunks = a.num_kv_heads * Chunks<NG>::C;
   for (int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); i < items; i += warps) {
     const int64_t t = i >> 1;
     const bool is_v = i & 1;
@@ -118,31 +177,14 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(rc_kv4_read_args a, 
       if (lane == 0) set_status(status, kStatusSlotRange);
       continue;
     }
-    const char* row = (const char*)(is_v ? a.v_pool : a.k_pool) + (int64_t)slot * a.num_kv_heads * RB;
+    const char* row = (const char*)(is_v ? a.v_pool : a.k_pool) +
+                      (int64_t)slot * a.num_kv_heads * Chunks<NG>::RB;
     T* out = is_v ? (T*)a.v_out + to * a.v_token_stride : (T*)a.k_out + to * a.k_token_stride;
     const int64_t hs = is_v ? a.v_head_stride : a.k_head_stride;
-    for (int c0 = 0; c0 < chunks; c0 += 32 * kAhead) {
-      uint32_t w[kAhead], p[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int c = c0 + 32 * u + lane;
-        if (c < chunks) {
-          const uint32_t* head = (const uint32_t*)(row + c / C * RB);
-          w[u] = head[c % C];
-          p[u] = head[C + c % NG];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int c = c0 + 32 * u + lane;
-        if (c >= chunks) continue;
-        const float s = bf16lo(p[u]), m = bf16hi(p[u]);
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = fmaf((float)(w[u] >> 4 * k & 15u), s, m);
-        Eight<T>::store(out + c / C * hs + c % NG * 32 + c % C / NG * 8, v);
-      }
-    }
+    int c0 = 0;
+    for (; c0 + 32 * kAhead <= chunks; c0 += 32 * kAhead)
+      read_chunks<T, NG, true>(row, out, hs, c0, chunks, lane);
+    if (c0 < chunks) read_chunks<T, NG, false>(row, out, hs, c0, chunks, lane);
   }
 }
 

@@ -216,6 +216,36 @@ def test_append_writes_the_bytes_and_read_gives_the_numbers(dtype, new, pad, h, 
 
 
 @pytest.mark.gpu
+def test_every_scale_and_its_ties():
+    """All significands of a scale at all exponents, elements on and beside the borders between codes;
+    widths just above and below what a scale covers."""
+    e = torch.arange(-82, 28).double()
+    scale = ((8 + torch.arange(8)).double() / 8 * torch.exp2(e)[:, None]).reshape(-1)   # [110 * 8]
+    k = torch.arange(14).double() + 0.5
+    eps = torch.tensor([0, 2.0 ** -22, -2.0 ** -22]).double()
+    rows = []
+    for shift in (0.0, -7.0):
+        x = torch.zeros((len(scale), 64), dtype=torch.float64)
+        x[:, 0], x[:, 1] = shift, 15 + shift
+        x[:, 2:16], x[:, 16:30] = k + shift, k * (1 + 2.0 ** -21) + shift
+        x[:, 30:32] = shift + 3
+        for i, d in enumerate(eps):   # the second group: widths at a scale's border
+            y = x.clone()
+            y[:, 32:48], y[:, 48:] = shift, 15 * (1 + d) + shift
+            rows.append(y * scale[:, None])
+    x = torch.cat(rows).float()[:, None]
+    n = x.shape[0]
+    loc = torch.arange(n, dtype=torch.int32, device="cuda")
+    ip = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    for dt in DT.values():
+        y = x.to(dt)
+        kp, vp = (torch.zeros((n, 1, 40), dtype=torch.uint8, device="cuda") for _ in "kv")
+        rc.kv4_append(y.cuda(), (-y).cuda(), loc, ip, kp, vp)
+        assert same(kp, R.quantise(y)) == [] and same(vp, R.quantise(-y)) == []
+    assert rc.device_status() == 0
+
+
+@pytest.mark.gpu
 def test_bad_slots_are_reported_and_skipped():
     g = torch.Generator().manual_seed(5)
     x = torch.randn((6, 2, 64), generator=g).cuda()
