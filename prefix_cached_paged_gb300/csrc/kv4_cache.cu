@@ -16,7 +16,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 4;   // chunks of a warp in flight
+constexpr int kAhead = 4;       // chunks of a warp in flight while it writes the cache
+constexpr int kReadAhead = 8;   // and while it reads it, 32 bits of codes each
 
 template <typename T>
 struct Eight;
@@ -141,9 +142,9 @@ template <typename T, int NG, bool FULL>
 __device__ __forceinline__ void read_chunks(const char* row, T* out, int64_t hs, int c0, int chunks,
                                             int lane) {
   using K = Chunks<NG>;
-  uint32_t w[kAhead], p[kAhead];
+  uint32_t w[kReadAhead], p[kReadAhead];
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
+  for (int u = 0; u < kReadAhead; ++u) {
     if (!FULL && c0 + 32 * u + lane >= chunks) continue;
     const uint32_t* head = (const uint32_t*)(row + K::head(c0, u, lane) * K::RB);
     const int c = K::of_head(c0, u, lane);
@@ -151,7 +152,7 @@ __device__ __forceinline__ void read_chunks(const char* row, T* out, int64_t hs,
     p[u] = head[K::C + c % NG];
   }
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
+  for (int u = 0; u < kReadAhead; ++u) {
     if (!FULL && c0 + 32 * u + lane >= chunks) continue;
     const float s = bf16lo(p[u]), m = bf16hi(p[u]);
     const int c = K::of_head(c0, u, lane);
@@ -182,15 +183,16 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(rc_kv4_read_args a, 
     T* out = is_v ? (T*)a.v_out + to * a.v_token_stride : (T*)a.k_out + to * a.k_token_stride;
     const int64_t hs = is_v ? a.v_head_stride : a.k_head_stride;
     int c0 = 0;
-    for (; c0 + 32 * kAhead <= chunks; c0 += 32 * kAhead)
+    for (; c0 + 32 * kReadAhead <= chunks; c0 += 32 * kReadAhead)
       read_chunks<T, NG, true>(row, out, hs, c0, chunks, lane);
     if (c0 < chunks) read_chunks<T, NG, false>(row, out, hs, c0, chunks, lane);
   }
 }
 
-// Two warps of work per token, at most what fits on the GPU at once.
+// Two warps of work per token; more CTAs than fit at once even out the tokens (reading 24 000 tokens of 32
+// heads: 4 for each SM 88.7 us, 8 90.6, 16 85.2).
 unsigned grid_of(int64_t tokens, int sms) {
-  return (unsigned)std::min<int64_t>((2 * tokens + kWarps - 1) / kWarps, (int64_t)sms * 8);
+  return (unsigned)std::min<int64_t>((2 * tokens + kWarps - 1) / kWarps, (int64_t)sms * 16);
 }
 
 template <typename T>

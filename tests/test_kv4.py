@@ -76,8 +76,8 @@ def test_decode_rejects_bad_arguments_before_any_device_work():
         return lib().rc_kv4_decode_attention(ctypes.byref(args(**kw)), ws, ws_bytes, None)
 
     for kw in (dict(dtype=3), dict(num_rows=-1), dict(num_rows=(1 << 20) + 1), dict(num_q_heads=7),
-               dict(num_kv_heads=0), dict(num_q_heads=34), dict(head_dim=96), dict(head_dim=256),
-               dict(max_seq_len=-1), dict(max_seq_len=(1 << 24) + 1),
+               dict(num_kv_heads=0), dict(num_q_heads=34), dict(num_q_heads=65537, num_kv_heads=65537),
+               dict(head_dim=96), dict(head_dim=256), dict(max_seq_len=-1), dict(max_seq_len=(1 << 24) + 1),
                dict(num_rows=1 << 20, num_q_heads=256, num_kv_heads=32)):
         assert call(**kw) == rc.RC_ERR_INVALID, kw
         n = ctypes.c_size_t()
