@@ -680,7 +680,8 @@ int rc_sparse_decode_attention(const rc_sparse_decode_args* args, void* workspac
 
 /* A cache held in 4 bits. Planes [num_slots, Hkv, d * 5 / 8] bytes for K and for V; of a head's d
  * elements 32 neighbours make a group j with a scale and a minimum, and an element stands for
- *   code * scale_j + minimum_j,   code 0 .. 15.
+ *   code * scale_j + minimum_j,   code 0 .. 15,
+ * the scale a number of four significant bits between 2^-80 and 2^28, or NaN.
  * A head's d * 5 / 8 bytes: d / 2 of codes, element 32 j + 8 t + n in nibble n of the little-endian
  * 32-bit word t * d / 32 + j; then scale and minimum of each group, bf16. As written by rc_kv4_append
  * (lo, hi the group's least and greatest element; differences, quotients and products in fp32):
@@ -750,7 +751,8 @@ int rc_kv4_read(const rc_kv4_read_args* args, void* stream);
  * also sets the device status word. A slot outside the pool sets it and that token weighs nothing; a row
  * of such tokens alone is as one of length 0. dtype is q's and o's; sm_scale > 0; Hq / Hkv <= 16;
  * head_dim 64 or 128; max_seq_len <= 2^24; num_rows <= 2^20; q and o
- * 16-byte aligned, planes as for rc_kv4_append. */
+ * 16-byte aligned, planes as for rc_kv4_append. An o that overlaps q, a plane or the workspace is
+ * refused. */
 typedef struct rc_kv4_decode_args {
   int32_t dtype;
   int32_t num_rows;

@@ -8,6 +8,12 @@ template cudaError_t launch<__nv_bfloat16>(const Params&, cudaStream_t);
 
 namespace {
 
+// Whether two ranges of bytes meet.
+bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + (uint64_t)nb && y < x + (uint64_t)na;
+}
+
 int validate(const rc_kv4_decode_args* a, const char* fn) {
   RC_CHECK_ARG(a != nullptr, "%s: args is NULL", fn);
   RC_CHECK_ARG(a->dtype == RC_DTYPE_BF16 || a->dtype == RC_DTYPE_F32, "%s: dtype %d", fn, a->dtype);
@@ -100,6 +106,14 @@ extern "C" int rc_kv4_decode_attention(const rc_kv4_decode_args* a, void* worksp
   p.w = rc::kv4::carve(workspace, p, &need);
   RC_CHECK_ARG(workspace && workspace_bytes >= need, "%s: workspace %zu bytes < %zu needed", fn,
                workspace ? workspace_bytes : 0, need);
+  // pairs that several CTAs share read q and the cache while others write o
+  const int64_t outs = (int64_t)a->num_rows * a->num_q_heads * a->head_dim *
+                       (a->dtype == RC_DTYPE_BF16 ? 2 : 4);
+  const int64_t plane = a->num_slots * p.stride;
+  RC_CHECK_ARG(!rc::kv4::meet(a->o, outs, a->q, outs) && !rc::kv4::meet(a->o, outs, a->k_pool, plane) &&
+                   !rc::kv4::meet(a->o, outs, a->v_pool, plane) &&
+                   !rc::kv4::meet(a->o, outs, workspace, (int64_t)need),
+               "%s: o overlaps q, a plane or the workspace", fn);
   p.status = rc::device_status_ptr();
   if (!p.status) return rc::fail(RC_ERR_CUDA, "%s: no device status word", fn);
   const cudaError_t e = a->dtype == RC_DTYPE_BF16

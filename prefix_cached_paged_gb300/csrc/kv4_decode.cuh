@@ -1,17 +1,26 @@
 // Decode attention over the cache held in 4 bits (format: kv4.cuh): the kernels and their launches.
 //
-// score(q, k) = sum_j [ s_j sum_{e in j} q_e c_e + m_j sum_{e in j} q_e ],   o = sum_t p_t (s_tj c_te + m_tj)
-// with the codes c, scales s and minima m of each group j: nothing is dequantised on the way. The work
-// is bound by HBM on paper (160 bytes of a token and KV head of 128, 16 tokens x 8 query heads
-// on one matrix instruction) and by instruction issue next to it: an SM has 23 bytes a clock of HBM and
-// so about 3.5 instruction lanes for each code.
+// score(q, k) = sum_j [ s_j sum_{e in j} q_e c_e + m_j sum_{e in j} q_e ]
+// o           = sum_t p_t [ s_tj (c_te - 8) + (m_tj + 8 s_tj) ] / sum_t p_t
+// with the codes c, scales s and minima m of each group j of 32 elements; both contractions on the matrix
+// units (16 tokens x 8 query heads an instruction), the scales of keys on their sums, those of values on
+// the codes (eight bits, exact in bf16). Codes need no conversion: four bits under a mask are the bf16
+// number code * 2^-133 or 16 times that, subnormal or next to it, which the units take as it is.
+//
+// Bound by HBM on paper: 160 bytes for a token and KV head of 128. Next to it stands instruction issue:
+// an SM has 23 bytes a clock of HBM, so 3.5 instruction lanes for each code; of about 345 warp
+// instructions for 16 tokens of a head 100 are the scores', 125 the values'. 128 rows of 512 .. 8192 tokens,
+// 32 + 32 heads: 338 us, 4.85 TB/s (floor 242); without the scores or without the values it would be
+// 275, the copies' own time 268.
 //
 // Work split: the steps of all (row, group of KV heads) pairs in one line, cut into as many equal ranges as
 // CTAs fit on the GPU at once, so long and short rows share them evenly; states of a pair that
 // ranges cut are joined by a second kernel, in the order of their tokens. In a CTA a warp takes one KV
-// head; with few KV heads several warps share a head's tokens. A step's tokens (16 for each warp) are
-// copied whole, all heads of the CTA from neighbouring lanes, into a ring that the warps share: 640
-// bytes at once reach 6.7 TB/s on scattered slots, 80 bytes for each head 3.2 (8 heads of 128).
+// head; with few KV heads several warps share a head's tokens. A step's tokens (32 for each warp) are
+// copied whole, all heads of the CTA by neighbouring lanes, into a ring that the warps share: 640 bytes at
+// once reach 6.7 TB/s on scattered slots, 80 bytes for each head 3.2 (8 heads of 128; bulk copies of a
+// row for each lane cost 25 instructions each). Two CTAs of eight warps: four of four warps read
+// half slots, 3 to 5 % slower.
 #pragma once
 #include <algorithm>
 #include <cfloat>
@@ -579,20 +588,20 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
       m01 = prmt(q0, q1, 0x7632), m23 = prmt(q2, q3, 0x7632);
     }
     const uint32_t s01 = mul2(r01, pow2_bf16x2(96)), s23 = mul2(r23, pow2_bf16x2(96));
-    if constexpr (!C::F32) {   // row g: weights times minima of the lane's group, with PAIRS in row g | 1
+    if constexpr (!C::F32) {
+      // row g: weights times minima of the lane's group (with PAIRS in row g | 1); row g + 8: times scales
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        float m[4];
+        mma_zero(m, m01, r01, m23, r23, b[nt][0][0], b[nt][0][1]);
+        mma(m, m01, r01, m23, r23, b[nt][1][0], b[nt][1][1]);
 #pragma unroll
-        for (int k = 0; k < PP; ++k) {
-          float (&m)[4] = *(float (*)[4])&M[nt][0];
-          mma(m, m01, r01, m23, r23, b[nt][k][0], b[nt][k][1]);
-        }
+        for (int k = 0; k < 4; ++k) M[nt][k] += m[k];
+      }
     }
-    uint32_t n01 = 0, n23 = 0, e01 = 0, e23 = 0;
-    if constexpr (C::F32) {   // -8 times the scale, and 16 times that
-      n01 = mul2(s01, kMinus | pow2_bf16x2(-126)), n23 = mul2(s23, kMinus | pow2_bf16x2(-126));
-      e01 = mul2(n01, pow2_bf16x2(-4)), e23 = mul2(n23, pow2_bf16x2(-4));
-    }
+    // -8 times the scale, 16 times that
+    const uint32_t e01 = mul2(s01, kMinus | pow2_bf16x2(-126)), e23 = mul2(s23, kMinus | pow2_bf16x2(-126));
+    const uint32_t d01 = mul2(e01, pow2_bf16x2(-4)), d23 = mul2(e23, pow2_bf16x2(-4));
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       uint32_t pairs[4];   // of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9: four elements, and four more
@@ -611,17 +620,15 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
         uint32_t v[2][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          // code * 2^-133 (16 times that) times scale * 2^96: eight bits, exact
+          // code * 2^-133 (16 times that) times scale * 2^96, less 8 scales: eight bits, exact. Around
+          // the groups' middles the sums stay small and lose less: with sums of code * scale 3.1 % of
+          // bf16 outputs are unlike those of 64 bits on a row of 131 071 tokens, so 0.9 (326 and
+          // 338 us on 128 rows of 512 .. 8192 tokens, 32 + 32 heads)
           const uint32_t va = v01 >> 8 * k, vb = v23 >> 8 * k;
           const uint32_t a0 = va & 0x000F000Fu, a1 = va & 0x00F000F0u;
           const uint32_t a2 = vb & 0x000F000Fu, a3 = vb & 0x00F000F0u;
-          if constexpr (C::F32) {   // of code - 8
-            v[k][0] = fma2(a0, s01, e01), v[k][1] = fma2(a1, s01, n01);
-            v[k][2] = fma2(a2, s23, e23), v[k][3] = fma2(a3, s23, n23);
-          } else {
-            v[k][0] = mul2(a0, s01), v[k][1] = mul2(a1, s01);
-            v[k][2] = mul2(a2, s23), v[k][3] = mul2(a3, s23);
-          }
+          v[k][0] = fma2(a0, s01, d01), v[k][1] = fma2(a1, s01, e01);
+          v[k][2] = fma2(a2, s23, d23), v[k][3] = fma2(a3, s23, e23);
         }
         if constexpr (C::F32) {   // sums in fp32, since a matrix instruction cuts its sums off
 #pragma unroll
@@ -657,7 +664,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   };
   auto outputs = [&](int nt, int c, int w, int h) {
     float m = M[nt][c];
-    if constexpr (!C::F32 && PAIRS) m = __shfl_sync(~0u, m, lane | 4);
+    if constexpr (!C::F32) m = fmaf(8.f, M[nt][2 + c], PAIRS ? __shfl_sync(~0u, m, lane | 4) : m);
     if constexpr (C::F32)
 #pragma unroll
       for (int j = 1; j < NG; ++j) m = vj == j ? M[nt][2 * j + c] : m;
@@ -804,7 +811,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
           mx[nt][c] = to;
           l[nt][c] *= f;
 #pragma unroll
-          for (int k = 0; k < (C::F32 ? NG : 1); ++k) M[nt][2 * k + c] *= f;
+          for (int k = 0; k < (C::F32 ? NG : 2); ++k) M[nt][2 * k + c] *= f;
 #pragma unroll
           for (int k = 0; k < 4 * NW; ++k) {
             float* o = &O[nt][0][0][0][0] + 4 * k + c;

@@ -237,6 +237,8 @@ class Engine:
             pos = np.arange(T) - np.repeat(plan.qo_indptr[:-1] - plan.prefix_len, S)
             batch.token_pos, batch.token_len, batch.token_row = self.dev.upload_i32(
                 [pos, pos + 1, np.repeat(row_ids, S)])
+        if self.kv_bits == 4:
+            batch.prefix = self._stage(batch)
         if self.stack_extend and B > 1:
             # stacking groups over the levels of the tree, each kept where it is estimated to pay
             G = self.n_q_heads // self.n_kv_heads
@@ -276,8 +278,6 @@ class Engine:
 
     def extend_layer(self, batch: ExtendBatch, layer: int, q, k_new, v_new, o, lse=None):
         if self.kv_bits == 4:
-            if batch.prefix is None:
-                batch.prefix = self._stage(batch)
             x = batch.prefix
             kv4_read(self.dev.k[layer], self.dev.v[layer], x.slots, x.k, x.v)
             extend_attention(q, k_new, v_new, x.out_loc, batch.qo_indptr, batch.prefix_len,

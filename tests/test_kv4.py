@@ -86,7 +86,9 @@ def test_decode_rejects_bad_arguments_before_any_device_work():
     for kw in (dict(max_seq_len=1001), dict(max_reqs=0), dict(num_slots=0), dict(sm_scale=0.0),
                dict(sm_scale=-1.0), dict(sm_scale=float("nan")), dict(sm_scale=float("inf")),
                dict(q=0), dict(seq_len=0), dict(v_pool=0), dict(o=0), dict(o=fake(6) + 8),
-               dict(k_pool=fake(4) + 2), dict(ws=fake(20) + 4)):
+               dict(k_pool=fake(4) + 2), dict(ws=fake(20) + 4), dict(o=fake(0)),
+               dict(o=fake(0) + 3 * 8 * 256 - 16), dict(o=fake(4)), dict(o=fake(5) + 16),
+               dict(o=fake(20) + 64)):
         assert call(**kw) == rc.RC_ERR_INVALID, kw
     if need.value:
         assert call(ws=0) == call(ws_bytes=need.value - 1) == rc.RC_ERR_INVALID

@@ -29,8 +29,7 @@ def test_every_cached_slot_has_one_row_and_every_new_token_one_behind_them():
     seqs = [np.concatenate([pre, synth.tokens(3, 5, 7)]).astype(np.int32), synth.tokens(3, 6, 1),
             np.concatenate([pre[:11], synth.tokens(3, 7, 2)]).astype(np.int32)]
     b = eng.extend_begin(seqs)
-    x = eng._stage(b)
-    plan = b.plan
+    x, plan = b.prefix, b.plan
     assert plan.prefix_len.tolist() == [20, 0, 11]
     U, T = len(x.slots), plan.num_tokens
     assert U == 20 and x.table.shape == (3, 28) and x.k.shape == x.v.shape == (U + T, 2, 64)
@@ -44,7 +43,7 @@ def test_every_cached_slot_has_one_row_and_every_new_token_one_behind_them():
     assert x.table[0, :11].tolist() == x.table[2, :11].tolist()
     eng.extend_end(b)
     b = eng.extend_begin([])
-    assert eng._stage(b).slots.tolist() == []
+    assert b.prefix.slots.tolist() == []
     eng.extend_end(b)
 
 
