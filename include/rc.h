@@ -693,8 +693,8 @@ int rc_sparse_decode_attention(const rc_sparse_decode_args* args, void* workspac
  * NaN.
  *
  * Writes new keys and values into their slots: token t's k[t], v[t] to k_pool[out_loc[t]],
- * v_pool[out_loc[t]]. Tokens at and past qo_indptr[num_reqs] (a padded batch) are not read, nor is
- * their out_loc. Slots of out_loc are distinct; a slot outside the pool sets the device status word
+ * v_pool[out_loc[t]]. Tokens at and past qo_indptr[num_reqs] (a padded batch) are not read, and
+ * their out_loc may hold anything. Slots of out_loc are distinct; a slot outside the pool sets the device status word
  * and that token is skipped. k, v [T, Hkv, d] with strides in elements, heads' elements contiguous;
  * head_dim 64, 128, 192 or 256; num_tokens <= 2^24; k, v and strides multiples of 16 bytes, planes
  * of 16 (head_dim 64 and 192: of 8). Planes that overlap one another or an input are refused. */

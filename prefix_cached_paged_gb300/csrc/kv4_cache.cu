@@ -118,12 +118,16 @@ template <typename T, int NG>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(rc_kv4_append_args a, int* status) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * kWarps;
+  int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  // a token's slot is on its way before it is needed, the first before the number of tokens is known
+  int next = i < 2 * a.num_tokens ? a.out_loc[i >> 1] : 0;
   const int64_t items = 2 * min(max((int64_t)a.qo_indptr[a.num_reqs], (int64_t)0), a.num_tokens);
   const int chunks = a.num_kv_heads * Chunks<NG>::C;
-  for (int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); i < items; i += warps) {
+  for (; i < items; i += warps) {
     const int64_t t = i >> 1;
     const bool is_v = i & 1;
-    const int slot = a.out_loc[t];
+    const int slot = next;
+    if (i + warps < items) next = a.out_loc[(i + warps) >> 1];
     if (slot < 0 || slot >= a.num_slots) {
       if (lane == 0) set_status(status, kStatusSlotRange);
       continue;
@@ -169,10 +173,13 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(rc_kv4_read_args a, 
   const int64_t warps = (int64_t)gridDim.x * kWarps;
   const int64_t items = 2 * a.num_tokens;
   const int chunks = a.num_kv_heads * Chunks<NG>::C;
-  for (int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); i < items; i += warps) {
+  int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  int next = i < items ? a.slots[i >> 1] : 0;   // as in kv4_append_kernel
+  for (; i < items; i += warps) {
     const int64_t t = i >> 1;
     const bool is_v = i & 1;
-    const int slot = a.slots[t];
+    const int slot = next;
+    if (i + warps < items) next = a.slots[(i + warps) >> 1];
     const int64_t to = a.out_loc ? a.out_loc[t] : t;
     if (slot < 0 || slot >= a.num_slots || to < 0 || to >= a.out_rows) {
       if (lane == 0) set_status(status, kStatusSlotRange);

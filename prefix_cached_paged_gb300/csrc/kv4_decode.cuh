@@ -172,11 +172,15 @@ __device__ __forceinline__ int steps_of(const Params& p, int len, int req) {
 }
 
 // How the line of steps is cut: range c is [total c / ctas, total (c + 1) / ctas).
+// Products of 32 bits, the usual case, are divided as such: a 64-bit division takes a few hundred cycles.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
 struct Cut {
   int64_t total;
   int ctas;
-  __device__ int64_t begin(int c) const { return total * c / ctas; }
-  __device__ int of(int64_t x) const { return (int)(((x + 1) * ctas - 1) / total); }
+  __device__ int64_t begin(int c) const { return quotient(total * c, ctas); }
+  __device__ int of(int64_t x) const { return (int)quotient((x + 1) * ctas - 1, total); }
 };
 
 // A pair in the line of steps and a CTA's part of it.
@@ -237,7 +241,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   const int64_t begin = idle ? 0 : cut.begin(blockIdx.x);
   const int64_t end = idle ? 0 : cut.begin(blockIdx.x + 1);
   if (!idle) {
-    const int64_t at = begin / p.groups;
+    const int64_t at = quotient(begin, p.groups);
     if (at >= upto - mine && at < upto) {
       int64_t before = upto - mine;
       int r = r0;
@@ -250,35 +254,39 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
       s_before = before * p.groups;
     }
   }
-  // rows without a token
-  for (int r = blockIdx.x; r < a.num_rows; r += gridDim.x) {
-    const int len = a.seq_len[r];
-    if (steps_of(p, len, a.req_idx[r])) continue;
-    if (len != 0 && threadIdx.x == 0) set_status(p.status, kStatusPosRange);
-    for (int x = threadIdx.x; x < a.num_q_heads * D; x += blockDim.x)
-      ((T*)a.o)[(int64_t)r * a.num_q_heads * D + x] = Elem<T>::from_f(0.f);
-    if (a.lse)
-      for (int x = threadIdx.x; x < a.num_q_heads; x += blockDim.x)
-        a.lse[(int64_t)r * a.num_q_heads + x] = -INFINITY;
-  }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    Range rg = {-1, 0, 0, 0, -1, 0, 0, 0};
-    if (!idle) {
-      int r = s_row;
-      const int n = max(1, steps_of(p, a.seq_len[r], a.req_idx[r]));
-      const int64_t at = s_before + (begin - s_before) / n * n;   // first step of the pair
-      if (at < begin) {
-        rg.row0 = r;
-        rg.hg0 = (int)((at - s_before) / n);
-        rg.start0 = cut.of(at);
-        rg.last0 = cut.of(at + n - 1);
-      }
-    }
-    p.w.range[blockIdx.x] = rg;   // row1 follows where the pair is met
-  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (idle) return;
+  // what has to be written beside the pairs: rows without a token, and the pair begun before this CTA
+  auto the_rest = [&] {
+    for (int r = blockIdx.x; r < a.num_rows; r += gridDim.x) {
+      const int len = a.seq_len[r];
+      if (steps_of(p, len, a.req_idx[r])) continue;
+      if (len != 0 && threadIdx.x == 0) set_status(p.status, kStatusPosRange);
+      for (int x = threadIdx.x; x < a.num_q_heads * D; x += blockDim.x)
+        ((T*)a.o)[(int64_t)r * a.num_q_heads * D + x] = Elem<T>::from_f(0.f);
+      if (a.lse)
+        for (int x = threadIdx.x; x < a.num_q_heads; x += blockDim.x)
+          a.lse[(int64_t)r * a.num_q_heads + x] = -INFINITY;
+    }
+    if (threadIdx.x != 0) return;
+    Range* rg = p.w.range + blockIdx.x;
+    rg->row0 = -1;
+    if (idle) return;
+    const int r = s_row;
+    const int n = max(1, steps_of(p, a.seq_len[r], a.req_idx[r]));
+    const int64_t at = s_before + quotient(begin - s_before, n) * n;   // first step of the pair
+    if (at < begin) {
+      rg->row0 = r;
+      rg->hg0 = (int)quotient(at - s_before, n);
+      rg->start0 = cut.of(at);
+      rg->last0 = cut.of(at + n - 1);
+    }
+  };
+  if (threadIdx.x == 0) p.w.range[blockIdx.x].row1 = -1;   // until a pair is begun and not ended
+  if (idle) {
+    the_rest();
+    return;
+  }
 
   // ---- copies: K and V of step n, each into the next half of the ring, are issued when step n - 2 has
   // been read: the halves then held V of step n - 3 and K of step n - 2. Of the tokens a warp takes
@@ -293,13 +301,14 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   // of the pairs that are copied and read in registers
   const int first_steps = max(1, steps_of(p, a.seq_len[s_row], a.req_idx[s_row]));
   const int64_t within = begin - s_before;
-  const int first_step = (int)(within % first_steps);
+  const int begun = (int)quotient(within, first_steps);   // pairs of the row
+  const int first_step = (int)(within - (int64_t)begun * first_steps);
   Place& copied = s_place[warp][0];
   Place& at = s_place[warp][1];
   int copy_left, left;
   {
     Place x;
-    x.row = s_row, x.hg = min(p.groups - 1, (int)(within / first_steps)), x.steps = first_steps;
+    x.row = s_row, x.hg = min(p.groups - 1, begun), x.steps = first_steps;
     x.begin = begin, x.end = end;
     x.here = (int)min((int64_t)(first_steps - first_step), end - begin);
     x.whole = first_step == 0, x.ends = first_step + x.here == first_steps;
@@ -760,6 +769,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   open_copies(first_step);
   issue();
   if (copy_left > 0) issue();
+  the_rest();   // while they are on their way
   begin_pair();
   uint32_t now = 0;             // the step that is read
   int now_half = 0;             // and its K
