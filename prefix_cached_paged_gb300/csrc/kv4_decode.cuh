@@ -82,25 +82,26 @@ __device__ __forceinline__ int place(int r) {
   return NG == 4 ? (r & 8) | (r & 1) << 2 | (r >> 1 & 3) : (r & 8) | (r & 3) << 1 | (r >> 2 & 1);
 }
 
-// Waits for the phase of that parity, at most about 2 s: then the thread sets the status word, waits
-// for its copies and leaves, as the others will. A wait that looks no more often than it has to, and in
-// few instructions: warps that wait share their scheduler with those that work.
-__device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, int* status) {
+// Waits for the phase of that parity, at most 2 s: then the thread sets the status word, waits for its
+// copies and leaves, as the others will. The hardware waits up to 20 us before it looks again: warps that
+// wait share their scheduler with those that work.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
       " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-  if (done) return;
-  for (int i = 0; i < 100000; ++i) {
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done) : "r"(bar), "r"(parity), "r"(20000) : "memory");   // 20 us
-    if (done) return;
+      : "=r"(done) : "r"(bar), "r"(parity), "r"(20000) : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, int* status) {
+  if (try_wait(bar, parity)) return;
+  const uint64_t t0 = global_timer_ns();
+  while (!try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > 2000000000ull) {
+      set_status(status, kStatusWaitExpired);
+      asm volatile("cp.async.wait_all;\n exit;" ::: "memory");
+    }
   }
-  set_status(status, kStatusWaitExpired);
-  asm volatile("cp.async.wait_all;\n exit;" ::: "memory");
 }
 
 // Bytes between tokens of a stage: an odd number of 16.
@@ -860,8 +861,8 @@ constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
 
 // Joins the states of pairs that ranges cut. The CTAs that share a pair share its heads; few states: a
-// warp for each head, many: all warps. Maxima and sums come first, all at once, then the outputs,
-// eight at a time (one row's 304 states of 64 heads: 16.8 us one by one, 10 together).
+// warp for each head, many: all warps. Maxima, sums and the first eight outputs are asked for at once, the
+// other outputs eight at a time (one row's 304 states of 64 heads: 16.8 us one by one, 10 so).
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads, 2) kv4_merge_kernel(const __grid_constant__ Params p) {
   __shared__ float so[kMergeWarps][D], sm[kMergeWarps], sl[kMergeWarps];
@@ -884,6 +885,20 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv4_merge_kernel(const __gri
         const int c = i0 + i * di;
         return ((int64_t)(start + c) * 2 + (c == 0)) * heads + h;
       };
+      // the first outputs are asked for with the maxima and sums
+      float x0[8][E];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x0[u][e] = 0.f;
+        if (u < mine) {
+          const float* o = p.w.o + at(u) * D + lane * E;
+          if constexpr (E == 4)
+            *(float4*)x0[u] = *(const float4*)o;
+          else
+            *(float2*)x0[u] = *(const float2*)o;
+        }
+      }
       float2 ml[3];
       static_assert(kSms * (kMaxWarpsPerSm / 3) <= 8 * 32 * 3, "a lane has at most three of a warp's states");
       float m = -FLT_MAX;
@@ -908,7 +923,13 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv4_merge_kernel(const __gri
       }
 #pragma unroll
       for (int x = 16; x; x >>= 1) den += __shfl_xor_sync(~0u, den, x);
-      for (int i = 0; i < mine; i += 8) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float fu = __shfl_sync(~0u, f[0], u);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = fmaf(fu, x0[u][e], v[e]);
+      }
+      for (int i = 8; i < mine; i += 8) {
         float x[8][E];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
