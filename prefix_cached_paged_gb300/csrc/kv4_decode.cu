@@ -52,6 +52,7 @@ Params params_of(const rc_kv4_decode_args* a) {
   p.TS = warps / p.HG;
   p.stride = a->num_kv_heads * kv4_row_bytes(a->head_dim);
   p.tokens = 16 * p.TS * by_kernel(*a, [](auto c) { return decltype(c)::U; });
+  while (1 << p.log_tokens < p.tokens) ++p.log_tokens;   // 8 and 4 by any number of heads, rounded down, are powers of two
   p.groups = a->num_kv_heads / p.HG;
   return p;
 }

@@ -51,7 +51,7 @@ struct Params {
   int* status;
   int G;          // query heads of a KV head
   int HG, TS;     // KV heads of a CTA, warps that share a head's tokens
-  int tokens;     // of a step
+  int tokens, log_tokens;   // of a step: a power of two
   int stride;     // bytes of a slot
   int groups;     // KV heads / HG
 };
@@ -169,7 +169,7 @@ __device__ __forceinline__ uint32_t take_part(float& lo, float& hi) {
 
 __device__ __forceinline__ int steps_of(const Params& p, int len, int req) {
   if (len <= 0 || len > p.a.max_seq_len || req < 0 || req >= p.a.max_reqs) return 0;
-  return (len + p.tokens - 1) / p.tokens;
+  return (len + p.tokens - 1) >> p.log_tokens;
 }
 
 // How the line of steps is cut: range c is [total c / ctas, total (c + 1) / ctas).
@@ -257,8 +257,23 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   }
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // what has to be written beside the pairs: rows without a token, and the pair begun before this CTA
+  if (threadIdx.x == 0) p.w.range[blockIdx.x].row1 = -1;   // until a pair is begun and not ended
+  // the first pair: the row's begun + 1st, of so many steps, the CTA's range beginning at that of them
+  int first_steps = 1, begun = 0, first_step = 0;
+  if (!idle) {
+    first_steps = max(1, steps_of(p, a.seq_len[s_row], a.req_idx[s_row]));
+    begun = (int)quotient(begin - s_before, first_steps);
+    first_step = (int)(begin - s_before - (int64_t)begun * first_steps);
+  }
+  // what has to be written beside the pairs: rows without a token, and which CTAs share the first pair
   auto the_rest = [&] {
+    if (warp == 0) {
+      Range* rg = p.w.range + blockIdx.x;
+      const int64_t at = begin - first_step;   // the pair's first step and, in odd lanes, its last
+      const int cta = idle ? 0 : cut.of(lane & 1 ? at + first_steps - 1 : at);
+      if (lane == 0) rg->row0 = first_step ? s_row : -1, rg->hg0 = begun, rg->start0 = cta;
+      if (lane == 1) rg->last0 = cta;
+    }
     for (int r = blockIdx.x; r < a.num_rows; r += gridDim.x) {
       const int len = a.seq_len[r];
       if (steps_of(p, len, a.req_idx[r])) continue;
@@ -269,25 +284,9 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
         for (int x = threadIdx.x; x < a.num_q_heads; x += blockDim.x)
           a.lse[(int64_t)r * a.num_q_heads + x] = -INFINITY;
     }
-    if (threadIdx.x != 0) return;
-    Range* rg = p.w.range + blockIdx.x;
-    rg->row0 = -1;
-    if (idle) return;
-    const int r = s_row;
-    const int n = max(1, steps_of(p, a.seq_len[r], a.req_idx[r]));
-    const int64_t at = s_before + quotient(begin - s_before, n) * n;   // first step of the pair
-    if (at < begin) {
-      rg->row0 = r;
-      rg->hg0 = (int)quotient(at - s_before, n);
-      rg->start0 = cut.of(at);
-      rg->last0 = cut.of(at + n - 1);
-    }
   };
-  if (threadIdx.x == 0) p.w.range[blockIdx.x].row1 = -1;   // until a pair is begun and not ended
-  if (idle) {
-    the_rest();
-    return;
-  }
+  the_rest();
+  if (idle) return;
 
   // ---- copies: K and V of step n, each into the next half of the ring, are issued when step n - 2 has
   // been read: the halves then held V of step n - 3 and K of step n - 2. Of the tokens a warp takes
@@ -300,10 +299,6 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   constexpr int MOST = FULL ? U / 2 + U % 2 : U;   // tokens of a lane
   // Where a warp is in the line: what it needs when a pair ends is kept in shared memory, the steps left
   // of the pairs that are copied and read in registers
-  const int first_steps = max(1, steps_of(p, a.seq_len[s_row], a.req_idx[s_row]));
-  const int64_t within = begin - s_before;
-  const int begun = (int)quotient(within, first_steps);   // pairs of the row
-  const int first_step = (int)(within - (int64_t)begun * first_steps);
   Place& copied = s_place[warp][0];
   Place& at = s_place[warp][1];
   int copy_left, left;
@@ -770,7 +765,6 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   open_copies(first_step);
   issue();
   if (copy_left > 0) issue();
-  the_rest();   // while they are on their way
   begin_pair();
   uint32_t now = 0;             // the step that is read
   int now_half = 0;             // and its K
