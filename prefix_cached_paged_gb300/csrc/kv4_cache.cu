@@ -196,28 +196,162 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(rc_kv4_read_args a, 
   }
 }
 
+// ---- few KV heads: the chunks of all tokens as one line, so that no lane is idle where a token has less
+// than a warp of them, and a warp has as many in flight as with many heads. blockIdx.y: K, V. For tokens of
+// up to kFlat chunks (bf16, a warp per token -> this way): 149 682 tokens of one head of 128 read in 76 ->
+// 25 us, 324 800 of one head of 64 written in 325 -> 60, the longest here of four heads of 128 (64 chunks)
+// read in 22 -> 17. More chunks lose, as each lane finds its own slot: eight heads of 128 written in
+// 38 -> 48, 32 heads in 116 -> 166.
+constexpr int kFlat = 64;
+// n / chunks for n < 2^30 (2^24 tokens at most) and chunks <= 64: by is 2^36 / chunks rounded up, its excess
+// times n below 2^-6
+__device__ __forceinline__ uint32_t token_of(uint32_t n, uint64_t by) { return (uint32_t)(n * by >> 36); }
+
+template <typename T, int NG>
+__global__ void __launch_bounds__(kThreads) kv4_append_flat_kernel(rc_kv4_append_args a, uint64_t by, int each,
+                                                                   int* status) {
+  constexpr int C = Chunks<NG>::C, RB = Chunks<NG>::RB;
+  const bool is_v = blockIdx.y;
+  const uint32_t chunks = a.num_kv_heads * C;
+  const uint32_t n =
+      (uint32_t)min(max((int64_t)a.qo_indptr[a.num_reqs], (int64_t)0), a.num_tokens) * chunks;
+  const T* x = (const T*)(is_v ? a.v : a.k);
+  const int64_t ts = is_v ? a.v_token_stride : a.k_token_stride;
+  const int64_t hs = is_v ? a.v_head_stride : a.k_head_stride;
+  char* pool = (char*)(is_v ? a.v_pool : a.k_pool);
+  for (uint32_t i0 = (blockIdx.x * kThreads + (threadIdx.x & ~31u)) * each; i0 < n;
+       i0 += gridDim.x * kThreads * each) {
+    Eight<T> e[kAhead];
+    int slot[kAhead];
+    uint32_t c[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const uint32_t i = i0 + 32 * u + (threadIdx.x & 31);
+      e[u] = Eight<T>();
+      slot[u] = -1, c[u] = 0;
+      if (u < each && i < n) {
+        const uint32_t t = token_of(i, by);
+        c[u] = i - t * chunks;
+        slot[u] = a.out_loc[t];
+        e[u].load(x + t * ts + c[u] / C * hs + c[u] % C * 8);
+        if ((slot[u] < 0 || slot[u] >= a.num_slots) && c[u] == 0) set_status(status, kStatusSlotRange);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      float v[8], lo, hi;
+      e[u].get(v);
+      e[u].extremes(lo, hi);   // a group's four lanes are of one token
+      const Kv4Group g = kv4_group<sizeof(T) == 4>(lo, hi);
+      const uint32_t w = kv4_codes(g, v);
+      if (slot[u] < 0 || slot[u] >= a.num_slots) continue;
+      const int k = c[u] % C, j = k / 4, q = k % 4;
+      uint32_t* head = (uint32_t*)(pool + ((int64_t)slot[u] * a.num_kv_heads + c[u] / C) * RB);
+      head[q * NG + j] = w;
+      if (q == 0) head[C + j] = g.pair;
+    }
+  }
+}
+
+template <typename T, int NG>
+__global__ void __launch_bounds__(kThreads) kv4_read_flat_kernel(rc_kv4_read_args a, uint64_t by, int each,
+                                                                 int* status) {
+  constexpr int C = Chunks<NG>::C, RB = Chunks<NG>::RB;
+  const bool is_v = blockIdx.y;
+  const uint32_t chunks = a.num_kv_heads * C, n = (uint32_t)a.num_tokens * chunks;
+  const char* pool = (const char*)(is_v ? a.v_pool : a.k_pool);
+  T* out = (T*)(is_v ? a.v_out : a.k_out);
+  const int64_t ts = is_v ? a.v_token_stride : a.k_token_stride;
+  const int64_t hs = is_v ? a.v_head_stride : a.k_head_stride;
+  for (uint32_t i0 = (blockIdx.x * kThreads + (threadIdx.x & ~31u)) * each; i0 < n;
+       i0 += gridDim.x * kThreads * each) {
+    uint32_t w[kReadAhead], p[kReadAhead], c[kReadAhead];
+    int64_t to[kReadAhead];
+#pragma unroll
+    for (int u = 0; u < kReadAhead; ++u) {
+      const uint32_t i = i0 + 32 * u + (threadIdx.x & 31);
+      to[u] = -1;
+      if (u < each && i < n) {
+        const uint32_t t = token_of(i, by);
+        c[u] = i - t * chunks;
+        const int slot = a.slots[t];
+        to[u] = a.out_loc ? a.out_loc[t] : t;
+        if (slot < 0 || slot >= a.num_slots || to[u] < 0 || to[u] >= a.out_rows) {
+          to[u] = -1;
+          if (c[u] == 0) set_status(status, kStatusSlotRange);
+        } else {
+          const uint32_t* head =
+              (const uint32_t*)(pool + ((int64_t)slot * a.num_kv_heads + c[u] / C) * RB);
+          w[u] = head[c[u] % C];
+          p[u] = head[C + c[u] % C % NG];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kReadAhead; ++u) {
+      if (to[u] < 0) continue;
+      const float s = bf16lo(p[u]), m = bf16hi(p[u]);
+      const int k = c[u] % C;
+      float v[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] = fmaf((float)(w[u] >> 4 * x & 15u), s, m);
+      Eight<T>::store(out + to[u] * ts + c[u] / C * hs + k % NG * 32 + k / NG * 8, v);
+    }
+  }
+}
+// A lane takes up to `ahead` chunks in a go, fewer where the GPU's lanes then have none.
+struct Flat {
+  uint64_t by;
+  int each;
+  dim3 grid;   // CTAs for each of K and V
+  Flat(int64_t tokens, int64_t chunks, int ahead, int sms) {
+    const int64_t n = tokens * chunks, most = (int64_t)sms * 4;
+    by = ((1ull << 36) + chunks - 1) / chunks;
+    each = (int)std::min<int64_t>(ahead, (n + most * kThreads - 1) / (most * kThreads));
+    grid = dim3((unsigned)std::min(most, (n + kThreads * each - 1) / (kThreads * each)), 2);
+  }
+};
+
 // Two warps of work per token; more CTAs than fit at once even out the tokens (reading 24 000 tokens of 32
 // heads: 4 for each SM 88.7 us, 8 90.6, 16 85.2).
 unsigned grid_of(int64_t tokens, int sms) {
   return (unsigned)std::min<int64_t>((2 * tokens + kWarps - 1) / kWarps, (int64_t)sms * 16);
 }
 
+template <typename T, int NG>
+void launch_append(const rc_kv4_append_args& a, int sms, int* st, cudaStream_t s) {
+  const int64_t chunks = (int64_t)a.num_kv_heads * Chunks<NG>::C;
+  if (chunks <= kFlat) {
+    const Flat f(a.num_tokens, chunks, kAhead, sms);
+    kv4_append_flat_kernel<T, NG><<<f.grid, kThreads, 0, s>>>(a, f.by, f.each, st);
+  } else
+    kv4_append_kernel<T, NG><<<grid_of(a.num_tokens, sms), kThreads, 0, s>>>(a, st);
+}
+template <typename T, int NG>
+void launch_read(const rc_kv4_read_args& a, int sms, int* st, cudaStream_t s) {
+  const int64_t chunks = (int64_t)a.num_kv_heads * Chunks<NG>::C;
+  if (chunks <= kFlat) {
+    const Flat f(a.num_tokens, chunks, kReadAhead, sms);
+    kv4_read_flat_kernel<T, NG><<<f.grid, kThreads, 0, s>>>(a, f.by, f.each, st);
+  } else
+    kv4_read_kernel<T, NG><<<grid_of(a.num_tokens, sms), kThreads, 0, s>>>(a, st);
+}
 template <typename T>
-void launch_append(const rc_kv4_append_args& a, unsigned grid, int* st, cudaStream_t s) {
+void launch_append(const rc_kv4_append_args& a, int sms, int* st, cudaStream_t s) {
   switch (a.head_dim / 64) {
-    case 1: kv4_append_kernel<T, 2><<<grid, kThreads, 0, s>>>(a, st); break;
-    case 2: kv4_append_kernel<T, 4><<<grid, kThreads, 0, s>>>(a, st); break;
-    case 3: kv4_append_kernel<T, 6><<<grid, kThreads, 0, s>>>(a, st); break;
-    default: kv4_append_kernel<T, 8><<<grid, kThreads, 0, s>>>(a, st); break;
+    case 1: launch_append<T, 2>(a, sms, st, s); break;
+    case 2: launch_append<T, 4>(a, sms, st, s); break;
+    case 3: launch_append<T, 6>(a, sms, st, s); break;
+    default: launch_append<T, 8>(a, sms, st, s); break;
   }
 }
 template <typename T>
-void launch_read(const rc_kv4_read_args& a, unsigned grid, int* st, cudaStream_t s) {
+void launch_read(const rc_kv4_read_args& a, int sms, int* st, cudaStream_t s) {
   switch (a.head_dim / 64) {
-    case 1: kv4_read_kernel<T, 2><<<grid, kThreads, 0, s>>>(a, st); break;
-    case 2: kv4_read_kernel<T, 4><<<grid, kThreads, 0, s>>>(a, st); break;
-    case 3: kv4_read_kernel<T, 6><<<grid, kThreads, 0, s>>>(a, st); break;
-    default: kv4_read_kernel<T, 8><<<grid, kThreads, 0, s>>>(a, st); break;
+    case 1: launch_read<T, 2>(a, sms, st, s); break;
+    case 2: launch_read<T, 4>(a, sms, st, s); break;
+    case 3: launch_read<T, 6>(a, sms, st, s); break;
+    default: launch_read<T, 8>(a, sms, st, s); break;
   }
 }
 
@@ -262,11 +396,10 @@ extern "C" int rc_kv4_append(const rc_kv4_append_args* a, void* stream) {
   int sms = 0;
   const int e = rc::sm_count(fn, &sms);
   if (e != RC_OK) return e;
-  const unsigned grid = rc::grid_of(T, sms);
   if (a->dtype == RC_DTYPE_BF16)
-    rc::launch_append<__nv_bfloat16>(*a, grid, st, (cudaStream_t)stream);
+    rc::launch_append<__nv_bfloat16>(*a, sms, st, (cudaStream_t)stream);
   else
-    rc::launch_append<float>(*a, grid, st, (cudaStream_t)stream);
+    rc::launch_append<float>(*a, sms, st, (cudaStream_t)stream);
   rc::count_launches(1);
   return rc::check_launch(fn);
 }
@@ -302,11 +435,10 @@ extern "C" int rc_kv4_read(const rc_kv4_read_args* a, void* stream) {
   int sms = 0;
   const int e = rc::sm_count(fn, &sms);
   if (e != RC_OK) return e;
-  const unsigned grid = rc::grid_of(a->num_tokens, sms);
   if (a->dtype == RC_DTYPE_BF16)
-    rc::launch_read<__nv_bfloat16>(*a, grid, st, (cudaStream_t)stream);
+    rc::launch_read<__nv_bfloat16>(*a, sms, st, (cudaStream_t)stream);
   else
-    rc::launch_read<float>(*a, grid, st, (cudaStream_t)stream);
+    rc::launch_read<float>(*a, sms, st, (cudaStream_t)stream);
   rc::count_launches(1);
   return rc::check_launch(fn);
 }

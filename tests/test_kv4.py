@@ -169,6 +169,8 @@ WRITES = [  # dtype, tokens of each request, padding, heads, d, fused (k and v s
     ("bf16", [0, 0], 4, 2, 128, True), ("bf16", [5, 0, 17], 6, 3, 128, True),
     ("bf16", [33], 0, 32, 128, False), ("bf16", [300, 211], 1, 5, 64, True),
     ("bf16", [7, 7], 0, 6, 192, True), ("bf16", [40], 2, 2, 256, False),
+    ("bf16", [2000, 3], 2, 1, 64, True), ("bf16", [700], 0, 8, 64, False),
+    ("bf16", [301], 3, 4, 128, True), ("bf16", [1001], 1, 2, 192, True), ("f32", [900], 0, 2, 256, False),
     ("f32", [1], 0, 1, 64, False), ("f32", [13, 2], 5, 3, 64, True), ("f32", [64], 0, 8, 128, True),
     ("f32", [9], 1, 7, 192, False), ("f32", [21], 0, 1, 256, True),
 ]
