@@ -171,6 +171,9 @@ WRITES = [  # dtype, tokens of each request, padding, heads, d, fused (k and v s
     ("bf16", [7, 7], 0, 6, 192, True), ("bf16", [40], 2, 2, 256, False),
     ("bf16", [2000, 3], 2, 1, 64, True), ("bf16", [700], 0, 8, 64, False),
     ("bf16", [301], 3, 4, 128, True), ("bf16", [1001], 1, 2, 192, True), ("f32", [900], 0, 2, 256, False),
+    ("bf16", [2500], 2, 9, 64, True), ("bf16", [700, 3], 1, 15, 128, False),
+    ("bf16", [420], 0, 16, 192, True), ("f32", [900], 0, 7, 256, True), ("f32", [2001], 3, 10, 64, False),
+    ("bf16", [1, 2], 1, 32, 256, True),
     ("f32", [1], 0, 1, 64, False), ("f32", [13, 2], 5, 3, 64, True), ("f32", [64], 0, 8, 128, True),
     ("f32", [9], 1, 7, 192, False), ("f32", [21], 0, 1, 256, True),
 ]
