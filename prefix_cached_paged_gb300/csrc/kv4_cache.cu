@@ -199,10 +199,10 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(rc_kv4_read_args a, 
 
 // ---- few KV heads: the chunks of all tokens as one line, so that no lane is idle where a token has less
 // than a warp of them, and a warp has as many in flight as with many heads. blockIdx.y: K, V. For tokens of
-// up to kFlat chunks (bf16, a warp per token -> this way): 149 682 tokens of one head of 128 read in 76 ->
-// 25 us, 324 800 of one head of 64 written in 325 -> 60, the longest here of four heads of 128 (64 chunks)
-// read in 22 -> 17. More chunks lose, as each lane finds its own slot: eight heads of 128 written in
-// 38 -> 48, 32 heads in 116 -> 166.
+// up to kFlat chunks (bf16, a warp per token -> this way; writes with the same tokens read back): 149 682
+// tokens of one head of 128 read in 76 -> 25 us, 324 800 of one head of 64 written in 325 -> 60, 24 000 of
+// four heads of 128 (64 chunks) read in 22 -> 17. More chunks lose, as each lane finds its own slot: eight
+// heads of 128 written in 38 -> 48, 32 heads in 116 -> 166.
 constexpr int kFlat = 64;
 // n / chunks: by is 2^36 / chunks rounded up. Exact for n * chunks <= 2^36: 2^24 tokens at most of up to 64
 // chunks, or n within the lanes of the GPU (under 2^18) and chunks within n.
@@ -301,8 +301,8 @@ __global__ void __launch_bounds__(kThreads) kv4_read_flat_kernel(rc_kv4_read_arg
   }
 }
 // A lane takes up to `ahead` chunks in a go, fewer where the GPU's lanes then have none. Also for few tokens
-// of many heads, whose chunks all find a lane of their own (two to four of 32 heads of 256 written in 12.6 ->
-// 8.2 us; up to four times as many chunks: 16 heads of fp32 14.4 -> 15.6).
+// of many heads, whose chunks all find a lane of their own (two to four of 32 heads of 256 written and read
+// back in 12.6 -> 8.2 us; up to four times as many chunks: 16 heads of fp32 14.4 -> 15.6).
 struct Flat {
   uint64_t by;
   int each;
