@@ -62,7 +62,9 @@ struct Cfg {
   static constexpr bool F32 = sizeof(T) == 4;
   static constexpr int QP = F32 ? 3 : 1;     // bf16 parts of a query element
   static constexpr int UNIT = F32 ? 2 : 7;   // scores are summed in 2^-UNIT
-  static constexpr int PP = F32 ? 3 : 2;     // of a weight
+  // of a weight: all its 24 bits. Two parts (16 bits) for bf16: 393 -> 348 us on 128 rows of 512 .. 8192
+  // tokens, 32 + 32 heads, and 0.22 % of outputs unlike those of 64 bits instead of 0.11
+  static constexpr int PP = 3;
   static constexpr int WARPS = NT > 1 || F32 ? 4 : 8;               // of a CTA, at most
   static constexpr int PER_SM = 2;                                  // CTAs of so many warps
   static constexpr int CH = 4 * NG;          // bytes of a copy: a head's row is five

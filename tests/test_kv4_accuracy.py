@@ -38,3 +38,49 @@ def test_sums_over_long_rows_are_fp32(dtype, g, hkv, d):
     rl = lens.double().log()[:, None].cuda()
     assert ((lse.double() - rl).abs() <= 4 * T.U * rl).all()     # whole numbers, log2, its product
     assert rc.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 128), ("f32", 64)])
+@pytest.mark.parametrize("g", [8, 16])
+def test_weights_keep_24_bits(dtype, d, g):
+    """Outputs that are differences of two weights 2^-15 of them apart, so that 8 bits of an output show the
+    weights' last ones. A query has one element, a power of two, and keys code * scale + minimum of 17 bits at
+    most: scores are exact. Tokens 2 i and 2 i + 1 have the same code and scale there, and minima that are
+    neighbours; their values are + and - 1 in element i, + and - 7 in element i + d / 2, zero elsewhere."""
+    hkv, n = 4, d
+    gen = torch.Generator().manual_seed(3 * d + g)
+    scale = 0.3
+
+    def pairs(t):
+        return t.repeat_interleave(2, 0)
+
+    k_code = pairs(torch.randint(0, 16, (n // 2, hkv, d), generator=gen))
+    k_step = pairs(torch.randint(8, 16, (n // 2, hkv, d // 32), generator=gen).double() / 128)
+    k_low = pairs(torch.randint(128, 255, (n // 2, hkv, d // 32), generator=gen).double())
+    k_low[1::2] += 1
+    k = T.held(k_code, k_step, k_low / 32768)
+    v_code = torch.full((n, hkv, d), 8)
+    i = torch.arange(n // 2)
+    v_code[2 * i, :, i], v_code[2 * i + 1, :, i] = 9, 7
+    v_code[2 * i, :, i + d // 2], v_code[2 * i + 1, :, i + d // 2] = 15, 1
+    one = torch.ones((n, hkv, d // 32), dtype=torch.float64)
+    v = T.held(v_code, one, -8 * one)
+    q = torch.zeros((1, hkv, g, d))
+    at = torch.randint(0, d, (hkv, g), generator=gen)
+    q.scatter_(-1, at[None, ..., None], torch.tensor([2.0, -2, 1, -1, 0.5, -0.5, 2, -1] * 2)[:g, None]
+               .expand(1, hkv, g, 1))
+    q = q.flatten(1, 2).to(DT[dtype])
+    o, lse = T.run(q, [(0, n)], torch.arange(n, dtype=torch.int32)[None], k, v, scale)
+    o = o[0].double().cpu()
+    # a weight of at most 2.1: the difference to the reference (half a step of 2 to 4, times ln 2) and exp2
+    # (2^-22), 5.4 u; a sum of 16 products of which two count (2 u); the quotient goes with the output
+    for h in range(hkv * g):
+        c, s, m = T.groups_of(k[:, h // g], d)
+        p = ((c * s + m) @ q[0, h].double() * scale).softmax(0)
+        c, s, m = T.groups_of(v[:, h // g], d)
+        ro = p @ (c * s + m)
+        limit = 8 * T.U * (p @ (c * s + m).abs())
+        beyond = (o[h] - ro).abs() - T.half_spacing(ro.abs() + limit, q.dtype)
+        assert (beyond <= limit + 40 * T.U * ro.abs()).all(), (h, float((beyond / limit).max()))
+    assert rc.device_status() == 0
