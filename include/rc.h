@@ -749,7 +749,8 @@ int rc_kv4_read(const rc_kv4_read_args* args, void* stream);
  * several rows (a chunk of new tokens: rows of growing seq_len). A row with seq_len 0 (whatever its
  * req_idx holds) gets o = 0, lse = -inf; so does a row whose seq_len or req_idx is out of range, which
  * also sets the device status word. A slot outside the pool sets it and that token weighs nothing; a row
- * of such tokens alone is as one of length 0. dtype is q's and o's; sm_scale > 0; Hq / Hkv <= 16;
+ * of such tokens alone is as one of length 0. A wait that gives up sets it, and outputs that were not
+ * computed are NaN. dtype is q's and o's; sm_scale > 0; Hq / Hkv <= 16;
  * head_dim 64 or 128; max_seq_len <= 2^24; num_rows <= 2^20; q and o
  * 16-byte aligned, planes as for rc_kv4_append. An o that overlaps q, a plane or the workspace is
  * refused. */
@@ -780,10 +781,11 @@ int rc_kv4_decode_attention(const rc_kv4_decode_args* args, void* workspace, siz
                             void* stream);
 
 /* Test hook; the pages have no counterpart. Bound, in nanoseconds, of every wait inside the
- * extend kernel (0 restores the default, 2 s). With a short bound waits give up: the kernel
- * records code 3 in the device status word, stops issuing work and returns without hanging; its
- * outputs are then not written. The wait that guards the release of tensor memory keeps the
- * default. Applies to launches made after the call, on every device. */
+ * extend kernel and rc_kv4_decode_attention (0 restores the default, 2 s). With a short bound waits
+ * give up: the kernel records code 3 in the device status word, stops issuing work and returns
+ * without hanging; the extend kernel's outputs are then not written, those of
+ * rc_kv4_decode_attention that were not computed are NaN. The wait that guards the release of
+ * tensor memory keeps the default. Applies to launches made after the call, on every device. */
 int rc_debug_set_wait_limit_ns(uint64_t ns);
 
 /* Read and clear the device status word of the current device (synchronises `stream`).

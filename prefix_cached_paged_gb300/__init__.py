@@ -46,8 +46,8 @@ def launch_count() -> int:
 
 
 def set_wait_limit_ns(ns: int) -> None:
-    """Test hook (rc_debug_set_wait_limit_ns): bound of the extend kernel's waits for later
-    launches; 0 restores the default."""
+    """Test hook (rc_debug_set_wait_limit_ns): bound of the waits of the extend kernel and of
+    kv4_decode_attention for later launches; 0 restores the default."""
     check(lib().rc_debug_set_wait_limit_ns(int(ns)), "rc_debug_set_wait_limit_ns")
 
 

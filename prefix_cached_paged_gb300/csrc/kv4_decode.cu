@@ -115,6 +115,7 @@ extern "C" int rc_kv4_decode_attention(const rc_kv4_decode_args* a, void* worksp
                    !rc::kv4::meet(a->o, outs, a->v_pool, plane) &&
                    !rc::kv4::meet(a->o, outs, workspace, (int64_t)need),
                "%s: o overlaps q, a plane or the workspace", fn);
+  p.wait_ns = rc::wait_limit_ns();
   p.status = rc::device_status_ptr();
   if (!p.status) return rc::fail(RC_ERR_CUDA, "%s: no device status word", fn);
   const cudaError_t e = a->dtype == RC_DTYPE_BF16

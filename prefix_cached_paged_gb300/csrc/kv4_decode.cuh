@@ -24,6 +24,7 @@
 #pragma once
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 #include <cmath>
 
 #include "host_common.h"
@@ -54,6 +55,7 @@ struct Params {
   int tokens, log_tokens;   // of a step: a power of two
   int stride;     // bytes of a slot
   int groups;     // KV heads / HG
+  uint64_t wait_ns;   // bound of a wait
 };
 
 template <typename T, int D, int NT>
@@ -84,26 +86,40 @@ __device__ __forceinline__ int place(int r) {
   return NG == 4 ? (r & 8) | (r & 1) << 2 | (r >> 1 & 3) : (r & 8) | (r & 3) << 1 | (r >> 2 & 1);
 }
 
-// Waits for the phase of that parity, at most 2 s: then the thread sets the status word, waits for its
-// copies and leaves, as the others will. The hardware waits up to 20 us before it looks again: warps that
-// wait share their scheduler with those that work.
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+// Whether the phase of that parity is complete; a warp that has to wait sleeps up to 20 us before it looks again,
+// as it shares its scheduler with those that work. Limits shorter than that are looked at without sleep.
+constexpr uint32_t kSleepNs = 20000;
+template <bool SLEEP>
+__device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity) {
   uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(done) : "r"(bar), "r"(parity), "r"(20000) : "memory");
-  return done != 0;
+  if constexpr (SLEEP)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done) : "r"(bar), "r"(parity), "r"(kSleepNs) : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+  return __all_sync(~0u, done);
 }
-__device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, int* status) {
-  if (try_wait(bar, parity)) return;
+// The warp waits for a phase, p.wait_ns at most: then it sets the status word, waits for its own copies and
+// says false.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, const Params& p) {
+  if (arrived<false>(bar, parity)) return true;
+  const bool sleep = p.wait_ns >= kSleepNs;
+  if (sleep && arrived<true>(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
-  while (!try_wait(bar, parity)) {
-    if (global_timer_ns() - t0 > 2000000000ull) {
-      set_status(status, kStatusWaitExpired);
-      asm volatile("cp.async.wait_all;\n exit;" ::: "memory");
+  while (!(sleep ? arrived<true>(bar, parity) : arrived<false>(bar, parity))) {
+    if (__any_sync(~0u, global_timer_ns() - t0 > p.wait_ns)) {
+      set_status(p.status, kStatusWaitExpired);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      return false;
     }
   }
+  return true;
 }
 
 // Bytes between tokens of a stage: an odd number of 16.
@@ -699,7 +715,16 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
       if (d == 0) *(float2*)(p.w.ml + i * 2) = make_float2(m, den);
     }
   };
+  // The step that is read; negative from a wait on that gave up: the warp then goes through its steps without
+  // waiting, copying or saying what it has read, and its pairs' sums, from this one on, are NaN. Others of
+  // the CTA give up in turn, or have what they need: no output is made of what did not arrive.
+  int now = 0;
+  auto give_up = [&] { now |= INT_MIN, copy_left = 0; };
   auto end_pair = [&](char* stage) {
+    if (now < 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = __int_as_float(0x7FC00000);
+    }
     if (threadIdx.x == 0 && at.whole && !at.ends) {
       Range* rg = p.w.range + blockIdx.x;
       rg->row1 = at.row, rg->hg1 = at.hg, rg->last1 = cut.of(at.begin + at.steps - 1);
@@ -771,11 +796,10 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
   issue();
   if (copy_left > 0) issue();
   begin_pair();
-  uint32_t now = 0;             // the step that is read
-  int now_half = 0;             // and its K
+  int now_half = 0;             // K of step `now`
   const int mine_at = ts * 16 * U * pitch + hw * RB;
   while (true) {
-    wait_for(full0 + 8 * (now & 3), now >> 2 & 1, p.status);
+    if (now >= 0 && !wait_for(full0 + 8 * (now & 3), now >> 2 & 1, p)) give_up();
     float x[U][NT][4];
 #pragma unroll
     for (int u = 0; u < U; ++u) scores(smem + now_half * half + mine_at + u * 16 * pitch, x[u]);
@@ -793,7 +817,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&s_read[now & 3]);
+    if (lane == 0 && now >= 0) mbar_arrive(&s_read[now & 3]);
     // the reference of a head's weights (to base 2) is a running maximum that follows once a score is
     // 2^8 times beyond it
     bool beyond = false;
@@ -844,8 +868,10 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     if (--left == 0) end_pair(vt);
     __syncwarp();
     if (copy_left > 0) {
-      wait_for(read0 + 8 * (now & 3), now >> 2 & 1, p.status);
-      issue();
+      if (wait_for(read0 + 8 * (now & 3), now >> 2 & 1, p))
+        issue();
+      else
+        give_up();
     }
     ++now;
     now_half = next_half(now_half, 2);
