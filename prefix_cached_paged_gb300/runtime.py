@@ -104,6 +104,10 @@ class HostCache:
         out, self._owed = self._owed, []
         return out
 
+    def owe(self, copies) -> None:
+        """Copies that a call could not make, oldest first: take_owed gives them out again."""
+        self._owed.extend(copies)
+
     def _release_on_error(self, nodes, fn, *args):
         """fn(*args); if it fails, the nodes this plan's match locked are unlocked first, so a
         failed plan leaves the tree as it found it apart from evictions (which are complete)."""
@@ -204,6 +208,16 @@ class HostCache:
             return order[:admitted].tolist()
         finally:
             self.host_seconds += time.perf_counter() - t0
+
+    def cancel(self, plan: Plan, owed=None) -> None:
+        """Take back a plan whose batch did not begin: its slots return to the pool and its nodes are
+        unlocked (evictions and loads from the host tier stand). owed: its host-tier copies, if they
+        have not been made; take_owed gives them out."""
+        self.pool.free(np.concatenate([plan.out_loc, plan.extra]))
+        for n in plan.nodes:
+            self.tree.unlock(int(n))
+        if owed is not None:
+            self.owe([owed])
 
     def finish(self, plan: Plan, keep_locked: bool = False):
         """Insert, free duplicates, unlock. Returns (end nodes, duplicates freed)."""

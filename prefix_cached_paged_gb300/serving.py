@@ -32,6 +32,7 @@ computes them.
 """
 from __future__ import annotations
 
+from contextlib import contextmanager
 from dataclasses import dataclass, field
 
 import numpy as np
@@ -213,17 +214,39 @@ class Engine:
 
     # ---------------------------------------------------------------- extend
     def _owed_copies(self):
-        """Host-tier copies a failed plan or allocation left owed: on the stream first."""
-        for c in self.host.take_owed():
-            self._tier_copies(c)
+        """Host-tier copies a failed call left owed: on the stream first. Those that fail now are
+        still owed."""
+        owed = self.host.take_owed()
+        try:
+            while owed:
+                self._tier_copies(owed[0])
+                owed.pop(0)
+        finally:
+            self.host.owe(owed)
+
+    @contextmanager
+    def _begin(self, plan: Plan):
+        """What a batch does on the device to begin, its plan's host-tier copies first. If any of it
+        fails, the plan's slots and locks and the rows taken go back, and copies not made are owed."""
+        rows, owed = list(self._free_rows), plan.copies
+        try:
+            self._tier_copies(owed)
+            owed = None
+            yield
+        except BaseException:
+            self._free_rows[:] = rows
+            self.host.cancel(plan, owed)
+            raise
 
     def extend_begin(self, seqs, extra: int = 0, match_all: bool = False) -> ExtendBatch:
-        # rows first: a plan allocates slots and locks prefixes, which a late failure would leak
         self._check_rows(len(seqs))
         self._owed_copies()
         plan = self.host.plan(seqs, extra=extra, match_all=match_all)
-        self._tier_copies(plan.copies)
-        B = len(seqs)
+        with self._begin(plan):
+            return self._extend_batch(plan)
+
+    def _extend_batch(self, plan: Plan) -> ExtendBatch:
+        B = len(plan.lengths)
         row_ids = self._take_rows(B)
         self.dev.write_rows(row_ids, plan.rows, plan.lengths)
         qo, pl, ri, ol = self.dev.upload_i32([plan.qo_indptr, plan.prefix_len, row_ids,
@@ -305,17 +328,17 @@ class Engine:
         self._check_rows(len(contexts))
         self._owed_copies()
         plan = self.host.plan(contexts, match_all=True)
-        self._tier_copies(plan.copies)
-        if plan.num_tokens:
-            self.host.pool.free(plan.out_loc)
-            for n in plan.nodes:
-                self.host.tree.unlock(int(n))
-            raise ValueError("decode_begin: every context must already be cached")
-        row_ids = self._take_rows(len(contexts))
+        with self._begin(plan):
+            if plan.num_tokens:
+                raise ValueError("decode_begin: every context must already be cached")
+            return self._decode_batch(plan)
+
+    def _decode_batch(self, plan: Plan) -> DecodeBatch:
+        row_ids = self._take_rows(len(plan.lengths))
         self.dev.write_rows(row_ids, plan.rows, plan.lengths)
         self._decode_plan = plan
         batch = DecodeBatch(row_ids, plan.nodes, plan.lengths.astype(np.int32),
-                            np.zeros(len(contexts), np.int32), context_rows=plan.rows,
+                            np.zeros(len(plan.lengths), np.int32), context_rows=plan.rows,
                             context_len=plan.lengths.astype(np.int64), gen_slots=[])
         if self.share_decode:
             # the contexts' slots never change while they decode (new tokens get new slots), so
