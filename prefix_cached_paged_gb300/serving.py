@@ -172,7 +172,8 @@ class Engine:
                                                dtype=dtype, device=self.dev.device)
         self.max_ctx = max_ctx
         self.kv_chunk = kv_chunk
-        # decode reads a context prefix that several requests share once for all of them
+        # decode reads a context prefix that several requests share once for all of them; with
+        # kv_bits=4 once for each of them, whatever this says
         self.share_decode = share_decode
         # extend stacks the new tokens of consecutive requests over a prefix they share, where
         # that is estimated to pay (True), for every group found ("always"), or never (False)
@@ -340,7 +341,7 @@ class Engine:
         batch = DecodeBatch(row_ids, plan.nodes, plan.lengths.astype(np.int32),
                             np.zeros(len(plan.lengths), np.int32), context_rows=plan.rows,
                             context_len=plan.lengths.astype(np.int64), gen_slots=[])
-        if self.share_decode:
+        if self.share_decode and self.kv_bits != 4:
             # the contexts' slots never change while they decode (new tokens get new slots), so
             # the groups hold for the whole batch
             G = self.n_q_heads // self.n_kv_heads

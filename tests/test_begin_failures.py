@@ -119,3 +119,18 @@ def test_owed_tier_copies_of_a_failed_beginning_are_made_by_the_next():
     assert len(spilled) == 1 and len(spilled[0][0]) >= 20
     eng.extend_end(batch)
     assert eng.host.take_owed() == []
+
+
+def test_contexts_of_a_4_bit_cache_are_not_grouped():
+    """Groups of requests that share a prefix are dense decode's: none are planned or uploaded."""
+    pre = synth.tokens(3, 1, 40)
+    seqs = [np.concatenate([pre, synth.tokens(3, 5 + i, 5)]).astype(np.int32) for i in range(3)]
+    for bits in (16, 4):
+        eng = _engine4()
+        eng.dev = _Failing()
+        eng.kv_bits, eng.share_decode, eng.kv_chunk = bits, True, 16
+        eng.extend_end(eng.extend_begin(seqs))
+        eng.dev.calls = 0
+        batch = eng.decode_begin(seqs)
+        assert batch.num_groups == (1 if bits == 16 else 0) and eng.dev.calls == (2 if bits == 16 else 1)
+        eng.decode_end(batch)
