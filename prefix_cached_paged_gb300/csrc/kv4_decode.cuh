@@ -162,15 +162,16 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // a += b, two by two
 __device__ __forceinline__ void add4(float* a, const float* b) {
 #pragma unroll
-  for (int k = 0; k < 4; k += 2) {
-    f32x2 s;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(s) : "l"(pack2(a[k], a[k + 1])), "l"(pack2(b[k], b[k + 1])));
-    unpack2(s, a[k], a[k + 1]);
-  }
+  for (int k = 0; k < 4; k += 2)
+    unpack2(add2(pack2(a[k], a[k + 1]), pack2(b[k], b[k + 1])), a[k], a[k + 1]);
 }
 __device__ __forceinline__ void ldmatrix_x2_trans(uint32_t at, uint32_t& r0, uint32_t& r1) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
@@ -732,6 +733,8 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
+      for (int c = 0; c < 2; ++c) mx[nt][c] = fmaxf(mx[nt][c] * F[nt][c], -FLT_MAX);   // to base 2
+#pragma unroll
       for (int x = 4; x < 32; x *= 2) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], x);
@@ -818,8 +821,9 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
     }
     __syncwarp();
     if (lane == 0 && now >= 0) mbar_arrive(&s_read[now & 3]);
-    // the reference of a head's weights (to base 2) is a running maximum that follows once a score is
-    // 2^8 times beyond it
+    // the reference of a head's weights is a running maximum, as the scores are summed, that follows once
+    // a weight is 2^8 and more. Differences are taken before the factor to base 2: against a product that
+    // was rounded, scores of 2^30 and more lost their greatest weight or made it infinite
     bool beyond = false;
     float top[NT][2];
 #pragma unroll
@@ -830,8 +834,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
         for (int u = 1; u < U; ++u)
           top[nt][c] = fmaxf(top[nt][c], fmaxf(x[u][nt][c], x[u][nt][2 + c]));
-        top[nt][c] *= F[nt][c];
-        beyond |= top[nt][c] > mx[nt][c] + 8.f;
+        beyond |= (top[nt][c] - mx[nt][c]) * F[nt][c] > 8.f;
       }
     if (__any_sync(~0u, beyond)) {
 #pragma unroll
@@ -841,7 +844,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
           for (int s = 4; s < 32; s *= 2)
             top[nt][c] = fmaxf(top[nt][c], __shfl_xor_sync(~0u, top[nt][c], s));
-          const float to = fmaxf(mx[nt][c], top[nt][c]), f = ex2(mx[nt][c] - to);
+          const float to = fmaxf(mx[nt][c], top[nt][c]), f = ex2((mx[nt][c] - to) * F[nt][c]);
           mx[nt][c] = to;
           l[nt][c] *= f;
 #pragma unroll
@@ -859,7 +862,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          x[u][nt][k] = ex2(fmaf(x[u][nt][k], F[nt][k & 1], -mx[nt][k & 1]));
+          x[u][nt][k] = ex2((x[u][nt][k] - mx[nt][k & 1]) * F[nt][k & 1]);
           l[nt][k & 1] += x[u][nt][k];
         }
     char* vt = smem + next_half(now_half, 1) * half;

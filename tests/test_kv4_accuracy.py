@@ -84,3 +84,35 @@ def test_weights_keep_24_bits(dtype, d, g):
         beyond = (o[h] - ro).abs() - T.half_spacing(ro.abs() + limit, q.dtype)
         assert (beyond <= limit + 40 * T.U * ro.abs()).all(), (h, float((beyond / limit).max()))
     assert rc.device_status() == 0
+
+
+def check_one_hot(q, k, v, scale, o, lse, h, kv):
+    """Query head h: its lse, and its output where one token has all the weight."""
+    d = q.shape[-1]
+    code, step, low = T.groups_of(k[:, kv], d)
+    x = q[0, h].double()
+    s = (code * step + low) @ x * scale
+    size = float(((code * step + low.abs() + 8 * step) @ x.abs()).max() * scale)
+    first, second = s.topk(2).values.tolist()
+    assert abs(float(lse[0, h]) - float(s.logsumexp(0))) <= 32 * T.U * size + 4 * T.U
+    one = first - second > 100 + 64 * T.U * size
+    if one:
+        assert torch.equal(o[0, h].cpu(), R.values(v[s.argmax(), kv], d).float().to(q.dtype))
+    return one
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [3, 50, 2100])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_any_size(dtype, n, sign):
+    """Scores of 1e3 to 1e30, all of them negative too (keys of one sign): the greatest has the weight."""
+    hkv, d, scale = 2, 128, 0.088
+    gen = torch.Generator().manual_seed(8 + n)
+    k = R.quantise(1e-6 * (torch.randn((n, hkv, d), generator=gen) * 0.3 + 4))
+    v = R.quantise(torch.randn((n, hkv, d), generator=gen))
+    q = torch.rand((1, 16, d), generator=gen) + 0.5
+    q = (q * sign * 10.0 ** torch.linspace(8, 35, 16)[:, None]).to(DT[dtype])
+    o, lse = T.run(q, [(0, n)], torch.arange(n, dtype=torch.int32)[None], k, v, scale)
+    assert sum(check_one_hot(q, k, v, scale, o, lse, h, h // 8) for h in range(16)) >= 8
+    assert rc.device_status() == 0
