@@ -745,7 +745,8 @@ int rc_kv4_read(const rc_kv4_read_args* args, void* stream);
  * tokens of its request's row req_idx[n] at positions below seq_len[n] (its own token included,
  * already in the pool: rc_kv4_append):
  *   o[n, h] = softmax(sm_scale * <q, k>) v,   k and v what the codes stand for, not rounded;
- * lse [num_rows, Hq] fp32 natural log (optional). Scores, weights and sums are fp32. A request may have
+ * lse [num_rows, Hq] fp32 natural log (optional). Scores, weights and sums are fp32; a query head whose
+ * largest magnitude times sm_scale is 2^120 or more may have NaN as output. A request may have
  * several rows (a chunk of new tokens: rows of growing seq_len). A row with seq_len 0 (whatever its
  * req_idx holds) gets o = 0, lse = -inf; so does a row whose seq_len or req_idx is out of range, which
  * also sets the device status word. A slot outside the pool sets it and that token weighs nothing; a row

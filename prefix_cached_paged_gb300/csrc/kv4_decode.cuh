@@ -454,9 +454,14 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
       }
       most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
       most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
-      // the head's elements over 2^e: below 2 in magnitude, exact
+      // the head's elements over 2^e: below 2 in magnitude, exact. Scores are summed over 2^(e - UNIT) and
+      // taken to base 2 by one factor: one too large for fp32 makes the scores NaN, one below its normal
+      // numbers goes with scores of next to nothing
       const int e = min(max((int)(__float_as_uint(most) >> 23) - 127, -126), 127);
-      const float down = __uint_as_float(e == 127 ? 1u << 22 : (uint32_t)(127 - e) << 23);
+      constexpr float unit = 1 << C::UNIT;
+      const float f = a.sm_scale * __uint_as_float((uint32_t)(127 + e) << 23) * (kLog2e * unit);
+      const float down = f > FLT_MAX ? __uint_as_float(0x7FC00000u)
+                                     : __uint_as_float(e == 127 ? 1u << 22 : (uint32_t)(127 - e) << 23);
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
@@ -482,12 +487,10 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
             for (int q = 0; q < QP; ++q) qf[q][nt][j][k][b] = take_part(lo, hi);
           }
       }
-      constexpr float unit = 1 << C::UNIT;
       float none = 0.f;
       sum /= unit;
 #pragma unroll
       for (int k = 0; k < 3; ++k) qm[nt][k] = take_part(none, sum);
-      const float f = a.sm_scale * (kLog2e * unit) * __uint_as_float((uint32_t)(127 + e) << 23);
       const float factor = fminf(fmaxf(f, FLT_MIN), FLT_MAX);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {

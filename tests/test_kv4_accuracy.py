@@ -116,3 +116,25 @@ def test_scores_of_any_size(dtype, n, sign):
     o, lse = T.run(q, [(0, n)], torch.arange(n, dtype=torch.int32)[None], k, v, scale)
     assert sum(check_one_hot(q, k, v, scale, o, lse, h, h // 8) for h in range(16)) >= 8
     assert rc.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,scale", [("bf16", 0.088), ("bf16", 1.0), ("bf16", 3e37), ("f32", 0.088),
+                                         ("f32", 1.0), ("f32", 1e37)])
+def test_the_largest_queries_are_right_or_nan(dtype, scale):
+    """Queries up to the largest numbers, or factors up to them, and keys small enough for finite scores."""
+    n, hkv, d = 50, 2, 128
+    gen = torch.Generator().manual_seed(8)
+    k = R.quantise(1e-6 * torch.randn((n, hkv, d), generator=gen))
+    v = R.quantise(torch.randn((n, hkv, d), generator=gen))
+    at = 10.0 ** torch.tensor([38.4, 37.5, 37.0, 36.6, 36.0, 35.0, 30.0, 20.0])
+    q = torch.randn((1, 8, d), generator=gen)
+    q = (q / q.abs().amax(-1, keepdim=True) * at[:, None] * min(1, 1 / scale)).to(DT[dtype])
+    o, lse = T.run(q, [(0, n)], torch.arange(n, dtype=torch.int32)[None], k, v, scale)
+    right = 0
+    for h in range(8):
+        if lse[0, h].isnan():
+            assert o[0, h].isnan().all() and float(q[0, h].double().abs().max()) * scale >= 2.0 ** 120
+        else:
+            right += check_one_hot(q, k, v, scale, o, lse, h, h // 4)
+    assert right >= 4 and rc.device_status() == 0   # 1e36 and less is below 2^120 (1.33e36), 4e36 is not
