@@ -455,8 +455,8 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
       most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
       most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
       // the head's elements over 2^e: below 2 in magnitude, exact. Scores are summed over 2^(e - UNIT) and
-      // taken to base 2 by one factor: one too large for fp32 makes the scores NaN, one below its normal
-      // numbers goes with scores of next to nothing
+      // taken to base 2 by one factor: one too large for fp32 makes the scores NaN, one below 2^-118
+      // goes with scores under 2^-80 (the first reference, the least number, is then still far below them)
       const int e = min(max((int)(__float_as_uint(most) >> 23) - 127, -126), 127);
       constexpr float unit = 1 << C::UNIT;
       const float f = a.sm_scale * __uint_as_float((uint32_t)(127 + e) << 23) * (kLog2e * unit);
@@ -491,7 +491,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
       sum /= unit;
 #pragma unroll
       for (int k = 0; k < 3; ++k) qm[nt][k] = take_part(none, sum);
-      const float factor = fminf(fmaxf(f, FLT_MIN), FLT_MAX);
+      const float factor = fminf(fmaxf(f, 0x1p-118f), FLT_MAX);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         F[nt][k] = __shfl_sync(~0u, factor, (2 * t + k) * 4);

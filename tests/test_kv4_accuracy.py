@@ -138,3 +138,42 @@ def test_the_largest_queries_are_right_or_nan(dtype, scale):
         else:
             right += check_one_hot(q, k, v, scale, o, lse, h, h // 4)
     assert right >= 4 and rc.device_status() == 0   # 1e36 and less is below 2^120 (1.33e36), 4e36 is not
+
+
+def beyond(o, ro, to, dtype):
+    """By how much outputs are further off than a rounding and the limit allow."""
+    return (o.double() - ro).abs() - T.half_spacing(ro.abs() + to, dtype) - to
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,hq,hkv,d", [
+    ("bf16", 8, 8, 128), ("bf16", 4, 1, 128), ("bf16", 6, 3, 64), ("bf16", 32, 2, 128), ("bf16", 10, 5, 64),
+    ("bf16", 64, 4, 64), ("f32", 4, 4, 128), ("f32", 16, 1, 64), ("f32", 12, 6, 64)])
+def test_every_token_counts_once(dtype, hq, hkv, d):
+    """Zero queries: lse is the logarithm of the number of tokens, and an element that is 1 in one token only
+    shows whether that token counted. Marked are the first tokens, those on both sides of steps, and others
+    anywhere; rows of all lengths in one call, and long ones alone, which all CTAs share."""
+    most = 131_071
+    gen = torch.Generator().manual_seed(hq + 3 * d)
+    edge = torch.cat([16 * 2 ** torch.arange(0, 13) + i for i in (-1, 0, 1)])
+    marks = torch.cat([torch.arange(min(300, hkv * d // 2)), edge, most - 1 - torch.arange(5),
+                       torch.randint(0, most, (hkv * d,), generator=gen)])[:hkv * d].reshape(hkv, d)
+    tokens, at = marks.flatten().unique(return_inverse=True)
+    code = torch.full((len(tokens), hkv, d), 8)
+    code[at.reshape(hkv, d), torch.arange(hkv)[:, None], torch.arange(d)] = 9
+    one = torch.ones((len(tokens), hkv, d // 32), dtype=torch.float64)
+    v = T.held(torch.full((1, 1, d), 8), one[:1, :1], -8 * one[:1, :1]).expand(most, hkv, -1).contiguous()
+    v[tokens] = T.held(code, one, -8 * one)
+    v, marks = v.cuda(), marks.cuda()
+    table = torch.arange(most, dtype=torch.int32)[None].cuda()
+    lens = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 512, 513, 1000, 2047,
+            2048, 2049, 4097, 9999, 33_333, most]
+    for some in (lens, [most], [40_000], [700, 2500], [100 + 3 * i for i in range(400)]):
+        q = torch.zeros((len(some), hq, d), dtype=DT[dtype], device="cuda")
+        o, lse = T.run(q, [(0, m) for m in some], table, v, v, 0.1)
+        n = torch.tensor(some, dtype=torch.float64, device="cuda")[:, None]
+        assert ((lse.double() - n.log()).abs() <= 4 * T.U * n.log()).all()
+        # whole numbers and one quotient, then the outputs' type
+        want = ((marks < n[..., None]) / n[..., None]).repeat_interleave(hq // hkv, 1)
+        assert (beyond(o, want, 2 * T.U * want, q.dtype) <= 0).all()
+    assert rc.device_status() == 0
