@@ -145,6 +145,74 @@ def beyond(o, ro, to, dtype):
     return (o.double() - ro).abs() - T.half_spacing(ro.abs() + to, dtype) - to
 
 
+def case(dtype, n, g, d, seed):
+    gen = torch.Generator().manual_seed(seed + n * 7 + g)
+    k, v = R.quantise(torch.randn((n, d), generator=gen)), R.quantise(torch.randn((n, d), generator=gen) + 0.3)
+    return torch.randn((g, d), generator=gen).to(DT[dtype]), k, v
+
+
+@pytest.mark.parametrize("dtype,n,g,d", [
+    ("bf16", 64, 4, 128), ("bf16", 700, 8, 64), ("bf16", 2049, 8, 128), ("bf16", 3500, 12, 128),
+    ("f32", 33, 4, 64), ("f32", 260, 2, 128), ("f32", 500, 4, 64), ("f32", 1111, 8, 128), ("f32", 2000, 16, 64)])
+def test_the_limits_see_what_they_are_for(dtype, n, g, d):
+    """Mistakes planted in the 64-bit form are beyond the limits: weights of one bf16 part, bf16 queries, one
+    token left out, one counted twice. The form itself, rounded, is within."""
+    q, k, v = case(dtype, n, g, d, 5)
+    scale = d ** -0.5
+    o, lse, to, tl = T.attend(q, k, v, scale)
+    kn, vn = R.values(k, d), R.values(v, d)
+
+    def outside(q=q, part=False, count=None):
+        s = q.double() @ kn.T * scale
+        w = (s - s.amax(-1, keepdim=True)).exp()
+        if count is not None:
+            w = w * count
+        x = (w.bfloat16().double() if part else w) @ vn / w.sum(-1, keepdim=True)
+        y = w.sum(-1).log() + s.amax(-1)
+        return bool((beyond(x.to(q.dtype), o, to, q.dtype) > 0).any()), \
+            bool(((y.float().double() - lse).abs() > tl).any())
+
+    assert outside() == (False, False)
+    assert outside(part=True)[0]
+    if dtype == "f32":
+        assert outside(q=q.bfloat16().float()) == (True, True)
+    for t in (0, n // 2, n - 1):
+        for times in (0.0, 2.0):
+            count = torch.ones(n, dtype=torch.float64)
+            count[t] = times
+            assert outside(count=count) == (True, True), (t, times)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,ctx,hq,hkv,d", [
+    ("bf16", [1], 1, 1, 128), ("bf16", [15, 16, 17], 8, 2, 128), ("bf16", [31, 32, 33, 63, 64, 65], 4, 4, 128),
+    ("bf16", [1000, 129, 700], 32, 8, 128), ("bf16", [2049, 40], 8, 8, 128), ("bf16", [901, 333], 6, 2, 128),
+    ("bf16", [1500], 10, 2, 64), ("bf16", [1200, 17], 16, 1, 128), ("bf16", [3500], 12, 1, 128),
+    ("bf16", [400, 90], 9, 3, 128), ("bf16", [257, 100], 14, 7, 128), ("bf16", [90, 1], 6, 6, 64),
+    ("bf16", [40_000, 7000], 8, 2, 64), ("bf16", [30_000, 5], 32, 2, 128),
+    ("f32", [1, 33], 2, 2, 64), ("f32", [700, 97], 6, 2, 64), ("f32", [1111], 8, 1, 128),
+    ("f32", [515], 13, 1, 128), ("f32", [260, 260], 4, 4, 128), ("f32", [2000], 16, 1, 64),
+    ("f32", [64, 1, 500], 16, 8, 128), ("f32", [40_000, 3000], 4, 2, 64)])
+def test_decode_within_close_limits(dtype, ctx, hq, hkv, d):
+    """Rows of all shapes, and repeated ones: a call's second row of each length is cut elsewhere."""
+    n, g = max(ctx), hq // hkv
+    gen = torch.Generator().manual_seed(sum(ctx) + hq + d)
+    k = R.quantise(torch.randn((min(n, 5000), hkv, d), generator=gen))
+    v = R.quantise(torch.randn((min(n, 5000), hkv, d), generator=gen) + 0.3)
+    table = torch.randint(0, k.shape[0], (len(ctx), n), generator=gen, dtype=torch.int32)
+    rows = [(b, m) for b, m in enumerate(ctx)] * 2
+    q = torch.randn((len(rows), hq, d), generator=gen).to(DT[dtype])
+    o, lse = T.run(q, rows, table, k, v, d ** -0.5)
+    for i, (b, m) in enumerate(rows):
+        at = table[b, :m].long()
+        for h in range(hkv):
+            own = slice(h * g, h * g + g)
+            ro, rl, to, tl = T.attend(q[i, own].cuda(), k[at, h].cuda(), v[at, h].cuda(), d ** -0.5)
+            assert (beyond(o[i, own], ro, to, q.dtype) <= 0).all(), (i, h)
+            assert ((lse[i, own].double() - rl).abs() <= tl).all(), (i, h)
+    assert rc.device_status() == 0
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype,hq,hkv,d", [
     ("bf16", 8, 8, 128), ("bf16", 4, 1, 128), ("bf16", 6, 3, 64), ("bf16", 32, 2, 128), ("bf16", 10, 5, 64),
