@@ -122,6 +122,8 @@ class Engine:
             raise ValueError("kv_bits must be 16 (the cache in dtype) or 4")
         if kv_bits == 4 and head_dim not in (64, 128):
             raise ValueError("kv_bits=4 attends to heads of 64 or 128")
+        if kv_bits == 4 and (n_q_heads % n_kv_heads or n_q_heads > 16 * n_kv_heads):
+            raise ValueError("kv_bits=4 attends with up to 16 query heads for each KV head")
         if kv_bits == 4 and sparse_block:
             raise ValueError("kv_bits=4 keeps no block bounds: sparse_block must be 0")
         if kv_bits == 4 and host_tier_slots and n_kv_heads * kv4_row_bytes(head_dim) % 16:

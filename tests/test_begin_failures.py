@@ -134,3 +134,12 @@ def test_contexts_of_a_4_bit_cache_are_not_grouped():
         batch = eng.decode_begin(seqs)
         assert batch.num_groups == (1 if bits == 16 else 0) and eng.dev.calls == (2 if bits == 16 else 1)
         eng.decode_end(batch)
+
+
+@pytest.mark.parametrize("hq,hkv", [(17, 1), (34, 2), (3, 2)])
+def test_head_counts_that_4_bit_decode_refuses_are_refused_before_any_prompt(hq, hkv):
+    args = dict(layers=1, head_dim=64, dtype=torch.float32, num_slots=64, max_reqs=2, max_ctx=32, device="cpu",
+                kv_bits=4)
+    with pytest.raises(ValueError):
+        serving.Engine(n_q_heads=hq, n_kv_heads=hkv, **args)
+    assert serving.Engine(n_q_heads=16 * hkv, n_kv_heads=hkv, **args).kv_bits == 4
