@@ -688,7 +688,8 @@ int rc_sparse_decode_attention(const rc_sparse_decode_args* args, void* workspac
  *   minimum = lo rounded down to bf16 (+0 for -0)
  *   scale   = (hi - minimum) / 15 rounded up to four significant bits, at least 2^-80
  *   code    = the integer nearest to (x - minimum) * (1 / scale), ties to even
- * so an element is at most half a scale (and a relative 2^-20 of it) from what it stands for. A group that
+ * so an element is at most half a scale, and what fp32 adds (45 * 2^-24 of a scale), from what it stands
+ * for. A group that
  * holds a NaN or a magnitude of 2^30 and more has NaN as scale and minimum: all its elements read as
  * NaN.
  *

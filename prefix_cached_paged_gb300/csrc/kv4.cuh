@@ -3,7 +3,8 @@
 //   minimum = lo rounded down to bf16
 //   scale   = (hi - minimum) / 15 rounded up to four significant bits, at least 2^-80
 //   code    = the integer nearest to (x - minimum) * (1 / scale), ties to even: 0 .. 15
-// and the element stands for code * scale + minimum, at most half a scale from x. The scale's four bits
+// and the element stands for code * scale + minimum, at most half a scale from x and what the three fp32
+// roundings add, 45 * 2^-24 of a scale (a code of 15 moves by 15 * 3 half steps). The scale's four bits
 // make code * scale exact in bf16, which is what attention feeds the matrix units with; they cost
 // at most an eighth of the step, 4 % on average. A group that holds a NaN, an infinity or a magnitude of
 // 2^30 and more has NaN as scale and minimum.

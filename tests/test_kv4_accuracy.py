@@ -245,3 +245,37 @@ def test_every_token_counts_once(dtype, hq, hkv, d):
         want = ((marks < n[..., None]) / n[..., None]).repeat_interleave(hq // hkv, 1)
         assert (beyond(o, want, 2 * T.U * want, q.dtype) <= 0).all()
     assert rc.device_status() == 0
+
+
+def test_elements_are_within_half_a_scale_and_what_fp32_adds():
+    """The code's difference, reciprocal and product are off by 3 half steps of fp32, 45 * 2^-24 of a scale at a code
+    of 15. More than 2^-20 of half a scale happens: the first row."""
+    g = torch.Generator().manual_seed(3)
+    x = torch.rand((20_000, 32), generator=g) * torch.rand((20_000, 1), generator=g) - 0.9
+    x[0] = torch.linspace(-0.9199936, -0.09474992, 32)
+    x[0, 5] = -0.24804693
+    x = torch.cat([x, x], 1)
+    code, step, low = T.groups_of(R.quantise(x), 64)
+    off = (code * step + low - x.double()).abs() / step - 0.5
+    assert off.max() <= 45 * 2.0 ** -24
+    assert off[0, 5] > 2.0 ** -20 / 2 and step[0, 5] == 0.05859375
+
+
+@pytest.mark.gpu
+def test_the_quotient_by_15_of_every_significand():
+    """Groups of 0 and w for all 2^23 significands of w: the scale is w / 15, rounded to fp32 and then up to four
+    significant bits. (A 64-bit quotient rounded to 24 bits is the quotient rounded once: 53 >= 2 * 24 + 2.)"""
+    n = 1 << 20
+    loc = torch.arange(n, dtype=torch.int32, device="cuda")
+    ip = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    kp, vp = (torch.zeros((n, 1, 40), dtype=torch.uint8, device="cuda") for _ in "kv")
+    x = torch.zeros((n, 1, 64), device="cuda")
+    for part in range(0, 1 << 23, 2 * n):
+        w = torch.arange(part, part + 2 * n, device="cuda").double() * 2.0 ** -23 + 1
+        x[:, 0, 9], x[:, 0, 40] = w[:n].float(), w[n:].float()
+        rc.kv4_append(x, x, loc, ip, kp, vp)
+        mant, e = torch.frexp((w / 15).float().double())
+        want = torch.ldexp((mant * 16).ceil() / 16, e)
+        got = kp[:, 0, 32:].contiguous().view(torch.bfloat16).double()
+        assert torch.equal(torch.cat([got[:, 0], got[:, 2]]), want) and not got[:, 1::2].any()
+    assert torch.equal(kp, vp) and rc.device_status() == 0
