@@ -8,10 +8,10 @@
 // number code * 2^-133 or 16 times that, subnormal or next to it, which the units take as it is.
 //
 // Bound by HBM on paper: 160 bytes for a token and KV head of 128. Next to it stands instruction issue:
-// an SM has 23 bytes a clock of HBM, so 3.5 instruction lanes for each code; of about 345 warp
-// instructions for 16 tokens of a head 100 are the scores', 125 the values'. 128 rows of 512 .. 8192 tokens,
-// 32 + 32 heads: 338 us, 4.85 TB/s (floor 242); without the scores or without the values it would be
-// 275, the copies' own time 268.
+// an SM has 23 bytes a clock of HBM, so 3.5 instruction lanes for each code; 16 tokens of a head take 418 warp
+// instructions, waits among them. 128 rows of 512 .. 8192 tokens, 32 + 32 heads: 405 us, 4.06 TB/s
+// (floor 242; the copies alone 268). 57 % of issue slots are used and no pipe is: 16 warps on an SM, each a chain
+// of scores, exponentials and values, are few.
 //
 // Work split: the steps of all (row, group of KV heads) pairs in one line, cut into as many equal ranges as
 // CTAs fit on the GPU at once, so long and short rows share them evenly; states of a pair that
@@ -64,8 +64,8 @@ struct Cfg {
   static constexpr bool F32 = sizeof(T) == 4;
   static constexpr int QP = F32 ? 3 : 1;     // bf16 parts of a query element
   static constexpr int UNIT = F32 ? 2 : 7;   // scores are summed in 2^-UNIT
-  // of a weight: all its 24 bits. Two parts (16 bits) for bf16: 393 -> 348 us on 128 rows of 512 .. 8192
-  // tokens, 32 + 32 heads, and 0.22 % of outputs unlike those of 64 bits instead of 0.11
+  // of a weight: all its 24 bits. Two parts (16 bits) would take 357 us instead of 405 on 128 rows of
+  // 512 .. 8192 tokens, 32 + 32 heads, with 0.22 % of bf16 outputs unlike those of 64 bits instead of 0.11
   static constexpr int PP = 3;
   static constexpr int WARPS = NT > 1 || F32 ? 4 : 8;               // of a CTA, at most
   static constexpr int PER_SM = 2;                                  // CTAs of so many warps
@@ -658,9 +658,9 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           // code * 2^-133 (16 times that) times scale * 2^96, less 8 scales: eight bits, exact. Around
-          // the groups' middles the sums stay small and lose less: with sums of code * scale 3.1 % of
-          // bf16 outputs are unlike those of 64 bits on a row of 131 071 tokens, so 0.9 (326 and
-          // 338 us on 128 rows of 512 .. 8192 tokens, 32 + 32 heads)
+          // the groups' middles the sums stay small and lose less: with sums of code * scale, kept in the
+          // matrix unit, 3.1 % of bf16 outputs were unlike those of 64 bits on a row of 131 071 tokens,
+          // so 0.9 (326 and 338 us on 128 rows of 512 .. 8192 tokens, 32 + 32 heads); now 0.07
           const uint32_t va = v01 >> 8 * k, vb = v23 >> 8 * k;
           const uint32_t a0 = va & 0x000F000Fu, a1 = va & 0x00F000F0u;
           const uint32_t a2 = vb & 0x000F000Fu, a3 = vb & 0x00F000F0u;
@@ -669,7 +669,7 @@ kv4_decode_kernel(const __grid_constant__ Params p) {
         }
         // sums of 16 tokens from zero, the least parts first, and those added in fp32: a matrix instruction
         // cuts its sums off, always towards zero (kept there, sums of 32 000 positive values were 800 half
-        // steps of fp32 too small; 128 rows of 512 .. 8192 tokens, 32 + 32 heads, take 337 -> 348 us)
+        // steps of fp32 too small, for 3 % less time)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float d[2][4];
